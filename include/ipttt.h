@@ -359,6 +359,133 @@ ipttt_status ipttt_z_backward_saved(const ipttt_problem *p, const void *H, const
                                     float *dW_gate, float *dW_up, void *ws, size_t ws_bytes,
                                     void *stream);
 
+/* ---------------------------------------------------------- attention half
+ *
+ * The other half of a block around the layer, over the same packed documents,
+ * streamed pieces and single tokens: the norm and position rotation of query
+ * and key heads, and causal attention with grouped heads.  fp32 arithmetic
+ * (fp32 data: fp32 matrix products), outputs rounded to dtype once; inside
+ * the attention the probabilities and their gradients are rounded to dtype
+ * once more, as operands of the matrix cores. */
+
+/* A [rows, heads, head_dim] tensor of dtype on the device: element (r, h, i)
+ * at data[r * row_stride + h * head_stride + i].  Slices of a fused projection
+ * and caches in either order of tokens and heads are such tensors.  Strides
+ * count elements, are multiples of 8 and at least head_dim; row_stride is at
+ * most 2^22.  data is 16-byte aligned. */
+typedef struct {
+  void *data;
+  int64_t row_stride, head_stride;
+} ipttt_heads;
+
+typedef struct {
+  int64_t tokens;      /* 1 .. 2^26 - 4                                          */
+  int64_t heads;       /* query heads, 1 .. 4096                                 */
+  int64_t kv_heads;    /* key (and value) heads, 1 .. 4096                       */
+  int64_t head_dim;    /* D: multiple of 8, 8 .. 128                             */
+  int64_t table_rows;  /* positions of the cos, sin table                        */
+  int64_t out_rows;    /* rows of k_out and v_out                                */
+  int32_t dtype;       /* ipttt_dtype                                            */
+  float eps;           /* added to the mean square; finite, >= 0                 */
+} ipttt_qk_problem;
+
+/* Per-head RMS norm and position rotation of queries and keys.  For each head
+ * x of each token, with r = 1 / sqrt(mean(x^2) + eps), y = x * r * w and the
+ * table row (c, s) of the token's position, for i < D/2:
+ *   out[i] = y[i] c[i] - y[i + D/2] s[i],   out[i + D/2] = y[i + D/2] c[i] + y[i] s[i].
+ *   q [tokens, heads, D], k [tokens, kv_heads, D]
+ *   w_q, w_k [D] (dtype)
+ *   positions [tokens] int32 (device); a token whose position is outside the
+ *             table gets NaN outputs
+ *   table     [table_rows, D] float: D/2 cosines, then D/2 sines
+ *   q_out [tokens, heads, D], k_out [out_rows, kv_heads, D] out; each may be
+ *             its input (same data and strides; k only without rows)
+ *   rows      NULL (token t's key goes to row t: out_rows >= tokens), or
+ *             [tokens] int32 (device): the row of k_out, such as a cache's,
+ *             that token t's key goes to.  A row outside [0, out_rows) drops
+ *             that token's key; rows given twice get one of the two.
+ *   v, v_out  NULL, or v [tokens, kv_heads, D] copied to the same rows of
+ *             v_out [out_rows, kv_heads, D]
+ * One launch. */
+ipttt_status ipttt_qk_norm_rope(const ipttt_qk_problem *p, const ipttt_heads *q, const ipttt_heads *k,
+                                const void *w_q, const void *w_k, const int32_t *positions,
+                                const float *table, const ipttt_heads *q_out, const ipttt_heads *k_out,
+                                const ipttt_heads *v, const ipttt_heads *v_out, const int32_t *rows,
+                                void *stream);
+
+/* Its gradients: from the cotangents dq_out [tokens, heads, D] and dk_out
+ * [tokens, kv_heads, D] of the outputs, dq and dk (same shapes, dtype) and
+ * dw_q, dw_k [D] float, summed over tokens and heads in a fixed order.  q, k,
+ * w_q, w_k, positions and table as in the forward (which saves nothing); dq
+ * may be dq_out and dk may be dk_out.  out_rows is not used.
+ * ws: ipttt_qk_backward_workspace_bytes(p), 256-byte aligned. */
+size_t ipttt_qk_backward_workspace_bytes(const ipttt_qk_problem *p);
+ipttt_status ipttt_qk_norm_rope_backward(const ipttt_qk_problem *p, const ipttt_heads *q,
+                                         const ipttt_heads *k, const void *w_q, const void *w_k,
+                                         const int32_t *positions, const float *table,
+                                         const ipttt_heads *dq_out, const ipttt_heads *dk_out,
+                                         const ipttt_heads *dq, const ipttt_heads *dk, float *dw_q,
+                                         float *dw_k, void *ws, size_t ws_bytes, void *stream);
+
+/* Sequences of an attention call.  Sequence i's queries are rows q_start[i] ..
+ * + q_len[i] of Q, its keys rows k_start[i] .. + k_len[i] of K and V; its
+ * queries are the last q_len positions of its keys: query t sees keys
+ *   j < k_len - q_len + t + 1
+ * (a whole prompt: q_len = k_len; a streamed piece: q_len < k_len, K and V in
+ * a cache; a single token: q_len = 1; a query before the first key sees none).
+ * Lengths may be 0.  Query ranges must be in order and must not overlap; key
+ * ranges may lie in any order, and may overlap in the forward (a shared
+ * prefix).  Rows in no range are neither read nor written. */
+typedef struct {
+  int64_t n_seqs;      /* 1 or more                                              */
+  int64_t heads;       /* query heads, 1 .. 4096, a multiple of kv_heads         */
+  int64_t kv_heads;    /* query head h reads key head h / (heads / kv_heads)     */
+  int64_t head_dim;    /* D: multiple of 8, 8 .. 128                             */
+  int64_t q_rows;      /* rows of Q, O, lse and their gradients                  */
+  int64_t k_rows;      /* rows of K, V and their gradients                       */
+  int32_t dtype;       /* ipttt_dtype                                            */
+  const int64_t *q_start, *q_len, *k_start, *k_len; /* HOST arrays [n_seqs], read
+                          during the call only                                   */
+} ipttt_attn_problem;
+
+/* The plan: how the sequences are cut into tiles, and long key ranges with few
+ * queries into parts that are joined afterwards.  ipttt_attn_plan writes it to
+ * a HOST buffer of ipttt_attn_plan_bytes(p) bytes (8-byte aligned; 0 for an
+ * invalid problem; no device is touched).  The caller copies those bytes to
+ * the device once and hands both copies to every call over these sequences,
+ * of all layers of a step: `plan` (HOST: the calls read its first 128 bytes)
+ * and `plan_dev` (DEVICE, 16-byte aligned, complete in stream order before
+ * the call).  The bytes are opaque and belong to this build of the library. */
+ipttt_status ipttt_attn_validate(const ipttt_attn_problem *p);
+size_t ipttt_attn_plan_bytes(const ipttt_attn_problem *p);
+ipttt_status ipttt_attn_plan(const ipttt_attn_problem *p, void *plan, size_t plan_bytes);
+
+/* Workspaces of the two calls (0: none needed, ws may be NULL; or not a plan). */
+size_t ipttt_attn_workspace_bytes(const void *plan);
+size_t ipttt_attn_backward_workspace_bytes(const void *plan);
+
+/* Attention forward: with s = scale q.k over the keys a query sees,
+ *   O = softmax(s) V,   lse = log sum e^s   (a query that sees nothing: 0, -inf).
+ *   q, o [q_rows, heads, D]     k, v [k_rows, kv_heads, D]
+ *   lse  [q_rows, heads] float out, contiguous
+ *   scale  finite, > 0
+ * Keys of a sequence that only some rows see are multiplied by 0 for the
+ * others, so V must be finite there; keys and values past k_len are not read. */
+ipttt_status ipttt_attention(const void *plan, const void *plan_dev, float scale, const ipttt_heads *q,
+                             const ipttt_heads *k, const ipttt_heads *v, const ipttt_heads *o, float *lse,
+                             void *ws, size_t ws_bytes, void *stream);
+
+/* Attention backward: the gradients of <O, dO> with respect to q, k and v, from
+ * the forward's o and lse for the same plan, scale, q, k and v.  dk and dv sum
+ * over the queries of every head of a group, in a fixed order (no atomics); keys
+ * that no query sees get 0.  IPTTT_ERR_SEGMENTS if two sequences share keys.
+ *   dO, dq [q_rows, heads, D]     dk, dv [k_rows, kv_heads, D] */
+ipttt_status ipttt_attention_backward(const void *plan, const void *plan_dev, float scale,
+                                      const ipttt_heads *q, const ipttt_heads *k, const ipttt_heads *v,
+                                      const ipttt_heads *o, const float *lse, const ipttt_heads *dO,
+                                      const ipttt_heads *dq, const ipttt_heads *dk, const ipttt_heads *dv,
+                                      void *ws, size_t ws_bytes, void *stream);
+
 /* ---- measurement aid (not a step of the method) --------------------------
  *
  * When a hook is set, every entry point calls hook(kernel, stream, user) on
@@ -366,7 +493,7 @@ ipttt_status ipttt_z_backward_saved(const ipttt_problem *p, const void *H, const
  * small kernels) on `stream`, with a short name: "gated_z", "segments",
  * "target_prep", "conv", "target_gemm", "gram_v", "gram", "alpha",
  * "scale_rows", "scan", "apply", and the backward's "rscan_fast", "nt",
- * "tn_fast", ...  A
+ * "tn_fast", ..., the attention half's "qk", "attn_fwd", "attn_join", ...  A
  * profiler records a stream event in the hook and times each kernel between
  * consecutive events on the stream's own timeline.  The hook must not call
  * back into the library.  NULL (the default) disables it.  The setting is

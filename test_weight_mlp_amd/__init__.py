@@ -27,6 +27,8 @@ __all__ = [
     "ipttt_z_backward", "Grads", "backward", "ipttt_saved_bytes", "ipttt_scan_apply_save",
     "ipttt_scan_apply_backward_saved", "ipttt_z_save", "ipttt_z_backward_saved", "ipttt_chunk_delta_noalloc",
     "IPTTT_NOALLOC_SCRATCH_BYTES", "ipttt_set_launch_hook",
+    "QKProblem", "QKGrads", "ipttt_qk_backward_workspace_bytes", "ipttt_qk_norm_rope", "ipttt_qk_norm_rope_backward",
+    "AttentionPlan", "AttentionBuffers", "ipttt_attention", "ipttt_attention_backward", "rotation_table",
 ]
 
 IPTTT_F32 = 0
@@ -419,3 +421,8 @@ def backward(p: Problem, buf: Buffers, H, X0, W_gate, W_up, W_down, conv_w, W_ta
     else:
         ipttt_z_backward(p, H, W_gate, W_up, g.dZ, g.dH, g.dW_gate, g.dW_up, g.ws, stream)
     return g
+
+
+from .attention import (AttentionBuffers, AttentionPlan, QKGrads, QKProblem, ipttt_attention,  # noqa: E402
+                        ipttt_attention_backward, ipttt_qk_backward_workspace_bytes, ipttt_qk_norm_rope,
+                        ipttt_qk_norm_rope_backward, rotation_table)

@@ -1,0 +1,88 @@
+// Attention: the plan's items and the launchers the C ABI layer calls.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stdint.h>
+
+namespace ipttt {
+namespace attn {
+
+// Tile sizes the plan cuts sequences into.  Rows are the flat (query, head of
+// the group) rows of one key head: row r is query r / G, head r % G of the group.
+constexpr int kRows = 128;      // rows of a forward tile, and of a dQ tile
+constexpr int kKeys = 64;       // keys of one step
+constexpr int kBwdKeys = 128;   // keys of a dK, dV tile
+constexpr int kBwdRows = 64;    // rows of one step of a dK, dV tile
+
+// One forward (or dQ) tile: rows [r0, min(r0 + tile rows, q_len * G)) of one
+// sequence over keys [k_begin, k_end) of it.  Query t sees keys below off + t + 1.
+struct RowItem {
+  int32_t q_start, q_len, r0;
+  int32_t k_start, off;      // off = k_len - q_len
+  int32_t k_begin, k_end;
+  int32_t part;              // -1: the whole of the rows' keys; else the slot of this partial result
+};
+
+// The partial results of one forward tile, slots [part, part + n).
+struct JoinItem {
+  int32_t q_start, q_len, r0, part, n;
+};
+
+// One dK, dV tile: keys [key0, min(key0 + kBwdKeys, k_len)) of one sequence
+// against its rows [r_begin, q_len * G).
+struct KeyItem {
+  int32_t q_start, q_len, r_begin;
+  int32_t k_start, k_len, off;
+  int32_t key0, part;
+};
+
+// What the plan table starts with; the items follow at these offsets (bytes).
+struct PlanHeader {
+  int32_t magic, dtype, heads, kv_heads, head_dim, n_seqs;
+  int32_t q_rows, k_rows;
+  int32_t n_rows, n_join, n_dq, n_key;
+  int32_t o_rows, o_join, o_dq, o_key;
+  int32_t parts, overlap;    // partial slots; whether two sequences share keys
+  int32_t bytes, pad[13];
+};
+static_assert(sizeof(PlanHeader) == 128, "plan header");
+constexpr int32_t kMagic = 0x41545031;
+
+struct View {             // [rows, heads, D] with element strides
+  void* p;
+  int64_t row, head;
+};
+
+struct Args {
+  int dtype, heads, kv_heads, G, D;
+  float scale;
+  const void* items;      // device
+  int n_items;
+  View q, k, v, o, dO, dq, dk, dv;
+  float *lse, *delta;     // [q rows, heads]
+  float *part_o, *part_lse;
+};
+
+hipError_t launch_forward(const Args& a, hipStream_t st);
+hipError_t launch_join(const Args& a, const void* items, int n, hipStream_t st);
+hipError_t launch_dq(const Args& a, hipStream_t st);
+hipError_t launch_dkv(const Args& a, hipStream_t st);
+
+}  // namespace attn
+
+struct QkArgs {
+  int dtype, heads, kv_heads, D;
+  int64_t tokens, table_rows, out_rows;
+  float eps;
+  attn::View q, k, v, q_out, k_out, v_out;   // backward: q_out, k_out are the cotangents
+  attn::View dq, dk;
+  const void *w_q, *w_k;
+  const int32_t *pos, *rows;
+  const float* table;
+  float *dw_q, *dw_k, *part;
+};
+constexpr int kQkParts = 512;   // partial weight gradients of the backward
+hipError_t launch_qk(const QkArgs& a, hipStream_t st);
+hipError_t launch_qk_backward(const QkArgs& a, hipStream_t st);
+
+}  // namespace ipttt

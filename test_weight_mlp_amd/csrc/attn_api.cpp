@@ -1,0 +1,464 @@
+// C ABI of the attention half: argument validation, the plan (built on the
+// host), workspace layout and the launches.  Nothing is launched and nothing is
+// written unless every argument checks out; nothing here allocates or throws.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "../../include/ipttt.h"
+#include "attn.h"
+
+using ipttt::attn::JoinItem;
+using ipttt::attn::KeyItem;
+using ipttt::attn::kBwdKeys;
+using ipttt::attn::kKeys;
+using ipttt::attn::kMagic;
+using ipttt::attn::kRows;
+using ipttt::attn::PlanHeader;
+using ipttt::attn::RowItem;
+using ipttt::attn::View;
+
+namespace {
+
+constexpr int64_t kMaxInt = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxGroups = (int64_t(1) << 24) - 1;  // workgroups of 256 threads in a grid's x dimension
+constexpr int64_t kMaxHeads = 4096;
+constexpr int64_t kMaxRowStride = int64_t(1) << 22;
+constexpr int64_t kMaxHeadStride = int64_t(1) << 40;
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+ipttt_status hip_status(hipError_t e) { return e == hipSuccess ? IPTTT_OK : IPTTT_ERR_HIP; }
+
+ipttt_status check_dims(int64_t heads, int64_t kv_heads, int64_t head_dim, int32_t dtype) {
+  if (dtype != IPTTT_F32 && dtype != IPTTT_BF16) return IPTTT_ERR_DTYPE;
+  if (heads < 1 || heads > kMaxHeads || kv_heads < 1 || kv_heads > kMaxHeads) return IPTTT_ERR_SHAPE;
+  if (head_dim < 8 || head_dim > 128 || head_dim % 8 != 0) return IPTTT_ERR_SHAPE;
+  return IPTTT_OK;
+}
+
+// One tensor of heads.  A tile's rows are addressed with 32-bit byte offsets
+// from the tile's first row: `rows` rows and `heads` heads have to fit.
+ipttt_status check_heads(const ipttt_heads* t, int64_t heads, int64_t rows, int64_t D, int32_t dtype, View* v) {
+  if (t == nullptr || t->data == nullptr) return IPTTT_ERR_NULL;
+  if (!aligned(t->data, 16)) return IPTTT_ERR_ALIGN;
+  if (t->row_stride < D || t->head_stride < D || t->row_stride % 8 != 0 || t->head_stride % 8 != 0)
+    return IPTTT_ERR_SHAPE;
+  if (t->row_stride > kMaxRowStride || t->head_stride > kMaxHeadStride) return IPTTT_ERR_SHAPE;
+  const int64_t es = dtype == IPTTT_BF16 ? 2 : 4;
+  if ((rows * t->row_stride + (heads - 1) * t->head_stride + D) * es > kMaxInt - 15) return IPTTT_ERR_SHAPE;
+  *v = View{t->data, t->row_stride, t->head_stride};
+  return IPTTT_OK;
+}
+
+// ------------------------------------------------------------------- plan
+
+ipttt_status check_attn(const ipttt_attn_problem* p) {
+  if (p == nullptr) return IPTTT_ERR_NULL;
+  const ipttt_status s = check_dims(p->heads, p->kv_heads, p->head_dim, p->dtype);
+  if (s != IPTTT_OK) return s;
+  if (p->heads % p->kv_heads != 0) return IPTTT_ERR_SHAPE;
+  if (p->n_seqs < 1 || p->n_seqs > kMaxInt || p->q_rows < 0 || p->k_rows < 0) return IPTTT_ERR_SHAPE;
+  const int64_t G = p->heads / p->kv_heads;
+  // flat rows, and the rows and keys of a tile past them, fit 31 bits
+  if (p->q_rows > (kMaxInt >> 1) / G - 512 || p->k_rows > (kMaxInt >> 1) / G - 512) return IPTTT_ERR_SHAPE;
+  if (p->q_start == nullptr || p->q_len == nullptr || p->k_start == nullptr || p->k_len == nullptr)
+    return IPTTT_ERR_NULL;
+  int64_t end = 0;
+  for (int64_t i = 0; i < p->n_seqs; ++i) {
+    if (p->q_len[i] < 0 || p->k_len[i] < 0 || p->q_start[i] < end || p->k_start[i] < 0) return IPTTT_ERR_SEGMENTS;
+    if (p->q_len[i] > p->q_rows || p->q_start[i] > p->q_rows - p->q_len[i]) return IPTTT_ERR_SEGMENTS;
+    if (p->k_len[i] > p->k_rows || p->k_start[i] > p->k_rows - p->k_len[i]) return IPTTT_ERR_SEGMENTS;
+    end = p->q_start[i] + p->q_len[i];
+  }
+  return IPTTT_OK;
+}
+
+int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Keys that some row of the tile [r0, r0 + n) of sequence i sees.
+int64_t tile_keys(const ipttt_attn_problem* p, int64_t i, int64_t r0, int64_t n) {
+  const int64_t G = p->heads / p->kv_heads, last = std::min(r0 + n, p->q_len[i] * G) - 1;
+  return std::max<int64_t>(0, p->k_len[i] - p->q_len[i] + last / G + 1);
+}
+
+// Keys of one part.  Workgroups that can run at once (two a CU) share the keys
+// of all tiles evenly when there are fewer tiles than that; a part is at least
+// four steps long, so that its join costs little beside it.
+int64_t part_keys(const ipttt_attn_problem* p) {
+  constexpr int64_t kGroups = 512, kLeast = 4 * kKeys;
+  const int64_t G = p->heads / p->kv_heads;
+  int64_t tiles = 0, keys = 0;
+  for (int64_t i = 0; i < p->n_seqs; ++i)
+    for (int64_t r0 = 0; r0 < p->q_len[i] * G; r0 += kRows) {
+      ++tiles;
+      keys += tile_keys(p, i, r0, kRows);
+    }
+  if (tiles * p->kv_heads >= kGroups) return kMaxInt;
+  return div_up(std::max(kLeast, div_up(keys * p->kv_heads, kGroups)), kKeys) * kKeys;
+}
+
+// Walks every item of the plan in sequence order.
+template <class Rows, class Join, class Dq, class Key>
+void walk(const ipttt_attn_problem* p, int64_t part, Rows&& rows, Join&& join, Dq&& dq, Key&& key) {
+  const int64_t G = p->heads / p->kv_heads;
+  int64_t slots = 0;
+  for (int64_t i = 0; i < p->n_seqs; ++i) {
+    const int32_t off = (int32_t)(p->k_len[i] - p->q_len[i]);
+    const int32_t qs = (int32_t)p->q_start[i], ql = (int32_t)p->q_len[i], ks = (int32_t)p->k_start[i],
+                  kl = (int32_t)p->k_len[i];
+    for (int64_t r0 = 0; r0 < p->q_len[i] * G; r0 += kRows) {
+      const int64_t n = tile_keys(p, i, r0, kRows), parts = n > part ? div_up(n, part) : 1;
+      dq(RowItem{qs, ql, (int32_t)r0, ks, off, 0, (int32_t)n, -1});
+      if (parts == 1) {
+        rows(RowItem{qs, ql, (int32_t)r0, ks, off, 0, (int32_t)n, -1});
+        continue;
+      }
+      join(JoinItem{qs, ql, (int32_t)r0, (int32_t)slots, (int32_t)parts});
+      for (int64_t j = 0; j < parts; ++j)
+        rows(RowItem{qs, ql, (int32_t)r0, ks, off, (int32_t)(j * part), (int32_t)std::min(n, (j + 1) * part),
+                     (int32_t)slots++});
+    }
+    for (int64_t k0 = 0; k0 < p->k_len[i]; k0 += kBwdKeys) {
+      const int64_t t0 = std::min<int64_t>(p->q_len[i], std::max<int64_t>(0, k0 - off));
+      key(KeyItem{qs, ql, (int32_t)(t0 * G), ks, kl, off, (int32_t)k0, -1});
+    }
+  }
+}
+
+struct Range {
+  int64_t start, len;
+};
+
+struct Sizes {
+  int64_t rows = 0, join = 0, dq = 0, key = 0, parts = 0;
+  int64_t o_rows, o_join, o_dq, o_key, o_ranges, bytes;
+};
+
+// Counts and offsets; false if the plan would not fit its own 31-bit fields.
+bool sizes_of(const ipttt_attn_problem* p, int64_t part, Sizes* s) {
+  walk(
+      p, part,
+      [&](const RowItem& x) {
+        ++s->rows;
+        s->parts += x.part >= 0;
+      },
+      [&](const JoinItem&) { ++s->join; }, [&](const RowItem&) { ++s->dq; }, [&](const KeyItem&) { ++s->key; });
+  s->o_rows = sizeof(PlanHeader);
+  s->o_dq = s->o_rows + s->rows * (int64_t)sizeof(RowItem);
+  s->o_key = s->o_dq + s->dq * (int64_t)sizeof(RowItem);
+  s->o_join = s->o_key + s->key * (int64_t)sizeof(KeyItem);
+  s->o_ranges = (s->o_join + s->join * (int64_t)sizeof(JoinItem) + 15) / 16 * 16;
+  s->bytes = s->o_ranges + p->n_seqs * (int64_t)sizeof(Range);
+  const int64_t most = std::max(std::max(s->rows, s->dq), s->key);
+  return s->bytes <= kMaxInt && most <= kMaxGroups / p->kv_heads;
+}
+
+const PlanHeader* header(const void* plan) {
+  if (plan == nullptr || !aligned(plan, 8)) return nullptr;
+  const PlanHeader* h = static_cast<const PlanHeader*>(plan);
+  return h->magic == kMagic ? h : nullptr;
+}
+
+struct FwdLayout {
+  size_t o, lse, total;
+};
+FwdLayout fwd_layout(const PlanHeader* h) {
+  FwdLayout l;
+  const size_t rows = (size_t)h->parts * h->kv_heads * kRows;
+  l.o = 0;
+  l.lse = align256(rows * h->head_dim * sizeof(float));
+  l.total = l.lse + align256(rows * sizeof(float));
+  return l;
+}
+
+size_t bwd_bytes(const PlanHeader* h) { return align256((size_t)h->q_rows * h->heads * sizeof(float)); }
+
+ipttt_status check_call(const void* plan, const void* plan_dev, float scale, void* ws, size_t ws_bytes, size_t need) {
+  if (plan == nullptr || plan_dev == nullptr) return IPTTT_ERR_NULL;
+  if (!aligned(plan, 8) || !aligned(plan_dev, 16)) return IPTTT_ERR_ALIGN;
+  if (header(plan) == nullptr || !std::isfinite(scale) || scale <= 0.0f) return IPTTT_ERR_ARG;
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return IPTTT_ERR_WORKSPACE;
+  if (need > 0 && !aligned(ws, 256)) return IPTTT_ERR_ALIGN;
+  return IPTTT_OK;
+}
+
+// q and o by tiles of rows (of every head of a group), k and v by tiles of keys.
+// A tensor of no rows may be NULL: no tile reads or writes it.
+ipttt_status q_view(const PlanHeader* h, const ipttt_heads* t, View* v) {
+  if (h->q_rows == 0) return IPTTT_OK;
+  return check_heads(t, h->heads / h->kv_heads, kRows + 1, h->head_dim, h->dtype, v);
+}
+ipttt_status k_view(const PlanHeader* h, const ipttt_heads* t, View* v) {
+  if (h->k_rows == 0) return IPTTT_OK;
+  return check_heads(t, 1, kBwdKeys, h->head_dim, h->dtype, v);
+}
+
+ipttt::attn::Args base_args(const PlanHeader* h, float scale) {
+  ipttt::attn::Args a = {};
+  a.dtype = h->dtype;
+  a.heads = h->heads;
+  a.kv_heads = h->kv_heads;
+  a.G = h->heads / h->kv_heads;
+  a.D = h->head_dim;
+  a.scale = scale;
+  return a;
+}
+
+// ------------------------------------------------------- norm and rotation
+
+ipttt_status check_qk(const ipttt_qk_problem* p) {
+  if (p == nullptr) return IPTTT_ERR_NULL;
+  const ipttt_status s = check_dims(p->heads, p->kv_heads, p->head_dim, p->dtype);
+  if (s != IPTTT_OK) return s;
+  if (p->tokens < 1 || p->tokens > 4 * kMaxGroups || p->table_rows < 1 || p->table_rows > kMaxInt) return IPTTT_ERR_SHAPE;
+  if (p->out_rows < 0 || p->out_rows > kMaxInt) return IPTTT_ERR_SHAPE;
+  if (!std::isfinite(p->eps) || p->eps < 0.0f) return IPTTT_ERR_ARG;
+  return IPTTT_OK;
+}
+
+// Every address is 64-bit here: only the strides' own rules apply.
+ipttt_status qk_view(const ipttt_qk_problem* p, const ipttt_heads* t, View* v) {
+  return check_heads(t, 1, 1, p->head_dim, p->dtype, v);
+}
+
+bool same(const View& a, const View& b) { return a.p == b.p && a.row == b.row && a.head == b.head; }
+
+size_t qk_part_bytes(const ipttt_qk_problem* p) {
+  return align256((size_t)ipttt::kQkParts * 2 * (size_t)p->head_dim * sizeof(float));
+}
+
+ipttt::QkArgs qk_args(const ipttt_qk_problem* p, const void* w_q, const void* w_k, const int32_t* positions,
+                      const float* table) {
+  ipttt::QkArgs a = {};
+  a.dtype = p->dtype;
+  a.heads = (int)p->heads;
+  a.kv_heads = (int)p->kv_heads;
+  a.D = (int)p->head_dim;
+  a.tokens = p->tokens;
+  a.table_rows = p->table_rows;
+  a.out_rows = p->out_rows;
+  a.eps = p->eps;
+  a.w_q = w_q;
+  a.w_k = w_k;
+  a.pos = positions;
+  a.table = table;
+  return a;
+}
+
+ipttt_status check_qk_inputs(const void* w_q, const void* w_k, const int32_t* positions, const float* table) {
+  if (w_q == nullptr || w_k == nullptr || positions == nullptr || table == nullptr) return IPTTT_ERR_NULL;
+  if (!aligned(w_q, 16) || !aligned(w_k, 16) || !aligned(table, 16) || !aligned(positions, 4)) return IPTTT_ERR_ALIGN;
+  return IPTTT_OK;
+}
+
+}  // namespace
+
+#define IPTTT_TRY(expr)                       \
+  do {                                        \
+    const ipttt_status status_ = (expr);      \
+    if (status_ != IPTTT_OK) return status_;  \
+  } while (0)
+
+extern "C" {
+
+ipttt_status ipttt_qk_norm_rope(const ipttt_qk_problem* p, const ipttt_heads* q, const ipttt_heads* k, const void* w_q,
+                                const void* w_k, const int32_t* positions, const float* table,
+                                const ipttt_heads* q_out, const ipttt_heads* k_out, const ipttt_heads* v,
+                                const ipttt_heads* v_out, const int32_t* rows, void* stream) {
+  IPTTT_TRY(check_qk(p));
+  IPTTT_TRY(check_qk_inputs(w_q, w_k, positions, table));
+  ipttt::QkArgs a = qk_args(p, w_q, w_k, positions, table);
+  IPTTT_TRY(qk_view(p, q, &a.q));
+  IPTTT_TRY(qk_view(p, k, &a.k));
+  IPTTT_TRY(qk_view(p, q_out, &a.q_out));
+  IPTTT_TRY(qk_view(p, k_out, &a.k_out));
+  if ((v == nullptr) != (v_out == nullptr)) return IPTTT_ERR_NULL;
+  if (v != nullptr) {
+    IPTTT_TRY(qk_view(p, v, &a.v));
+    IPTTT_TRY(qk_view(p, v_out, &a.v_out));
+  }
+  if (!aligned(rows, 4)) return IPTTT_ERR_ALIGN;
+  if (rows == nullptr && p->out_rows < p->tokens) return IPTTT_ERR_SHAPE;
+  // an output over its input has to be that input, row for row
+  if (a.q_out.p == a.q.p && !same(a.q_out, a.q)) return IPTTT_ERR_ARG;
+  if (a.k_out.p == a.k.p && (rows != nullptr || !same(a.k_out, a.k))) return IPTTT_ERR_ARG;
+  a.rows = rows;
+  return hip_status(ipttt::launch_qk(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t ipttt_qk_backward_workspace_bytes(const ipttt_qk_problem* p) {
+  return check_qk(p) == IPTTT_OK ? qk_part_bytes(p) : 0;
+}
+
+ipttt_status ipttt_qk_norm_rope_backward(const ipttt_qk_problem* p, const ipttt_heads* q, const ipttt_heads* k,
+                                         const void* w_q, const void* w_k, const int32_t* positions,
+                                         const float* table, const ipttt_heads* dq_out, const ipttt_heads* dk_out,
+                                         const ipttt_heads* dq, const ipttt_heads* dk, float* dw_q, float* dw_k,
+                                         void* ws, size_t ws_bytes, void* stream) {
+  IPTTT_TRY(check_qk(p));
+  IPTTT_TRY(check_qk_inputs(w_q, w_k, positions, table));
+  ipttt::QkArgs a = qk_args(p, w_q, w_k, positions, table);
+  IPTTT_TRY(qk_view(p, q, &a.q));
+  IPTTT_TRY(qk_view(p, k, &a.k));
+  IPTTT_TRY(qk_view(p, dq_out, &a.q_out));
+  IPTTT_TRY(qk_view(p, dk_out, &a.k_out));
+  IPTTT_TRY(qk_view(p, dq, &a.dq));
+  IPTTT_TRY(qk_view(p, dk, &a.dk));
+  if (dw_q == nullptr || dw_k == nullptr) return IPTTT_ERR_NULL;
+  if (!aligned(dw_q, 16) || !aligned(dw_k, 16)) return IPTTT_ERR_ALIGN;
+  if (a.dq.p == a.q_out.p && !same(a.dq, a.q_out)) return IPTTT_ERR_ARG;
+  if (a.dk.p == a.k_out.p && !same(a.dk, a.k_out)) return IPTTT_ERR_ARG;
+  if (ws == nullptr || ws_bytes < qk_part_bytes(p)) return IPTTT_ERR_WORKSPACE;
+  if (!aligned(ws, 256)) return IPTTT_ERR_ALIGN;
+  a.dw_q = dw_q;
+  a.dw_k = dw_k;
+  a.part = static_cast<float*>(ws);
+  return hip_status(ipttt::launch_qk_backward(a, static_cast<hipStream_t>(stream)));
+}
+
+ipttt_status ipttt_attn_validate(const ipttt_attn_problem* p) {
+  IPTTT_TRY(check_attn(p));
+  Sizes s;
+  return sizes_of(p, part_keys(p), &s) ? IPTTT_OK : IPTTT_ERR_SHAPE;
+}
+
+size_t ipttt_attn_plan_bytes(const ipttt_attn_problem* p) {
+  Sizes s;
+  return check_attn(p) == IPTTT_OK && sizes_of(p, part_keys(p), &s) ? (size_t)s.bytes : 0;
+}
+
+ipttt_status ipttt_attn_plan(const ipttt_attn_problem* p, void* plan, size_t plan_bytes) {
+  IPTTT_TRY(check_attn(p));
+  const int64_t part = part_keys(p);
+  Sizes s;
+  if (!sizes_of(p, part, &s)) return IPTTT_ERR_SHAPE;
+  if (plan == nullptr || plan_bytes < (size_t)s.bytes) return IPTTT_ERR_WORKSPACE;
+  if (!aligned(plan, 8)) return IPTTT_ERR_ALIGN;
+  std::memset(plan, 0, (size_t)s.bytes);
+  char* base = static_cast<char*>(plan);
+  RowItem* rows = reinterpret_cast<RowItem*>(base + s.o_rows);
+  RowItem* dq = reinterpret_cast<RowItem*>(base + s.o_dq);
+  KeyItem* key = reinterpret_cast<KeyItem*>(base + s.o_key);
+  JoinItem* join = reinterpret_cast<JoinItem*>(base + s.o_join);
+  walk(p, part, [&](const RowItem& x) { *rows++ = x; }, [&](const JoinItem& x) { *join++ = x; },
+       [&](const RowItem& x) { *dq++ = x; }, [&](const KeyItem& x) { *key++ = x; });
+  // the longest first, so that the last workgroups to start are short ones
+  const auto longer = [](const RowItem& x, const RowItem& y) {
+    const int32_t a = x.k_end - x.k_begin, b = y.k_end - y.k_begin;
+    if (a != b) return a > b;
+    return x.q_start != y.q_start ? x.q_start < y.q_start : x.r0 != y.r0 ? x.r0 < y.r0 : x.k_begin < y.k_begin;
+  };
+  std::sort(rows - s.rows, rows, longer);
+  std::sort(dq - s.dq, dq, longer);
+  const int32_t G = (int32_t)(p->heads / p->kv_heads);
+  std::sort(key - s.key, key, [G](const KeyItem& x, const KeyItem& y) {
+    const int32_t a = x.q_len * G - x.r_begin, b = y.q_len * G - y.r_begin;
+    if (a != b) return a > b;
+    return x.k_start != y.k_start ? x.k_start < y.k_start : x.key0 < y.key0;
+  });
+  // whether two sequences share keys
+  Range* r = reinterpret_cast<Range*>(base + s.o_ranges);
+  int64_t n = 0;
+  for (int64_t i = 0; i < p->n_seqs; ++i)
+    if (p->k_len[i] > 0) r[n++] = Range{p->k_start[i], p->k_len[i]};
+  std::sort(r, r + n, [](const Range& x, const Range& y) { return x.start < y.start; });
+  bool overlap = false;
+  for (int64_t i = 1; i < n; ++i) overlap = overlap || r[i].start < r[i - 1].start + r[i - 1].len;
+
+  PlanHeader* h = static_cast<PlanHeader*>(plan);
+  h->magic = kMagic;
+  h->dtype = p->dtype;
+  h->heads = (int32_t)p->heads;
+  h->kv_heads = (int32_t)p->kv_heads;
+  h->head_dim = (int32_t)p->head_dim;
+  h->n_seqs = (int32_t)p->n_seqs;
+  h->q_rows = (int32_t)p->q_rows;
+  h->k_rows = (int32_t)p->k_rows;
+  h->n_rows = (int32_t)s.rows;
+  h->n_join = (int32_t)s.join;
+  h->n_dq = (int32_t)s.dq;
+  h->n_key = (int32_t)s.key;
+  h->o_rows = (int32_t)s.o_rows;
+  h->o_join = (int32_t)s.o_join;
+  h->o_dq = (int32_t)s.o_dq;
+  h->o_key = (int32_t)s.o_key;
+  h->parts = (int32_t)s.parts;
+  h->overlap = overlap;
+  h->bytes = (int32_t)s.bytes;
+  return IPTTT_OK;
+}
+
+size_t ipttt_attn_workspace_bytes(const void* plan) {
+  const PlanHeader* h = header(plan);
+  return h == nullptr ? 0 : fwd_layout(h).total;
+}
+
+size_t ipttt_attn_backward_workspace_bytes(const void* plan) {
+  const PlanHeader* h = header(plan);
+  return h == nullptr ? 0 : bwd_bytes(h);
+}
+
+ipttt_status ipttt_attention(const void* plan, const void* plan_dev, float scale, const ipttt_heads* q,
+                             const ipttt_heads* k, const ipttt_heads* v, const ipttt_heads* o, float* lse, void* ws,
+                             size_t ws_bytes, void* stream) {
+  IPTTT_TRY(check_call(plan, plan_dev, scale, ws, ws_bytes, ipttt_attn_workspace_bytes(plan)));
+  const PlanHeader* h = header(plan);
+  ipttt::attn::Args a = base_args(h, scale);
+  IPTTT_TRY(q_view(h, q, &a.q));
+  IPTTT_TRY(k_view(h, k, &a.k));
+  IPTTT_TRY(k_view(h, v, &a.v));
+  IPTTT_TRY(q_view(h, o, &a.o));
+  if (lse == nullptr && h->q_rows > 0) return IPTTT_ERR_NULL;
+  if (!aligned(lse, 16)) return IPTTT_ERR_ALIGN;
+  const FwdLayout l = fwd_layout(h);
+  a.lse = lse;
+  a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + l.o);
+  a.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + l.lse);
+  const char* dev = static_cast<const char*>(plan_dev);
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (h->n_rows == 0) return IPTTT_OK;
+  a.items = dev + h->o_rows;
+  a.n_items = h->n_rows;
+  IPTTT_TRY(hip_status(ipttt::attn::launch_forward(a, st)));
+  if (h->n_join == 0) return IPTTT_OK;
+  return hip_status(ipttt::attn::launch_join(a, dev + h->o_join, h->n_join, st));
+}
+
+ipttt_status ipttt_attention_backward(const void* plan, const void* plan_dev, float scale, const ipttt_heads* q,
+                                      const ipttt_heads* k, const ipttt_heads* v, const ipttt_heads* o,
+                                      const float* lse, const ipttt_heads* dO, const ipttt_heads* dq,
+                                      const ipttt_heads* dk, const ipttt_heads* dv, void* ws, size_t ws_bytes,
+                                      void* stream) {
+  IPTTT_TRY(check_call(plan, plan_dev, scale, ws, ws_bytes, ipttt_attn_backward_workspace_bytes(plan)));
+  const PlanHeader* h = header(plan);
+  if (h->overlap) return IPTTT_ERR_SEGMENTS;
+  ipttt::attn::Args a = base_args(h, scale);
+  IPTTT_TRY(q_view(h, q, &a.q));
+  IPTTT_TRY(k_view(h, k, &a.k));
+  IPTTT_TRY(k_view(h, v, &a.v));
+  IPTTT_TRY(q_view(h, o, &a.o));
+  IPTTT_TRY(q_view(h, dO, &a.dO));
+  IPTTT_TRY(q_view(h, dq, &a.dq));
+  IPTTT_TRY(k_view(h, dk, &a.dk));
+  IPTTT_TRY(k_view(h, dv, &a.dv));
+  if (lse == nullptr && h->q_rows > 0) return IPTTT_ERR_NULL;
+  if (!aligned(lse, 16)) return IPTTT_ERR_ALIGN;
+  a.lse = const_cast<float*>(lse);
+  a.delta = static_cast<float*>(ws);
+  const char* dev = static_cast<const char*>(plan_dev);
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (h->n_dq > 0) {
+    a.items = dev + h->o_dq;
+    a.n_items = h->n_dq;
+    IPTTT_TRY(hip_status(ipttt::attn::launch_dq(a, st)));
+  }
+  if (h->n_key > 0) {
+    a.items = dev + h->o_key;
+    a.n_items = h->n_key;
+    IPTTT_TRY(hip_status(ipttt::attn::launch_dkv(a, st)));
+  }
+  return IPTTT_OK;
+}
+
+}  // extern "C"
