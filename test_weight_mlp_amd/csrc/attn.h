@@ -12,7 +12,6 @@ namespace attn {
 constexpr int kRows = 128;      // rows of a forward tile, and of a dQ tile
 constexpr int kKeys = 64;       // keys of one step
 constexpr int kBwdKeys = 128;   // keys of a dK, dV tile
-constexpr int kBwdRows = 64;    // rows of one step of a dK, dV tile
 
 // One forward (or dQ) tile: rows [r0, min(r0 + tile rows, q_len * G)) of one
 // sequence over keys [k_begin, k_end) of it.  Query t sees keys below off + t + 1.
@@ -59,7 +58,7 @@ struct Args {
   const void* items;      // device
   int n_items;
   View q, k, v, o, dO, dq, dk, dv;
-  float *lse, *delta;     // [q rows, heads]
+  float *lse, *lse2, *delta;  // [q rows, heads]; lse2 = lse * log2(e), +inf on rows that see nothing
   float *part_o, *part_lse;
 };
 

@@ -172,7 +172,9 @@ FwdLayout fwd_layout(const PlanHeader* h) {
   return l;
 }
 
-size_t bwd_bytes(const PlanHeader* h) { return align256((size_t)h->q_rows * h->heads * sizeof(float)); }
+// lse2, then delta, of every row
+size_t row_stat_bytes(const PlanHeader* h) { return align256((size_t)h->q_rows * h->heads * sizeof(float)); }
+size_t bwd_bytes(const PlanHeader* h) { return 2 * row_stat_bytes(h); }
 
 ipttt_status check_call(const void* plan, const void* plan_dev, float scale, void* ws, size_t ws_bytes, size_t need) {
   if (plan == nullptr || plan_dev == nullptr) return IPTTT_ERR_NULL;
@@ -445,7 +447,8 @@ ipttt_status ipttt_attention_backward(const void* plan, const void* plan_dev, fl
   if (lse == nullptr && h->q_rows > 0) return IPTTT_ERR_NULL;
   if (!aligned(lse, 16)) return IPTTT_ERR_ALIGN;
   a.lse = const_cast<float*>(lse);
-  a.delta = static_cast<float*>(ws);
+  a.lse2 = static_cast<float*>(ws);
+  a.delta = reinterpret_cast<float*>(static_cast<char*>(ws) + row_stat_bytes(h));
   const char* dev = static_cast<const char*>(plan_dev);
   const hipStream_t st = static_cast<hipStream_t>(stream);
   if (h->n_dq > 0) {

@@ -10,121 +10,165 @@
 #include "attn.h"
 #include "launch.h"
 
+#include <type_traits>
+
 namespace ipttt {
 namespace attn {
 namespace {
 
+// Rows that see at most this many keys get delta = sum_j P dP from the keys
+// themselves (one pass more over them); the others from the forward's O.  In
+// bf16, O's rounding (2^-9 of it) goes into delta, and it is not small beside dP
+// while O averages few values: dQ's error against 64 bits, random data of 2, 64 and
+// 256 keys, is 0.0049, 0.0027, 0.0025 with O and 0.0024, 0.0024, 0.0023 without.
+constexpr int kExactDelta = 256;
+
 // dQ of one tile of 128 flat rows, 32 a wave: over the keys the rows see,
 // S^T = K Q^T and dP^T = V dO^T, then dQ^T += K^T dS^T with K read transposed.
+// Leaves lse * log2(e) and delta of its rows for the dK, dV kernel.
 template <typename T, int DP>
-__global__ __launch_bounds__(256, 1) void dq_kernel(Args a) {
+__device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kvh, const char* __restrict__ K,
+                                        const char* __restrict__ V, char* lds) {
   typedef Tile<T, DP> TL;
+  typedef Groups<T, DP> GR;
   typedef typename Elt<T>::frag frag;
-  constexpr int NW = 4, ES = sizeof(T), KT = sizeof(T) == 2 ? kKeys : kKeys / 2, TB = KT * TL::RB;
-  constexpr int EPL = Elt<T>::EPL;
-  __shared__ __attribute__((aligned(1024))) char lds[4 * TB];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5;
-  const int kvh = blockIdx.x % a.kv_heads;
-  const RowItem it = static_cast<const RowItem*>(a.items)[blockIdx.x / a.kv_heads];
-  const int G = a.G, D = a.D, n_rows = it.q_len * G;
+  constexpr int NW = 4, ES = sizeof(T), KT = ES == 2 ? kKeys : kKeys / 2, TB = TL::bytes(KT), EPL = Elt<T>::EPL;
+  constexpr int DB = DP / 32, H = GR::H;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
+  const int D = a.D;
   const float sl2 = a.scale * kLog2e;
+  const Row row(it, a.G, wave, lane);
+  const int64_t at = it.q_start + (int64_t)row.t;
+  const int head = kvh * a.G + row.g;
 
-  const RowMap rm(it.r0 + wave * 32, G);
-  const int r = it.r0 + wave * 32 + (lane & 31);
-  int t, g;
-  rm.of(lane & 31, &t, &g);
-  t += rm.t0;
-  const bool live = r < n_rows;
-  const int lim = live ? min(it.off + t + 1, it.k_end) : 0;
-  const int all = __builtin_amdgcn_readfirstlane(min(it.off + rm.t0 + 1, it.k_end));
-  const int r_last = min(it.r0 + wave * 32 + 31, n_rows - 1);
-  const int any = __builtin_amdgcn_readfirstlane(
-      it.r0 + wave * 32 < n_rows ? min(it.off + r_last / G + 1, it.k_end) : 0);
-  const int64_t row = it.q_start + (int64_t)t;
-  const int head = kvh * G + g;
+  const At<T, DP> here(lane);
+  const RowStream<T, DP, NW, KT> ks(a.k.row, D, wave, lane), vs(a.v.row, D, wave, lane);
+  const int k_len = it.off + it.q_len, steps = (it.k_end + KT - 1) / KT;
+  auto load = [&](int s, int buf) {
+    ks.issue(K, (int64_t)it.k_start + s * KT, k_len - s * KT, lds + 2 * buf * TB, wave);
+    vs.issue(V, (int64_t)it.k_start + s * KT, k_len - s * KT, lds + (2 * buf + 1) * TB, wave);
+  };
+  if (steps > 0) load(0, 0);
 
   frag qf[TL::STEPS], df[TL::STEPS];
-  row_frags<T, DP>(static_cast<const char*>(a.q.p) + (row * a.q.row + head * a.q.head) * ES, live, D, h, qf);
-  row_frags<T, DP>(static_cast<const char*>(a.dO.p) + (row * a.dO.row + head * a.dO.head) * ES, live, D, h, df);
+  row_frags<T, DP>(static_cast<const char*>(a.q.p) + (at * a.q.row + head * a.q.head) * ES, row.live, D, h, qf);
+  row_frags<T, DP>(static_cast<const char*>(a.dO.p) + (at * a.dO.row + head * a.dO.head) * ES, row.live, D, h, df);
+  float lse2 = INFINITY;  // P = 0 on rows that see nothing, and past the sequence
+  if (row.live) {
+    const float x = a.lse[at * a.heads + head];
+    if (x != -INFINITY) lse2 = x * kLog2e;
+  }
   float delta = 0.0f;
-  {
+  if (ES == 2 && it.k_end <= kExactDelta) {
+    for (int s = 0; s < steps; ++s) {
+      tiles_landed();
+      for (int kb = 0; kb < KT / 32; ++kb) {
+        floatx16 x, dp;
+        zero16(x);
+        zero16(dp);
+#pragma unroll
+        for (int q = 0; q < TL::STEPS; ++q) {
+          x = Elt<T>::mma(TL::row(lds, here.row, 32 * kb, q), qf[q], x);
+          dp = Elt<T>::mma(TL::row(lds + TB, here.row, 32 * kb, q), df[q], dp);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float p = __builtin_amdgcn_exp2f(fmaf(x[i], sl2, -lse2));
+          if (s * KT + 32 * kb + 8 * (i >> 2) + 4 * h + (i & 3) < row.lim) delta = fmaf(p, dp[i], delta);
+        }
+      }
+      tiles_landed();  // every wave is done with the tile
+      load(s + 1 < steps ? s + 1 : 0, 0);
+    }
+  } else {
     frag of[TL::STEPS];
-    row_frags<T, DP>(static_cast<const char*>(a.o.p) + (row * a.o.row + head * a.o.head) * ES, live, D, h, of);
+    row_frags<T, DP>(static_cast<const char*>(a.o.p) + (at * a.o.row + head * a.o.head) * ES, row.live, D, h, of);
 #pragma unroll
     for (int s = 0; s < TL::STEPS; ++s)
 #pragma unroll
       for (int e = 0; e < EPL; ++e) delta = fmaf((float)of[s][e], (float)df[s][e], delta);
-    delta += other_half(delta);
   }
-  float lse2 = INFINITY;  // P = 0 on rows that see nothing, and past the sequence
-  if (live) {
-    const float x = a.lse[row * a.heads + head];
-    if (x != -INFINITY) lse2 = x * kLog2e;
-    if (h == 0) a.delta[row * a.heads + head] = delta;
+  delta = half_sum(delta);
+  if (row.live && h == 0) {
+    a.lse2[at * a.heads + head] = lse2;
+    a.delta[at * a.heads + head] = delta;
   }
 
-  floatx16 acc[DP / 32];
+  floatx16 acc[DB];
 #pragma unroll
-  for (int db = 0; db < DP / 32; ++db)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[db][i] = 0.0f;
+  for (int db = 0; db < DB; ++db) zero16(acc[db]);
 
-  const uint32_t ks = (uint32_t)(a.k.row * ES), vs = (uint32_t)(a.v.row * ES);
-  const char* K = static_cast<const char*>(a.k.p) + (int64_t)kvh * a.k.head * ES;
-  const char* V = static_cast<const char*>(a.v.p) + (int64_t)kvh * a.v.head * ES;
-  const int k_len = it.off + it.q_len;
-  auto issue = [&](int key0, int buf) {
-    const int64_t at = (int64_t)it.k_start + key0, left = k_len - key0;
-    load_rows<T, DP, NW, KT>(rsrc_of(K + at * (int64_t)ks, (left - 1) * (int64_t)ks + D * ES), ks, D,
-                             lds + 2 * buf * TB, wave, lane);
-    load_rows<T, DP, NW, KT>(rsrc_of(V + at * (int64_t)vs, (left - 1) * (int64_t)vs + D * ES), vs, D,
-                             lds + (2 * buf + 1) * TB, wave, lane);
-  };
-  const int steps = (it.k_end + KT - 1) / KT;
-  if (steps > 0) issue(0, 0);
-  for (int st = 0; st < steps; ++st) {
-    const int key0 = st * KT;
-    __syncthreads();
-    if (st + 1 < steps) issue(key0 + KT, (st + 1) & 1);
-    if (key0 >= any) continue;
-    const char* kt = lds + 2 * (st & 1) * TB;
-    const char* vt = kt + TB;
+  auto step = [&](int st, auto odd) {
+    constexpr int B = decltype(odd)::value;
+    tiles_landed();
+    if (st + 1 < steps) load(st + 1, B ^ 1);
+    const char *kt = lds + 2 * B * TB, *vt = kt + TB;
+    frag f[2][4];
+    int cur = 0;
+    GR::rows(kt, here, 0, 0, f[0]);
 #pragma unroll
     for (int kb = 0; kb < KT / 32; ++kb) {
+      const int key0 = st * KT + 32 * kb;
       floatx16 s, dp;
+      zero16(s);
+      zero16(dp);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
+      for (int g = 0; g < H; ++g) {
+        if (g + 1 < H) GR::rows(kt, here, 32 * kb, g + 1, f[cur ^ 1]);
+        else GR::rows(vt, here, 32 * kb, 0, f[cur ^ 1]);
 #pragma unroll
-      for (int q = 0; q < TL::STEPS; ++q) {
-        s = Elt<T>::mma(TL::row(kt, 32 * kb + (lane & 31), 2 * q + h), qf[q], s);
-        dp = Elt<T>::mma(TL::row(vt, 32 * kb + (lane & 31), 2 * q + h), df[q], dp);
+        for (int x = 0; x < 4; ++x) s = Elt<T>::mma(f[cur][x], qf[4 * g + x], s);
+        cur ^= 1;
+        __builtin_amdgcn_sched_barrier(0);
       }
-      if (key0 + 32 * kb + 32 > all) {
+      if (key0 + 32 > row.all) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (key0 + 32 * kb + 8 * (i >> 2) + 4 * h + (i & 3) >= lim) s[i] = -INFINITY;
+          if (key0 + 8 * (i >> 2) + 4 * h + (i & 3) >= row.lim) s[i] = -INFINITY;
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], sl2, -lse2)) * (dp[i] - delta);
+      for (int g = 0; g < H; ++g) {
+        if (g + 1 < H) GR::rows(vt, here, 32 * kb, g + 1, f[cur ^ 1]);
+        else GR::cols(kt, here, 32 * kb, 0, f[cur ^ 1]);
+#pragma unroll
+        for (int i = g * (16 / H); i < (g + 1) * (16 / H); ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], sl2, -lse2));
+#pragma unroll
+        for (int x = 0; x < 4; ++x) dp = Elt<T>::mma(f[cur][x], df[4 * g + x], dp);
+        cur ^= 1;
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i] *= dp[i] - delta;
       // a softmax over one key has no gradient: exactly 0, whatever rounding
-      // the stored O put between dP and delta
-      if (key0 + 32 * kb == 0 && all <= 1 && lim == 1) {
+      // put between dP and delta
+      if (key0 == 0 && row.all <= 1 && row.lim == 1) zero16(s);
+      frag p[GR::NP];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = 0.0f;
-      }
+      for (int j = 0; j < GR::NP; ++j) p[j] = pack<T>(s, j * EPL);
 #pragma unroll
-      for (int j = 0; j < 16 / EPL; ++j) {
-        const frag p = pack<T>(s, j * EPL);
+      for (int g = 0; g < H; ++g) {
+        if (g + 1 < H) GR::cols(kt, here, 32 * kb, g + 1, f[cur ^ 1]);
+        else if (kb + 1 < KT / 32) GR::rows(kt, here, 32 * (kb + 1), 0, f[cur ^ 1]);
 #pragma unroll
-        for (int db = 0; db < DP / 32; ++db)
-          acc[db] = Elt<T>::mma(TL::col(kt, 32 * kb + 2 * EPL * j, db, lane), p, acc[db]);
+        for (int x = 0; x < 4; ++x) {
+          const int y = 4 * g + x;
+          acc[y % DB] = Elt<T>::mma(f[cur][x], p[y / DB], acc[y % DB]);
+        }
+        cur ^= 1;
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
+  };
+  int st = 0;
+  while (st < steps) {
+    step(st++, std::integral_constant<int, 0>());
+    if (st >= steps) break;
+    step(st++, std::integral_constant<int, 1>());
   }
-  if (!live) return;
-  T* out = static_cast<T*>(a.dq.p) + row * a.dq.row + head * a.dq.head;
+  if (!row.live) return;
+  T* out = static_cast<T*>(a.dq.p) + at * a.dq.row + head * a.dq.head;
 #pragma unroll
-  for (int db = 0; db < DP / 32; ++db)
+  for (int db = 0; db < DB; ++db)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int d = 32 * db + 8 * j + 4 * h;
@@ -134,150 +178,210 @@ __global__ __launch_bounds__(256, 1) void dq_kernel(Args a) {
     }
 }
 
-// dK and dV of one tile of 128 keys, 32 a wave, K and V of the wave's keys in
-// registers: over the flat rows that see any of them (all heads of the group),
-// S = Q K^T and dP = dO V^T (a lane holds one key), then dV^T += dO^T P and
-// dK^T += Q^T dS with dO and Q read transposed.
 template <typename T, int DP>
-__global__ __launch_bounds__(256, 1) void dkv_kernel(Args a) {
-  typedef Tile<T, DP> TL;
-  typedef typename Elt<T>::frag frag;
-  constexpr int NW = 4, ES = sizeof(T), RT = sizeof(T) == 2 ? kBwdRows : kBwdRows / 2, TB = RT * TL::RB;
-  constexpr int EPL = Elt<T>::EPL;
-  __shared__ __attribute__((aligned(1024))) char lds[4 * TB];
-  __shared__ __attribute__((aligned(16))) float stat[2][2][RT];  // [buffer][lse * log2(e), delta][row]
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5;
+__global__ __launch_bounds__(256, sizeof(T) * DP > 256 ? 1 : 2) void dq_kernel(Args a) {
+  __shared__ __attribute__((aligned(16))) char lds[4 * Tile<T, DP>::bytes(sizeof(T) == 2 ? kKeys : kKeys / 2)];
   const int kvh = blockIdx.x % a.kv_heads;
-  const KeyItem it = static_cast<const KeyItem*>(a.items)[blockIdx.x / a.kv_heads];
+  const RowItem it = static_cast<const RowItem*>(a.items)[blockIdx.x / a.kv_heads];
+  dq_tile<T, DP>(a, it, kvh, static_cast<const char*>(a.k.p) + (int64_t)kvh * a.k.head * (int)sizeof(T),
+                 static_cast<const char*>(a.v.p) + (int64_t)kvh * a.v.head * (int)sizeof(T), lds);
+}
+
+// dK and dV of one tile of 128 keys, 32 a wave: over the flat rows that see any
+// of them (all heads of the group), 32 a step, S = Q K^T and dP = dO V^T (a lane
+// holds one key), then dV^T += dO^T P and dK^T += Q^T dS with dO and Q read
+// transposed.  K stays in registers; V stays in LDS, which keeps a wave within
+// half a SIMD's registers, so that two run at once.
+template <typename T, int DP>
+struct KeyTile {
+  typedef Tile<T, DP> TL;
+  static constexpr int RT = 32, TB = TL::bytes(RT), VB = TL::bytes(kBwdKeys);
+  static constexpr int STAT = VB + 4 * TB;           // [buffer][lse2, delta][row]
+  static constexpr int LDS = STAT + 2 * 2 * RT * 4;
+};
+
+template <typename T, int DP>
+__device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int kvh, const char* __restrict__ Q,
+                                         const char* __restrict__ dO, const float* __restrict__ lse2,
+                                         const float* __restrict__ delta, const char* __restrict__ K,
+                                         const char* __restrict__ V, char* lds) {
+  typedef Tile<T, DP> TL;
+  typedef Groups<T, DP> GR;
+  typedef KeyTile<T, DP> KT;
+  typedef typename Elt<T>::frag frag;
+  constexpr int NW = 4, ES = sizeof(T), RT = KT::RT, TB = KT::TB, EPL = Elt<T>::EPL, DB = DP / 32, H = GR::H;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
   const int G = a.G, D = a.D, n_rows = it.q_len * G;
   const float sl2 = a.scale * kLog2e;
 
-  const int key = it.key0 + wave * 32 + (lane & 31);
+  const At<T, DP> here(lane);
+  const int wkey = it.key0 + wave * 32, key = wkey + (lane & 31);
   const bool live = key < it.k_len;
   const int64_t krow = (int64_t)it.k_start + key;
-  frag kf[TL::STEPS], vf[TL::STEPS];
-  row_frags<T, DP>(static_cast<const char*>(a.k.p) + (krow * a.k.row + (int64_t)kvh * a.k.head) * ES, live, D, h, kf);
-  row_frags<T, DP>(static_cast<const char*>(a.v.p) + (krow * a.v.row + (int64_t)kvh * a.v.head) * ES, live, D, h, vf);
+  {
+    const RowStream<T, DP, NW, kBwdKeys> vs(a.v.row, D, wave, lane);
+    vs.issue(V, (int64_t)it.k_start + it.key0, it.k_len - it.key0, lds, wave);
+  }
+  frag kf[TL::STEPS];
+  row_frags<T, DP>(K + krow * a.k.row * ES, live, D, h, kf);
   // the first flat row that sees this key, the wave's first key, its last
   const int from = live ? max(0, key - it.off) * G : 0x7FFFFFFF;
-  const int wkey = it.key0 + wave * 32;
-  const int any = __builtin_amdgcn_readfirstlane(wkey < it.k_len ? max(0, wkey - it.off) * G : 0x7FFFFFFF);
-  const int all = __builtin_amdgcn_readfirstlane(max(0, wkey + 31 - it.off) * G);
+  const int any = wkey < it.k_len ? max(0, wkey - it.off) * G : 0x7FFFFFFF;
+  const int all = wkey + 32 > it.k_len ? 0x7FFFFFFF : max(0, wkey + 31 - it.off) * G;
   // the end of the flat rows that see key 0 alone (none before its first row)
   const int one = wkey == 0 && it.off <= 0 ? (1 - it.off) * G : 0;
   const int one_row = key == 0 ? one : 0;
 
-  floatx16 dk[DP / 32], dv[DP / 32];
+  floatx16 dk[DB], dv[DB];
 #pragma unroll
-  for (int db = 0; db < DP / 32; ++db)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) dk[db][i] = dv[db][i] = 0.0f;
+  for (int db = 0; db < DB; ++db) {
+    zero16(dk[db]);
+    zero16(dv[db]);
+  }
 
-  // rows of a step: Q and dO straight to LDS, their lse and delta through registers
-  auto issue = [&](int r0, int buf) {
-    const RowMap rm(r0, G);
+  // rows [32 s, 32 s + 32) from r_begin, straight to LDS; rows past the end
+  // read as zeros, which add nothing
+  RowMap rm(it.r_begin, G);
+  const int t_step = RT / G, g_step = RT - t_step * G;
+  auto load = [&](int r0, int buf) {
     const int64_t row = it.q_start + (int64_t)rm.t0;
-    const __amdgpu_buffer_rsrc_t rq = rsrc_of(
-        static_cast<const char*>(a.q.p) + (row * a.q.row + (int64_t)kvh * G * a.q.head) * ES, kMaxBytes);
-    const __amdgpu_buffer_rsrc_t rd = rsrc_of(
-        static_cast<const char*>(a.dO.p) + (row * a.dO.row + (int64_t)kvh * G * a.dO.head) * ES, kMaxBytes);
-    constexpr int PER_WAVE = RT / (NW * TL::RPI);
-    static_assert(RT % (NW * TL::RPI) == 0, "rows per wave");
+    const __amdgpu_buffer_rsrc_t rq = rsrc_of(Q + row * a.q.row * ES, kMaxBytes);
+    const __amdgpu_buffer_rsrc_t rd = rsrc_of(dO + row * a.dO.row * ES, kMaxBytes);
+    constexpr int N = RT / (NW * TL::RPI);
+    static_assert(N > 0 && RT % (NW * TL::RPI) == 0, "rows per wave");
+    char* qt = lds + KT::VB + 2 * buf * TB;
 #pragma unroll
-    for (int j = 0; j < PER_WAVE; ++j) {
-      const int blk = wave * PER_WAVE + j;
-      const int i = blk * TL::RPI + lane / TL::SLOTS;
-      const int c = (lane % TL::SLOTS) ^ TL::f(i);
-      int t, g;
+    for (int j = 0; j < N; ++j) {
+      const int blk = wave * N + j;
+      int i, c, t, g;
+      TL::source(lane, &i, &c);
+      i += blk * TL::RPI;
       rm.of(i, &t, &g);
       const bool ok = r0 + i < n_rows && c * 16 < D * ES;
       const uint32_t oq = (uint32_t)(t * (int)a.q.row + g * (int)a.q.head) * ES + (uint32_t)c * 16u;
       const uint32_t od = (uint32_t)(t * (int)a.dO.row + g * (int)a.dO.head) * ES + (uint32_t)c * 16u;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, (lds_ptr_t)(lds + 2 * buf * TB + blk * 1024), 16, ok ? oq : kOob, 0,
-                                               0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (lds_ptr_t)(lds + (2 * buf + 1) * TB + blk * 1024), 16,
-                                               ok ? od : kOob, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, (lds_ptr_t)(qt + blk * TL::PITCH), 16, ok ? oq : kOob, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (lds_ptr_t)(qt + TB + blk * TL::PITCH), 16, ok ? od : kOob, 0, 0, 0);
     }
-  };
-  auto stats = [&](int r0, float* x) {  // thread i of the first 2 RT: lse or delta of row r0 + i % RT
-    const int i = threadIdx.x % RT;
-    *x = threadIdx.x < RT ? INFINITY : 0.0f;
-    if ((int)threadIdx.x < 2 * RT && r0 + i < n_rows) {
-      const RowMap rm(r0, G);
+    if (wave < 2) {  // lse2 by wave 0, delta by wave 1, 32 lanes each
+      const __amdgpu_buffer_rsrc_t rs = rsrc_of((wave == 0 ? lse2 : delta) + row * a.heads, kMaxBytes);
       int t, g;
-      rm.of(i, &t, &g);
-      const int64_t at = (it.q_start + (int64_t)rm.t0 + t) * a.heads + kvh * G + g;
-      if ((int)threadIdx.x >= RT) *x = a.delta[at];
-      else *x = a.lse[at] * kLog2e;
+      rm.of(lane & 31, &t, &g);
+      const bool ok = r0 + (lane & 31) < n_rows;
+      if (lane < 32)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(lds + KT::STAT + (2 * buf + wave) * RT * 4), 4,
+                                                 ok ? (uint32_t)(t * a.heads + g) * 4u : kOob, 0, 0, 0);
+    }
+    // the next step's first row
+    rm.t0 += t_step;
+    rm.g0 += g_step;
+    if (rm.g0 >= G) {
+      rm.g0 -= G;
+      ++rm.t0;
     }
   };
 
-  const int steps = it.r_begin < n_rows ? (n_rows - it.r_begin + RT - 1) / RT : 0;
-  float x = 0.0f;
-  if (steps > 0) {
-    issue(it.r_begin, 0);
-    stats(it.r_begin, &x);
-  }
-  for (int st = 0; st < steps; ++st) {
-    const int r0 = it.r_begin + st * RT;
-    if ((int)threadIdx.x < 2 * RT) stat[st & 1][threadIdx.x / RT][threadIdx.x % RT] = x;
-    __syncthreads();
-    if (st + 1 < steps) {
-      issue(r0 + RT, (st + 1) & 1);
-      stats(r0 + RT, &x);
+  auto step = [&](int r0, auto odd) {
+    constexpr int B = decltype(odd)::value;
+    tiles_landed();
+    if (r0 + RT < n_rows) load(r0 + RT, B ^ 1);
+    if (r0 + RT <= any) return;  // no row of these sees a key of this wave
+    const char *qt = lds + KT::VB + 2 * B * TB, *ot = qt + TB;
+    const float* stat = reinterpret_cast<const float*>(lds + KT::STAT + 2 * B * RT * 4);
+    frag f[2][4];
+    int cur = 0;
+    GR::rows(qt, here, 0, 0, f[0]);
+    floatx16 s, dp;
+    zero16(s);
+    zero16(dp);
+    auto pair = [&](int g, frag(&x)[4]) {  // two fragments of dO, two of V
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x[i] = TL::row(ot, here.row, 0, 2 * g + i);
+        x[2 + i] = TL::row(lds, here.row + wave * TL::bytes(32), 0, 2 * g + i);
+      }
+    };
+#pragma unroll
+    for (int g = 0; g < H; ++g) {
+      if (g + 1 < H) GR::rows(qt, here, 0, g + 1, f[cur ^ 1]);
+      else pair(0, f[cur ^ 1]);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) s = Elt<T>::mma(f[cur][x], kf[4 * g + x], s);
+      cur ^= 1;
+      __builtin_amdgcn_sched_barrier(0);
     }
-    const char* qt = lds + 2 * (st & 1) * TB;
-    const char* ot = qt + TB;
+    if (r0 < all) {
 #pragma unroll
-    for (int rb = 0; rb < RT / 32; ++rb) {
-      if (r0 + 32 * rb + 32 <= any) continue;  // no row of these sees a key of this wave
-      floatx16 s, dp;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
-#pragma unroll
-      for (int q = 0; q < TL::STEPS; ++q) {
-        s = Elt<T>::mma(TL::row(qt, 32 * rb + (lane & 31), 2 * q + h), kf[q], s);
-        dp = Elt<T>::mma(TL::row(ot, 32 * rb + (lane & 31), 2 * q + h), vf[q], dp);
-      }
-      if (r0 + 32 * rb < all || wkey + 32 > it.k_len) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (r0 + 32 * rb + 8 * (i >> 2) + 4 * h + (i & 3) < from) s[i] = -INFINITY;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4_t ls = *reinterpret_cast<const float4_t*>(&stat[st & 1][0][32 * rb + 8 * j + 4 * h]);
-        const float4_t de = *reinterpret_cast<const float4_t*>(&stat[st & 1][1][32 * rb + 8 * j + 4 * h]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // a masked entry is 0 whatever lse is (-inf on a row that sees nothing)
-          const float e = fmaf(s[4 * j + i], sl2, -ls[i]);
-          s[4 * j + i] = s[4 * j + i] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(e);
-          dp[4 * j + i] = s[4 * j + i] * (dp[4 * j + i] - de[i]);
-        }
-      }
-      // rows that see this one key have no gradient through the softmax
-      if (r0 + 32 * rb < one) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (r0 + 32 * rb + 8 * (i >> 2) + 4 * h + (i & 3) < one_row) dp[i] = 0.0f;
-      }
-#pragma unroll
-      for (int j = 0; j < 16 / EPL; ++j) {
-        const frag p = pack<T>(s, j * EPL), d = pack<T>(dp, j * EPL);
-#pragma unroll
-        for (int db = 0; db < DP / 32; ++db) {
-          dv[db] = Elt<T>::mma(TL::col(ot, 32 * rb + 2 * EPL * j, db, lane), p, dv[db]);
-          dk[db] = Elt<T>::mma(TL::col(qt, 32 * rb + 2 * EPL * j, db, lane), d, dk[db]);
-        }
-      }
+      for (int i = 0; i < 16; ++i)
+        if (r0 + 8 * (i >> 2) + 4 * h + (i & 3) < from) s[i] = -INFINITY;
     }
+#pragma unroll
+    for (int g = 0; g < 2 * H; ++g) {
+      if (g + 1 < 2 * H) pair(g + 1, f[cur ^ 1]);
+      else GR::cols(ot, here, 0, 0, f[cur ^ 1]);
+      constexpr int EX = 16 / (2 * H);
+#pragma unroll
+      for (int i = g * EX; i < (g + 1) * EX; ++i) {
+        // -inf stays -inf: lse2 of a row that sees any key is finite
+        const float e = fmaf(s[i], sl2, -stat[8 * (i >> 2) + 4 * h + (i & 3)]);
+        s[i] = __builtin_amdgcn_exp2f(e);
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) dp = Elt<T>::mma(f[cur][x], f[cur][2 + x], dp);
+      cur ^= 1;
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    frag p[GR::NP], d[GR::NP];
+#pragma unroll
+    for (int j = 0; j < GR::NP; ++j) p[j] = pack<T>(s, j * EPL);
+#pragma unroll
+    for (int g = 0; g < H; ++g) {
+      if (g + 1 < H) GR::cols(ot, here, 0, g + 1, f[cur ^ 1]);
+      else GR::cols(qt, here, 0, 0, f[cur ^ 1]);
+#pragma unroll
+      for (int i = g * (16 / H); i < (g + 1) * (16 / H); ++i)
+        dp[i] = s[i] * (dp[i] - stat[RT + 8 * (i >> 2) + 4 * h + (i & 3)]);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int y = 4 * g + x;
+        dv[y % DB] = Elt<T>::mma(f[cur][x], p[y / DB], dv[y % DB]);
+      }
+      cur ^= 1;
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // rows that see this one key have no gradient through the softmax
+    if (r0 < one) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (r0 + 8 * (i >> 2) + 4 * h + (i & 3) < one_row) dp[i] = 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < GR::NP; ++j) d[j] = pack<T>(dp, j * EPL);
+#pragma unroll
+    for (int g = 0; g < H; ++g) {
+      if (g + 1 < H) GR::cols(qt, here, 0, g + 1, f[cur ^ 1]);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int y = 4 * g + x;
+        dk[y % DB] = Elt<T>::mma(f[cur][x], d[y / DB], dk[y % DB]);
+      }
+      cur ^= 1;
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  int r0 = it.r_begin;
+  if (r0 < n_rows) load(r0, 0);
+  while (r0 < n_rows) {
+    step(r0, std::integral_constant<int, 0>());
+    if ((r0 += RT) >= n_rows) break;
+    step(r0, std::integral_constant<int, 1>());
+    r0 += RT;
   }
   if (!live) return;
   T* ok = static_cast<T*>(a.dk.p) + krow * a.dk.row + (int64_t)kvh * a.dk.head;
   T* ov = static_cast<T*>(a.dv.p) + krow * a.dv.row + (int64_t)kvh * a.dv.head;
 #pragma unroll
-  for (int db = 0; db < DP / 32; ++db)
+  for (int db = 0; db < DB; ++db)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int d = 32 * db + 8 * j + 4 * h;
@@ -287,6 +391,19 @@ __global__ __launch_bounds__(256, 1) void dkv_kernel(Args a) {
         store4<T>(ov + d, dv[db][4 * j], dv[db][4 * j + 1], dv[db][4 * j + 2], dv[db][4 * j + 3]);
       }
     }
+}
+
+template <typename T, int DP>
+__global__ __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2) void dkv_kernel(Args a) {
+  __shared__ __attribute__((aligned(16))) char lds[KeyTile<T, DP>::LDS];
+  constexpr int ES = sizeof(T);
+  const int kvh = blockIdx.x % a.kv_heads;
+  const KeyItem it = static_cast<const KeyItem*>(a.items)[blockIdx.x / a.kv_heads];
+  const int64_t q = (int64_t)kvh * a.G;
+  dkv_tile<T, DP>(a, it, kvh, static_cast<const char*>(a.q.p) + q * a.q.head * ES,
+                  static_cast<const char*>(a.dO.p) + q * a.dO.head * ES, a.lse2 + q, a.delta + q,
+                  static_cast<const char*>(a.k.p) + (int64_t)kvh * a.k.head * ES,
+                  static_cast<const char*>(a.v.p) + (int64_t)kvh * a.v.head * ES, lds);
 }
 
 }  // namespace

@@ -16,6 +16,7 @@
 // probabilities never leave their registers: no LDS trip, no lane exchange.
 #pragma once
 
+#include "attn.h"
 #include "common.h"
 
 namespace ipttt {
@@ -47,50 +48,113 @@ template <> struct Elt<float> {
   }
 };
 
-// Tile of R rows of RB bytes.  Chunk c of row r sits in slot c ^ f(r): the 16
-// rows that 16 neighbouring lanes read with one chunk index fall on 16
-// distinct bank quads (64 banks of 4 bytes), and so do the rows of a transposed
-// read (bf16: 4 rows of 64 bytes; fp32: rows r and r + 4 of 128 bytes).
+// A tile of rows in LDS.  A 1 KB block, the 64 lanes' 16 bytes of one direct
+// load, holds RPI rows; blocks follow at PITCH = 1024 + 16 (or 32) bytes.  In a
+// block the rows alternate in units of 64 bytes (fp32 of width 128: 128 bytes),
+// so that whatever step of head_dim, block of columns or group of rows a
+// fragment takes only adds a constant: each kind of read has one address per
+// lane and immediate offsets.  Free of bank conflicts (64 banks of 4 bytes) for
+// the 16 lanes of a 16-byte read, one chunk of 16 rows each, and the 32 lanes
+// of a transposed read, 64 bytes of 4 rows.
 template <typename T, int DP>
 struct Tile {
   static constexpr int RB = DP * (int)sizeof(T);
-  static constexpr int SLOTS = RB / 16;
-  static constexpr int STEPS = RB / 32;       // MFMA steps over head_dim
-  static constexpr int RPI = 1024 / RB;       // rows of one wave-wide 16-byte load
+  static constexpr int STEPS = RB / 32;  // MFMA steps over head_dim
+  static constexpr int RPI = 1024 / RB;  // rows of a block
+  static constexpr int PITCH = RB == 128 ? 1056 : 1040;
   typedef typename Elt<T>::frag frag;
+  static constexpr int bytes(int rows) { return rows / RPI * PITCH; }
 
-  static __device__ __forceinline__ int f(int r) {
-    if constexpr (sizeof(T) == 4) return ((r & 7) << 1) | ((r >> 3) & 1);
-    if constexpr (RB == 256) return ((r & 3) << 2) | ((r >> 2) & 3);
-    return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);  // RB 128: two rows per 256 bytes
+  // Row and chunk that lane l's 16 bytes of a block hold.
+  static __device__ __forceinline__ void source(int l, int* row, int* chunk) {
+    if constexpr (RB == 512) {
+      *row = (l >> 3) & 1;
+      *chunk = 8 * (l >> 4) + (l & 7);
+    } else if constexpr (RB == 256) {
+      *row = (l >> 2) & 3;
+      *chunk = 4 * (l >> 4) + (l & 3);
+    } else {  // rows i and i + 4 share banks: their chunks 0, 1 (and 2, 3) change places
+      *row = (l >> 2) & 7;
+      *chunk = 4 * (l >> 5) + ((l & 3) ^ (*row >> 2));
+    }
   }
-  static __device__ __forceinline__ int at(int r, int c) { return r * RB + ((c ^ f(r)) << 4); }
 
-  // Chunk c of row r: a lane's fragment of an operand contracted over head_dim.
-  static __device__ __forceinline__ frag row(const char* t, int r, int c) {
-    return *reinterpret_cast<const frag*>(t + at(r, c));
+  // Chunk 2 q + lane / 32 of row r0 + lane % 32, r0 a multiple of 32: a lane's
+  // fragment of an operand contracted over head_dim.
+  static __device__ __forceinline__ int row_base(int lane) {
+    const int r = lane & 31, h = lane >> 5, i = r % RPI, at = r / RPI * PITCH;
+    if constexpr (RB == 512) return at + 128 * i + 16 * h;
+    if constexpr (RB == 256) return at + 64 * i + 16 * h;
+    return at + 64 * i + 16 * (h ^ (i >> 2));
+  }
+  static constexpr int row_step(int q) {
+    return RB == 512 ? 256 * (q >> 2) + 32 * (q & 3) : (RB == 256 ? 256 : 512) * (q >> 1) + 32 * (q & 1);
+  }
+  static __device__ __forceinline__ frag row(const char* t, int base, int r0, int q) {
+    return *reinterpret_cast<const frag*>(t + base + r0 / RPI * PITCH + row_step(q));
   }
 
   // Fragment of the tile transposed, columns (head_dim) 32 db + lane % 32 as
-  // the A rows, contracted over EPL rows of the tile from row0 in the C
-  // block's order.
-  static __device__ __forceinline__ frag col(const char* t, int row0, int db, int lane) {
+  // the A rows, contracted over EPL rows (a C block's order) from r0, a
+  // multiple of 2 EPL.
+  static __device__ __forceinline__ int col_base(int lane) {
     const int h = lane >> 5;
     if constexpr (sizeof(T) == 2) {
-      const int r = row0 + 4 * h + ((lane >> 2) & 3), c = 4 * db + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
-      const int b = 8 * (lane & 1);
-      const short4_t x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4_t)(t + at(r, c) + b));
-      const short4_t x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4_t)(t + at(r + 8, c) + b));
+      const int r = (lane >> 2) & 3, c = 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1), b = 8 * (lane & 1);
+      return RB == 256 ? h * PITCH + 64 * r + 16 * c + b : 64 * (4 * h + r) + 16 * (c ^ h) + b;
+    } else {
+      const int d = lane & 31;
+      return RB == 512 ? 2 * h * PITCH + 4 * d : h * PITCH + 256 * (d >> 4) + 4 * (d & 15);
+    }
+  }
+  static __device__ __forceinline__ frag col(const char* t, int base, int r0, int db) {
+    const char* at = t + base + r0 / RPI * PITCH;
+    if constexpr (sizeof(T) == 2) {
+      at += (RB == 256 ? 256 : 512) * db;
+      const short4_t x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4_t)at);
+      const short4_t x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4_t)(at + 8 / RPI * PITCH));
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
-      const int d = lane & 31, c = 8 * db + (d >> 2), b = 4 * (d & 3);
       frag x;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float*>(t + at(row0 + 4 * h + i, c) + b);
+      for (int i = 0; i < 4; ++i)
+        x[i] = *reinterpret_cast<const float*>(RB == 512 ? at + 256 * db + (i >> 1) * PITCH + 128 * (i & 1)
+                                                         : at + 512 * db + 64 * i);
       return x;
     }
   }
 };
+
+// Where this lane reads in any tile.
+template <typename T, int DP>
+struct At {
+  int row, col;
+  __device__ __forceinline__ explicit At(int lane)
+      : row(Tile<T, DP>::row_base(lane)), col(Tile<T, DP>::col_base(lane)) {}
+};
+
+// One group of four row fragments (A operands contracted over head_dim), or of
+// transposed ones (contracted over EPL rows each, DB blocks of head_dim).
+template <typename T, int DP>
+struct Groups {
+  typedef Tile<T, DP> TL;
+  typedef typename Elt<T>::frag frag;
+  static constexpr int EPL = Elt<T>::EPL, DB = DP / 32, H = TL::STEPS / 4, NP = 16 / EPL;
+  static_assert(NP * DB == 4 * H, "equal groups");
+  static __device__ __forceinline__ void rows(const char* t, const At<T, DP>& at, int r0, int g, frag (&f)[4]) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) f[x] = TL::row(t, at.row, r0, 4 * g + x);
+  }
+  static __device__ __forceinline__ void cols(const char* t, const At<T, DP>& at, int r0, int g, frag (&f)[4]) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) f[x] = TL::col(t, at.col, r0 + 2 * EPL * ((4 * g + x) / DB), (4 * g + x) % DB);
+  }
+};
+
+__device__ __forceinline__ void zero16(floatx16& x) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+}
 
 // EPL registers of a C block, from register i0, as a B fragment (bf16: rounded
 // to nearest even, the one rounding of a probability or its gradient).
@@ -102,30 +166,65 @@ __device__ __forceinline__ typename Elt<T>::frag pack(const floatx16& x, int i0)
   return p;
 }
 
-__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32, 64); }
+// max and sum over lanes l and l ^ 32, in both
+__device__ __forceinline__ void both_halves(float x, float* lo, float* hi) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  *lo = __builtin_bit_cast(float, (uint32_t)r[0]);
+  *hi = __builtin_bit_cast(float, (uint32_t)r[1]);
+}
+__device__ __forceinline__ float half_max(float x) {
+  float a, b;
+  both_halves(x, &a, &b);
+  return fmaxf(a, b);
+}
+__device__ __forceinline__ float half_sum(float x) {
+  float a, b;
+  both_halves(x, &a, &b);
+  return a + b;
+}
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p, int64_t bytes) {
   const int n = (int)(bytes < 0 ? 0 : bytes > kMaxBytes ? kMaxBytes : bytes);
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, n, 0x00020000);
 }
 
-// Direct-to-LDS copy of R rows of one head into a tile, NW waves sharing it:
-// row r of the resource at r * stride; rows past its end and columns past D
-// read as zero.
+// Rows of one head streamed into LDS tiles of R rows, NW waves sharing each:
+// 16 bytes a lane straight to LDS.  The resource is set to the tile's first row
+// with 64-bit arithmetic, so that offsets inside it are 32-bit however long the
+// cache; rows past the sequence's end and columns past D read as zero.
 template <typename T, int DP, int NW, int R>
-__device__ __forceinline__ void load_rows(__amdgpu_buffer_rsrc_t rs, uint32_t stride, int D, char* tile, int wave,
-                                          int lane) {
+struct RowStream {
   typedef Tile<T, DP> TL;
-  constexpr int PER_WAVE = R / (NW * TL::RPI);
+  static constexpr int N = R / (NW * TL::RPI);  // loads per wave and tile
   static_assert(R % (NW * TL::RPI) == 0, "rows per wave");
+  uint32_t off[N];
+  uint32_t stride;  // bytes
+  int tail;         // bytes of one row
+
+  __device__ __forceinline__ RowStream(int64_t row_stride, int D, int wave, int lane)
+      : stride((uint32_t)(row_stride * (int)sizeof(T))), tail(D * (int)sizeof(T)) {
 #pragma unroll
-  for (int j = 0; j < PER_WAVE; ++j) {
-    const int blk = wave * PER_WAVE + j;
-    const int r = blk * TL::RPI + lane / TL::SLOTS;
-    const int c = (lane % TL::SLOTS) ^ TL::f(r);
-    const uint32_t off = c * 16 < D * (int)sizeof(T) ? (uint32_t)r * stride + (uint32_t)c * 16u : kOob;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(tile + blk * 1024), 16, off, 0, 0, 0);
+    for (int j = 0; j < N; ++j) {
+      int r, c;
+      TL::source(lane, &r, &c);
+      r += (wave * N + j) * TL::RPI;
+      off[j] = c * 16 < tail ? (uint32_t)r * stride + (uint32_t)c * 16u : kOob;
+    }
   }
+  // tile <- rows [row, row + min(R, left)) of the head at base; left >= 1
+  __device__ __forceinline__ void issue(const char* base, int64_t row, int left, char* tile, int wave) const {
+    const __amdgpu_buffer_rsrc_t rs = rsrc_of(base + row * (int64_t)stride, (left - 1) * (int64_t)stride + tail);
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(tile + (wave * N + j) * TL::PITCH), 16, off[j], 0, 0, 0);
+  }
+};
+
+// Workgroup barrier after this wave's own loads to LDS have landed.
+__device__ __forceinline__ void tiles_landed() {
+  __builtin_amdgcn_s_waitcnt((0x7 << 4) | (0xF << 8));  // vmcnt(0)
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 // A lane's chunks of one row in global memory (zeros where it has none).
@@ -169,6 +268,25 @@ struct RowMap {
     const int n = g0 + i;
     *t = G == 1 ? n : (int)__umulhi((uint32_t)n, m);
     *g = n - *t * G;
+  }
+};
+
+// One lane's row of a tile, and what its wave's rows see.
+struct Row {
+  int r, t, g;      // flat row, query, head of the group
+  bool live;
+  int lim;          // it sees keys below lim
+  int all;          // every row of the wave sees the keys below all
+
+  __device__ __forceinline__ Row(const RowItem& it, int G, int wave, int lane) {
+    const int n_rows = it.q_len * G, r0 = it.r0 + wave * 32;
+    const RowMap rm(r0, G);
+    r = r0 + (lane & 31);
+    rm.of(lane & 31, &t, &g);
+    t += rm.t0;
+    live = r < n_rows;
+    lim = live ? min(it.off + t + 1, it.k_end) : 0;
+    all = __builtin_amdgcn_readfirstlane(min(it.off + rm.t0 + 1, it.k_end));
   }
 };
 

@@ -12,68 +12,163 @@
 #include "attn.h"
 #include "launch.h"
 
+#include <type_traits>
+
 namespace ipttt {
 namespace attn {
 namespace {
 
+// The work of one wave on one step of kKeys keys, in phases of MFMAs with the
+// softmax of the other block of 32 keys between them: while the matrix cores
+// form the next step's scores and this step's O, the vector units raise this
+// step's scores to probabilities.  Fragments are read from LDS one group of
+// four MFMAs ahead.
 template <typename T, int DP>
-__global__ __launch_bounds__(256, 1) void fwd_kernel(Args a) {
+struct Step {
   typedef Tile<T, DP> TL;
+  typedef Groups<T, DP> GR;
   typedef typename Elt<T>::frag frag;
-  constexpr int NW = 4, ES = sizeof(T), TB = kKeys * TL::RB, EPL = Elt<T>::EPL;
-  __shared__ __attribute__((aligned(1024))) char lds[4 * TB];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5;
-  const int kvh = blockIdx.x % a.kv_heads;
-  const RowItem it = static_cast<const RowItem*>(a.items)[blockIdx.x / a.kv_heads];
-  const int G = a.G, D = a.D, n_rows = it.q_len * G;
-  const float sl2 = a.scale * kLog2e;
+  static constexpr int EPL = Elt<T>::EPL, DB = DP / 32, H = GR::H;
+  static constexpr int EX = 16 / H;  // scores raised per group of MFMAs
 
-  // this lane's row: query t of head kvh * G + g; it sees keys below lim
-  const RowMap rm(it.r0 + wave * 32, G);
-  const int r = it.r0 + wave * 32 + (lane & 31);
-  int t, g;
-  rm.of(lane & 31, &t, &g);
-  t += rm.t0;
-  const bool live = r < n_rows;
-  const int lim = live ? min(it.off + t + 1, it.k_end) : 0;
-  // the wave's first and last limits: keys every row sees, keys any row sees
-  const int all = __builtin_amdgcn_readfirstlane(min(it.off + rm.t0 + 1, it.k_end));
-  const int r_last = min(it.r0 + wave * 32 + 31, n_rows - 1);
-  const int any = __builtin_amdgcn_readfirstlane(
-      it.r0 + wave * 32 < n_rows ? min(it.off + r_last / G + 1, it.k_end) : 0);
-
-  const int64_t row = it.q_start + (int64_t)t;
-  const int head = kvh * G + g;
-  frag qf[TL::STEPS];
-  row_frags<T, DP>(static_cast<const char*>(a.q.p) + (row * a.q.row + head * a.q.head) * ES, live, D, h, qf);
-
-  floatx16 o[DP / 32];
+  // scores [i0, i0 + EX) of a block to probabilities
+  static __device__ __forceinline__ void raise(floatx16& s, int i0, float sl2, float m, float& l) {
 #pragma unroll
-  for (int db = 0; db < DP / 32; ++db)
+    for (int i = 0; i < EX; ++i) {
+      s[i0 + i] = __builtin_amdgcn_exp2f(fmaf(s[i0 + i], sl2, -m));
+      l += s[i0 + i];
+    }
+  }
+
+  // s: this step's scores in, the next step's out (if NEXT); kt: the next
+  // step's keys, vt: this step's values
+  template <bool NEXT>
+  static __device__ __forceinline__ void run(const char* kt, const char* vt, const frag (&qf)[TL::STEPS],
+                                             floatx16 (&s)[2], floatx16 (&o)[DB], float sl2, float m, float& l,
+                                             const At<T, DP>& at) {
+    frag f[2][4];
+    floatx16 n[2];
+    int cur = 0;
+    if constexpr (NEXT) {
+      GR::rows(kt, at, 32 * 0, 0, f[0]);
+    } else {
+      GR::cols(vt, at, 32 * 0, 0, f[0]);
+#pragma unroll
+      for (int g = 0; g < H; ++g) raise(s[0], g * EX, sl2, m, l);
+    }
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      if constexpr (NEXT) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) n[kb][i] = 0.0f;
+#pragma unroll
+        for (int g = 0; g < H; ++g) {
+          if (g + 1 < H) GR::rows(kt, at, 32 * kb, g + 1, f[cur ^ 1]);
+          else GR::cols(vt, at, 32 * kb, 0, f[cur ^ 1]);
+          if (kb == 0) raise(s[0], g * EX, sl2, m, l);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) n[kb] = Elt<T>::mma(f[cur][x], qf[4 * g + x], n[kb]);
+          cur ^= 1;
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      frag p[16 / EPL];
+#pragma unroll
+      for (int j = 0; j < 16 / EPL; ++j) p[j] = pack<T>(s[kb], j * EPL);
+#pragma unroll
+      for (int g = 0; g < H; ++g) {
+        if (g + 1 < H) GR::cols(vt, at, 32 * kb, g + 1, f[cur ^ 1]);
+        else if (kb == 0 && NEXT) GR::rows(kt, at, 32 * 1, 0, f[cur ^ 1]);
+        else if (kb == 0) GR::cols(vt, at, 32 * 1, 0, f[cur ^ 1]);
+        if (kb == 0) raise(s[1], g * EX, sl2, m, l);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int y = 4 * g + x;
+          o[y % DB] = Elt<T>::mma(f[cur][x], p[y / DB], o[y % DB]);
+        }
+        cur ^= 1;
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if constexpr (NEXT) {
+      s[0] = n[0];
+      s[1] = n[1];
+    }
+  }
+};
+
+// Masks a step's scores and moves m up if a row's maximum passed it by more
+// than 2^8: sums and O are relative to m, exact for any m near the maximum, so
+// they are rescaled (one multiplication an element) only then, which after
+// the first few steps is rare.
+template <int DB>
+__device__ __forceinline__ void settle(floatx16 (&s)[2], int key0, const Row& row, float sl2, floatx16 (&o)[DB],
+                                       float& m, float& l, int lane) {
+  if (key0 + kKeys > row.all) {
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (key0 + 32 * kb + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= row.lim) s[kb][i] = -INFINITY;
+  }
+  float x = fmaxf(s[0][0], s[1][0]);
+#pragma unroll
+  for (int i = 1; i < 16; ++i) x = fmaxf(fmaxf(x, s[0][i]), s[1][i]);
+  x = half_max(x) * sl2;
+  if (__any(x > m + 8.0f)) {
+    const float mn = fmaxf(m, x), c = __builtin_amdgcn_exp2f(m - mn);
+    m = mn;
+    l *= c;
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[db][i] *= c;
+  }
+}
+
+template <typename T, int DP>
+__device__ __forceinline__ void fwd_tile(const Args& a, const RowItem& it, int kvh, const char* __restrict__ K,
+                                         const char* __restrict__ V, char* lds) {
+  typedef Tile<T, DP> TL;
+  typedef Step<T, DP> ST;
+  typedef typename Elt<T>::frag frag;
+  constexpr int NW = 4, ES = sizeof(T), TB = TL::bytes(kKeys), DB = DP / 32;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
+  const int D = a.D;
+  const float sl2 = a.scale * kLog2e;
+  const Row row(it, a.G, wave, lane);
+  const int64_t at = it.q_start + (int64_t)row.t;
+  const int head = kvh * a.G + row.g;
+
+  const At<T, DP> here(lane);
+  const RowStream<T, DP, NW, kKeys> ks(a.k.row, D, wave, lane), vs(a.v.row, D, wave, lane);
+  const int k_len = it.off + it.q_len, steps = (it.k_end - it.k_begin + kKeys - 1) / kKeys;
+  // keys in buffers 0 and 1, values in 2 and 3, step s in buffer s & 1
+  auto keys = [&](int s) {
+    const int key = it.k_begin + s * kKeys;
+    ks.issue(K, (int64_t)it.k_start + key, k_len - key, lds + (s & 1) * TB, wave);
+  };
+  auto values = [&](int s) {
+    const int key = it.k_begin + s * kKeys;
+    vs.issue(V, (int64_t)it.k_start + key, k_len - key, lds + (2 + (s & 1)) * TB, wave);
+  };
+  if (steps > 0) keys(0);
+
+  frag qf[TL::STEPS];
+  row_frags<T, DP>(static_cast<const char*>(a.q.p) + (at * a.q.row + head * a.q.head) * ES, row.live, D, h, qf);
+  floatx16 o[DB];
+#pragma unroll
+  for (int db = 0; db < DB; ++db)
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[db][i] = 0.0f;
-  float m = -INFINITY, l = 0.0f;
+  // m starts below every score and stays finite, so that masked scores (-inf)
+  // of a row that has seen nothing give 0, not NaN
+  float m = -1e38f, l = 0.0f;
 
-  const uint32_t ks = (uint32_t)(a.k.row * ES), vs = (uint32_t)(a.v.row * ES);
-  const char* K = static_cast<const char*>(a.k.p) + (int64_t)kvh * a.k.head * ES;
-  const char* V = static_cast<const char*>(a.v.p) + (int64_t)kvh * a.v.head * ES;
-  const int last_key = it.off + it.q_len;  // = k_len
-  auto issue = [&](int key0, int buf) {
-    const int64_t at = (int64_t)it.k_start + key0, left = last_key - key0;
-    load_rows<T, DP, NW, kKeys>(rsrc_of(K + at * (int64_t)ks, (left - 1) * (int64_t)ks + D * ES), ks, D, lds + 2 * buf * TB,
-                         wave, lane);
-    load_rows<T, DP, NW, kKeys>(rsrc_of(V + at * (int64_t)vs, (left - 1) * (int64_t)vs + D * ES), vs, D,
-                         lds + (2 * buf + 1) * TB, wave, lane);
-  };
-  const int steps = (it.k_end - it.k_begin + kKeys - 1) / kKeys;
-  if (steps > 0) issue(it.k_begin, 0);
-  for (int st = 0; st < steps; ++st) {
-    const int key0 = it.k_begin + st * kKeys;
-    __syncthreads();  // this step's tiles have landed; the other buffer's readers are done
-    if (st + 1 < steps) issue(key0 + kKeys, (st + 1) & 1);
-    if (key0 >= any) continue;  // no row of this wave sees these keys
-    const char* kt = lds + 2 * (st & 1) * TB;
-    const char* vt = kt + TB;
+  if (steps > 0) {
+    tiles_landed();
+    values(0);
+    if (steps > 1) keys(1);
     floatx16 s[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
@@ -81,57 +176,41 @@ __global__ __launch_bounds__(256, 1) void fwd_kernel(Args a) {
       for (int i = 0; i < 16; ++i) s[kb][i] = 0.0f;
 #pragma unroll
       for (int q = 0; q < TL::STEPS; ++q)
-        s[kb] = Elt<T>::mma(TL::row(kt, 32 * kb + (lane & 31), 2 * q + h), qf[q], s[kb]);
+        s[kb] = Elt<T>::mma(TL::row(lds, here.row, 32 * kb, q), qf[q], s[kb]);
     }
-    if (key0 + kKeys > all) {
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (key0 + 32 * kb + 8 * (i >> 2) + 4 * h + (i & 3) >= lim) s[kb][i] = -INFINITY;
+    settle<DB>(s, it.k_begin, row, sl2, o, m, l, lane);
+    // one step with another to follow; its buffers are known at compile time, so
+    // that the LDS addresses of all fragments are a few registers plus immediate
+    // offsets.  A wave whose rows see none of the next keys scores them all the
+    // same (as -inf): at most the last step or two of a tile.
+    auto step = [&](int st, auto odd) {
+      constexpr int B = decltype(odd)::value;
+      // this step's values and the next one's keys are here, and every wave is
+      // done with the buffers that the loads below fill
+      tiles_landed();
+      values(st + 1);
+      if (st + 2 < steps) keys(st + 2);
+      ST::template run<true>(lds + (B ^ 1) * TB, lds + (2 + B) * TB, qf, s, o, sl2, m, l, here);
+      settle<DB>(s, it.k_begin + (st + 1) * kKeys, row, sl2, o, m, l, lane);
+    };
+    int st = 0;
+    while (st < steps - 1) {
+      step(st++, std::integral_constant<int, 0>());
+      if (st >= steps - 1) break;
+      step(st++, std::integral_constant<int, 1>());
     }
-    float mx = s[0][0];
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[kb][i]);
-    mx = fmaxf(mx, other_half(mx)) * sl2;
-    const float mn = fmaxf(m, mx);
-    const float mu = mn == -INFINITY ? 0.0f : mn;  // a row that has seen nothing yet
-    const float c = __builtin_amdgcn_exp2f(m - mu);
-    m = mn;
-    float sum = 0.0f;
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[kb][i] = __builtin_amdgcn_exp2f(fmaf(s[kb][i], sl2, -mu));
-        sum += s[kb][i];
-      }
-    l = l * c + sum;
-#pragma unroll
-    for (int db = 0; db < DP / 32; ++db)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[db][i] *= c;
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int j = 0; j < 16 / EPL; ++j) {
-        const frag p = pack<T>(s[kb], j * EPL);
-#pragma unroll
-        for (int db = 0; db < DP / 32; ++db)
-          o[db] = Elt<T>::mma(TL::col(vt, 32 * kb + 2 * EPL * j, db, lane), p, o[db]);
-      }
+    tiles_landed();
+    ST::template run<false>(lds, lds + (2 + (st & 1)) * TB, qf, s, o, sl2, m, l, here);
   }
-  l += other_half(l);
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-  const float lse = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
-  if (!live) return;
+  l = half_sum(l);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const float lse = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+  if (!row.live) return;
   if (it.part >= 0) {
-    const int64_t slot = ((int64_t)it.part * a.kv_heads + kvh) * kRows + (r - it.r0);
+    const int64_t slot = ((int64_t)it.part * a.kv_heads + kvh) * kRows + (row.r - it.r0);
     if (h == 0) a.part_lse[slot] = lse;
 #pragma unroll
-    for (int db = 0; db < DP / 32; ++db)
+    for (int db = 0; db < DB; ++db)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int d = 32 * db + 8 * j + 4 * h;
@@ -141,16 +220,27 @@ __global__ __launch_bounds__(256, 1) void fwd_kernel(Args a) {
       }
     return;
   }
-  if (h == 0) a.lse[row * a.heads + head] = lse;
-  T* out = static_cast<T*>(a.o.p) + row * a.o.row + head * a.o.head;
+  if (h == 0) a.lse[at * a.heads + head] = lse;
+  T* out = static_cast<T*>(a.o.p) + at * a.o.row + head * a.o.head;
 #pragma unroll
-  for (int db = 0; db < DP / 32; ++db)
+  for (int db = 0; db < DB; ++db)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int d = 32 * db + 8 * j + 4 * h;
       if (d < D)
         store4<T>(out + d, o[db][4 * j] * inv, o[db][4 * j + 1] * inv, o[db][4 * j + 2] * inv, o[db][4 * j + 3] * inv);
     }
+}
+
+// Two waves a SIMD (256 registers a wave) where the tiles allow it; fp32 of
+// width 128 needs the registers of one.
+template <typename T, int DP>
+__global__ __launch_bounds__(256, sizeof(T) * DP > 256 ? 1 : 2) void fwd_kernel(Args a) {
+  __shared__ __attribute__((aligned(16))) char lds[4 * Tile<T, DP>::bytes(kKeys)];
+  const int kvh = blockIdx.x % a.kv_heads;
+  const RowItem it = static_cast<const RowItem*>(a.items)[blockIdx.x / a.kv_heads];
+  fwd_tile<T, DP>(a, it, kvh, static_cast<const char*>(a.k.p) + (int64_t)kvh * a.k.head * (int)sizeof(T),
+                  static_cast<const char*>(a.v.p) + (int64_t)kvh * a.v.head * (int)sizeof(T), lds);
 }
 
 // Joins the partial results of one tile: with each part's lse, its weight is
