@@ -12,6 +12,7 @@ namespace attn {
 constexpr int kRows = 128;      // rows of a forward tile, and of a dQ tile
 constexpr int kKeys = 64;       // keys of one step
 constexpr int kBwdKeys = 128;   // keys of a dK, dV tile
+constexpr int kBwdRows = 32;    // rows of one step of it
 
 // One forward (or dQ) tile: rows [r0, min(r0 + tile rows, q_len * G)) of one
 // sequence over keys [k_begin, k_end) of it.  Query t sees keys below off + t + 1.
@@ -28,11 +29,17 @@ struct JoinItem {
 };
 
 // One dK, dV tile: keys [key0, min(key0 + kBwdKeys, k_len)) of one sequence
-// against its rows [r_begin, q_len * G).
+// against its rows [r_begin, r_end), both whole steps of kBwdRows but for the last.
 struct KeyItem {
-  int32_t q_start, q_len, r_begin;
-  int32_t k_start, k_len, off;
-  int32_t key0, part;
+  int32_t q_start, q_len, r_begin, r_end;
+  int32_t k_start, off, key0;
+  int32_t part;              // -1: all rows that see the keys; else the slot of this partial result
+};
+
+// The partial results of one dK, dV tile, slots [part, part + n), for the
+// n_keys rows of dK and dV from k_row on.
+struct KeyJoin {
+  int32_t k_row, n_keys, part, n;
 };
 
 // What the plan table starts with; the items follow at these offsets (bytes).
@@ -42,7 +49,9 @@ struct PlanHeader {
   int32_t n_rows, n_join, n_dq, n_key;
   int32_t o_rows, o_join, o_dq, o_key;
   int32_t parts, overlap;    // partial slots; whether two sequences share keys
-  int32_t bytes, pad[13];
+  int32_t bytes;
+  int32_t n_key_join, o_key_join, key_parts;
+  int32_t pad[10];
 };
 static_assert(sizeof(PlanHeader) == 128, "plan header");
 constexpr int32_t kMagic = 0x41545031;
@@ -58,7 +67,8 @@ struct Args {
   const void* items;      // device
   int n_items;
   View q, k, v, o, dO, dq, dk, dv;
-  float *lse, *lse2, *delta;  // [q rows, heads]; lse2 = lse * log2(e), +inf on rows that see nothing
+  float *lse;             // [q rows, heads]
+  float *nlse, *ndelta;   // same: -lse / scale (-inf on rows that see nothing), -delta
   float *part_o, *part_lse;
 };
 
@@ -66,6 +76,7 @@ hipError_t launch_forward(const Args& a, hipStream_t st);
 hipError_t launch_join(const Args& a, const void* items, int n, hipStream_t st);
 hipError_t launch_dq(const Args& a, hipStream_t st);
 hipError_t launch_dkv(const Args& a, hipStream_t st);
+hipError_t launch_join_keys(const Args& a, const void* items, int n, hipStream_t st);
 
 }  // namespace attn
 

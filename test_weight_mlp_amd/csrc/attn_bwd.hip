@@ -25,7 +25,7 @@ constexpr int kExactDelta = 256;
 
 // dQ of one tile of 128 flat rows, 32 a wave: over the keys the rows see,
 // S^T = K Q^T and dP^T = V dO^T, then dQ^T += K^T dS^T with K read transposed.
-// Leaves lse * log2(e) and delta of its rows for the dK, dV kernel.
+// Leaves -lse / scale and -delta of its rows for the dK, dV kernel.
 template <typename T, int DP>
 __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kvh, const char* __restrict__ K,
                                         const char* __restrict__ V, char* lds) {
@@ -53,10 +53,13 @@ __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kv
   frag qf[TL::STEPS], df[TL::STEPS];
   row_frags<T, DP>(static_cast<const char*>(a.q.p) + (at * a.q.row + head * a.q.head) * ES, row.live, D, h, qf);
   row_frags<T, DP>(static_cast<const char*>(a.dO.p) + (at * a.dO.row + head * a.dO.head) * ES, row.live, D, h, df);
-  float lse2 = INFINITY;  // P = 0 on rows that see nothing, and past the sequence
+  // the scores' accumulators start at -lse / scale, dP's at -delta: what comes
+  // out of the products is ready for the exponential and for dS = P (dP - delta).
+  // -inf (P = 0) on rows that see nothing, and past the sequence
+  float nlse = -INFINITY;
   if (row.live) {
     const float x = a.lse[at * a.heads + head];
-    if (x != -INFINITY) lse2 = x * kLog2e;
+    if (x != -INFINITY) nlse = -x / a.scale;
   }
   float delta = 0.0f;
   if (ES == 2 && it.k_end <= kExactDelta) {
@@ -64,8 +67,8 @@ __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kv
       tiles_landed();
       for (int kb = 0; kb < KT / 32; ++kb) {
         floatx16 x, dp;
-        zero16(x);
-        zero16(dp);
+        fill16(x, nlse);
+        fill16(dp, 0.0f);
 #pragma unroll
         for (int q = 0; q < TL::STEPS; ++q) {
           x = Elt<T>::mma(TL::row(lds, here.row, 32 * kb, q), qf[q], x);
@@ -73,7 +76,7 @@ __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kv
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float p = __builtin_amdgcn_exp2f(fmaf(x[i], sl2, -lse2));
+          const float p = __builtin_amdgcn_exp2f(x[i] * sl2);
           if (s * KT + 32 * kb + 8 * (i >> 2) + 4 * h + (i & 3) < row.lim) delta = fmaf(p, dp[i], delta);
         }
       }
@@ -90,13 +93,13 @@ __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kv
   }
   delta = half_sum(delta);
   if (row.live && h == 0) {
-    a.lse2[at * a.heads + head] = lse2;
-    a.delta[at * a.heads + head] = delta;
+    a.nlse[at * a.heads + head] = nlse;
+    a.ndelta[at * a.heads + head] = -delta;
   }
 
   floatx16 acc[DB];
 #pragma unroll
-  for (int db = 0; db < DB; ++db) zero16(acc[db]);
+  for (int db = 0; db < DB; ++db) fill16(acc[db], 0.0f);
 
   auto step = [&](int st, auto odd) {
     constexpr int B = decltype(odd)::value;
@@ -110,8 +113,8 @@ __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kv
     for (int kb = 0; kb < KT / 32; ++kb) {
       const int key0 = st * KT + 32 * kb;
       floatx16 s, dp;
-      zero16(s);
-      zero16(dp);
+      start16(s, nlse);
+      start16(dp, -delta);
 #pragma unroll
       for (int g = 0; g < H; ++g) {
         if (g + 1 < H) GR::rows(kt, here, 32 * kb, g + 1, f[cur ^ 1]);
@@ -131,17 +134,17 @@ __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kv
         if (g + 1 < H) GR::rows(vt, here, 32 * kb, g + 1, f[cur ^ 1]);
         else GR::cols(kt, here, 32 * kb, 0, f[cur ^ 1]);
 #pragma unroll
-        for (int i = g * (16 / H); i < (g + 1) * (16 / H); ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], sl2, -lse2));
+        for (int i = g * (16 / H); i < (g + 1) * (16 / H); ++i) s[i] = __builtin_amdgcn_exp2f(s[i] * sl2);
 #pragma unroll
         for (int x = 0; x < 4; ++x) dp = Elt<T>::mma(f[cur][x], df[4 * g + x], dp);
         cur ^= 1;
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] *= dp[i] - delta;
+      for (int i = 0; i < 16; ++i) s[i] *= dp[i];
       // a softmax over one key has no gradient: exactly 0, whatever rounding
       // put between dP and delta
-      if (key0 == 0 && row.all <= 1 && row.lim == 1) zero16(s);
+      if (key0 == 0 && row.all <= 1 && row.lim == 1) fill16(s, 0.0f);
       frag p[GR::NP];
 #pragma unroll
       for (int j = 0; j < GR::NP; ++j) p[j] = pack<T>(s, j * EPL);
@@ -195,15 +198,25 @@ __global__ __launch_bounds__(256, sizeof(T) * DP > 256 ? 1 : 2) void dq_kernel(A
 template <typename T, int DP>
 struct KeyTile {
   typedef Tile<T, DP> TL;
-  static constexpr int RT = 32, TB = TL::bytes(RT), VB = TL::bytes(kBwdKeys);
-  static constexpr int STAT = VB + 4 * TB;           // [buffer][lse2, delta][row]
+  static constexpr int RT = kBwdRows, TB = TL::bytes(RT), VB = TL::bytes(kBwdKeys);
+  static constexpr int STAT = VB + 4 * TB;           // [buffer][-lse / scale, -delta][row]
   static constexpr int LDS = STAT + 2 * 2 * RT * 4;
 };
 
+// The C block's rows of 32 row values: rows 8 j + 4 h + i in registers 4 j + i.
+__device__ __forceinline__ void row_stats(const float* x, int h, floatx16& c) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float4_t v = *reinterpret_cast<const float4_t*>(x + 8 * j + 4 * h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[4 * j + i] = v[i];
+  }
+}
+
 template <typename T, int DP>
 __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int kvh, const char* __restrict__ Q,
-                                         const char* __restrict__ dO, const float* __restrict__ lse2,
-                                         const float* __restrict__ delta, const char* __restrict__ K,
+                                         const char* __restrict__ dO, const float* __restrict__ nlse,
+                                         const float* __restrict__ ndelta, const char* __restrict__ K,
                                          const char* __restrict__ V, char* lds) {
   typedef Tile<T, DP> TL;
   typedef Groups<T, DP> GR;
@@ -211,23 +224,23 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
   typedef typename Elt<T>::frag frag;
   constexpr int NW = 4, ES = sizeof(T), RT = KT::RT, TB = KT::TB, EPL = Elt<T>::EPL, DB = DP / 32, H = GR::H;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
-  const int G = a.G, D = a.D, n_rows = it.q_len * G;
+  const int G = a.G, D = a.D, r_end = it.r_end, k_len = it.off + it.q_len;
   const float sl2 = a.scale * kLog2e;
 
   const At<T, DP> here(lane);
   const int wkey = it.key0 + wave * 32, key = wkey + (lane & 31);
-  const bool live = key < it.k_len;
+  const bool live = key < k_len;
   const int64_t krow = (int64_t)it.k_start + key;
   {
     const RowStream<T, DP, NW, kBwdKeys> vs(a.v.row, D, wave, lane);
-    vs.issue(V, (int64_t)it.k_start + it.key0, it.k_len - it.key0, lds, wave);
+    vs.issue(V, (int64_t)it.k_start + it.key0, k_len - it.key0, lds, wave);
   }
   frag kf[TL::STEPS];
   row_frags<T, DP>(K + krow * a.k.row * ES, live, D, h, kf);
   // the first flat row that sees this key, the wave's first key, its last
   const int from = live ? max(0, key - it.off) * G : 0x7FFFFFFF;
-  const int any = wkey < it.k_len ? max(0, wkey - it.off) * G : 0x7FFFFFFF;
-  const int all = wkey + 32 > it.k_len ? 0x7FFFFFFF : max(0, wkey + 31 - it.off) * G;
+  const int any = wkey < k_len ? max(0, wkey - it.off) * G : 0x7FFFFFFF;
+  const int all = wkey + 32 > k_len ? 0x7FFFFFFF : max(0, wkey + 31 - it.off) * G;
   // the end of the flat rows that see key 0 alone (none before its first row)
   const int one = wkey == 0 && it.off <= 0 ? (1 - it.off) * G : 0;
   const int one_row = key == 0 ? one : 0;
@@ -235,8 +248,8 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
   floatx16 dk[DB], dv[DB];
 #pragma unroll
   for (int db = 0; db < DB; ++db) {
-    zero16(dk[db]);
-    zero16(dv[db]);
+    fill16(dk[db], 0.0f);
+    fill16(dv[db], 0.0f);
   }
 
   // rows [32 s, 32 s + 32) from r_begin, straight to LDS; rows past the end
@@ -257,17 +270,17 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
       TL::source(lane, &i, &c);
       i += blk * TL::RPI;
       rm.of(i, &t, &g);
-      const bool ok = r0 + i < n_rows && c * 16 < D * ES;
+      const bool ok = r0 + i < r_end && c * 16 < D * ES;
       const uint32_t oq = (uint32_t)(t * (int)a.q.row + g * (int)a.q.head) * ES + (uint32_t)c * 16u;
       const uint32_t od = (uint32_t)(t * (int)a.dO.row + g * (int)a.dO.head) * ES + (uint32_t)c * 16u;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, (lds_ptr_t)(qt + blk * TL::PITCH), 16, ok ? oq : kOob, 0, 0, 0);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (lds_ptr_t)(qt + TB + blk * TL::PITCH), 16, ok ? od : kOob, 0, 0, 0);
     }
-    if (wave < 2) {  // lse2 by wave 0, delta by wave 1, 32 lanes each
-      const __amdgpu_buffer_rsrc_t rs = rsrc_of((wave == 0 ? lse2 : delta) + row * a.heads, kMaxBytes);
+    if (wave < 2) {  // -lse / scale by wave 0, -delta by wave 1, 32 lanes each
+      const __amdgpu_buffer_rsrc_t rs = rsrc_of((wave == 0 ? nlse : ndelta) + row * a.heads, kMaxBytes);
       int t, g;
       rm.of(lane & 31, &t, &g);
-      const bool ok = r0 + (lane & 31) < n_rows;
+      const bool ok = r0 + (lane & 31) < r_end;
       if (lane < 32)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(lds + KT::STAT + (2 * buf + wave) * RT * 4), 4,
                                                  ok ? (uint32_t)(t * a.heads + g) * 4u : kOob, 0, 0, 0);
@@ -284,16 +297,18 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
   auto step = [&](int r0, auto odd) {
     constexpr int B = decltype(odd)::value;
     tiles_landed();
-    if (r0 + RT < n_rows) load(r0 + RT, B ^ 1);
-    if (r0 + RT <= any) return;  // no row of these sees a key of this wave
+    if (r0 + RT <= any) {  // no row of these sees a key of this wave
+      if (r0 + RT < r_end) load(r0 + RT, B ^ 1);
+      return;
+    }
     const char *qt = lds + KT::VB + 2 * B * TB, *ot = qt + TB;
     const float* stat = reinterpret_cast<const float*>(lds + KT::STAT + 2 * B * RT * 4);
     frag f[2][4];
     int cur = 0;
     GR::rows(qt, here, 0, 0, f[0]);
     floatx16 s, dp;
-    zero16(s);
-    zero16(dp);
+    row_stats(stat, h, s);
+    row_stats(stat + RT, h, dp);
     auto pair = [&](int g, frag(&x)[4]) {  // two fragments of dO, two of V
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -309,6 +324,8 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
       for (int x = 0; x < 4; ++x) s = Elt<T>::mma(f[cur][x], kf[4 * g + x], s);
       cur ^= 1;
       __builtin_amdgcn_sched_barrier(0);
+      // the next step's loads, while the matrix cores are busy
+      if (g == 0 && r0 + RT < r_end) load(r0 + RT, B ^ 1);
     }
     if (r0 < all) {
 #pragma unroll
@@ -321,11 +338,7 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
       else GR::cols(ot, here, 0, 0, f[cur ^ 1]);
       constexpr int EX = 16 / (2 * H);
 #pragma unroll
-      for (int i = g * EX; i < (g + 1) * EX; ++i) {
-        // -inf stays -inf: lse2 of a row that sees any key is finite
-        const float e = fmaf(s[i], sl2, -stat[8 * (i >> 2) + 4 * h + (i & 3)]);
-        s[i] = __builtin_amdgcn_exp2f(e);
-      }
+      for (int i = g * EX; i < (g + 1) * EX; ++i) s[i] = __builtin_amdgcn_exp2f(s[i] * sl2);
 #pragma unroll
       for (int x = 0; x < 2; ++x) dp = Elt<T>::mma(f[cur][x], f[cur][2 + x], dp);
       cur ^= 1;
@@ -340,7 +353,7 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
       else GR::cols(qt, here, 0, 0, f[cur ^ 1]);
 #pragma unroll
       for (int i = g * (16 / H); i < (g + 1) * (16 / H); ++i)
-        dp[i] = s[i] * (dp[i] - stat[RT + 8 * (i >> 2) + 4 * h + (i & 3)]);
+        dp[i] *= s[i];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int y = 4 * g + x;
@@ -370,14 +383,28 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
     }
   };
   int r0 = it.r_begin;
-  if (r0 < n_rows) load(r0, 0);
-  while (r0 < n_rows) {
+  if (r0 < r_end) load(r0, 0);
+  while (r0 < r_end) {
     step(r0, std::integral_constant<int, 0>());
-    if ((r0 += RT) >= n_rows) break;
+    if ((r0 += RT) >= r_end) break;
     step(r0, std::integral_constant<int, 1>());
     r0 += RT;
   }
   if (!live) return;
+  if (it.part >= 0) {
+    float* o = a.part_o + (((int64_t)it.part * a.kv_heads + kvh) * 2 * kBwdKeys + (key - it.key0)) * D;
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int d = 32 * db + 8 * j + 4 * h;
+        if (d < D) {
+          store4<float>(o + d, dk[db][4 * j], dk[db][4 * j + 1], dk[db][4 * j + 2], dk[db][4 * j + 3]);
+          store4<float>(o + kBwdKeys * D + d, dv[db][4 * j], dv[db][4 * j + 1], dv[db][4 * j + 2], dv[db][4 * j + 3]);
+        }
+      }
+    return;
+  }
   T* ok = static_cast<T*>(a.dk.p) + krow * a.dk.row + (int64_t)kvh * a.dk.head;
   T* ov = static_cast<T*>(a.dv.p) + krow * a.dv.row + (int64_t)kvh * a.dv.head;
 #pragma unroll
@@ -401,12 +428,43 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2) void dkv_kernel(Args a
   const KeyItem it = static_cast<const KeyItem*>(a.items)[blockIdx.x / a.kv_heads];
   const int64_t q = (int64_t)kvh * a.G;
   dkv_tile<T, DP>(a, it, kvh, static_cast<const char*>(a.q.p) + q * a.q.head * ES,
-                  static_cast<const char*>(a.dO.p) + q * a.dO.head * ES, a.lse2 + q, a.delta + q,
+                  static_cast<const char*>(a.dO.p) + q * a.dO.head * ES, a.nlse + q, a.ndelta + q,
                   static_cast<const char*>(a.k.p) + (int64_t)kvh * a.k.head * ES,
                   static_cast<const char*>(a.v.p) + (int64_t)kvh * a.v.head * ES, lds);
 }
 
+// Sums the partial dK and dV of one tile in slot order: a block the keys from
+// 16 blockIdx.z on, a thread four columns of one key at a time.
+template <typename T>
+__global__ __launch_bounds__(256) void join_keys_kernel(Args a, const KeyJoin* items) {
+  const KeyJoin it = items[blockIdx.x];
+  const int kvh = blockIdx.y, D = a.D, quads = D / 4;
+  const int64_t step = (int64_t)a.kv_heads * 2 * kBwdKeys * D;
+  const int keys = min(16, it.n_keys - 16 * (int)blockIdx.z);
+  for (int e = threadIdx.x; e < keys * quads; e += 256) {
+    const int i = 16 * blockIdx.z + e / quads, d = e % quads * 4;
+    const float* p = a.part_o + (((int64_t)it.part * a.kv_heads + kvh) * 2 * kBwdKeys + i) * D + d;
+    float4_t k = {0.0f, 0.0f, 0.0f, 0.0f}, v = k;
+    for (int j = 0; j < it.n; ++j) {
+      k += *reinterpret_cast<const float4_t*>(p + j * step);
+      v += *reinterpret_cast<const float4_t*>(p + j * step + (int64_t)kBwdKeys * D);
+    }
+    const int64_t row = (int64_t)it.k_row + i;
+    k *= a.scale;
+    store4<T>(static_cast<T*>(a.dk.p) + row * a.dk.row + kvh * a.dk.head + d, k[0], k[1], k[2], k[3]);
+    store4<T>(static_cast<T*>(a.dv.p) + row * a.dv.row + kvh * a.dv.head + d, v[0], v[1], v[2], v[3]);
+  }
+}
+
 }  // namespace
+
+hipError_t launch_join_keys(const Args& a, const void* items, int n, hipStream_t st) {
+  const dim3 grid((unsigned)n, (unsigned)a.kv_heads, kBwdKeys / 16);
+  note_launch("attn_join_keys", st);
+  if (a.dtype == 1) join_keys_kernel<bf16><<<grid, 256, 0, st>>>(a, static_cast<const KeyJoin*>(items));
+  else join_keys_kernel<float><<<grid, 256, 0, st>>>(a, static_cast<const KeyJoin*>(items));
+  return hipGetLastError();
+}
 
 hipError_t launch_dq(const Args& a, hipStream_t st) {
   const dim3 grid((unsigned)(a.n_items * a.kv_heads));

@@ -151,9 +151,16 @@ struct Groups {
   }
 };
 
-__device__ __forceinline__ void zero16(floatx16& x) {
+__device__ __forceinline__ void fill16(floatx16& x, float v) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+  for (int i = 0; i < 16; ++i) x[i] = v;
+}
+
+// The same for a value that a loop does not change: without the empty asm the
+// compiler keeps 16 copies of it in registers for the whole loop.
+__device__ __forceinline__ void start16(floatx16& x, float v) {
+  asm volatile("" : "+v"(v));
+  fill16(x, v);
 }
 
 // EPL registers of a C block, from register i0, as a B fragment (bf16: rounded

@@ -244,39 +244,39 @@ __global__ __launch_bounds__(256, sizeof(T) * DP > 256 ? 1 : 2) void fwd_kernel(
 }
 
 // Joins the partial results of one tile: with each part's lse, its weight is
-// e^(lse_i - lse), lse = log sum e^(lse_i).  One wave a row, in slot order.
+// e^(lse_i - lse), lse = log sum e^(lse_i).  A wave a row, two columns a lane,
+// parts in slot order.
 template <typename T>
 __global__ __launch_bounds__(256) void join_kernel(Args a, const JoinItem* items) {
-  const int kvh = blockIdx.y;
+  const int kvh = blockIdx.y, lane = threadIdx.x & 63, i = blockIdx.z * 4 + (threadIdx.x >> 6);
   const JoinItem it = items[blockIdx.x];
-  const int G = a.G, D = a.D, lane = threadIdx.x & 63;
-  const int rows = min(kRows, it.q_len * G - it.r0);
-  for (int i = threadIdx.x >> 6; i < rows; i += 4) {
-    const int r = it.r0 + i, t = r / G, head = kvh * G + r - t * G;
-    const int64_t slot0 = ((int64_t)it.part * a.kv_heads + kvh) * kRows + i, step = (int64_t)a.kv_heads * kRows;
-    float m = -INFINITY;
-    for (int p = 0; p < it.n; ++p) m = fmaxf(m, a.part_lse[slot0 + p * step]);
-    const float mu = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f, x0 = 0.0f, x1 = 0.0f;
-    for (int p = 0; p < it.n; ++p) {
-      const int64_t s = slot0 + p * step;
-      const float w = __builtin_amdgcn_exp2f((a.part_lse[s] - mu) * kLog2e);
-      l += w;
-      if (w > 0.0f) {
-        if (2 * lane < D) {
-          x0 = fmaf(w, a.part_o[s * D + 2 * lane], x0);
-          x1 = fmaf(w, a.part_o[s * D + 2 * lane + 1], x1);
-        }
-      }
-    }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    const int64_t row = it.q_start + (int64_t)t;
-    if (lane == 0) a.lse[row * a.heads + head] = l > 0.0f ? mu + __builtin_amdgcn_logf(l) * kLn2 : -INFINITY;
-    T* out = static_cast<T*>(a.o.p) + row * a.o.row + head * a.o.head;
-    if (2 * lane < D) {
-      out[2 * lane] = (T)(x0 * inv);
-      out[2 * lane + 1] = (T)(x1 * inv);
-    }
+  const int G = a.G, D = a.D, r = it.r0 + i;
+  if (r >= it.q_len * G) return;
+  const int t = r / G, head = kvh * G + r - t * G;
+  const int64_t slot0 = ((int64_t)it.part * a.kv_heads + kvh) * kRows + i, step = (int64_t)a.kv_heads * kRows;
+  float m = -INFINITY;
+  for (int p = lane; p < it.n; p += 64) m = fmaxf(m, a.part_lse[slot0 + p * step]);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+  const float mu = m == -INFINITY ? 0.0f : m;
+  const bool on = 2 * lane < D;
+  const float* x = a.part_o + slot0 * D + (on ? 2 * lane : 0);
+  float l = 0.0f, x0 = 0.0f, x1 = 0.0f;
+#pragma unroll 4
+  for (int p = 0; p < it.n; ++p) {
+    const float w = __builtin_amdgcn_exp2f((a.part_lse[slot0 + p * step] - mu) * kLog2e);
+    const float2_t v = *reinterpret_cast<const float2_t*>(x + p * step * D);
+    l += w;
+    x0 = fmaf(w, v[0], x0);
+    x1 = fmaf(w, v[1], x1);
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const int64_t row = it.q_start + (int64_t)t;
+  if (lane == 0) a.lse[row * a.heads + head] = l == 0.0f ? -INFINITY : mu + __builtin_amdgcn_logf(l) * kLn2;
+  T* out = static_cast<T*>(a.o.p) + row * a.o.row + head * a.o.head;
+  if (on) {
+    out[2 * lane] = (T)(x0 * inv);
+    out[2 * lane + 1] = (T)(x1 * inv);
   }
 }
 
@@ -293,7 +293,7 @@ hipError_t launch_forward(const Args& a, hipStream_t st) {
 }
 
 hipError_t launch_join(const Args& a, const void* items, int n, hipStream_t st) {
-  const dim3 grid((unsigned)n, (unsigned)a.kv_heads);
+  const dim3 grid((unsigned)n, (unsigned)a.kv_heads, kRows / 4);
   note_launch("attn_join", st);
   if (a.dtype == 1) join_kernel<bf16><<<grid, 256, 0, st>>>(a, static_cast<const JoinItem*>(items));
   else join_kernel<float><<<grid, 256, 0, st>>>(a, static_cast<const JoinItem*>(items));

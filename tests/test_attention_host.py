@@ -66,7 +66,8 @@ class Plan:
     def __init__(self, p):
         raw = p._host.view(np.int32)
         names = ["magic", "dtype", "heads", "kv_heads", "head_dim", "n_seqs", "q_rows", "k_rows", "n_rows", "n_join",
-                 "n_dq", "n_key", "o_rows", "o_join", "o_dq", "o_key", "parts", "overlap", "bytes"]
+                 "n_dq", "n_key", "o_rows", "o_join", "o_dq", "o_key", "parts", "overlap", "bytes", "n_key_join",
+                 "o_key_join", "key_parts"]
         self.h = dict(zip(names, raw[:len(names)].tolist()))
 
         def items(o, n, fields):
@@ -78,7 +79,8 @@ class Plan:
         self.dq = items(self.h["o_dq"], self.h["n_dq"], row)
         self.join = items(self.h["o_join"], self.h["n_join"], ["q_start", "q_len", "r0", "part", "n"])
         self.key = items(self.h["o_key"], self.h["n_key"],
-                         ["q_start", "q_len", "r_begin", "k_start", "k_len", "off", "key0", "part"])
+                         ["q_start", "q_len", "r_begin", "r_end", "k_start", "off", "key0", "part"])
+        self.key_join = items(self.h["o_key_join"], self.h["n_key_join"], ["k_row", "n_keys", "part", "n"])
 
 
 CASES = [
@@ -87,6 +89,7 @@ CASES = [
     (6, 2, [100, 31], [40, 0]),
     (32, 8, [1] * 5, [1, 64, 4097, 300, 16000]),
     (8, 8, [700, 1], [2100, 130]),
+    (32, 8, [3000], [3001]),
 ]
 
 
@@ -116,13 +119,25 @@ def test_plan_tiles_cover_what_each_query_sees(heads, kv, ql, kl):
                 assert len(parts) == 1 and parts[0]["part"] == -1
     assert {(j["q_start"], j["r0"]): list(range(j["part"], j["part"] + j["n"])) for j in pl.join} == seen
     assert sorted(x for v in seen.values() for x in v) == list(range(pl.h["parts"]))
-    # keys: every tile of every sequence once, from the first row that sees its first key
-    want = {(int(ks[i]), k0): (i, min(n, max(0, k0 - (m - n)) if n else 0) * G)
+    # keys: every tile of every sequence, over all rows from the first that sees its first key
+    want = {(int(ks[i]), k0): (i, min(n, max(0, k0 - (m - n))) * G)
             for i, (n, m) in enumerate(zip(ql, kl)) for k0 in range(0, m, 128)}
-    assert len(pl.key) == len(want)
+    got = {key: [] for key in want}
     for x in pl.key:
-        i, r = want.pop((x["k_start"], x["key0"]))
-        assert x["r_begin"] == min(r, ql[i] * G) and x["k_len"] == kl[i]
+        got[(x["k_start"], x["key0"])].append(x)
+    joins = {}
+    for (k0, key0), parts in got.items():
+        i, first = want[(k0, key0)]
+        parts.sort(key=lambda x: x["r_begin"])
+        assert parts[0]["r_begin"] == first and parts[-1]["r_end"] == ql[i] * G
+        assert all(a["r_end"] == b["r_begin"] and (b["r_begin"] - first) % 32 == 0 for a, b in zip(parts, parts[1:]))
+        assert all(x["off"] == kl[i] - ql[i] and x["q_start"] == qs[i] for x in parts)
+        if len(parts) > 1:
+            joins[(k0 + key0, min(128, kl[i] - key0))] = [x["part"] for x in parts]
+        else:
+            assert parts[0]["part"] == -1
+    assert {(j["k_row"], j["n_keys"]): list(range(j["part"], j["part"] + j["n"])) for j in pl.key_join} == joins
+    assert sorted(x for v in joins.values() for x in v) == list(range(pl.h["key_parts"]))
     # long tiles come first
     cost = [x["k_end"] - x["k_begin"] for x in pl.rows]
     assert cost == sorted(cost, reverse=True)

@@ -90,6 +90,7 @@ SHAPES = [
     (32, 1, 64, [1, 3], [2500, 64]),
     (16, 8, 24, [4, 0, 6], [0, 5, 6]),               # no keys; no queries
     (3, 3, 104, [256], [256]),
+    (8, 1, 64, [900, 3], [900, 3]),                  # dK, dV summed from several parts
 ]
 
 
