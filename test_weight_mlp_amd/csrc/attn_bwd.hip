@@ -101,62 +101,74 @@ __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kv
 #pragma unroll
   for (int db = 0; db < DB; ++db) fill16(acc[db], 0.0f);
 
+  // One tile of keys, in blocks of 32: the products of a block run while the
+  // vector units work on the scores or gradients of the block before.
   auto step = [&](int st, auto odd) {
     constexpr int B = decltype(odd)::value;
+    constexpr int NB = KT / 32;
     tiles_landed();
-    if (st + 1 < steps) load(st + 1, B ^ 1);
     const char *kt = lds + 2 * B * TB, *vt = kt + TB;
-    frag f[2][4];
+    frag f[2][4], p[NB][GR::NP];
+    floatx16 s[NB], dp[NB];
     int cur = 0;
     GR::rows(kt, here, 0, 0, f[0]);
+    // dS of block b from its P and dP - delta
+    auto grad = [&](int b) {
 #pragma unroll
-    for (int kb = 0; kb < KT / 32; ++kb) {
-      const int key0 = st * KT + 32 * kb;
-      floatx16 s, dp;
-      start16(s, nlse);
-      start16(dp, -delta);
+      for (int i = 0; i < 16; ++i) s[b][i] *= dp[b][i];
+      // a softmax over one key has no gradient: exactly 0, whatever rounding
+      // put between dP and delta
+      if (b == 0 && st == 0 && row.all <= 1 && row.lim == 1) fill16(s[b], 0.0f);
+#pragma unroll
+      for (int j = 0; j < GR::NP; ++j) p[b][j] = pack<T>(s[b], j * EPL);
+    };
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      start16(s[b], nlse);
+      start16(dp[b], -delta);
 #pragma unroll
       for (int g = 0; g < H; ++g) {
-        if (g + 1 < H) GR::rows(kt, here, 32 * kb, g + 1, f[cur ^ 1]);
-        else GR::rows(vt, here, 32 * kb, 0, f[cur ^ 1]);
+        if (g + 1 < H) GR::rows(kt, here, 32 * b, g + 1, f[cur ^ 1]);
+        else GR::rows(vt, here, 32 * b, 0, f[cur ^ 1]);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) s = Elt<T>::mma(f[cur][x], qf[4 * g + x], s);
+        for (int x = 0; x < 4; ++x) s[b] = Elt<T>::mma(f[cur][x], qf[4 * g + x], s[b]);
+        if (b > 0 && g == 0) grad(b - 1);
         cur ^= 1;
         __builtin_amdgcn_sched_barrier(0);
+        if (b == 0 && g == 0 && st + 1 < steps) load(st + 1, B ^ 1);
       }
+      const int key0 = st * KT + 32 * b;
       if (key0 + 32 > row.all) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (key0 + 8 * (i >> 2) + 4 * h + (i & 3) >= row.lim) s[i] = -INFINITY;
+          if (key0 + 8 * (i >> 2) + 4 * h + (i & 3) >= row.lim) s[b][i] = -INFINITY;
       }
 #pragma unroll
       for (int g = 0; g < H; ++g) {
-        if (g + 1 < H) GR::rows(vt, here, 32 * kb, g + 1, f[cur ^ 1]);
-        else GR::cols(kt, here, 32 * kb, 0, f[cur ^ 1]);
+        if (g + 1 < H) GR::rows(vt, here, 32 * b, g + 1, f[cur ^ 1]);
+        else if (b + 1 < NB) GR::rows(kt, here, 32 * (b + 1), 0, f[cur ^ 1]);
+        else GR::cols(kt, here, 0, 0, f[cur ^ 1]);
 #pragma unroll
-        for (int i = g * (16 / H); i < (g + 1) * (16 / H); ++i) s[i] = __builtin_amdgcn_exp2f(s[i] * sl2);
+        for (int i = g * (16 / H); i < (g + 1) * (16 / H); ++i) s[b][i] = __builtin_amdgcn_exp2f(s[b][i] * sl2);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) dp = Elt<T>::mma(f[cur][x], df[4 * g + x], dp);
+        for (int x = 0; x < 4; ++x) dp[b] = Elt<T>::mma(f[cur][x], df[4 * g + x], dp[b]);
         cur ^= 1;
         __builtin_amdgcn_sched_barrier(0);
       }
+    }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] *= dp[i];
-      // a softmax over one key has no gradient: exactly 0, whatever rounding
-      // put between dP and delta
-      if (key0 == 0 && row.all <= 1 && row.lim == 1) fill16(s, 0.0f);
-      frag p[GR::NP];
-#pragma unroll
-      for (int j = 0; j < GR::NP; ++j) p[j] = pack<T>(s, j * EPL);
+    for (int b = 0; b < NB; ++b) {
+      if (NB == 1) grad(0);
 #pragma unroll
       for (int g = 0; g < H; ++g) {
-        if (g + 1 < H) GR::cols(kt, here, 32 * kb, g + 1, f[cur ^ 1]);
-        else if (kb + 1 < KT / 32) GR::rows(kt, here, 32 * (kb + 1), 0, f[cur ^ 1]);
+        if (g + 1 < H) GR::cols(kt, here, 32 * b, g + 1, f[cur ^ 1]);
+        else if (b + 1 < NB) GR::cols(kt, here, 32 * (b + 1), 0, f[cur ^ 1]);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int y = 4 * g + x;
-          acc[y % DB] = Elt<T>::mma(f[cur][x], p[y / DB], acc[y % DB]);
+          acc[y % DB] = Elt<T>::mma(f[cur][x], p[b][y / DB], acc[y % DB]);
         }
+        if (b + 1 < NB && g == 0) grad(b + 1);
         cur ^= 1;
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -252,9 +264,12 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
     fill16(dv[db], 0.0f);
   }
 
-  // rows [32 s, 32 s + 32) from r_begin, straight to LDS; rows past the end
-  // read as zeros, which add nothing
-  RowMap rm(it.r_begin, G);
+  // Steps of 32 rows from r_begin, the last first: tiles of other keys of the
+  // sequence end at the same row, so workgroups that start together read the
+  // same rows at the same time.  Straight to LDS; rows past the end read as
+  // zeros, which add nothing.
+  const int r_last = it.r_begin + max(0, it.r_end - it.r_begin - 1) / RT * RT;
+  RowMap rm(r_last, G);
   const int t_step = RT / G, g_step = RT - t_step * G;
   auto load = [&](int r0, int buf) {
     const int64_t row = it.q_start + (int64_t)rm.t0;
@@ -286,11 +301,11 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
                                                  ok ? (uint32_t)(t * a.heads + g) * 4u : kOob, 0, 0, 0);
     }
     // the next step's first row
-    rm.t0 += t_step;
-    rm.g0 += g_step;
-    if (rm.g0 >= G) {
-      rm.g0 -= G;
-      ++rm.t0;
+    rm.t0 -= t_step;
+    rm.g0 -= g_step;
+    if (rm.g0 < 0) {
+      rm.g0 += G;
+      --rm.t0;
     }
   };
 
@@ -298,7 +313,7 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
     constexpr int B = decltype(odd)::value;
     tiles_landed();
     if (r0 + RT <= any) {  // no row of these sees a key of this wave
-      if (r0 + RT < r_end) load(r0 + RT, B ^ 1);
+      if (r0 > it.r_begin) load(r0 - RT, B ^ 1);
       return;
     }
     const char *qt = lds + KT::VB + 2 * B * TB, *ot = qt + TB;
@@ -325,7 +340,7 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
       cur ^= 1;
       __builtin_amdgcn_sched_barrier(0);
       // the next step's loads, while the matrix cores are busy
-      if (g == 0 && r0 + RT < r_end) load(r0 + RT, B ^ 1);
+      if (g == 0 && r0 > it.r_begin) load(r0 - RT, B ^ 1);
     }
     if (r0 < all) {
 #pragma unroll
@@ -382,13 +397,12 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  int r0 = it.r_begin;
-  if (r0 < r_end) load(r0, 0);
-  while (r0 < r_end) {
+  if (it.r_begin < r_end) load(r_last, 0);
+  for (int r0 = r_last; it.r_begin < r_end;) {
     step(r0, std::integral_constant<int, 0>());
-    if ((r0 += RT) >= r_end) break;
+    if ((r0 -= RT) < it.r_begin) break;
     step(r0, std::integral_constant<int, 1>());
-    r0 += RT;
+    if ((r0 -= RT) < it.r_begin) break;
   }
   if (!live) return;
   if (it.part >= 0) {

@@ -18,10 +18,12 @@ namespace ipttt {
 namespace attn {
 namespace {
 
-// The work of one wave on one step of kKeys keys, in phases of MFMAs with the
-// softmax of the other block of 32 keys between them: while the matrix cores
-// form the next step's scores and this step's O, the vector units raise this
-// step's scores to probabilities.  Fragments are read from LDS one group of
+// The work of one wave on one step of kKeys keys, in four phases of MFMAs: the
+// next step's scores (two blocks of 32 keys), then this step's part of O from
+// each block.  The vector units meanwhile raise this step's scores to
+// probabilities, spread evenly over the first three phases (the second phase's
+// end must have the first block's, the third's the second's), and take the
+// next scores' maximum in the last.  Fragments are read from LDS one group of
 // four MFMAs ahead.
 template <typename T, int DP>
 struct Step {
@@ -29,58 +31,65 @@ struct Step {
   typedef Groups<T, DP> GR;
   typedef typename Elt<T>::frag frag;
   static constexpr int EPL = Elt<T>::EPL, DB = DP / 32, H = GR::H;
-  static constexpr int EX = 16 / H;  // scores raised per group of MFMAs
 
-  // scores [i0, i0 + EX) of a block to probabilities
-  static __device__ __forceinline__ void raise(floatx16& s, int i0, float sl2, float m, float& l) {
+  // scores [e0, e0 + n) of the step's 32 to probabilities
+  template <int N>
+  static __device__ __forceinline__ void raise(floatx16 (&s)[2], int e0, float sl2, float m, float& l) {
 #pragma unroll
-    for (int i = 0; i < EX; ++i) {
-      s[i0 + i] = __builtin_amdgcn_exp2f(fmaf(s[i0 + i], sl2, -m));
-      l += s[i0 + i];
+    for (int e = e0; e < e0 + N; ++e) {
+      s[e >> 4][e & 15] = __builtin_amdgcn_exp2f(fmaf(s[e >> 4][e & 15], sl2, -m));
+      l += s[e >> 4][e & 15];
     }
   }
 
-  // s: this step's scores in, the next step's out (if NEXT); kt: the next
-  // step's keys, vt: this step's values
-  template <bool NEXT>
+  // s: this step's scores in, the next step's out (if NEXT) and top their
+  // largest; kt: the next step's keys, vt: this step's values; issue() starts
+  // the loads of later steps
+  template <bool NEXT, class Issue>
   static __device__ __forceinline__ void run(const char* kt, const char* vt, const frag (&qf)[TL::STEPS],
                                              floatx16 (&s)[2], floatx16 (&o)[DB], float sl2, float m, float& l,
-                                             const At<T, DP>& at) {
+                                             float& top, const At<T, DP>& at, Issue issue) {
     frag f[2][4];
     floatx16 n[2];
     int cur = 0;
     if constexpr (NEXT) {
-      GR::rows(kt, at, 32 * 0, 0, f[0]);
-    } else {
-      GR::cols(vt, at, 32 * 0, 0, f[0]);
+      GR::rows(kt, at, 0, 0, f[0]);
 #pragma unroll
-      for (int g = 0; g < H; ++g) raise(s[0], g * EX, sl2, m, l);
-    }
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      if constexpr (NEXT) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) n[kb][i] = 0.0f;
+      for (int kb = 0; kb < 2; ++kb) {
+        fill16(n[kb], 0.0f);
 #pragma unroll
         for (int g = 0; g < H; ++g) {
           if (g + 1 < H) GR::rows(kt, at, 32 * kb, g + 1, f[cur ^ 1]);
-          else GR::cols(vt, at, 32 * kb, 0, f[cur ^ 1]);
-          if (kb == 0) raise(s[0], g * EX, sl2, m, l);
+          else if (kb == 0) GR::rows(kt, at, 32, 0, f[cur ^ 1]);
+          else GR::cols(vt, at, 0, 0, f[cur ^ 1]);
+          raise<12 / H>(s, (kb * H + g) * (12 / H), sl2, m, l);
 #pragma unroll
           for (int x = 0; x < 4; ++x) n[kb] = Elt<T>::mma(f[cur][x], qf[4 * g + x], n[kb]);
           cur ^= 1;
           __builtin_amdgcn_sched_barrier(0);
+          if (kb == 0 && g == 0) issue();
         }
       }
-      frag p[16 / EPL];
+    } else {
+      GR::cols(vt, at, 0, 0, f[0]);
+      raise<24>(s, 0, sl2, m, l);
+    }
 #pragma unroll
-      for (int j = 0; j < 16 / EPL; ++j) p[j] = pack<T>(s[kb], j * EPL);
+    for (int kb = 0; kb < 2; ++kb) {
+      frag p[GR::NP];
+#pragma unroll
+      for (int j = 0; j < GR::NP; ++j) p[j] = pack<T>(s[kb], j * EPL);
 #pragma unroll
       for (int g = 0; g < H; ++g) {
         if (g + 1 < H) GR::cols(vt, at, 32 * kb, g + 1, f[cur ^ 1]);
-        else if (kb == 0 && NEXT) GR::rows(kt, at, 32 * 1, 0, f[cur ^ 1]);
-        else if (kb == 0) GR::cols(vt, at, 32 * 1, 0, f[cur ^ 1]);
-        if (kb == 0) raise(s[1], g * EX, sl2, m, l);
+        else if (kb == 0) GR::cols(vt, at, 32, 0, f[cur ^ 1]);
+        if (kb == 0) {
+          raise<8 / H>(s, 24 + g * (8 / H), sl2, m, l);
+        } else if constexpr (NEXT) {
+          if (g == 0) top = fmaxf(n[0][0], n[1][0]);
+#pragma unroll
+          for (int i = g * (16 / H); i < (g + 1) * (16 / H); ++i) top = fmaxf(fmaxf(top, n[0][i]), n[1][i]);
+        }
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int y = 4 * g + x;
@@ -97,24 +106,29 @@ struct Step {
   }
 };
 
-// Masks a step's scores and moves m up if a row's maximum passed it by more
-// than 2^8: sums and O are relative to m, exact for any m near the maximum, so
-// they are rescaled (one multiplication an element) only then, which after
-// the first few steps is rare.
+__device__ __forceinline__ float largest(const floatx16 (&s)[2]) {
+  float x = fmaxf(s[0][0], s[1][0]);
+#pragma unroll
+  for (int i = 1; i < 16; ++i) x = fmaxf(fmaxf(x, s[0][i]), s[1][i]);
+  return x;
+}
+
+// Masks a step's scores (whose largest is top) and moves m up if a row's
+// maximum passed it by more than 2^8: sums and O are relative to m, exact for any
+// m near the maximum, so they are rescaled (one multiplication an element)
+// only then, which after the first few steps is rare.
 template <int DB>
-__device__ __forceinline__ void settle(floatx16 (&s)[2], int key0, const Row& row, float sl2, floatx16 (&o)[DB],
-                                       float& m, float& l, int lane) {
+__device__ __forceinline__ void settle(floatx16 (&s)[2], float top, int key0, const Row& row, float sl2,
+                                       floatx16 (&o)[DB], float& m, float& l, int lane) {
   if (key0 + kKeys > row.all) {
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         if (key0 + 32 * kb + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= row.lim) s[kb][i] = -INFINITY;
+    top = largest(s);
   }
-  float x = fmaxf(s[0][0], s[1][0]);
-#pragma unroll
-  for (int i = 1; i < 16; ++i) x = fmaxf(fmaxf(x, s[0][i]), s[1][i]);
-  x = half_max(x) * sl2;
+  const float x = half_max(top) * sl2;
   if (__any(x > m + 8.0f)) {
     const float mn = fmaxf(m, x), c = __builtin_amdgcn_exp2f(m - mn);
     m = mn;
@@ -178,7 +192,8 @@ __device__ __forceinline__ void fwd_tile(const Args& a, const RowItem& it, int k
       for (int q = 0; q < TL::STEPS; ++q)
         s[kb] = Elt<T>::mma(TL::row(lds, here.row, 32 * kb, q), qf[q], s[kb]);
     }
-    settle<DB>(s, it.k_begin, row, sl2, o, m, l, lane);
+    settle<DB>(s, largest(s), it.k_begin, row, sl2, o, m, l, lane);
+    float top = 0.0f;
     // one step with another to follow; its buffers are known at compile time, so
     // that the LDS addresses of all fragments are a few registers plus immediate
     // offsets.  A wave whose rows see none of the next keys scores them all the
@@ -188,10 +203,11 @@ __device__ __forceinline__ void fwd_tile(const Args& a, const RowItem& it, int k
       // this step's values and the next one's keys are here, and every wave is
       // done with the buffers that the loads below fill
       tiles_landed();
-      values(st + 1);
-      if (st + 2 < steps) keys(st + 2);
-      ST::template run<true>(lds + (B ^ 1) * TB, lds + (2 + B) * TB, qf, s, o, sl2, m, l, here);
-      settle<DB>(s, it.k_begin + (st + 1) * kKeys, row, sl2, o, m, l, lane);
+      ST::template run<true>(lds + (B ^ 1) * TB, lds + (2 + B) * TB, qf, s, o, sl2, m, l, top, here, [&] {
+        values(st + 1);
+        if (st + 2 < steps) keys(st + 2);
+      });
+      settle<DB>(s, top, it.k_begin + (st + 1) * kKeys, row, sl2, o, m, l, lane);
     };
     int st = 0;
     while (st < steps - 1) {
@@ -200,7 +216,7 @@ __device__ __forceinline__ void fwd_tile(const Args& a, const RowItem& it, int k
       step(st++, std::integral_constant<int, 1>());
     }
     tiles_landed();
-    ST::template run<false>(lds, lds + (2 + (st & 1)) * TB, qf, s, o, sl2, m, l, here);
+    ST::template run<false>(lds, lds + (2 + (st & 1)) * TB, qf, s, o, sl2, m, l, top, here, [] {});
   }
   l = half_sum(l);
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
