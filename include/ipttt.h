@@ -371,8 +371,9 @@ ipttt_status ipttt_z_backward_saved(const ipttt_problem *p, const void *H, const
 /* A [rows, heads, head_dim] tensor of dtype on the device: element (r, h, i)
  * at data[r * row_stride + h * head_stride + i].  Slices of a fused projection
  * and caches in either order of tokens and heads are such tensors.  Strides
- * count elements, are multiples of 8 and at least head_dim; row_stride is at
- * most 2^22.  data is 16-byte aligned. */
+ * count elements, are multiples of 8 and at least head_dim (that of a dimension
+ * of one element is not used); row_stride is at most 2^22.  data is 16-byte
+ * aligned. */
 typedef struct {
   void *data;
   int64_t row_stride, head_stride;

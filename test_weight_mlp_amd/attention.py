@@ -9,18 +9,15 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from typing import Optional, Sequence
 
 import numpy as np
 import torch
 
-from . import IPTTT_BF16, IPTTT_F32, _check, _ptr, _stream, library
+from . import IPTTT_BF16, IPTTT_F32, _check, library
 
 _DTYPES = {IPTTT_F32: torch.float32, IPTTT_BF16: torch.bfloat16}
-
-
-class _CHeads(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 class _CQKProblem(ctypes.Structure):
@@ -44,7 +41,8 @@ def _lib() -> ctypes.CDLL:
     global _bound
     if _bound is None:
         lib = library()
-        vp, f32, i32, sz, H = ctypes.c_void_p, ctypes.c_float, ctypes.c_int, ctypes.c_size_t, ctypes.POINTER(_CHeads)
+        vp, f32, i32, sz = ctypes.c_void_p, ctypes.c_float, ctypes.c_int, ctypes.c_size_t
+        H = ctypes.c_char_p  # ipttt_heads, packed by _heads
         Q, A = ctypes.POINTER(_CQKProblem), ctypes.POINTER(_CAttnProblem)
         sigs = {
             "ipttt_qk_norm_rope": (i32, [Q, H, H, vp, vp, vp, vp, H, H, H, H, vp, vp]),
@@ -65,25 +63,35 @@ def _lib() -> ctypes.CDLL:
     return _bound
 
 
-def _heads(t: torch.Tensor, rows: int, heads: int, dim: int, dtype: torch.dtype, what: str) -> _CHeads:
-    if t.dtype is not dtype or t.shape != (rows, heads, dim) or t.device.type != "cuda":
-        raise ValueError(f"{what} must be a [{rows}, {heads}, {dim}] {dtype} device tensor, not "
-                         f"{list(t.shape)} {t.dtype} on {t.device}")
-    s = t.stride()
-    if s[2] != 1:
-        raise ValueError(f"{what}'s last dimension must be contiguous")
-    # a dimension of one element has no stride of its own
-    return _CHeads(t.data_ptr(), s[0] if rows > 1 else max(dim, heads * dim), s[1] if heads > 1 else dim)
+# Argument marshalling is most of a single-token call's time, so it looks at
+# each tensor once, in as few attribute reads as the checks need.
+
+_pack_heads = struct.Struct("Pqq").pack  # ipttt_heads: data, row_stride, head_stride
 
 
-def _flat(t: torch.Tensor, shape, dtype: torch.dtype, what: str):
-    if t.dtype is not dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device.type != "cuda":
-        raise ValueError(f"{what} must be a contiguous {list(shape)} {dtype} device tensor")
+def _heads(t: torch.Tensor, shape, dtype: torch.dtype, what: str) -> bytes:
+    """The ipttt_heads of a [rows, heads, head_dim] device tensor."""
+    row, head, one = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if t.shape != shape or t.dtype is not dtype or one != 1 or not t.is_cuda:
+        raise ValueError(f"{what} must be a {list(shape)} {dtype} device tensor with a contiguous last dimension, not "
+                         f"{list(t.shape)} {t.dtype} of strides {t.stride()} on {t.device}")
+    return _pack_heads(t.data_ptr(), row, head)
+
+
+def _flat(t: torch.Tensor, shape, dtype: torch.dtype, what: str) -> int:
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{what} must be a contiguous {list(shape)} {dtype} device tensor, not {list(t.shape)} "
+                         f"{t.dtype} on {t.device}")
     return t.data_ptr()
 
 
 def _ws(ws: Optional[torch.Tensor]):
-    return (None, 0) if ws is None or ws.numel() == 0 else (_ptr(ws), ws.numel())
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
+
+
+def _on(stream, t: torch.Tensor) -> int:
+    """The given stream, or the current one of the tensor's device."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
 
 
 # ------------------------------------------------------- norm and rotation
@@ -106,6 +114,10 @@ class QKProblem:
         self.out_rows = tokens if out_rows is None else out_rows
         self._c = _CQKProblem(tokens, heads, kv_heads, head_dim, table_rows, self.out_rows, dtype, eps)
         self.ref = ctypes.byref(self._c)
+        # the shapes that the calls check their tensors against
+        self.q_shape, self.k_shape = (tokens, heads, head_dim), (tokens, kv_heads, head_dim)
+        self.out_shape = (self.out_rows, kv_heads, head_dim)
+        self.w_shape, self.pos_shape, self.table_shape = (head_dim,), (tokens,), (table_rows, head_dim)
 
     @property
     def torch_dtype(self) -> torch.dtype:
@@ -116,20 +128,16 @@ def ipttt_qk_norm_rope(p: QKProblem, q, k, w_q, w_k, positions, table, q_out, k_
                        stream=None):
     """Norms and rotates q and k into q_out and k_out; with ``rows`` the keys (and
     v, if given) go to those rows of k_out (and v_out).  q_out may be q."""
-    dt, n, hq, hk, d = p.torch_dtype, p.tokens, p.heads, p.kv_heads, p.head_dim
-    out = p.out_rows
+    dt = _DTYPES[p.dtype]
     if (v is None) != (v_out is None):
         raise ValueError("v and v_out go together")
-    hv = hvo = None
-    if v is not None:
-        hv = ctypes.byref(_heads(v, n, hk, d, dt, "v"))
-        hvo = ctypes.byref(_heads(v_out, out, hk, d, dt, "v_out"))
     _check(_lib().ipttt_qk_norm_rope(
-        p.ref, ctypes.byref(_heads(q, n, hq, d, dt, "q")), ctypes.byref(_heads(k, n, hk, d, dt, "k")),
-        _flat(w_q, (d,), dt, "w_q"), _flat(w_k, (d,), dt, "w_k"), _flat(positions, (n,), torch.int32, "positions"),
-        _flat(table, (p.table_rows, d), torch.float32, "table"), ctypes.byref(_heads(q_out, n, hq, d, dt, "q_out")),
-        ctypes.byref(_heads(k_out, out, hk, d, dt, "k_out")), hv, hvo,
-        None if rows is None else _flat(rows, (n,), torch.int32, "rows"), _stream(stream)), "ipttt_qk_norm_rope")
+        p.ref, _heads(q, p.q_shape, dt, "q"), _heads(k, p.k_shape, dt, "k"), _flat(w_q, p.w_shape, dt, "w_q"),
+        _flat(w_k, p.w_shape, dt, "w_k"), _flat(positions, p.pos_shape, torch.int32, "positions"),
+        _flat(table, p.table_shape, torch.float32, "table"), _heads(q_out, p.q_shape, dt, "q_out"),
+        _heads(k_out, p.out_shape, dt, "k_out"), None if v is None else _heads(v, p.k_shape, dt, "v"),
+        None if v is None else _heads(v_out, p.out_shape, dt, "v_out"),
+        None if rows is None else _flat(rows, p.pos_shape, torch.int32, "rows"), _on(stream, q)), "ipttt_qk_norm_rope")
 
 
 def ipttt_qk_backward_workspace_bytes(p: QKProblem) -> int:
@@ -150,15 +158,15 @@ class QKGrads:
 
 def ipttt_qk_norm_rope_backward(p: QKProblem, q, k, w_q, w_k, positions, table, dq_out, dk_out, dq, dk, dw_q, dw_k, ws,
                                 stream=None):
-    dt, n, hq, hk, d = p.torch_dtype, p.tokens, p.heads, p.kv_heads, p.head_dim
+    dt, f32 = _DTYPES[p.dtype], torch.float32
     w, wn = _ws(ws)
     _check(_lib().ipttt_qk_norm_rope_backward(
-        p.ref, ctypes.byref(_heads(q, n, hq, d, dt, "q")), ctypes.byref(_heads(k, n, hk, d, dt, "k")),
-        _flat(w_q, (d,), dt, "w_q"), _flat(w_k, (d,), dt, "w_k"), _flat(positions, (n,), torch.int32, "positions"),
-        _flat(table, (p.table_rows, d), torch.float32, "table"), ctypes.byref(_heads(dq_out, n, hq, d, dt, "dq_out")),
-        ctypes.byref(_heads(dk_out, n, hk, d, dt, "dk_out")), ctypes.byref(_heads(dq, n, hq, d, dt, "dq")),
-        ctypes.byref(_heads(dk, n, hk, d, dt, "dk")), _flat(dw_q, (d,), torch.float32, "dw_q"),
-        _flat(dw_k, (d,), torch.float32, "dw_k"), w, wn, _stream(stream)), "ipttt_qk_norm_rope_backward")
+        p.ref, _heads(q, p.q_shape, dt, "q"), _heads(k, p.k_shape, dt, "k"), _flat(w_q, p.w_shape, dt, "w_q"),
+        _flat(w_k, p.w_shape, dt, "w_k"), _flat(positions, p.pos_shape, torch.int32, "positions"),
+        _flat(table, p.table_shape, f32, "table"), _heads(dq_out, p.q_shape, dt, "dq_out"),
+        _heads(dk_out, p.k_shape, dt, "dk_out"), _heads(dq, p.q_shape, dt, "dq"), _heads(dk, p.k_shape, dt, "dk"),
+        _flat(dw_q, p.w_shape, f32, "dw_q"), _flat(dw_k, p.w_shape, f32, "dw_k"), w, wn, _on(stream, q)),
+        "ipttt_qk_norm_rope_backward")
 
 
 # --------------------------------------------------------------- attention
@@ -186,6 +194,9 @@ class AttentionPlan:
         self.q_rows = ends[0] if q_rows is None else q_rows
         self.k_rows = ends[1] if k_rows is None else k_rows
         self.scale = 1.0 / math.sqrt(head_dim) if scale is None else float(scale)
+        # the shapes that the calls check their tensors against
+        self.q_shape, self.k_shape = (self.q_rows, heads, head_dim), (self.k_rows, kv_heads, head_dim)
+        self.lse_shape = (self.q_rows, heads)
         P = ctypes.POINTER(ctypes.c_int64)
         c = _CAttnProblem(ql.size, heads, kv_heads, head_dim, self.q_rows, self.k_rows, dtype,
                           *(x.ctypes.data_as(P) for x in arrays))
@@ -196,6 +207,7 @@ class AttentionPlan:
         self.ref = self._host.ctypes.data
         _check(lib.ipttt_attn_plan(ref, self.ref, n), "ipttt_attn_plan")
         self.table = torch.from_numpy(self._host).to(device)
+        self.dev = self.table.data_ptr()
         self.workspace_bytes = int(lib.ipttt_attn_workspace_bytes(self.ref))
         self.backward_workspace_bytes = int(lib.ipttt_attn_backward_workspace_bytes(self.ref))
 
@@ -209,10 +221,9 @@ class AttentionBuffers:
     the backward too (one workspace serves both calls in turn)."""
 
     def __init__(self, plan: AttentionPlan, grads: bool = False, device="cuda"):
-        dt, q, k = plan.torch_dtype, (plan.q_rows, plan.heads, plan.head_dim), \
-            (plan.k_rows, plan.kv_heads, plan.head_dim)
+        dt, q, k = plan.torch_dtype, plan.q_shape, plan.k_shape
         self.o = torch.empty(q, dtype=dt, device=device)
-        self.lse = torch.empty(q[:2], dtype=torch.float32, device=device)
+        self.lse = torch.empty(plan.lse_shape, dtype=torch.float32, device=device)
         need = max(plan.workspace_bytes, plan.backward_workspace_bytes if grads else 0)
         self.ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
         self.dq = torch.empty(q, dtype=dt, device=device) if grads else None
@@ -221,24 +232,20 @@ class AttentionBuffers:
 
 
 def ipttt_attention(plan: AttentionPlan, q, k, v, o, lse, ws=None, stream=None):
-    dt, hq, hk, d = plan.torch_dtype, plan.heads, plan.kv_heads, plan.head_dim
-    nq, nk = plan.q_rows, plan.k_rows
+    dt = _DTYPES[plan.dtype]
     w, wn = _ws(ws)
     _check(_lib().ipttt_attention(
-        plan.ref, plan.table.data_ptr(), plan.scale, ctypes.byref(_heads(q, nq, hq, d, dt, "q")),
-        ctypes.byref(_heads(k, nk, hk, d, dt, "k")), ctypes.byref(_heads(v, nk, hk, d, dt, "v")),
-        ctypes.byref(_heads(o, nq, hq, d, dt, "o")), _flat(lse, (nq, hq), torch.float32, "lse"), w, wn,
-        _stream(stream)), "ipttt_attention")
+        plan.ref, plan.dev, plan.scale, _heads(q, plan.q_shape, dt, "q"), _heads(k, plan.k_shape, dt, "k"),
+        _heads(v, plan.k_shape, dt, "v"), _heads(o, plan.q_shape, dt, "o"),
+        _flat(lse, plan.lse_shape, torch.float32, "lse"), w, wn, _on(stream, q)), "ipttt_attention")
 
 
 def ipttt_attention_backward(plan: AttentionPlan, q, k, v, o, lse, dO, dq, dk, dv, ws, stream=None):
-    dt, hq, hk, d = plan.torch_dtype, plan.heads, plan.kv_heads, plan.head_dim
-    nq, nk = plan.q_rows, plan.k_rows
+    dt = _DTYPES[plan.dtype]
     w, wn = _ws(ws)
     _check(_lib().ipttt_attention_backward(
-        plan.ref, plan.table.data_ptr(), plan.scale, ctypes.byref(_heads(q, nq, hq, d, dt, "q")),
-        ctypes.byref(_heads(k, nk, hk, d, dt, "k")), ctypes.byref(_heads(v, nk, hk, d, dt, "v")),
-        ctypes.byref(_heads(o, nq, hq, d, dt, "o")), _flat(lse, (nq, hq), torch.float32, "lse"),
-        ctypes.byref(_heads(dO, nq, hq, d, dt, "dO")), ctypes.byref(_heads(dq, nq, hq, d, dt, "dq")),
-        ctypes.byref(_heads(dk, nk, hk, d, dt, "dk")), ctypes.byref(_heads(dv, nk, hk, d, dt, "dv")), w, wn,
-        _stream(stream)), "ipttt_attention_backward")
+        plan.ref, plan.dev, plan.scale, _heads(q, plan.q_shape, dt, "q"), _heads(k, plan.k_shape, dt, "k"),
+        _heads(v, plan.k_shape, dt, "v"), _heads(o, plan.q_shape, dt, "o"),
+        _flat(lse, plan.lse_shape, torch.float32, "lse"), _heads(dO, plan.q_shape, dt, "dO"),
+        _heads(dq, plan.q_shape, dt, "dq"), _heads(dk, plan.k_shape, dt, "dk"), _heads(dv, plan.k_shape, dt, "dv"), w,
+        wn, _on(stream, q)), "ipttt_attention_backward")

@@ -39,17 +39,19 @@ ipttt_status check_dims(int64_t heads, int64_t kv_heads, int64_t head_dim, int32
   return IPTTT_OK;
 }
 
-// One tensor of heads.  A tile's rows are addressed with 32-bit byte offsets
-// from the tile's first row: `rows` rows and `heads` heads have to fit.
-ipttt_status check_heads(const ipttt_heads* t, int64_t heads, int64_t rows, int64_t D, int32_t dtype, View* v) {
+// One [rows, heads, D] tensor.  A tile's rows are addressed with 32-bit byte
+// offsets from the tile's first row: tile_rows rows of tile_heads heads have to
+// fit.  The stride of a dimension of one element is not looked at.
+ipttt_status check_heads(const ipttt_heads* t, int64_t rows, int64_t heads, int64_t D, int32_t dtype,
+                         int64_t tile_rows, int64_t tile_heads, View* v) {
   if (t == nullptr || t->data == nullptr) return IPTTT_ERR_NULL;
   if (!aligned(t->data, 16)) return IPTTT_ERR_ALIGN;
-  if (t->row_stride < D || t->head_stride < D || t->row_stride % 8 != 0 || t->head_stride % 8 != 0)
-    return IPTTT_ERR_SHAPE;
-  if (t->row_stride > kMaxRowStride || t->head_stride > kMaxHeadStride) return IPTTT_ERR_SHAPE;
+  const int64_t row = rows == 1 ? D : t->row_stride, head = heads == 1 ? D : t->head_stride;
+  if (row < D || head < D || row % 8 != 0 || head % 8 != 0) return IPTTT_ERR_SHAPE;
+  if (row > kMaxRowStride || head > kMaxHeadStride) return IPTTT_ERR_SHAPE;
   const int64_t es = dtype == IPTTT_BF16 ? 2 : 4;
-  if ((rows * t->row_stride + (heads - 1) * t->head_stride + D) * es > kMaxInt - 15) return IPTTT_ERR_SHAPE;
-  *v = View{t->data, t->row_stride, t->head_stride};
+  if ((tile_rows * row + (tile_heads - 1) * head + D) * es > kMaxInt - 15) return IPTTT_ERR_SHAPE;
+  *v = View{t->data, row, head};
   return IPTTT_OK;
 }
 
@@ -238,11 +240,11 @@ ipttt_status check_call(const void* plan, const void* plan_dev, float scale, voi
 // A tensor of no rows may be NULL: no tile reads or writes it.
 ipttt_status q_view(const PlanHeader* h, const ipttt_heads* t, View* v) {
   if (h->q_rows == 0) return IPTTT_OK;
-  return check_heads(t, h->heads / h->kv_heads, kRows + 1, h->head_dim, h->dtype, v);
+  return check_heads(t, h->q_rows, h->heads, h->head_dim, h->dtype, kRows + 1, h->heads / h->kv_heads, v);
 }
 ipttt_status k_view(const PlanHeader* h, const ipttt_heads* t, View* v) {
   if (h->k_rows == 0) return IPTTT_OK;
-  return check_heads(t, 1, kBwdKeys, h->head_dim, h->dtype, v);
+  return check_heads(t, h->k_rows, h->kv_heads, h->head_dim, h->dtype, kBwdKeys, 1, v);
 }
 
 ipttt::attn::Args base_args(const PlanHeader* h, float scale) {
@@ -269,8 +271,8 @@ ipttt_status check_qk(const ipttt_qk_problem* p) {
 }
 
 // Every address is 64-bit here: only the strides' own rules apply.
-ipttt_status qk_view(const ipttt_qk_problem* p, const ipttt_heads* t, View* v) {
-  return check_heads(t, 1, 1, p->head_dim, p->dtype, v);
+ipttt_status qk_view(const ipttt_qk_problem* p, const ipttt_heads* t, int64_t rows, int64_t heads, View* v) {
+  return check_heads(t, rows, heads, p->head_dim, p->dtype, 1, 1, v);
 }
 
 bool same(const View& a, const View& b) { return a.p == b.p && a.row == b.row && a.head == b.head; }
@@ -320,14 +322,14 @@ ipttt_status ipttt_qk_norm_rope(const ipttt_qk_problem* p, const ipttt_heads* q,
   IPTTT_TRY(check_qk(p));
   IPTTT_TRY(check_qk_inputs(w_q, w_k, positions, table));
   ipttt::QkArgs a = qk_args(p, w_q, w_k, positions, table);
-  IPTTT_TRY(qk_view(p, q, &a.q));
-  IPTTT_TRY(qk_view(p, k, &a.k));
-  IPTTT_TRY(qk_view(p, q_out, &a.q_out));
-  IPTTT_TRY(qk_view(p, k_out, &a.k_out));
+  IPTTT_TRY(qk_view(p, q, p->tokens, p->heads, &a.q));
+  IPTTT_TRY(qk_view(p, k, p->tokens, p->kv_heads, &a.k));
+  IPTTT_TRY(qk_view(p, q_out, p->tokens, p->heads, &a.q_out));
+  IPTTT_TRY(qk_view(p, k_out, p->out_rows, p->kv_heads, &a.k_out));
   if ((v == nullptr) != (v_out == nullptr)) return IPTTT_ERR_NULL;
   if (v != nullptr) {
-    IPTTT_TRY(qk_view(p, v, &a.v));
-    IPTTT_TRY(qk_view(p, v_out, &a.v_out));
+    IPTTT_TRY(qk_view(p, v, p->tokens, p->kv_heads, &a.v));
+    IPTTT_TRY(qk_view(p, v_out, p->out_rows, p->kv_heads, &a.v_out));
   }
   if (!aligned(rows, 4)) return IPTTT_ERR_ALIGN;
   if (rows == nullptr && p->out_rows < p->tokens) return IPTTT_ERR_SHAPE;
@@ -350,12 +352,12 @@ ipttt_status ipttt_qk_norm_rope_backward(const ipttt_qk_problem* p, const ipttt_
   IPTTT_TRY(check_qk(p));
   IPTTT_TRY(check_qk_inputs(w_q, w_k, positions, table));
   ipttt::QkArgs a = qk_args(p, w_q, w_k, positions, table);
-  IPTTT_TRY(qk_view(p, q, &a.q));
-  IPTTT_TRY(qk_view(p, k, &a.k));
-  IPTTT_TRY(qk_view(p, dq_out, &a.q_out));
-  IPTTT_TRY(qk_view(p, dk_out, &a.k_out));
-  IPTTT_TRY(qk_view(p, dq, &a.dq));
-  IPTTT_TRY(qk_view(p, dk, &a.dk));
+  IPTTT_TRY(qk_view(p, q, p->tokens, p->heads, &a.q));
+  IPTTT_TRY(qk_view(p, k, p->tokens, p->kv_heads, &a.k));
+  IPTTT_TRY(qk_view(p, dq_out, p->tokens, p->heads, &a.q_out));
+  IPTTT_TRY(qk_view(p, dk_out, p->tokens, p->kv_heads, &a.k_out));
+  IPTTT_TRY(qk_view(p, dq, p->tokens, p->heads, &a.dq));
+  IPTTT_TRY(qk_view(p, dk, p->tokens, p->kv_heads, &a.dk));
   if (dw_q == nullptr || dw_k == nullptr) return IPTTT_ERR_NULL;
   if (!aligned(dw_q, 16) || !aligned(dw_k, 16)) return IPTTT_ERR_ALIGN;
   if (a.dq.p == a.q_out.p && !same(a.dq, a.q_out)) return IPTTT_ERR_ARG;

@@ -202,7 +202,7 @@ def test_plan_buffer_is_checked():
 
 
 def _heads(data=256, row=256, head=64):
-    return ctypes.byref(at._CHeads(data, row, head))
+    return at._pack_heads(data or 0, row, head)
 
 
 @needs_lib
@@ -277,6 +277,6 @@ def test_binding_checks_tensors():
     x = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
     for t, rows in ((x, 3), (x.float(), 3), (x, 4)):
         with pytest.raises(ValueError):
-            at._heads(t, rows, 4, 64, torch.bfloat16, "q")      # not on a device, another type, another shape
+            at._heads(t, (rows, 4, 64), torch.bfloat16, "q")    # not on a device, another type, another shape
     with pytest.raises(ValueError):
         ip.AttentionPlan(4, 2, 64, [1, 2], [1], device="cpu")
