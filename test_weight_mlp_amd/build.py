@@ -28,7 +28,7 @@ SAN_LIB = os.path.join(SAN_OBJDIR, "libipttt.so")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 
 SOURCES = ["seg.hip", "gated_z.hip", "target.hip", "delta.hip", "apply.hip", "backward.hip", "noalloc.hip",
-           "qk.hip", "attn_fwd.hip", "attn_bwd.hip", "api.cpp", "attn_api.cpp"]
+           "qk.hip", "attn_fwd.hip", "attn_few.hip", "attn_bwd.hip", "api.cpp", "attn_api.cpp"]
 
 # Packed-fp32 instructions stay off: plain fp32 code is what every kernel here
 # is written and tested as.

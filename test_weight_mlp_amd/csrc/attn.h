@@ -11,6 +11,8 @@ namespace attn {
 // the group) rows of one key head: row r is query r / G, head r % G of the group.
 constexpr int kRows = 128;      // rows of a forward tile, and of a dQ tile
 constexpr int kKeys = 64;       // keys of one step
+constexpr int kFewRows = 32;    // most rows of a sequence that the kernel of few rows takes, in one tile
+constexpr int kPartRows = 32;   // rows of a slot of partial results (a forward tile takes kRows / kPartRows of them)
 constexpr int kBwdKeys = 128;   // keys of a dK, dV tile
 constexpr int kBwdRows = 32;    // rows of one step of it
 
@@ -23,9 +25,9 @@ struct RowItem {
   int32_t part;              // -1: the whole of the rows' keys; else the slot of this partial result
 };
 
-// The partial results of one forward tile, slots [part, part + n).
+// The n partial results of one forward tile, in slots part, part + step, ...
 struct JoinItem {
-  int32_t q_start, q_len, r0, part, n;
+  int32_t q_start, q_len, r0, part, n, step;
 };
 
 // One dK, dV tile: keys [key0, min(key0 + kBwdKeys, k_len)) of one sequence
@@ -51,7 +53,9 @@ struct PlanHeader {
   int32_t parts, overlap;    // partial slots; whether two sequences share keys
   int32_t bytes;
   int32_t n_key_join, o_key_join, key_parts;
-  int32_t pad[10];
+  int32_t n_few, o_few;      // items of the kernel of few rows
+  int32_t join_rows;         // most rows of a joined tile
+  int32_t pad[7];
 };
 static_assert(sizeof(PlanHeader) == 128, "plan header");
 constexpr int32_t kMagic = 0x41545031;
@@ -73,7 +77,8 @@ struct Args {
 };
 
 hipError_t launch_forward(const Args& a, hipStream_t st);
-hipError_t launch_join(const Args& a, const void* items, int n, hipStream_t st);
+hipError_t launch_few(const Args& a, hipStream_t st);
+hipError_t launch_join(const Args& a, const void* items, int n, int rows, hipStream_t st);
 hipError_t launch_dq(const Args& a, hipStream_t st);
 hipError_t launch_dkv(const Args& a, hipStream_t st);
 hipError_t launch_join_keys(const Args& a, const void* items, int n, hipStream_t st);

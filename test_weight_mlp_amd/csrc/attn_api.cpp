@@ -13,7 +13,9 @@ using ipttt::attn::KeyItem;
 using ipttt::attn::kBwdKeys;
 using ipttt::attn::kBwdRows;
 using ipttt::attn::KeyJoin;
+using ipttt::attn::kFewRows;
 using ipttt::attn::kKeys;
+using ipttt::attn::kPartRows;
 using ipttt::attn::kMagic;
 using ipttt::attn::kRows;
 using ipttt::attn::PlanHeader;
@@ -101,23 +103,33 @@ constexpr int64_t kGroups = 512;
 // How far the tiles are cut into parts.
 struct Cut {
   int64_t keys;   // most keys of a forward part
+  int64_t few;    // most keys of a part of few rows
   int64_t steps;  // most steps of a dK, dV part
 };
 
+bool few_rows(const ipttt_attn_problem* p, int64_t i) { return p->q_len[i] * (p->heads / p->kv_heads) <= kFewRows; }
+
 // Forward: where there are fewer tiles than workgroups that run at once, they
 // share the keys of all tiles evenly; a part is at least four steps long, so that
-// its join costs little beside it.  dK, dV: the first keys of a causal sequence
-// meet all its rows and the last almost none, so a tile's steps are cut to
-// the average of what a workgroup gets; at least 16, for the same reason.
-// (8k tokens, 32 heads over 8 of width 128: 1.70 ms uncut, 1.19 ms cut and joined.)
+// its join costs little beside it.  Few rows: only reading matters, so parts are
+// short enough that four rounds of workgroups even out, but at least two blocks
+// of 32 keys for each of a workgroup's two waves.  dK, dV: the first keys of a
+// causal sequence meet all its rows and the last almost none, so a tile's steps
+// are cut to the average of what a workgroup gets; at least 16, for the same
+// reason as above.  (8k tokens, 32 heads over 8 of width 128: 1.70 ms uncut, 1.19 ms
+// cut and joined.)
 Cut cut_of(const ipttt_attn_problem* p) {
-  constexpr int64_t kLeastKeys = 4 * kKeys, kLeastSteps = 16;
+  constexpr int64_t kLeastKeys = 4 * kKeys, kLeastFew = 128, kLeastSteps = 16;
   const int64_t G = p->heads / p->kv_heads;
-  int64_t tiles = 0, keys = 0, steps = 0;
+  int64_t tiles = 0, keys = 0, few = 0, steps = 0;
   for (int64_t i = 0; i < p->n_seqs; ++i) {
-    for (int64_t r0 = 0; r0 < p->q_len[i] * G; r0 += kRows) {
-      ++tiles;
-      keys += tile_keys(p, i, r0, kRows);
+    if (few_rows(p, i)) {
+      few += p->k_len[i];
+    } else {
+      for (int64_t r0 = 0; r0 < p->q_len[i] * G; r0 += kRows) {
+        ++tiles;
+        keys += tile_keys(p, i, r0, kRows);
+      }
     }
     for (int64_t k0 = 0; k0 < p->k_len[i]; k0 += kBwdKeys) steps += key_steps(p, i, k0);
   }
@@ -125,29 +137,37 @@ Cut cut_of(const ipttt_attn_problem* p) {
   c.keys = tiles * p->kv_heads >= kGroups
                ? kMaxInt
                : div_up(std::max(kLeastKeys, div_up(keys * p->kv_heads, kGroups)), kKeys) * kKeys;
+  c.few = div_up(std::max(kLeastFew, div_up(few * p->kv_heads, 4 * kGroups)), 64) * 64;
   c.steps = std::max(kLeastSteps, div_up(steps * p->kv_heads, kGroups));
   return c;
 }
 
 // Walks every item of the plan in sequence order.
-template <class Rows, class Join, class Dq, class Key, class KJoin>
-void walk(const ipttt_attn_problem* p, const Cut& cut, Rows&& rows, Join&& join, Dq&& dq, Key&& key, KJoin&& kjoin) {
+template <class Rows, class FewRows, class Join, class Dq, class Key, class KJoin>
+void walk(const ipttt_attn_problem* p, const Cut& cut, Rows&& rows, FewRows&& few, Join&& join, Dq&& dq, Key&& key,
+          KJoin&& kjoin) {
   const int64_t G = p->heads / p->kv_heads;
   int64_t slots = 0, key_slots = 0;
   for (int64_t i = 0; i < p->n_seqs; ++i) {
     const int32_t off = (int32_t)(p->k_len[i] - p->q_len[i]);
     const int32_t qs = (int32_t)p->q_start[i], ql = (int32_t)p->q_len[i], ks = (int32_t)p->k_start[i];
-    for (int64_t r0 = 0; r0 < p->q_len[i] * G; r0 += kRows) {
-      const int64_t n = tile_keys(p, i, r0, kRows), parts = n > cut.keys ? div_up(n, cut.keys) : 1;
-      dq(RowItem{qs, ql, (int32_t)r0, ks, off, 0, (int32_t)n, -1});
+    // one tile over its keys, in parts of at most `most`, each of `step` slots
+    const auto tile = [&](int64_t r0, int64_t n, int64_t most, int64_t step, auto& emit) {
+      const int64_t parts = std::max<int64_t>(1, div_up(n, most));
       if (parts == 1) {
-        rows(RowItem{qs, ql, (int32_t)r0, ks, off, 0, (int32_t)n, -1});
-        continue;
+        emit(RowItem{qs, ql, (int32_t)r0, ks, off, 0, (int32_t)n, -1});
+        return;
       }
-      join(JoinItem{qs, ql, (int32_t)r0, (int32_t)slots, (int32_t)parts});
-      for (int64_t j = 0; j < parts; ++j)
-        rows(RowItem{qs, ql, (int32_t)r0, ks, off, (int32_t)(j * cut.keys),
-                     (int32_t)std::min(n, (j + 1) * cut.keys), (int32_t)slots++});
+      join(JoinItem{qs, ql, (int32_t)r0, (int32_t)slots, (int32_t)parts, (int32_t)step});
+      for (int64_t j = 0; j < parts; ++j, slots += step)
+        emit(RowItem{qs, ql, (int32_t)r0, ks, off, (int32_t)(j * most), (int32_t)std::min(n, (j + 1) * most),
+                     (int32_t)slots});
+    };
+    if (p->q_len[i] > 0 && few_rows(p, i)) tile(0, tile_keys(p, i, 0, kFewRows), cut.few, 1, few);
+    for (int64_t r0 = 0; r0 < p->q_len[i] * G; r0 += kRows) {
+      const int64_t n = tile_keys(p, i, r0, kRows);
+      dq(RowItem{qs, ql, (int32_t)r0, ks, off, 0, (int32_t)n, -1});
+      if (!few_rows(p, i)) tile(r0, n, cut.keys, kRows / kPartRows, rows);
     }
     for (int64_t k0 = 0; k0 < p->k_len[i]; k0 += kBwdKeys) {
       const int64_t r0 = key_rows(p, i, k0), end = p->q_len[i] * G;
@@ -173,32 +193,36 @@ struct Range {
 };
 
 struct Sizes {
-  int64_t rows = 0, join = 0, dq = 0, key = 0, kjoin = 0, parts = 0, key_parts = 0;
-  int64_t o_rows, o_join, o_dq, o_key, o_kjoin, o_ranges, bytes;
+  int64_t rows = 0, few = 0, join = 0, dq = 0, key = 0, kjoin = 0, parts = 0, key_parts = 0, join_rows = 0;
+  int64_t o_rows, o_few, o_join, o_dq, o_key, o_kjoin, o_ranges, bytes;
 };
 
 // Counts and offsets; false if the plan would not fit its own 31-bit fields.
 bool sizes_of(const ipttt_attn_problem* p, const Cut& cut, Sizes* s) {
+  const int64_t G = p->heads / p->kv_heads;
   walk(
       p, cut,
-      [&](const RowItem& x) {
-        ++s->rows;
-        s->parts += x.part >= 0;
+      [&](const RowItem&) { ++s->rows; }, [&](const RowItem&) { ++s->few; },
+      [&](const JoinItem& x) {
+        ++s->join;
+        s->parts += (int64_t)x.n * x.step;
+        s->join_rows = std::max(s->join_rows, std::min<int64_t>(x.step * kPartRows, x.q_len * G - x.r0));
       },
-      [&](const JoinItem&) { ++s->join; }, [&](const RowItem&) { ++s->dq; },
+      [&](const RowItem&) { ++s->dq; },
       [&](const KeyItem& x) {
         ++s->key;
         s->key_parts += x.part >= 0;
       },
       [&](const KeyJoin&) { ++s->kjoin; });
   s->o_rows = sizeof(PlanHeader);
-  s->o_dq = s->o_rows + s->rows * (int64_t)sizeof(RowItem);
+  s->o_few = s->o_rows + s->rows * (int64_t)sizeof(RowItem);
+  s->o_dq = s->o_few + s->few * (int64_t)sizeof(RowItem);
   s->o_key = s->o_dq + s->dq * (int64_t)sizeof(RowItem);
   s->o_join = s->o_key + s->key * (int64_t)sizeof(KeyItem);
   s->o_kjoin = (s->o_join + s->join * (int64_t)sizeof(JoinItem) + 15) / 16 * 16;
   s->o_ranges = s->o_kjoin + s->kjoin * (int64_t)sizeof(KeyJoin);
   s->bytes = s->o_ranges + p->n_seqs * (int64_t)sizeof(Range);
-  const int64_t most = std::max(std::max(s->rows, s->dq), s->key);
+  const int64_t most = std::max(std::max(s->rows, s->few), std::max(s->dq, s->key));
   return s->bytes <= kMaxInt && most <= kMaxGroups / p->kv_heads;
 }
 
@@ -213,7 +237,7 @@ struct FwdLayout {
 };
 FwdLayout fwd_layout(const PlanHeader* h) {
   FwdLayout l;
-  const size_t rows = (size_t)h->parts * h->kv_heads * kRows;
+  const size_t rows = (size_t)h->parts * h->kv_heads * kPartRows;
   l.o = 0;
   l.lse = align256(rows * h->head_dim * sizeof(float));
   l.total = l.lse + align256(rows * sizeof(float));
@@ -395,7 +419,9 @@ ipttt_status ipttt_attn_plan(const ipttt_attn_problem* p, void* plan, size_t pla
   KeyItem* key = reinterpret_cast<KeyItem*>(base + s.o_key);
   JoinItem* join = reinterpret_cast<JoinItem*>(base + s.o_join);
   KeyJoin* kjoin = reinterpret_cast<KeyJoin*>(base + s.o_kjoin);
-  walk(p, cut, [&](const RowItem& x) { *rows++ = x; }, [&](const JoinItem& x) { *join++ = x; },
+  RowItem* few = reinterpret_cast<RowItem*>(base + s.o_few);
+  walk(p, cut, [&](const RowItem& x) { *rows++ = x; }, [&](const RowItem& x) { *few++ = x; },
+       [&](const JoinItem& x) { *join++ = x; },
        [&](const RowItem& x) { *dq++ = x; }, [&](const KeyItem& x) { *key++ = x; },
        [&](const KeyJoin& x) { *kjoin++ = x; });
   // the longest first, so that the last workgroups to start are short ones
@@ -405,6 +431,7 @@ ipttt_status ipttt_attn_plan(const ipttt_attn_problem* p, void* plan, size_t pla
     return x.q_start != y.q_start ? x.q_start < y.q_start : x.r0 != y.r0 ? x.r0 < y.r0 : x.k_begin < y.k_begin;
   };
   std::sort(rows - s.rows, rows, longer);
+  std::sort(few - s.few, few, longer);
   std::sort(dq - s.dq, dq, longer);
   std::sort(key - s.key, key, [](const KeyItem& x, const KeyItem& y) {
     const int32_t a = x.r_end - x.r_begin, b = y.r_end - y.r_begin;
@@ -430,6 +457,9 @@ ipttt_status ipttt_attn_plan(const ipttt_attn_problem* p, void* plan, size_t pla
   h->q_rows = (int32_t)p->q_rows;
   h->k_rows = (int32_t)p->k_rows;
   h->n_rows = (int32_t)s.rows;
+  h->n_few = (int32_t)s.few;
+  h->o_few = (int32_t)s.o_few;
+  h->join_rows = (int32_t)s.join_rows;
   h->n_join = (int32_t)s.join;
   h->n_dq = (int32_t)s.dq;
   h->n_key = (int32_t)s.key;
@@ -474,12 +504,18 @@ ipttt_status ipttt_attention(const void* plan, const void* plan_dev, float scale
   a.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + l.lse);
   const char* dev = static_cast<const char*>(plan_dev);
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  if (h->n_rows == 0) return IPTTT_OK;
-  a.items = dev + h->o_rows;
-  a.n_items = h->n_rows;
-  IPTTT_TRY(hip_status(ipttt::attn::launch_forward(a, st)));
+  if (h->n_rows > 0) {
+    a.items = dev + h->o_rows;
+    a.n_items = h->n_rows;
+    IPTTT_TRY(hip_status(ipttt::attn::launch_forward(a, st)));
+  }
+  if (h->n_few > 0) {
+    a.items = dev + h->o_few;
+    a.n_items = h->n_few;
+    IPTTT_TRY(hip_status(ipttt::attn::launch_few(a, st)));
+  }
   if (h->n_join == 0) return IPTTT_OK;
-  return hip_status(ipttt::attn::launch_join(a, dev + h->o_join, h->n_join, st));
+  return hip_status(ipttt::attn::launch_join(a, dev + h->o_join, h->n_join, h->join_rows, st));
 }
 
 ipttt_status ipttt_attention_backward(const void* plan, const void* plan_dev, float scale, const ipttt_heads* q,

@@ -51,8 +51,8 @@ __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kv
   if (steps > 0) load(0, 0);
 
   frag qf[TL::STEPS], df[TL::STEPS];
-  row_frags<T, DP>(static_cast<const char*>(a.q.p) + (at * a.q.row + head * a.q.head) * ES, row.live, D, h, qf);
-  row_frags<T, DP>(static_cast<const char*>(a.dO.p) + (at * a.dO.row + head * a.dO.head) * ES, row.live, D, h, df);
+  row_frags<T, DP>(a.q, it, row, kvh, a.G, D, h, qf);
+  row_frags<T, DP>(a.dO, it, row, kvh, a.G, D, h, df);
   // the scores' accumulators start at -lse / scale, dP's at -delta: what comes
   // out of the products is ready for the exponential and for dS = P (dP - delta).
   // -inf (P = 0) on rows that see nothing, and past the sequence
@@ -85,7 +85,7 @@ __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kv
     }
   } else {
     frag of[TL::STEPS];
-    row_frags<T, DP>(static_cast<const char*>(a.o.p) + (at * a.o.row + head * a.o.head) * ES, row.live, D, h, of);
+    row_frags<T, DP>(a.o, it, row, kvh, a.G, D, h, of);
 #pragma unroll
     for (int s = 0; s < TL::STEPS; ++s)
 #pragma unroll
@@ -248,7 +248,8 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
     vs.issue(V, (int64_t)it.k_start + it.key0, k_len - it.key0, lds, wave);
   }
   frag kf[TL::STEPS];
-  row_frags<T, DP>(K + krow * a.k.row * ES, live, D, h, kf);
+  row_frags<T, DP>(rsrc_of(K + ((int64_t)it.k_start + it.key0) * a.k.row * ES, kMaxBytes),
+                   live ? (uint32_t)((key - it.key0) * (int)a.k.row) * ES : kOob, D, h, kf);
   // the first flat row that sees this key, the wave's first key, its last
   const int from = live ? max(0, key - it.off) * G : 0x7FFFFFFF;
   const int any = wkey < k_len ? max(0, wkey - it.off) * G : 0x7FFFFFFF;

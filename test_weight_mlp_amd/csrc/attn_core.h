@@ -221,29 +221,48 @@ struct RowStream {
   }
   // tile <- rows [row, row + min(R, left)) of the head at base; left >= 1
   __device__ __forceinline__ void issue(const char* base, int64_t row, int left, char* tile, int wave) const {
-    const __amdgpu_buffer_rsrc_t rs = rsrc_of(base + row * (int64_t)stride, (left - 1) * (int64_t)stride + tail);
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(base + row * (int64_t)stride), (short)0, (min(left, R) - 1) * (int)stride + tail, 0x00020000);
 #pragma unroll
     for (int j = 0; j < N; ++j)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(tile + (wave * N + j) * TL::PITCH), 16, off[j], 0, 0, 0);
   }
 };
 
+// Waits until at most N of this wave's vector-memory operations are pending.
+template <int N>
+__device__ __forceinline__ void loads_pending() {
+  static_assert(N < 64, "vmcnt");
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+  asm volatile("" ::: "memory");
+}
+
+// Waits until every LDS read of this wave has returned.
+__device__ __forceinline__ void reads_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// Row i of the partial results in slot part: slots hold kPartRows rows of every
+// key head.
+__device__ __forceinline__ int64_t part_row(int part, int kv_heads, int kvh, int i) {
+  return ((int64_t)(part + i / kPartRows) * kv_heads + kvh) * kPartRows + i % kPartRows;
+}
+
 // Workgroup barrier after this wave's own loads to LDS have landed.
 __device__ __forceinline__ void tiles_landed() {
-  __builtin_amdgcn_s_waitcnt((0x7 << 4) | (0xF << 8));  // vmcnt(0)
+  loads_pending<0>();
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// A lane's chunks of one row in global memory (zeros where it has none).
+// A lane's chunks of one row in global memory, its byte offset in the resource
+// given (kOob: no row); zeros where it has none.
 template <typename T, int DP>
-__device__ __forceinline__ void row_frags(const char* row, bool live, int D, int h,
+__device__ __forceinline__ void row_frags(__amdgpu_buffer_rsrc_t rs, uint32_t off, int D, int h,
                                           typename Elt<T>::frag (&f)[Tile<T, DP>::STEPS]) {
 #pragma unroll
   for (int s = 0; s < Tile<T, DP>::STEPS; ++s) {
-    const int c = 2 * s + h;
-#pragma unroll
-    for (int e = 0; e < Elt<T>::EPL; ++e) f[s][e] = (T)0.0f;
-    if (live && c * 16 < D * (int)sizeof(T)) f[s] = *reinterpret_cast<const typename Elt<T>::frag*>(row + c * 16);
+    const uint32_t at = (uint32_t)(2 * s + h) * 16u;
+    f[s] = __builtin_bit_cast(typename Elt<T>::frag,
+                              __builtin_amdgcn_raw_buffer_load_b128(
+                                  rs, at < (uint32_t)D * sizeof(T) && off != kOob ? off + at : kOob, 0, 0));
   }
 }
 
@@ -284,10 +303,12 @@ struct Row {
   bool live;
   int lim;          // it sees keys below lim
   int all;          // every row of the wave sees the keys below all
+  int t0;           // the wave's first query
 
   __device__ __forceinline__ Row(const RowItem& it, int G, int wave, int lane) {
     const int n_rows = it.q_len * G, r0 = it.r0 + wave * 32;
     const RowMap rm(r0, G);
+    t0 = rm.t0;
     r = r0 + (lane & 31);
     rm.of(lane & 31, &t, &g);
     t += rm.t0;
@@ -296,6 +317,18 @@ struct Row {
     all = __builtin_amdgcn_readfirstlane(min(it.off + rm.t0 + 1, it.k_end));
   }
 };
+
+// This lane's chunks of its row of a [rows, heads, D] tensor: the resource
+// starts at the wave's first query, so that offsets are 32-bit.
+template <typename T, int DP>
+__device__ __forceinline__ void row_frags(const View& v, const RowItem& it, const Row& row, int kvh, int G, int D, int h,
+                                          typename Elt<T>::frag (&f)[Tile<T, DP>::STEPS]) {
+  constexpr int ES = sizeof(T);
+  const char* base = static_cast<const char*>(v.p) +
+                     ((it.q_start + (int64_t)row.t0) * v.row + (int64_t)kvh * G * v.head) * ES;
+  const uint32_t off = (uint32_t)((row.t - row.t0) * (int)v.row + row.g * (int)v.head) * ES;
+  row_frags<T, DP>(rsrc_of(base, kMaxBytes), row.live ? off : kOob, D, h, f);
+}
 
 }  // namespace attn
 }  // namespace ipttt

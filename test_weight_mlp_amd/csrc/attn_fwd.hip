@@ -169,12 +169,10 @@ __device__ __forceinline__ void fwd_tile(const Args& a, const RowItem& it, int k
   if (steps > 0) keys(0);
 
   frag qf[TL::STEPS];
-  row_frags<T, DP>(static_cast<const char*>(a.q.p) + (at * a.q.row + head * a.q.head) * ES, row.live, D, h, qf);
+  row_frags<T, DP>(a.q, it, row, kvh, a.G, D, h, qf);
   floatx16 o[DB];
 #pragma unroll
-  for (int db = 0; db < DB; ++db)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[db][i] = 0.0f;
+  for (int db = 0; db < DB; ++db) fill16(o[db], 0.0f);
   // m starts below every score and stays finite, so that masked scores (-inf)
   // of a row that has seen nothing give 0, not NaN
   float m = -1e38f, l = 0.0f;
@@ -186,8 +184,7 @@ __device__ __forceinline__ void fwd_tile(const Args& a, const RowItem& it, int k
     floatx16 s[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s[kb][i] = 0.0f;
+      fill16(s[kb], 0.0f);
 #pragma unroll
       for (int q = 0; q < TL::STEPS; ++q)
         s[kb] = Elt<T>::mma(TL::row(lds, here.row, 32 * kb, q), qf[q], s[kb]);
@@ -223,7 +220,7 @@ __device__ __forceinline__ void fwd_tile(const Args& a, const RowItem& it, int k
   const float lse = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
   if (!row.live) return;
   if (it.part >= 0) {
-    const int64_t slot = ((int64_t)it.part * a.kv_heads + kvh) * kRows + (row.r - it.r0);
+    const int64_t slot = part_row(it.part, a.kv_heads, kvh, row.r - it.r0);
     if (h == 0) a.part_lse[slot] = lse;
 #pragma unroll
     for (int db = 0; db < DB; ++db)
@@ -269,7 +266,7 @@ __global__ __launch_bounds__(256) void join_kernel(Args a, const JoinItem* items
   const int G = a.G, D = a.D, r = it.r0 + i;
   if (r >= it.q_len * G) return;
   const int t = r / G, head = kvh * G + r - t * G;
-  const int64_t slot0 = ((int64_t)it.part * a.kv_heads + kvh) * kRows + i, step = (int64_t)a.kv_heads * kRows;
+  const int64_t slot0 = part_row(it.part, a.kv_heads, kvh, i), step = (int64_t)it.step * a.kv_heads * kPartRows;
   float m = -INFINITY;
   for (int p = lane; p < it.n; p += 64) m = fmaxf(m, a.part_lse[slot0 + p * step]);
 #pragma unroll
@@ -308,8 +305,8 @@ hipError_t launch_forward(const Args& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-hipError_t launch_join(const Args& a, const void* items, int n, hipStream_t st) {
-  const dim3 grid((unsigned)n, (unsigned)a.kv_heads, kRows / 4);
+hipError_t launch_join(const Args& a, const void* items, int n, int rows, hipStream_t st) {
+  const dim3 grid((unsigned)n, (unsigned)a.kv_heads, (unsigned)(rows + 3) / 4);
   note_launch("attn_join", st);
   if (a.dtype == 1) join_kernel<bf16><<<grid, 256, 0, st>>>(a, static_cast<const JoinItem*>(items));
   else join_kernel<float><<<grid, 256, 0, st>>>(a, static_cast<const JoinItem*>(items));
