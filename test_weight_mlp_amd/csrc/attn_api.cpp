@@ -102,12 +102,18 @@ constexpr int64_t kGroups = 512;
 
 // How far the tiles are cut into parts.
 struct Cut {
+  bool rows;      // whether there are tiles of many rows
   int64_t keys;   // most keys of a forward part
   int64_t few;    // most keys of a part of few rows
   int64_t steps;  // most steps of a dK, dV part
 };
 
-bool few_rows(const ipttt_attn_problem* p, int64_t i) { return p->q_len[i] * (p->heads / p->kv_heads) <= kFewRows; }
+// A sequence of few rows: the kernel for them reads the keys with every wave.
+// Over few keys it is worth no launch of its own beside the tiles of many rows.
+bool fits_few(const ipttt_attn_problem* p, int64_t i) { return p->q_len[i] * (p->heads / p->kv_heads) <= kFewRows; }
+bool few_rows(const ipttt_attn_problem* p, const Cut& cut, int64_t i) {
+  return fits_few(p, i) && !(cut.rows && p->k_len[i] <= 4 * kKeys);
+}
 
 // Forward: where there are fewer tiles than workgroups that run at once, they
 // share the keys of all tiles evenly; a part is at least four steps long, so that
@@ -121,9 +127,11 @@ bool few_rows(const ipttt_attn_problem* p, int64_t i) { return p->q_len[i] * (p-
 Cut cut_of(const ipttt_attn_problem* p) {
   constexpr int64_t kLeastKeys = 4 * kKeys, kLeastFew = 128, kLeastSteps = 16;
   const int64_t G = p->heads / p->kv_heads;
+  Cut c = {};
+  for (int64_t i = 0; i < p->n_seqs; ++i) c.rows = c.rows || !fits_few(p, i);
   int64_t tiles = 0, keys = 0, few = 0, steps = 0;
   for (int64_t i = 0; i < p->n_seqs; ++i) {
-    if (few_rows(p, i)) {
+    if (few_rows(p, c, i)) {
       few += p->k_len[i];
     } else {
       for (int64_t r0 = 0; r0 < p->q_len[i] * G; r0 += kRows) {
@@ -133,7 +141,6 @@ Cut cut_of(const ipttt_attn_problem* p) {
     }
     for (int64_t k0 = 0; k0 < p->k_len[i]; k0 += kBwdKeys) steps += key_steps(p, i, k0);
   }
-  Cut c;
   c.keys = tiles * p->kv_heads >= kGroups
                ? kMaxInt
                : div_up(std::max(kLeastKeys, div_up(keys * p->kv_heads, kGroups)), kKeys) * kKeys;
@@ -163,11 +170,12 @@ void walk(const ipttt_attn_problem* p, const Cut& cut, Rows&& rows, FewRows&& fe
         emit(RowItem{qs, ql, (int32_t)r0, ks, off, (int32_t)(j * most), (int32_t)std::min(n, (j + 1) * most),
                      (int32_t)slots});
     };
-    if (p->q_len[i] > 0 && few_rows(p, i)) tile(0, tile_keys(p, i, 0, kFewRows), cut.few, 1, few);
+    const bool is_few = few_rows(p, cut, i);
+    if (p->q_len[i] > 0 && is_few) tile(0, tile_keys(p, i, 0, kFewRows), cut.few, 1, few);
     for (int64_t r0 = 0; r0 < p->q_len[i] * G; r0 += kRows) {
       const int64_t n = tile_keys(p, i, r0, kRows);
       dq(RowItem{qs, ql, (int32_t)r0, ks, off, 0, (int32_t)n, -1});
-      if (!few_rows(p, i)) tile(r0, n, cut.keys, kRows / kPartRows, rows);
+      if (!is_few) tile(r0, n, cut.keys, kRows / kPartRows, rows);
     }
     for (int64_t k0 = 0; k0 < p->k_len[i]; k0 += kBwdKeys) {
       const int64_t r0 = key_rows(p, i, k0), end = p->q_len[i] * G;

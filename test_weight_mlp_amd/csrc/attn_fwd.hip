@@ -275,14 +275,25 @@ __global__ __launch_bounds__(256) void join_kernel(Args a, const JoinItem* items
   const bool on = 2 * lane < D;
   const float* x = a.part_o + slot0 * D + (on ? 2 * lane : 0);
   float l = 0.0f, x0 = 0.0f, x1 = 0.0f;
-#pragma unroll 4
-  for (int p = 0; p < it.n; ++p) {
-    const float w = __builtin_amdgcn_exp2f((a.part_lse[slot0 + p * step] - mu) * kLog2e);
-    const float2_t v = *reinterpret_cast<const float2_t*>(x + p * step * D);
+  for (int p0 = 0; p0 < it.n; p0 += 64) {  // lane p holds part p0 + p's weight
+    const int n = min(64, it.n - p0);
+    const float w = lane < n ? __builtin_amdgcn_exp2f((a.part_lse[slot0 + (p0 + lane) * step] - mu) * kLog2e) : 0.0f;
     l += w;
-    x0 = fmaf(w, v[0], x0);
-    x1 = fmaf(w, v[1], x1);
+    for (int p = 0; p < n; p += 8) {  // eight parts' loads in flight
+      float2_t v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = *reinterpret_cast<const float2_t*>(x + (p0 + min(p + i, n - 1)) * step * D);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float wi = __shfl(w, p + i, 64);  // 0 past the last part
+        x0 = fmaf(wi, v[i][0], x0);
+        x1 = fmaf(wi, v[i][1], x1);
+      }
+    }
   }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) l += __shfl_xor(l, o, 64);
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const int64_t row = it.q_start + (int64_t)t;
   if (lane == 0) a.lse[row * a.heads + head] = l == 0.0f ? -INFINITY : mu + __builtin_amdgcn_logf(l) * kLn2;
