@@ -55,7 +55,9 @@ struct PlanHeader {
   int32_t n_key_join, o_key_join, key_parts;
   int32_t n_few, o_few;      // items of the kernel of few rows
   int32_t join_rows;         // most rows of a joined tile
-  int32_t pad[7];
+  int32_t n_tiles, o_tiles;  // tiles of rows, uncut
+  int32_t n_dq_join, o_dq_join, dq_parts;
+  int32_t pad[2];
 };
 static_assert(sizeof(PlanHeader) == 128, "plan header");
 constexpr int32_t kMagic = 0x41545031;
@@ -68,20 +70,21 @@ struct View {             // [rows, heads, D] with element strides
 struct Args {
   int dtype, heads, kv_heads, G, D;
   float scale;
-  const void* items;      // device
-  int n_items;
+  const void *items, *dq_items;  // device
+  int n_items, n_dq;
   View q, k, v, o, dO, dq, dk, dv;
   float *lse;             // [q rows, heads]
   float *nlse, *ndelta;   // same: -lse / scale (-inf on rows that see nothing), -delta
-  float *part_o, *part_lse;
+  float *part_o, *part_lse, *part_dq;
 };
 
 hipError_t launch_forward(const Args& a, hipStream_t st);
 hipError_t launch_few(const Args& a, hipStream_t st);
 hipError_t launch_join(const Args& a, const void* items, int n, int rows, hipStream_t st);
-hipError_t launch_dq(const Args& a, hipStream_t st);
-hipError_t launch_dkv(const Args& a, hipStream_t st);
-hipError_t launch_join_keys(const Args& a, const void* items, int n, hipStream_t st);
+hipError_t launch_delta(const Args& a, hipStream_t st);
+hipError_t launch_backward(const Args& a, hipStream_t st);
+hipError_t launch_join_backward(const Args& a, const void* dq_items, int n_dq, const void* key_items, int n_key,
+                                hipStream_t st);
 
 }  // namespace attn
 

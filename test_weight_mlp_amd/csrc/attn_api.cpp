@@ -105,6 +105,7 @@ struct Cut {
   bool rows;      // whether there are tiles of many rows
   int64_t keys;   // most keys of a forward part
   int64_t few;    // most keys of a part of few rows
+  int64_t dq;     // most keys of a dQ part
   int64_t steps;  // most steps of a dK, dV part
 };
 
@@ -116,66 +117,77 @@ bool few_rows(const ipttt_attn_problem* p, const Cut& cut, int64_t i) {
 }
 
 // Forward: where there are fewer tiles than workgroups that run at once, they
-// share the keys of all tiles evenly; a part is at least four steps long, so that
-// its join costs little beside it.  Few rows: only reading matters, so parts are
-// short enough that four rounds of workgroups even out, but at least two blocks
-// of 32 keys for each of a workgroup's two waves.  dK, dV: the first keys of a
-// causal sequence meet all its rows and the last almost none, so a tile's steps
-// are cut to the average of what a workgroup gets; at least 16, for the same
-// reason as above.  (8k tokens, 32 heads over 8 of width 128: 1.70 ms uncut, 1.19 ms
-// cut and joined.)
+// share the keys of all tiles evenly; a part is at least a few steps long, so that
+// its join costs little beside it (fp32 steps take longer).  Few rows: only
+// reading matters, so parts are short enough that four rounds of workgroups even
+// out, but at least two blocks of 32 keys for each of a workgroup's two waves.
+// Backward: the first keys of a causal sequence meet all its rows and the last
+// almost none, and a call's last workgroup ends it, so no tile of keys is longer
+// than what a workgroup gets on average (8k tokens, 32 heads over 8 of width 128:
+// 1.70 ms uncut, 1.19 ms cut and joined); where workgroups would stay idle, tiles
+// of rows are cut alike.  A step of rows is 128 x 64 x 3 products, one of keys
+// 32 x 128 x 4: three to two.
 Cut cut_of(const ipttt_attn_problem* p) {
-  constexpr int64_t kLeastKeys = 4 * kKeys, kLeastFew = 128, kLeastSteps = 16;
+  const bool f32 = p->dtype == IPTTT_F32;
+  const int64_t least = (f32 ? 2 : 4) * kKeys, least_few = 128, least_steps = f32 ? 4 : 8;
   const int64_t G = p->heads / p->kv_heads;
   Cut c = {};
   for (int64_t i = 0; i < p->n_seqs; ++i) c.rows = c.rows || !fits_few(p, i);
-  int64_t tiles = 0, keys = 0, few = 0, steps = 0;
+  int64_t tiles = 0, keys = 0, few = 0, bwd_tiles = 0, work = 0;
   for (int64_t i = 0; i < p->n_seqs; ++i) {
-    if (few_rows(p, c, i)) {
-      few += p->k_len[i];
-    } else {
-      for (int64_t r0 = 0; r0 < p->q_len[i] * G; r0 += kRows) {
-        ++tiles;
-        keys += tile_keys(p, i, r0, kRows);
-      }
+    if (few_rows(p, c, i)) few += p->k_len[i];
+    for (int64_t r0 = 0; r0 < p->q_len[i] * G; r0 += kRows) {
+      const int64_t n = tile_keys(p, i, r0, kRows);
+      ++bwd_tiles;
+      work += 3 * div_up(n, kKeys);
+      if (few_rows(p, c, i)) continue;
+      ++tiles;
+      keys += n;
     }
-    for (int64_t k0 = 0; k0 < p->k_len[i]; k0 += kBwdKeys) steps += key_steps(p, i, k0);
+    for (int64_t k0 = 0; k0 < p->k_len[i]; k0 += kBwdKeys) {
+      ++bwd_tiles;
+      work += 2 * key_steps(p, i, k0);
+    }
   }
   c.keys = tiles * p->kv_heads >= kGroups
                ? kMaxInt
-               : div_up(std::max(kLeastKeys, div_up(keys * p->kv_heads, kGroups)), kKeys) * kKeys;
-  c.few = div_up(std::max(kLeastFew, div_up(few * p->kv_heads, 4 * kGroups)), 64) * 64;
-  c.steps = std::max(kLeastSteps, div_up(steps * p->kv_heads, kGroups));
+               : div_up(std::max(least, div_up(keys * p->kv_heads, kGroups)), kKeys) * kKeys;
+  c.few = div_up(std::max(least_few, div_up(few * p->kv_heads, 4 * kGroups)), 64) * 64;
+  const int64_t each = div_up(work * p->kv_heads, kGroups);
+  c.steps = std::max(least_steps, div_up(each, 2));
+  c.dq = bwd_tiles * p->kv_heads >= kGroups ? kMaxInt : std::max(least, div_up(each, 3) * kKeys);
   return c;
 }
 
 // Walks every item of the plan in sequence order.
-template <class Rows, class FewRows, class Join, class Dq, class Key, class KJoin>
-void walk(const ipttt_attn_problem* p, const Cut& cut, Rows&& rows, FewRows&& few, Join&& join, Dq&& dq, Key&& key,
-          KJoin&& kjoin) {
+template <class Rows, class FewRows, class Join, class Tiles, class Dq, class DqJoin, class Key, class KJoin>
+void walk(const ipttt_attn_problem* p, const Cut& cut, Rows&& rows, FewRows&& few, Join&& join, Tiles&& tiles, Dq&& dq,
+          DqJoin&& dq_join, Key&& key, KJoin&& kjoin) {
   const int64_t G = p->heads / p->kv_heads;
-  int64_t slots = 0, key_slots = 0;
+  int64_t slots = 0, dq_slots = 0, key_slots = 0;
   for (int64_t i = 0; i < p->n_seqs; ++i) {
     const int32_t off = (int32_t)(p->k_len[i] - p->q_len[i]);
     const int32_t qs = (int32_t)p->q_start[i], ql = (int32_t)p->q_len[i], ks = (int32_t)p->k_start[i];
-    // one tile over its keys, in parts of at most `most`, each of `step` slots
-    const auto tile = [&](int64_t r0, int64_t n, int64_t most, int64_t step, auto& emit) {
+    // one tile over its keys, in parts of `most` (the last may be shorter), each
+    // of `step` slots
+    const auto tile = [&](int64_t r0, int64_t n, int64_t most, int64_t step, int64_t& slot, auto& emit, auto& joined) {
       const int64_t parts = std::max<int64_t>(1, div_up(n, most));
       if (parts == 1) {
         emit(RowItem{qs, ql, (int32_t)r0, ks, off, 0, (int32_t)n, -1});
         return;
       }
-      join(JoinItem{qs, ql, (int32_t)r0, (int32_t)slots, (int32_t)parts, (int32_t)step});
-      for (int64_t j = 0; j < parts; ++j, slots += step)
+      joined(JoinItem{qs, ql, (int32_t)r0, (int32_t)slot, (int32_t)parts, (int32_t)step});
+      for (int64_t j = 0; j < parts; ++j, slot += step)
         emit(RowItem{qs, ql, (int32_t)r0, ks, off, (int32_t)(j * most), (int32_t)std::min(n, (j + 1) * most),
-                     (int32_t)slots});
+                     (int32_t)slot});
     };
     const bool is_few = few_rows(p, cut, i);
-    if (p->q_len[i] > 0 && is_few) tile(0, tile_keys(p, i, 0, kFewRows), cut.few, 1, few);
+    if (p->q_len[i] > 0 && is_few) tile(0, tile_keys(p, i, 0, kFewRows), cut.few, 1, slots, few, join);
     for (int64_t r0 = 0; r0 < p->q_len[i] * G; r0 += kRows) {
       const int64_t n = tile_keys(p, i, r0, kRows);
-      dq(RowItem{qs, ql, (int32_t)r0, ks, off, 0, (int32_t)n, -1});
-      if (!is_few) tile(r0, n, cut.keys, kRows / kPartRows, rows);
+      tiles(RowItem{qs, ql, (int32_t)r0, ks, off, 0, (int32_t)n, -1});
+      tile(r0, n, cut.dq, kRows / kPartRows, dq_slots, dq, dq_join);
+      if (!is_few) tile(r0, n, cut.keys, kRows / kPartRows, slots, rows, join);
     }
     for (int64_t k0 = 0; k0 < p->k_len[i]; k0 += kBwdKeys) {
       const int64_t r0 = key_rows(p, i, k0), end = p->q_len[i] * G;
@@ -201,8 +213,9 @@ struct Range {
 };
 
 struct Sizes {
-  int64_t rows = 0, few = 0, join = 0, dq = 0, key = 0, kjoin = 0, parts = 0, key_parts = 0, join_rows = 0;
-  int64_t o_rows, o_few, o_join, o_dq, o_key, o_kjoin, o_ranges, bytes;
+  int64_t rows = 0, few = 0, join = 0, tiles = 0, dq = 0, dq_join = 0, key = 0, kjoin = 0;
+  int64_t parts = 0, dq_parts = 0, key_parts = 0, join_rows = 0;
+  int64_t o_rows, o_few, o_join, o_tiles, o_dq_join, o_dq, o_key, o_kjoin, o_ranges, bytes;
 };
 
 // Counts and offsets; false if the plan would not fit its own 31-bit fields.
@@ -216,7 +229,11 @@ bool sizes_of(const ipttt_attn_problem* p, const Cut& cut, Sizes* s) {
         s->parts += (int64_t)x.n * x.step;
         s->join_rows = std::max(s->join_rows, std::min<int64_t>(x.step * kPartRows, x.q_len * G - x.r0));
       },
-      [&](const RowItem&) { ++s->dq; },
+      [&](const RowItem&) { ++s->tiles; }, [&](const RowItem&) { ++s->dq; },
+      [&](const JoinItem& x) {
+        ++s->dq_join;
+        s->dq_parts += (int64_t)x.n * x.step;
+      },
       [&](const KeyItem& x) {
         ++s->key;
         s->key_parts += x.part >= 0;
@@ -224,13 +241,15 @@ bool sizes_of(const ipttt_attn_problem* p, const Cut& cut, Sizes* s) {
       [&](const KeyJoin&) { ++s->kjoin; });
   s->o_rows = sizeof(PlanHeader);
   s->o_few = s->o_rows + s->rows * (int64_t)sizeof(RowItem);
-  s->o_dq = s->o_few + s->few * (int64_t)sizeof(RowItem);
+  s->o_tiles = s->o_few + s->few * (int64_t)sizeof(RowItem);
+  s->o_dq = s->o_tiles + s->tiles * (int64_t)sizeof(RowItem);
   s->o_key = s->o_dq + s->dq * (int64_t)sizeof(RowItem);
   s->o_join = s->o_key + s->key * (int64_t)sizeof(KeyItem);
-  s->o_kjoin = (s->o_join + s->join * (int64_t)sizeof(JoinItem) + 15) / 16 * 16;
+  s->o_dq_join = s->o_join + s->join * (int64_t)sizeof(JoinItem);
+  s->o_kjoin = (s->o_dq_join + s->dq_join * (int64_t)sizeof(JoinItem) + 15) / 16 * 16;
   s->o_ranges = s->o_kjoin + s->kjoin * (int64_t)sizeof(KeyJoin);
   s->bytes = s->o_ranges + p->n_seqs * (int64_t)sizeof(Range);
-  const int64_t most = std::max(std::max(s->rows, s->few), std::max(s->dq, s->key));
+  const int64_t most = std::max(std::max(s->rows, s->few), std::max(s->tiles, s->dq + s->key));
   return s->bytes <= kMaxInt && most <= kMaxGroups / p->kv_heads;
 }
 
@@ -252,11 +271,20 @@ FwdLayout fwd_layout(const PlanHeader* h) {
   return l;
 }
 
-// -lse / scale of every row, -delta of every row, then the partial dK and dV.
-size_t row_stat_bytes(const PlanHeader* h) { return align256((size_t)h->q_rows * h->heads * sizeof(float)); }
-size_t bwd_bytes(const PlanHeader* h) {
-  return 2 * row_stat_bytes(h) +
-         align256((size_t)h->key_parts * h->kv_heads * 2 * kBwdKeys * h->head_dim * sizeof(float));
+// -lse / scale of every row | -delta of every row | partial dK, dV | partial dQ
+struct BwdLayout {
+  size_t nlse, ndelta, keys, dq, total;
+};
+BwdLayout bwd_layout(const PlanHeader* h) {
+  BwdLayout l;
+  const size_t stat = align256((size_t)h->q_rows * h->heads * sizeof(float));
+  const size_t row = (size_t)h->kv_heads * h->head_dim * sizeof(float);
+  l.nlse = 0;
+  l.ndelta = stat;
+  l.keys = 2 * stat;
+  l.dq = l.keys + align256((size_t)h->key_parts * 2 * kBwdKeys * row);
+  l.total = l.dq + align256((size_t)h->dq_parts * kPartRows * row);
+  return l;
 }
 
 ipttt_status check_call(const void* plan, const void* plan_dev, float scale, void* ws, size_t ws_bytes, size_t need) {
@@ -426,11 +454,14 @@ ipttt_status ipttt_attn_plan(const ipttt_attn_problem* p, void* plan, size_t pla
   RowItem* dq = reinterpret_cast<RowItem*>(base + s.o_dq);
   KeyItem* key = reinterpret_cast<KeyItem*>(base + s.o_key);
   JoinItem* join = reinterpret_cast<JoinItem*>(base + s.o_join);
+  RowItem* tiles = reinterpret_cast<RowItem*>(base + s.o_tiles);
+  JoinItem* dq_join = reinterpret_cast<JoinItem*>(base + s.o_dq_join);
   KeyJoin* kjoin = reinterpret_cast<KeyJoin*>(base + s.o_kjoin);
   RowItem* few = reinterpret_cast<RowItem*>(base + s.o_few);
   walk(p, cut, [&](const RowItem& x) { *rows++ = x; }, [&](const RowItem& x) { *few++ = x; },
-       [&](const JoinItem& x) { *join++ = x; },
-       [&](const RowItem& x) { *dq++ = x; }, [&](const KeyItem& x) { *key++ = x; },
+       [&](const JoinItem& x) { *join++ = x; }, [&](const RowItem& x) { *tiles++ = x; },
+       [&](const RowItem& x) { *dq++ = x; }, [&](const JoinItem& x) { *dq_join++ = x; },
+       [&](const KeyItem& x) { *key++ = x; },
        [&](const KeyJoin& x) { *kjoin++ = x; });
   // the longest first, so that the last workgroups to start are short ones
   const auto longer = [](const RowItem& x, const RowItem& y) {
@@ -465,6 +496,11 @@ ipttt_status ipttt_attn_plan(const ipttt_attn_problem* p, void* plan, size_t pla
   h->q_rows = (int32_t)p->q_rows;
   h->k_rows = (int32_t)p->k_rows;
   h->n_rows = (int32_t)s.rows;
+  h->n_tiles = (int32_t)s.tiles;
+  h->o_tiles = (int32_t)s.o_tiles;
+  h->n_dq_join = (int32_t)s.dq_join;
+  h->o_dq_join = (int32_t)s.o_dq_join;
+  h->dq_parts = (int32_t)s.dq_parts;
   h->n_few = (int32_t)s.few;
   h->o_few = (int32_t)s.o_few;
   h->join_rows = (int32_t)s.join_rows;
@@ -491,7 +527,7 @@ size_t ipttt_attn_workspace_bytes(const void* plan) {
 
 size_t ipttt_attn_backward_workspace_bytes(const void* plan) {
   const PlanHeader* h = header(plan);
-  return h == nullptr ? 0 : bwd_bytes(h);
+  return h == nullptr ? 0 : bwd_layout(h).total;
 }
 
 ipttt_status ipttt_attention(const void* plan, const void* plan_dev, float scale, const ipttt_heads* q,
@@ -546,24 +582,29 @@ ipttt_status ipttt_attention_backward(const void* plan, const void* plan_dev, fl
   if (lse == nullptr && h->q_rows > 0) return IPTTT_ERR_NULL;
   if (!aligned(lse, 16)) return IPTTT_ERR_ALIGN;
   a.lse = const_cast<float*>(lse);
-  a.nlse = static_cast<float*>(ws);
-  a.ndelta = reinterpret_cast<float*>(static_cast<char*>(ws) + row_stat_bytes(h));
-  a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * row_stat_bytes(h));
+  const BwdLayout l = bwd_layout(h);
+  const auto region = [ws](size_t at) { return reinterpret_cast<float*>(static_cast<char*>(ws) + at); };
+  a.nlse = region(l.nlse);
+  a.ndelta = region(l.ndelta);
+  a.part_o = region(l.keys);
+  a.part_dq = region(l.dq);
   const char* dev = static_cast<const char*>(plan_dev);
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  if (h->n_dq > 0) {
-    a.items = dev + h->o_dq;
-    a.n_items = h->n_dq;
-    IPTTT_TRY(hip_status(ipttt::attn::launch_dq(a, st)));
+  if (h->n_tiles > 0) {
+    a.items = dev + h->o_tiles;
+    a.n_items = h->n_tiles;
+    IPTTT_TRY(hip_status(ipttt::attn::launch_delta(a, st)));
   }
-  if (h->n_key > 0) {
+  if (h->n_key + h->n_dq > 0) {
     a.items = dev + h->o_key;
     a.n_items = h->n_key;
-    IPTTT_TRY(hip_status(ipttt::attn::launch_dkv(a, st)));
+    a.dq_items = dev + h->o_dq;
+    a.n_dq = h->n_dq;
+    IPTTT_TRY(hip_status(ipttt::attn::launch_backward(a, st)));
   }
-  if (h->n_key_join > 0)
-    IPTTT_TRY(hip_status(ipttt::attn::launch_join_keys(a, dev + h->o_key_join, h->n_key_join, st)));
-  return IPTTT_OK;
+  if (h->n_dq_join + h->n_key_join == 0) return IPTTT_OK;
+  return hip_status(ipttt::attn::launch_join_backward(a, dev + h->o_dq_join, h->n_dq_join, dev + h->o_key_join,
+                                                      h->n_key_join, st));
 }
 
 }  // extern "C"

@@ -1,11 +1,12 @@
 // Causal attention backward over packed sequences with grouped heads.  With
 // P = e^(scale q.k - lse), dP = dO V^T and delta = sum_d dO O:
 //   dS = P (dP - delta),  dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO.
-// Two kernels, each recomputing P from lse: one per tile of rows (dQ, and delta
-// on the way), one per tile of keys (dK, dV, summed over the rows of every head
-// of the group).  Seven products instead of the five that one kernel with atomic
-// adds to dQ would do, but every sum runs in a fixed order: the gradients are
-// the same bits in every run.
+// Every tile recomputes P from lse: tiles of rows form dQ, tiles of keys dK and
+// dV (summed over the rows of every head of the group), all in one launch, so
+// that the ends of the one kind are filled by the other.  Seven products instead
+// of the five that tiles of keys with atomic adds to dQ would do, but every sum
+// runs in a fixed order: the gradients are the same bits in every run.  A small
+// launch before it forms delta.
 #include "attn_core.h"
 #include "attn.h"
 #include "launch.h"
@@ -23,9 +24,82 @@ namespace {
 // 256 keys, is 0.0049, 0.0027, 0.0025 with O and 0.0024, 0.0024, 0.0023 without.
 constexpr int kExactDelta = 256;
 
+// -lse / scale and -delta of one tile of 128 flat rows, 32 a wave.
+template <typename T, int DP>
+__device__ __forceinline__ void delta_tile(const Args& a, const RowItem& it, int kvh, const char* __restrict__ K,
+                                           const char* __restrict__ V, char* lds) {
+  typedef Tile<T, DP> TL;
+  typedef typename Elt<T>::frag frag;
+  constexpr int NW = 4, TB = TL::bytes(kKeys), EPL = Elt<T>::EPL;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
+  const int D = a.D;
+  const Row row(it, a.G, wave, lane);
+  const int64_t at = (it.q_start + (int64_t)row.t) * a.heads + kvh * a.G + row.g;
+  float nlse = -INFINITY;
+  if (row.live) {
+    const float x = a.lse[at];
+    if (x != -INFINITY) nlse = -x / a.scale;
+  }
+  frag df[TL::STEPS];
+  row_frags<T, DP>(a.dO, it, row, kvh, a.G, D, h, df);
+  float delta = 0.0f;
+  if (sizeof(T) == 2 && it.k_end <= kExactDelta) {
+    frag qf[TL::STEPS];
+    row_frags<T, DP>(a.q, it, row, kvh, a.G, D, h, qf);
+    const float sl2 = a.scale * kLog2e;
+    const At<T, DP> here(lane);
+    const RowStream<T, DP, NW, kKeys> ks(a.k.row, D, wave, lane), vs(a.v.row, D, wave, lane);
+    for (int key0 = 0; key0 < it.k_end; key0 += kKeys) {
+      const int left = it.off + it.q_len - key0;
+      ks.issue(K, (int64_t)it.k_start + key0, left, lds, wave);
+      vs.issue(V, (int64_t)it.k_start + key0, left, lds + TB, wave);
+      tiles_landed();
+#pragma unroll 1
+      for (int kb = 0; kb < kKeys / 32; ++kb) {
+        floatx16 x, dp;
+        fill16(x, nlse);
+        fill16(dp, 0.0f);
+#pragma unroll
+        for (int q = 0; q < TL::STEPS; ++q) {
+          x = Elt<T>::mma(TL::row(lds + kb * TL::bytes(32), here.row, 0, q), qf[q], x);
+          dp = Elt<T>::mma(TL::row(lds + TB + kb * TL::bytes(32), here.row, 0, q), df[q], dp);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float p = __builtin_amdgcn_exp2f(x[i] * sl2);
+          if (key0 + 32 * kb + 8 * (i >> 2) + 4 * h + (i & 3) < row.lim) delta = fmaf(p, dp[i], delta);
+        }
+      }
+      tiles_landed();  // every wave is done with the tile
+    }
+  } else {
+    frag of[TL::STEPS];
+    row_frags<T, DP>(a.o, it, row, kvh, a.G, D, h, of);
+#pragma unroll
+    for (int s = 0; s < TL::STEPS; ++s)
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) delta = fmaf((float)of[s][e], (float)df[s][e], delta);
+  }
+  delta = half_sum(delta);
+  if (row.live && h == 0) {
+    a.nlse[at] = nlse;
+    a.ndelta[at] = -delta;
+  }
+}
+
+template <typename T, int DP>
+__global__ __launch_bounds__(256) void delta_kernel(Args a) {
+  __shared__ __attribute__((aligned(16))) char lds[sizeof(T) == 2 ? 2 * Tile<T, DP>::bytes(kKeys) : 16];
+  const int kvh = blockIdx.x % a.kv_heads;
+  const RowItem it = static_cast<const RowItem*>(a.items)[blockIdx.x / a.kv_heads];
+  delta_tile<T, DP>(a, it, kvh, static_cast<const char*>(a.k.p) + (int64_t)kvh * a.k.head * (int)sizeof(T),
+                    static_cast<const char*>(a.v.p) + (int64_t)kvh * a.v.head * (int)sizeof(T), lds);
+}
+
 // dQ of one tile of 128 flat rows, 32 a wave: over the keys the rows see,
 // S^T = K Q^T and dP^T = V dO^T, then dQ^T += K^T dS^T with K read transposed.
-// Leaves -lse / scale and -delta of its rows for the dK, dV kernel.
+// The scores' accumulators start at -lse / scale, dP's at -delta: what comes out
+// of the products is ready for the exponential and for dS = P (dP - delta).
 template <typename T, int DP>
 __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kvh, const char* __restrict__ K,
                                         const char* __restrict__ V, char* lds) {
@@ -43,59 +117,20 @@ __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kv
 
   const At<T, DP> here(lane);
   const RowStream<T, DP, NW, KT> ks(a.k.row, D, wave, lane), vs(a.v.row, D, wave, lane);
-  const int k_len = it.off + it.q_len, steps = (it.k_end + KT - 1) / KT;
+  const int k_len = it.off + it.q_len, steps = (it.k_end - it.k_begin + KT - 1) / KT;
   auto load = [&](int s, int buf) {
-    ks.issue(K, (int64_t)it.k_start + s * KT, k_len - s * KT, lds + 2 * buf * TB, wave);
-    vs.issue(V, (int64_t)it.k_start + s * KT, k_len - s * KT, lds + (2 * buf + 1) * TB, wave);
+    const int key = it.k_begin + s * KT;
+    ks.issue(K, (int64_t)it.k_start + key, k_len - key, lds + 2 * buf * TB, wave);
+    vs.issue(V, (int64_t)it.k_start + key, k_len - key, lds + (2 * buf + 1) * TB, wave);
   };
   if (steps > 0) load(0, 0);
 
   frag qf[TL::STEPS], df[TL::STEPS];
   row_frags<T, DP>(a.q, it, row, kvh, a.G, D, h, qf);
   row_frags<T, DP>(a.dO, it, row, kvh, a.G, D, h, df);
-  // the scores' accumulators start at -lse / scale, dP's at -delta: what comes
-  // out of the products is ready for the exponential and for dS = P (dP - delta).
   // -inf (P = 0) on rows that see nothing, and past the sequence
-  float nlse = -INFINITY;
-  if (row.live) {
-    const float x = a.lse[at * a.heads + head];
-    if (x != -INFINITY) nlse = -x / a.scale;
-  }
-  float delta = 0.0f;
-  if (ES == 2 && it.k_end <= kExactDelta) {
-    for (int s = 0; s < steps; ++s) {
-      tiles_landed();
-      for (int kb = 0; kb < KT / 32; ++kb) {
-        floatx16 x, dp;
-        fill16(x, nlse);
-        fill16(dp, 0.0f);
-#pragma unroll
-        for (int q = 0; q < TL::STEPS; ++q) {
-          x = Elt<T>::mma(TL::row(lds, here.row, 32 * kb, q), qf[q], x);
-          dp = Elt<T>::mma(TL::row(lds + TB, here.row, 32 * kb, q), df[q], dp);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float p = __builtin_amdgcn_exp2f(x[i] * sl2);
-          if (s * KT + 32 * kb + 8 * (i >> 2) + 4 * h + (i & 3) < row.lim) delta = fmaf(p, dp[i], delta);
-        }
-      }
-      tiles_landed();  // every wave is done with the tile
-      load(s + 1 < steps ? s + 1 : 0, 0);
-    }
-  } else {
-    frag of[TL::STEPS];
-    row_frags<T, DP>(a.o, it, row, kvh, a.G, D, h, of);
-#pragma unroll
-    for (int s = 0; s < TL::STEPS; ++s)
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) delta = fmaf((float)of[s][e], (float)df[s][e], delta);
-  }
-  delta = half_sum(delta);
-  if (row.live && h == 0) {
-    a.nlse[at * a.heads + head] = nlse;
-    a.ndelta[at * a.heads + head] = -delta;
-  }
+  const float nlse = row.live ? a.nlse[at * a.heads + head] : -INFINITY;
+  const float ndelta = row.live ? a.ndelta[at * a.heads + head] : 0.0f;
 
   floatx16 acc[DB];
 #pragma unroll
@@ -118,14 +153,14 @@ __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kv
       for (int i = 0; i < 16; ++i) s[b][i] *= dp[b][i];
       // a softmax over one key has no gradient: exactly 0, whatever rounding
       // put between dP and delta
-      if (b == 0 && st == 0 && row.all <= 1 && row.lim == 1) fill16(s[b], 0.0f);
+      if (b == 0 && st == 0 && it.k_begin == 0 && row.all <= 1 && row.lim == 1) fill16(s[b], 0.0f);
 #pragma unroll
       for (int j = 0; j < GR::NP; ++j) p[b][j] = pack<T>(s[b], j * EPL);
     };
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       start16(s[b], nlse);
-      start16(dp[b], -delta);
+      start16(dp[b], ndelta);
 #pragma unroll
       for (int g = 0; g < H; ++g) {
         if (g + 1 < H) GR::rows(kt, here, 32 * b, g + 1, f[cur ^ 1]);
@@ -137,7 +172,7 @@ __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kv
         __builtin_amdgcn_sched_barrier(0);
         if (b == 0 && g == 0 && st + 1 < steps) load(st + 1, B ^ 1);
       }
-      const int key0 = st * KT + 32 * b;
+      const int key0 = it.k_begin + st * KT + 32 * b;
       if (key0 + 32 > row.all) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -181,6 +216,17 @@ __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kv
     step(st++, std::integral_constant<int, 1>());
   }
   if (!row.live) return;
+  if (it.part >= 0) {
+    float* x = a.part_dq + part_row(it.part, a.kv_heads, kvh, row.r - it.r0) * D;
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int d = 32 * db + 8 * j + 4 * h;
+        if (d < D) store4<float>(x + d, acc[db][4 * j], acc[db][4 * j + 1], acc[db][4 * j + 2], acc[db][4 * j + 3]);
+      }
+    return;
+  }
   T* out = static_cast<T*>(a.dq.p) + at * a.dq.row + head * a.dq.head;
 #pragma unroll
   for (int db = 0; db < DB; ++db)
@@ -191,15 +237,6 @@ __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kv
         store4<T>(out + d, acc[db][4 * j] * a.scale, acc[db][4 * j + 1] * a.scale, acc[db][4 * j + 2] * a.scale,
                   acc[db][4 * j + 3] * a.scale);
     }
-}
-
-template <typename T, int DP>
-__global__ __launch_bounds__(256, sizeof(T) * DP > 256 ? 1 : 2) void dq_kernel(Args a) {
-  __shared__ __attribute__((aligned(16))) char lds[4 * Tile<T, DP>::bytes(sizeof(T) == 2 ? kKeys : kKeys / 2)];
-  const int kvh = blockIdx.x % a.kv_heads;
-  const RowItem it = static_cast<const RowItem*>(a.items)[blockIdx.x / a.kv_heads];
-  dq_tile<T, DP>(a, it, kvh, static_cast<const char*>(a.k.p) + (int64_t)kvh * a.k.head * (int)sizeof(T),
-                 static_cast<const char*>(a.v.p) + (int64_t)kvh * a.v.head * (int)sizeof(T), lds);
 }
 
 // dK and dV of one tile of 128 keys, 32 a wave: over the flat rows that see any
@@ -435,31 +472,55 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
     }
 }
 
+// The tiles of keys (longest first), then those of rows.  bf16: two waves a SIMD.
 template <typename T, int DP>
-__global__ __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2) void dkv_kernel(Args a) {
-  __shared__ __attribute__((aligned(16))) char lds[KeyTile<T, DP>::LDS];
-  constexpr int ES = sizeof(T);
-  const int kvh = blockIdx.x % a.kv_heads;
-  const KeyItem it = static_cast<const KeyItem*>(a.items)[blockIdx.x / a.kv_heads];
-  const int64_t q = (int64_t)kvh * a.G;
-  dkv_tile<T, DP>(a, it, kvh, static_cast<const char*>(a.q.p) + q * a.q.head * ES,
-                  static_cast<const char*>(a.dO.p) + q * a.dO.head * ES, a.nlse + q, a.ndelta + q,
-                  static_cast<const char*>(a.k.p) + (int64_t)kvh * a.k.head * ES,
-                  static_cast<const char*>(a.v.p) + (int64_t)kvh * a.v.head * ES, lds);
+__global__ __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2) void bwd_kernel(Args a) {
+  constexpr int ES = sizeof(T), DQ = 4 * Tile<T, DP>::bytes(ES == 2 ? kKeys : kKeys / 2);
+  __shared__ __attribute__((aligned(16))) char lds[KeyTile<T, DP>::LDS > DQ ? KeyTile<T, DP>::LDS : DQ];
+  const int kvh = blockIdx.x % a.kv_heads, i = blockIdx.x / a.kv_heads;
+  const char* K = static_cast<const char*>(a.k.p) + (int64_t)kvh * a.k.head * ES;
+  const char* V = static_cast<const char*>(a.v.p) + (int64_t)kvh * a.v.head * ES;
+  if (i < a.n_items) {
+    const int64_t q = (int64_t)kvh * a.G;
+    dkv_tile<T, DP>(a, static_cast<const KeyItem*>(a.items)[i], kvh, static_cast<const char*>(a.q.p) + q * a.q.head * ES,
+                    static_cast<const char*>(a.dO.p) + q * a.dO.head * ES, a.nlse + q, a.ndelta + q, K, V, lds);
+  } else {
+    dq_tile<T, DP>(a, static_cast<const RowItem*>(a.dq_items)[i - a.n_items], kvh, K, V, lds);
+  }
 }
 
-// Sums the partial dK and dV of one tile in slot order: a block the keys from
-// 16 blockIdx.z on, a thread four columns of one key at a time.
+// Sums the partial gradients of one tile in slot order, a block 16 rows or keys
+// of it, a thread four columns of one at a time: dQ of the first n_dq items, dK
+// and dV of the others.
 template <typename T>
-__global__ __launch_bounds__(256) void join_keys_kernel(Args a, const KeyJoin* items) {
-  const KeyJoin it = items[blockIdx.x];
-  const int kvh = blockIdx.y, D = a.D, quads = D / 4;
+__global__ __launch_bounds__(256) void join_bwd_kernel(Args a, const JoinItem* dq_items, int n_dq,
+                                                       const KeyJoin* key_items) {
+  const int kvh = blockIdx.y, D = a.D, quads = D / 4, G = a.G, i0 = 16 * blockIdx.z;
+  if ((int)blockIdx.x < n_dq) {
+    const JoinItem it = dq_items[blockIdx.x];
+    const int64_t step = (int64_t)it.step * a.kv_heads * kPartRows * D;
+    const int rows = min(16, min(kRows, it.q_len * G - it.r0) - i0);
+    for (int e = threadIdx.x; e < rows * quads; e += 256) {
+      const int i = i0 + e / quads, d = e % quads * 4;
+      const float* p = a.part_dq + part_row(it.part, a.kv_heads, kvh, i) * D + d;
+      float4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+      for (int j = 0; j < it.n; ++j) x += *reinterpret_cast<const float4_t*>(p + j * step);
+      x *= a.scale;
+      const int r = it.r0 + i, t = r / G, head = kvh * G + r - t * G;
+      store4<T>(static_cast<T*>(a.dq.p) + (it.q_start + (int64_t)t) * a.dq.row + head * a.dq.head + d, x[0], x[1],
+                x[2], x[3]);
+    }
+    return;
+  }
+  const KeyJoin it = key_items[blockIdx.x - n_dq];
   const int64_t step = (int64_t)a.kv_heads * 2 * kBwdKeys * D;
-  const int keys = min(16, it.n_keys - 16 * (int)blockIdx.z);
+  const int keys = min(16, it.n_keys - i0);
   for (int e = threadIdx.x; e < keys * quads; e += 256) {
-    const int i = 16 * blockIdx.z + e / quads, d = e % quads * 4;
+    const int i = i0 + e / quads, d = e % quads * 4;
     const float* p = a.part_o + (((int64_t)it.part * a.kv_heads + kvh) * 2 * kBwdKeys + i) * D + d;
     float4_t k = {0.0f, 0.0f, 0.0f, 0.0f}, v = k;
+#pragma unroll 4
     for (int j = 0; j < it.n; ++j) {
       k += *reinterpret_cast<const float4_t*>(p + j * step);
       v += *reinterpret_cast<const float4_t*>(p + j * step + (int64_t)kBwdKeys * D);
@@ -473,31 +534,35 @@ __global__ __launch_bounds__(256) void join_keys_kernel(Args a, const KeyJoin* i
 
 }  // namespace
 
-hipError_t launch_join_keys(const Args& a, const void* items, int n, hipStream_t st) {
-  const dim3 grid((unsigned)n, (unsigned)a.kv_heads, kBwdKeys / 16);
-  note_launch("attn_join_keys", st);
-  if (a.dtype == 1) join_keys_kernel<bf16><<<grid, 256, 0, st>>>(a, static_cast<const KeyJoin*>(items));
-  else join_keys_kernel<float><<<grid, 256, 0, st>>>(a, static_cast<const KeyJoin*>(items));
+hipError_t launch_delta(const Args& a, hipStream_t st) {
+  const dim3 grid((unsigned)(a.n_items * a.kv_heads));
+  note_launch("attn_delta", st);
+  if (a.dtype == 1 && a.D <= 64) delta_kernel<bf16, 64><<<grid, 256, 0, st>>>(a);
+  else if (a.dtype == 1) delta_kernel<bf16, 128><<<grid, 256, 0, st>>>(a);
+  else if (a.D <= 64) delta_kernel<float, 64><<<grid, 256, 0, st>>>(a);
+  else delta_kernel<float, 128><<<grid, 256, 0, st>>>(a);
   return hipGetLastError();
 }
 
-hipError_t launch_dq(const Args& a, hipStream_t st) {
-  const dim3 grid((unsigned)(a.n_items * a.kv_heads));
-  note_launch("attn_dq", st);
-  if (a.dtype == 1 && a.D <= 64) dq_kernel<bf16, 64><<<grid, 256, 0, st>>>(a);
-  else if (a.dtype == 1) dq_kernel<bf16, 128><<<grid, 256, 0, st>>>(a);
-  else if (a.D <= 64) dq_kernel<float, 64><<<grid, 256, 0, st>>>(a);
-  else dq_kernel<float, 128><<<grid, 256, 0, st>>>(a);
+hipError_t launch_backward(const Args& a, hipStream_t st) {
+  const dim3 grid((unsigned)((a.n_items + a.n_dq) * a.kv_heads));
+  note_launch("attn_bwd", st);
+  if (a.dtype == 1 && a.D <= 64) bwd_kernel<bf16, 64><<<grid, 256, 0, st>>>(a);
+  else if (a.dtype == 1) bwd_kernel<bf16, 128><<<grid, 256, 0, st>>>(a);
+  else if (a.D <= 64) bwd_kernel<float, 64><<<grid, 256, 0, st>>>(a);
+  else bwd_kernel<float, 128><<<grid, 256, 0, st>>>(a);
   return hipGetLastError();
 }
 
-hipError_t launch_dkv(const Args& a, hipStream_t st) {
-  const dim3 grid((unsigned)(a.n_items * a.kv_heads));
-  note_launch("attn_dkv", st);
-  if (a.dtype == 1 && a.D <= 64) dkv_kernel<bf16, 64><<<grid, 256, 0, st>>>(a);
-  else if (a.dtype == 1) dkv_kernel<bf16, 128><<<grid, 256, 0, st>>>(a);
-  else if (a.D <= 64) dkv_kernel<float, 64><<<grid, 256, 0, st>>>(a);
-  else dkv_kernel<float, 128><<<grid, 256, 0, st>>>(a);
+hipError_t launch_join_backward(const Args& a, const void* dq_items, int n_dq, const void* key_items, int n_key,
+                                hipStream_t st) {
+  static_assert(kRows == kBwdKeys, "one grid for both kinds of tile");
+  const dim3 grid((unsigned)(n_dq + n_key), (unsigned)a.kv_heads, kRows / 16);
+  const JoinItem* q = static_cast<const JoinItem*>(dq_items);
+  const KeyJoin* k = static_cast<const KeyJoin*>(key_items);
+  note_launch("attn_join_bwd", st);
+  if (a.dtype == 1) join_bwd_kernel<bf16><<<grid, 256, 0, st>>>(a, q, n_dq, k);
+  else join_bwd_kernel<float><<<grid, 256, 0, st>>>(a, q, n_dq, k);
   return hipGetLastError();
 }
 

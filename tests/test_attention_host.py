@@ -67,7 +67,8 @@ class Plan:
         raw = p._host.view(np.int32)
         names = ["magic", "dtype", "heads", "kv_heads", "head_dim", "n_seqs", "q_rows", "k_rows", "n_rows", "n_join",
                  "n_dq", "n_key", "o_rows", "o_join", "o_dq", "o_key", "parts", "overlap", "bytes", "n_key_join",
-                 "o_key_join", "key_parts", "n_few", "o_few", "join_rows"]
+                 "o_key_join", "key_parts", "n_few", "o_few", "join_rows",
+                 "n_tiles", "o_tiles", "n_dq_join", "o_dq_join", "dq_parts"]
         self.h = dict(zip(names, raw[:len(names)].tolist()))
 
         def items(o, n, fields):
@@ -78,7 +79,9 @@ class Plan:
         self.rows = items(self.h["o_rows"], self.h["n_rows"], row)
         self.dq = items(self.h["o_dq"], self.h["n_dq"], row)
         self.few = items(self.h["o_few"], self.h["n_few"], row)
-        self.join = items(self.h["o_join"], self.h["n_join"], ["q_start", "q_len", "r0", "part", "n", "step"])
+        self.tiles = items(self.h["o_tiles"], self.h["n_tiles"], row)
+        self.join, self.dq_join = (items(self.h["o" + w], self.h["n" + w], ["q_start", "q_len", "r0", "part", "n", "step"])
+                                   for w in ("_join", "_dq_join"))
         self.key = items(self.h["o_key"], self.h["n_key"],
                          ["q_start", "q_len", "r_begin", "r_end", "k_start", "off", "key0", "part"])
         self.key_join = items(self.h["o_key_join"], self.h["n_key_join"], ["k_row", "n_keys", "part", "n"])
@@ -100,11 +103,10 @@ def test_plan_tiles_cover_what_each_query_sees(heads, kv, ql, kl):
     p = ip.AttentionPlan(heads, kv, 64, ql, kl, device="cpu")
     pl, G = Plan(p), heads // kv
     qs, ks = np.concatenate([[0], np.cumsum(ql)]), np.concatenate([[0], np.cumsum(kl)])
-    seen = {}
     assert all(x["q_len"] * G <= 32 for x in pl.few)
-    for items in (pl.rows + pl.few, pl.dq):
-        need = {(int(qs[i]), r0): 0 for i, n in enumerate(ql) for r0 in range(0, n * G, 128)}
-        got = {key: [] for key in need}
+    for items, joined, slots in ((pl.rows + pl.few, pl.join, "parts"), (pl.tiles, [], None),
+                                 (pl.dq, pl.dq_join, "dq_parts")):
+        got, seen = {(int(qs[i]), r0): [] for i, n in enumerate(ql) for r0 in range(0, n * G, 128)}, {}
         for x in items:
             got[(x["q_start"], x["r0"])].append(x)
         for (q0, r0), parts in got.items():
@@ -115,17 +117,16 @@ def test_plan_tiles_cover_what_each_query_sees(heads, kv, ql, kl):
             assert parts[0]["k_begin"] == 0 and parts[-1]["k_end"] == sees
             assert all(a["k_end"] == b["k_begin"] and b["k_begin"] % 64 == 0 for a, b in zip(parts, parts[1:]))
             assert all(x["k_start"] == ks[i] and x["off"] == kl[i] - ql[i] and x["q_len"] == ql[i] for x in parts)
-            if items is not pl.dq and len(parts) > 1:
+            if len(parts) > 1:
                 seen[(q0, r0)] = [x["part"] for x in parts]
             else:
-                assert len(parts) == 1 and parts[0]["part"] == -1
-    joins = {(j["q_start"], j["r0"]): [j["part"] + x * j["step"] for x in range(j["n"])] for j in pl.join}
-    assert joins == seen
-    few = {x["q_start"] for x in pl.few}
-    assert all(j["step"] == (1 if j["q_start"] in few else 4) for j in pl.join)
+                assert parts[0]["part"] == -1
+        assert {(j["q_start"], j["r0"]): [j["part"] + x * j["step"] for x in range(j["n"])] for j in joined} == seen
+        few = {x["q_start"] for x in pl.few} if slots == "parts" else set()
+        assert all(j["step"] == (1 if j["q_start"] in few else 4) for j in joined)
+        used = sorted(j["part"] + x for j in joined for x in range(j["n"] * j["step"]))
+        assert used == list(range(pl.h[slots] if slots else 0))
     assert all(min(32 * j["step"], j["q_len"] * G - j["r0"]) <= pl.h["join_rows"] for j in pl.join)
-    used = sorted(j["part"] + x for j in pl.join for x in range(j["n"] * j["step"]))
-    assert used == list(range(pl.h["parts"]))
     # keys: every tile of every sequence, over all rows from the first that sees its first key
     want = {(int(ks[i]), k0): (i, min(n, max(0, k0 - (m - n))) * G)
             for i, (n, m) in enumerate(zip(ql, kl)) for k0 in range(0, m, 128)}
