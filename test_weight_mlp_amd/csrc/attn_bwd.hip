@@ -49,11 +49,16 @@ __device__ __forceinline__ void delta_tile(const Args& a, const RowItem& it, int
     const float sl2 = a.scale * kLog2e;
     const At<T, DP> here(lane);
     const RowStream<T, DP, NW, kKeys> ks(a.k.row, D, wave, lane), vs(a.v.row, D, wave, lane);
-    for (int key0 = 0; key0 < it.k_end; key0 += kKeys) {
+    auto load = [&](int key0, char* tile) {
       const int left = it.off + it.q_len - key0;
-      ks.issue(K, (int64_t)it.k_start + key0, left, lds, wave);
-      vs.issue(V, (int64_t)it.k_start + key0, left, lds + TB, wave);
+      ks.issue(K, (int64_t)it.k_start + key0, left, tile, wave);
+      vs.issue(V, (int64_t)it.k_start + key0, left, tile + TB, wave);
+    };
+    if (it.k_end > 0) load(0, lds);
+    for (int key0 = 0, odd = 0; key0 < it.k_end; key0 += kKeys, odd ^= 1) {
+      const char* tile = lds + odd * 2 * TB;
       tiles_landed();
+      if (key0 + kKeys < it.k_end) load(key0 + kKeys, lds + (odd ^ 1) * 2 * TB);
 #pragma unroll 1
       for (int kb = 0; kb < kKeys / 32; ++kb) {
         floatx16 x, dp;
@@ -61,8 +66,8 @@ __device__ __forceinline__ void delta_tile(const Args& a, const RowItem& it, int
         fill16(dp, 0.0f);
 #pragma unroll
         for (int q = 0; q < TL::STEPS; ++q) {
-          x = Elt<T>::mma(TL::row(lds + kb * TL::bytes(32), here.row, 0, q), qf[q], x);
-          dp = Elt<T>::mma(TL::row(lds + TB + kb * TL::bytes(32), here.row, 0, q), df[q], dp);
+          x = Elt<T>::mma(TL::row(tile + kb * TL::bytes(32), here.row, 0, q), qf[q], x);
+          dp = Elt<T>::mma(TL::row(tile + TB + kb * TL::bytes(32), here.row, 0, q), df[q], dp);
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -70,7 +75,6 @@ __device__ __forceinline__ void delta_tile(const Args& a, const RowItem& it, int
           if (key0 + 32 * kb + 8 * (i >> 2) + 4 * h + (i & 3) < row.lim) delta = fmaf(p, dp[i], delta);
         }
       }
-      tiles_landed();  // every wave is done with the tile
     }
   } else {
     frag of[TL::STEPS];
@@ -89,7 +93,7 @@ __device__ __forceinline__ void delta_tile(const Args& a, const RowItem& it, int
 
 template <typename T, int DP>
 __global__ __launch_bounds__(256) void delta_kernel(Args a) {
-  __shared__ __attribute__((aligned(16))) char lds[sizeof(T) == 2 ? 2 * Tile<T, DP>::bytes(kKeys) : 16];
+  __shared__ __attribute__((aligned(16))) char lds[sizeof(T) == 2 ? 4 * Tile<T, DP>::bytes(kKeys) : 16];
   const int kvh = blockIdx.x % a.kv_heads;
   const RowItem it = static_cast<const RowItem*>(a.items)[blockIdx.x / a.kv_heads];
   delta_tile<T, DP>(a, it, kvh, static_cast<const char*>(a.k.p) + (int64_t)kvh * a.k.head * (int)sizeof(T),

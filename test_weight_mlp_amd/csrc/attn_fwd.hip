@@ -12,6 +12,7 @@
 #include "attn.h"
 #include "launch.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace ipttt {
@@ -257,14 +258,42 @@ __global__ __launch_bounds__(256, sizeof(T) * DP > 256 ? 1 : 2) void fwd_kernel(
 }
 
 // Joins the partial results of one tile: with each part's lse, its weight is
-// e^(lse_i - lse), lse = log sum e^(lse_i).  A wave a row, two columns a lane,
-// parts in slot order.
+// e^(lse_i - lse), lse = log sum e^(lse_i); parts in slot order, eight parts'
+// loads in flight.  A tile of many rows: a thread takes four columns of one row.
+// One of few rows, which has many parts: a wave takes one row, two columns a
+// lane, and its lanes hold the weights of 64 parts (one token over 4097 keys, 33
+// parts: 4.3 us, 5.2 as the other kind).
 template <typename T>
-__global__ __launch_bounds__(256) void join_kernel(Args a, const JoinItem* items) {
-  const int kvh = blockIdx.y, lane = threadIdx.x & 63, i = blockIdx.z * 4 + (threadIdx.x >> 6);
-  const JoinItem it = items[blockIdx.x];
-  const int G = a.G, D = a.D, r = it.r0 + i;
-  if (r >= it.q_len * G) return;
+__device__ __forceinline__ void join_many(const Args& a, const JoinItem& it, int kvh) {
+  const int G = a.G, D = a.D, quads = D / 4, per = 256 / quads;
+  const int i = blockIdx.z * per + threadIdx.x / quads, r = it.r0 + i, d = threadIdx.x % quads * 4;
+  if ((int)threadIdx.x >= per * quads || i >= it.step * kPartRows || r >= it.q_len * G) return;
+  const int64_t slot0 = part_row(it.part, a.kv_heads, kvh, i), step = (int64_t)it.step * a.kv_heads * kPartRows;
+  const float* ls = a.part_lse + slot0;
+  const float* x = a.part_o + slot0 * D + d;
+  float m = -INFINITY;
+#pragma unroll 8
+  for (int p = 0; p < it.n; ++p) m = fmaxf(m, ls[p * step]);
+  const float mu = m == -INFINITY ? 0.0f : m;
+  float l = 0.0f;
+  float4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+  for (int p = 0; p < it.n; ++p) {
+    const float w = __builtin_amdgcn_exp2f((ls[p * step] - mu) * kLog2e);
+    l += w;
+    o += w * *reinterpret_cast<const float4_t*>(x + p * step * D);
+  }
+  o *= l == 0.0f ? 0.0f : 1.0f / l;
+  const int t = r / G, head = kvh * G + r - t * G;
+  const int64_t row = it.q_start + (int64_t)t;
+  if (d == 0) a.lse[row * a.heads + head] = l == 0.0f ? -INFINITY : mu + __builtin_amdgcn_logf(l) * kLn2;
+  store4<T>(static_cast<T*>(a.o.p) + row * a.o.row + head * a.o.head + d, o[0], o[1], o[2], o[3]);
+}
+
+template <typename T>
+__device__ __forceinline__ void join_few(const Args& a, const JoinItem& it, int kvh) {
+  const int G = a.G, D = a.D, lane = threadIdx.x & 63, i = blockIdx.z * 4 + (threadIdx.x >> 6), r = it.r0 + i;
+  if (i >= it.step * kPartRows || r >= it.q_len * G) return;
   const int t = r / G, head = kvh * G + r - t * G;
   const int64_t slot0 = part_row(it.part, a.kv_heads, kvh, i), step = (int64_t)it.step * a.kv_heads * kPartRows;
   float m = -INFINITY;
@@ -279,16 +308,16 @@ __global__ __launch_bounds__(256) void join_kernel(Args a, const JoinItem* items
     const int n = min(64, it.n - p0);
     const float w = lane < n ? __builtin_amdgcn_exp2f((a.part_lse[slot0 + (p0 + lane) * step] - mu) * kLog2e) : 0.0f;
     l += w;
-    for (int p = 0; p < n; p += 8) {  // eight parts' loads in flight
+    for (int p = 0; p < n; p += 8) {
       float2_t v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        v[i] = *reinterpret_cast<const float2_t*>(x + (p0 + min(p + i, n - 1)) * step * D);
+      for (int j = 0; j < 8; ++j)
+        v[j] = *reinterpret_cast<const float2_t*>(x + (p0 + min(p + j, n - 1)) * step * D);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float wi = __shfl(w, p + i, 64);  // 0 past the last part
-        x0 = fmaf(wi, v[i][0], x0);
-        x1 = fmaf(wi, v[i][1], x1);
+      for (int j = 0; j < 8; ++j) {
+        const float wj = __shfl(w, p + j, 64);  // 0 past the last part
+        x0 = fmaf(wj, v[j][0], x0);
+        x1 = fmaf(wj, v[j][1], x1);
       }
     }
   }
@@ -304,6 +333,13 @@ __global__ __launch_bounds__(256) void join_kernel(Args a, const JoinItem* items
   }
 }
 
+template <typename T>
+__global__ __launch_bounds__(256) void join_kernel(Args a, const JoinItem* items) {
+  const JoinItem it = items[blockIdx.x];
+  if (it.step == 1) join_few<T>(a, it, blockIdx.y);
+  else join_many<T>(a, it, blockIdx.y);
+}
+
 }  // namespace
 
 hipError_t launch_forward(const Args& a, hipStream_t st) {
@@ -317,7 +353,9 @@ hipError_t launch_forward(const Args& a, hipStream_t st) {
 }
 
 hipError_t launch_join(const Args& a, const void* items, int n, int rows, hipStream_t st) {
-  const dim3 grid((unsigned)n, (unsigned)a.kv_heads, (unsigned)(rows + 3) / 4);
+  // rows of a block: 4 of a tile of few rows, per of one of many
+  const int per = 256 / (a.D / 4), z = std::max((std::min(rows, kFewRows) + 3) / 4, (rows + per - 1) / per);
+  const dim3 grid((unsigned)n, (unsigned)a.kv_heads, (unsigned)z);
   note_launch("attn_join", st);
   if (a.dtype == 1) join_kernel<bf16><<<grid, 256, 0, st>>>(a, static_cast<const JoinItem*>(items));
   else join_kernel<float><<<grid, 256, 0, st>>>(a, static_cast<const JoinItem*>(items));
