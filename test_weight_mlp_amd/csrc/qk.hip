@@ -35,10 +35,19 @@ __device__ __forceinline__ void store_vec(T* p, const float (&x)[VEC]) {
   *reinterpret_cast<typename VecOf<T, VEC>::type*>(p) = v;
 }
 
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float x) {
+  return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, true));
+}
+
+// Sum over each group of LG lanes, in all of them: neighbours, then pairs, then
+// (once quads are equal) the mirrored half and whole row of 16.
 template <int LG>
 __device__ __forceinline__ float group_sum(float x) {
-#pragma unroll
-  for (int o = LG / 2; o > 0; o >>= 1) x += __shfl_xor(x, o, 64);
+  if constexpr (LG > 1) x = dpp_add<0xB1>(x);   // quad_perm 1 0 3 2
+  if constexpr (LG > 2) x = dpp_add<0x4E>(x);   // quad_perm 2 3 0 1
+  if constexpr (LG > 4) x = dpp_add<0x141>(x);  // row_half_mirror
+  if constexpr (LG > 8) x = dpp_add<0x140>(x);  // row_mirror
   return x;
 }
 
@@ -55,7 +64,7 @@ __device__ __forceinline__ void load_angles(const QkArgs& a, int64_t t, int d, b
   const int pos = a.pos[t];
   const bool ok = pos >= 0 && pos < a.table_rows;
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) c[i] = s[i] = __builtin_nanf("");
+  for (int i = 0; i < VEC; ++i) c[i] = s[i] = on ? __builtin_nanf("") : 0.0f;
   if (ok && on) {
     load_vec<float, VEC>(a.table + (int64_t)pos * a.D + d, c);
     load_vec<float, VEC>(a.table + (int64_t)pos * a.D + a.D / 2 + d, s);
@@ -114,53 +123,56 @@ __global__ __launch_bounds__(256) void qk_kernel(QkArgs a) {
   }
 }
 
-// Backward: the rotation transposed, then the norm's; each wave sums the
-// weight gradients of its tokens in registers, each block writes one partial.
-template <typename T, int VEC, int LG>
-__global__ __launch_bounds__(256) void qk_bwd_kernel(QkArgs a) {
+// Backward: the rotation transposed, then the norm's; all query heads, then all
+// key heads, so that only one of the weight gradients is in registers.  Each
+// wave sums them over its tokens, each block writes one partial.  FULL: the
+// group's lanes hold exactly one half (D of 64 and 128, for instance); otherwise
+// the lanes past it hold nothing.  Bound by memory: 16k tokens, 40 heads of width
+// 128 in 0.098 ms, 5.2 TB/s (two or four heads a group at once: 0.101, 0.118).
+template <typename T, int VEC, int LG, bool FULL>
+__global__ __launch_bounds__(256, 2) void qk_bwd_kernel(QkArgs a) {
   constexpr int GPW = 64 / LG;
-  __shared__ float red[4][2][2][LG * VEC];
+  typedef typename VecOf<T, VEC>::type vec;
+  __shared__ float red[4][2][LG * VEC];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, group = lane / LG, d = (lane % LG) * VEC;
-  const int half = a.D / 2, nq = a.heads, n = nq + a.kv_heads;
-  const bool on = d < half;
-  float dw[2][2][VEC];  // [q, k][half][element]
+  const int half = a.D / 2;
+  const bool on = FULL || d < half;
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const int heads = which == 0 ? a.heads : a.kv_heads;
+    const View xv = which == 0 ? a.q : a.k, zv = which == 0 ? a.q_out : a.k_out, ov = which == 0 ? a.dq : a.dk;
+    float dwl[VEC], dwh[VEC], wl[VEC], wh[VEC];
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) dw[0][0][i] = dw[0][1][i] = dw[1][0][i] = dw[1][1][i] = 0.0f;
-  for (int64_t t = (int64_t)blockIdx.x * 4 + wave; t < a.tokens; t += (int64_t)gridDim.x * 4) {
-    float c[VEC], s[VEC];
-    load_angles<VEC>(a, t, d, on, c, s);
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      const int h0 = which == 0 ? 0 : nq, h1 = which == 0 ? nq : n;
-      const View &xv = which == 0 ? a.q : a.k, &zv = which == 0 ? a.q_out : a.k_out, &ov = which == 0 ? a.dq : a.dk;
-      float wl[VEC], wh[VEC];
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) wl[i] = wh[i] = 0.0f;
-      if (on) {
-        const T* w = static_cast<const T*>(which == 0 ? a.w_q : a.w_k) + d;
-        load_vec<T, VEC>(w, wl);
-        load_vec<T, VEC>(w + half, wh);
-      }
-      for (int hd = group; hd < h1 - h0; hd += GPW) {
-        float lo[VEC], hi[VEC], zl[VEC], zh[VEC], sq = 0.0f, dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) lo[i] = hi[i] = zl[i] = zh[i] = 0.0f;
+    for (int i = 0; i < VEC; ++i) dwl[i] = dwh[i] = wl[i] = wh[i] = 0.0f;
+    if (on) {
+      const T* w = static_cast<const T*>(which == 0 ? a.w_q : a.w_k) + d;
+      load_vec<T, VEC>(w, wl);
+      load_vec<T, VEC>(w + half, wh);
+    }
+#pragma unroll 1
+    for (int64_t t = (int64_t)blockIdx.x * 4 + wave; t < a.tokens; t += (int64_t)gridDim.x * 4) {
+      float c[VEC], s[VEC];
+      load_angles<VEC>(a, t, d, on, c, s);
+#pragma unroll 1
+      for (int hd = group; hd < heads; hd += GPW) {
+        vec raw[4] = {};
         if (on) {
           const T* x = head_ptr<T>(xv, t, hd) + d;
           const T* z = head_ptr<T>(zv, t, hd) + d;
-          load_vec<T, VEC>(x, lo);
-          load_vec<T, VEC>(x + half, hi);
-          load_vec<T, VEC>(z, zl);
-          load_vec<T, VEC>(z + half, zh);
+          raw[0] = *reinterpret_cast<const vec*>(x);
+          raw[1] = *reinterpret_cast<const vec*>(x + half);
+          raw[2] = *reinterpret_cast<const vec*>(z);
+          raw[3] = *reinterpret_cast<const vec*>(z + half);
         }
+        float lo[VEC], hi[VEC], zl[VEC], zh[VEC], sq = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
+          lo[i] = (float)raw[0][i];
+          hi[i] = (float)raw[1][i];
+          const float a0 = (float)raw[2][i], a1 = (float)raw[3][i];
+          zl[i] = a0 * c[i] + a1 * s[i];
+          zh[i] = a1 * c[i] - a0 * s[i];
           sq = fmaf(lo[i], lo[i], fmaf(hi[i], hi[i], sq));
-          if (on) {
-            const float u = zl[i] * c[i] + zh[i] * s[i], v = zh[i] * c[i] - zl[i] * s[i];
-            zl[i] = u;
-            zh[i] = v;
-          }
           dot = fmaf(zl[i] * wl[i], lo[i], fmaf(zh[i] * wh[i], hi[i], dot));
         }
         const float r = rsqrtf(group_sum<LG>(sq) / (float)a.D + a.eps);
@@ -168,8 +180,8 @@ __global__ __launch_bounds__(256) void qk_bwd_kernel(QkArgs a) {
         if (!on) continue;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          dw[which][0][i] = fmaf(zl[i], lo[i] * r, dw[which][0][i]);
-          dw[which][1][i] = fmaf(zh[i], hi[i] * r, dw[which][1][i]);
+          dwl[i] = fmaf(zl[i], lo[i] * r, dwl[i]);
+          dwh[i] = fmaf(zh[i], hi[i] * r, dwh[i]);
           lo[i] = r * (zl[i] * wl[i] - lo[i] * k);
           hi[i] = r * (zh[i] * wh[i] - hi[i] * k);
         }
@@ -178,23 +190,26 @@ __global__ __launch_bounds__(256) void qk_bwd_kernel(QkArgs a) {
         store_vec<T, VEC>(o + half, hi);
       }
     }
-  }
 #pragma unroll
-  for (int which = 0; which < 2; ++which)
+    for (int i = 0; i < VEC; ++i) {
+      float x = dwl[i], y = dwh[i];
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        float x = dw[which][hf][i];
-#pragma unroll
-        for (int o = LG; o < 64; o <<= 1) x += __shfl_xor(x, o, 64);
-        if (group == 0) red[wave][which][hf][d + i] = x;
+      for (int o = LG; o < 64; o <<= 1) {
+        x += __shfl_xor(x, o, 64);
+        y += __shfl_xor(y, o, 64);
       }
-  __syncthreads();
-  for (int e = threadIdx.x; e < 2 * a.D; e += 256) {
-    const int which = e / a.D, x = e % a.D, hf = x / half, at = x % half;
-    a.part[(int64_t)blockIdx.x * 2 * a.D + e] =
-        red[0][which][hf][at] + red[1][which][hf][at] + red[2][which][hf][at] + red[3][which][hf][at];
+      if (group == 0) {
+        red[wave][0][d + i] = x;
+        red[wave][1][d + i] = y;
+      }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.D; e += 256) {
+      const int hf = e / half, at = e % half;
+      a.part[((int64_t)blockIdx.x * 2 + which) * a.D + e] =
+          red[0][hf][at] + red[1][hf][at] + red[2][hf][at] + red[3][hf][at];
+    }
+    __syncthreads();
   }
 }
 
@@ -216,13 +231,19 @@ __global__ __launch_bounds__(256) void qk_sum_kernel(const float* part, int n, i
 
 // Lanes of a head: its half in pieces of VEC elements, up to a power of two
 // (D <= 128, so at most 16).
+template <int LG, typename F>
+void with_full(bool full, F&& f) {
+  if (full) f(std::integral_constant<int, LG>(), std::true_type());
+  else f(std::integral_constant<int, LG>(), std::false_type());
+}
 template <typename F>
-void with_lanes(int lanes, F&& f) {
-  if (lanes <= 1) f(std::integral_constant<int, 1>());
-  else if (lanes <= 2) f(std::integral_constant<int, 2>());
-  else if (lanes <= 4) f(std::integral_constant<int, 4>());
-  else if (lanes <= 8) f(std::integral_constant<int, 8>());
-  else f(std::integral_constant<int, 16>());
+void with_lanes(int half, int vec, F&& f) {
+  const int lanes = (half + vec - 1) / vec;
+  if (lanes <= 1) with_full<1>(half == vec, f);
+  else if (lanes <= 2) with_full<2>(half == 2 * vec, f);
+  else if (lanes <= 4) with_full<4>(half == 4 * vec, f);
+  else if (lanes <= 8) with_full<8>(half == 8 * vec, f);
+  else with_full<16>(half == 16 * vec, f);
 }
 
 // 16-byte pieces where half a head is whole 16-byte pieces (fp32 always, as D
@@ -240,7 +261,7 @@ hipError_t launch_qk(const QkArgs& a, hipStream_t st) {
   note_launch("qk", st);
   with_types(a, [&](auto type, auto vec) {
     constexpr int VEC = decltype(vec)::value;
-    with_lanes((a.D / 2 + VEC - 1) / VEC, [&](auto lg) {
+    with_lanes(a.D / 2, VEC, [&](auto lg, auto) {
       constexpr int LG = decltype(lg)::value;
       const int heads = a.heads + a.kv_heads * (a.v.p != nullptr ? 2 : 1);
       const int64_t bx = (a.tokens + 3) / 4, trips = (heads + 64 / LG - 1) / (64 / LG);
@@ -257,8 +278,8 @@ hipError_t launch_qk_backward(const QkArgs& a, hipStream_t st) {
   note_launch("qk_bwd", st);
   with_types(a, [&](auto type, auto vec) {
     constexpr int VEC = decltype(vec)::value;
-    with_lanes((a.D / 2 + VEC - 1) / VEC, [&](auto lg) {
-      qk_bwd_kernel<decltype(type), VEC, decltype(lg)::value><<<blocks, 256, 0, st>>>(a);
+    with_lanes(a.D / 2, VEC, [&](auto lg, auto full) {
+      qk_bwd_kernel<decltype(type), VEC, decltype(lg)::value, decltype(full)::value><<<blocks, 256, 0, st>>>(a);
     });
   });
   const hipError_t e = hipGetLastError();
