@@ -57,7 +57,8 @@ struct PlanHeader {
   int32_t join_rows;         // most rows of a joined tile
   int32_t n_tiles, o_tiles;  // tiles of rows, uncut
   int32_t n_dq_join, o_dq_join, dq_parts;
-  int32_t pad[2];
+  int32_t rows_cut;          // whether tiles of many rows are cut into parts
+  int32_t pad;
 };
 static_assert(sizeof(PlanHeader) == 128, "plan header");
 constexpr int32_t kMagic = 0x41545031;
@@ -72,6 +73,7 @@ struct Args {
   float scale;
   const void *items, *dq_items;  // device
   int n_items, n_dq;
+  bool cut;               // tiles of the forward are cut into parts
   View q, k, v, o, dO, dq, dk, dv;
   float *lse;             // [q rows, heads]
   float *nlse, *ndelta;   // same: -lse / scale (-inf on rows that see nothing), -delta

@@ -215,6 +215,7 @@ struct Range {
 struct Sizes {
   int64_t rows = 0, few = 0, join = 0, tiles = 0, dq = 0, dq_join = 0, key = 0, kjoin = 0;
   int64_t parts = 0, dq_parts = 0, key_parts = 0, join_rows = 0;
+  bool rows_cut = false;
   int64_t o_rows, o_few, o_join, o_tiles, o_dq_join, o_dq, o_key, o_kjoin, o_ranges, bytes;
 };
 
@@ -223,7 +224,11 @@ bool sizes_of(const ipttt_attn_problem* p, const Cut& cut, Sizes* s) {
   const int64_t G = p->heads / p->kv_heads;
   walk(
       p, cut,
-      [&](const RowItem&) { ++s->rows; }, [&](const RowItem&) { ++s->few; },
+      [&](const RowItem& x) {
+        ++s->rows;
+        s->rows_cut = s->rows_cut || x.part >= 0;
+      },
+      [&](const RowItem&) { ++s->few; },
       [&](const JoinItem& x) {
         ++s->join;
         s->parts += (int64_t)x.n * x.step;
@@ -504,6 +509,7 @@ ipttt_status ipttt_attn_plan(const ipttt_attn_problem* p, void* plan, size_t pla
   h->n_few = (int32_t)s.few;
   h->o_few = (int32_t)s.o_few;
   h->join_rows = (int32_t)s.join_rows;
+  h->rows_cut = s.rows_cut;
   h->n_join = (int32_t)s.join;
   h->n_dq = (int32_t)s.dq;
   h->n_key = (int32_t)s.key;
@@ -551,6 +557,7 @@ ipttt_status ipttt_attention(const void* plan, const void* plan_dev, float scale
   if (h->n_rows > 0) {
     a.items = dev + h->o_rows;
     a.n_items = h->n_rows;
+    a.cut = h->rows_cut != 0;
     IPTTT_TRY(hip_status(ipttt::attn::launch_forward(a, st)));
   }
   if (h->n_few > 0) {

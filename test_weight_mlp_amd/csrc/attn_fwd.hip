@@ -19,23 +19,22 @@ namespace ipttt {
 namespace attn {
 namespace {
 
-// The work of one wave on one step of kKeys keys, in four phases of MFMAs: the
-// next step's scores (two blocks of 32 keys), then this step's part of O from
-// each block.  The vector units meanwhile raise this step's scores to
-// probabilities, spread evenly over the first three phases (the second phase's
-// end must have the first block's, the third's the second's), and take the
-// next scores' maximum in the last.  Fragments are read from LDS one group of
-// four MFMAs ahead.
-template <typename T, int DP>
+// The work of one wave on one step of NB blocks of 32 keys, in phases of MFMAs:
+// the next step's scores, a phase a block, then this step's part of O from each
+// block.  The vector units meanwhile raise this step's scores to probabilities,
+// spread evenly over the phases of scores and the first half of the others (a
+// block's phase must find its own raised), and take the next scores' maximum in
+// the second half.  Fragments are read from LDS one group of four MFMAs ahead.
+template <typename T, int DP, int NB>
 struct Step {
   typedef Tile<T, DP> TL;
   typedef Groups<T, DP> GR;
   typedef typename Elt<T>::frag frag;
   static constexpr int EPL = Elt<T>::EPL, DB = DP / 32, H = GR::H;
 
-  // scores [e0, e0 + n) of the step's 32 to probabilities
+  // scores [e0, e0 + n) of the step's 16 NB to probabilities
   template <int N>
-  static __device__ __forceinline__ void raise(floatx16 (&s)[2], int e0, float sl2, float m, float& l) {
+  static __device__ __forceinline__ void raise(floatx16 (&s)[NB], int e0, float sl2, float m, float& l) {
 #pragma unroll
     for (int e = e0; e < e0 + N; ++e) {
       s[e >> 4][e & 15] = __builtin_amdgcn_exp2f(fmaf(s[e >> 4][e & 15], sl2, -m));
@@ -48,20 +47,20 @@ struct Step {
   // the loads of later steps
   template <bool NEXT, class Issue>
   static __device__ __forceinline__ void run(const char* kt, const char* vt, const frag (&qf)[TL::STEPS],
-                                             floatx16 (&s)[2], floatx16 (&o)[DB], float sl2, float m, float& l,
+                                             floatx16 (&s)[NB], floatx16 (&o)[DB], float sl2, float m, float& l,
                                              float& top, const At<T, DP>& at, Issue issue) {
     frag f[2][4];
-    floatx16 n[2];
+    floatx16 n[NB];
     int cur = 0;
     if constexpr (NEXT) {
       GR::rows(kt, at, 0, 0, f[0]);
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
+      for (int kb = 0; kb < NB; ++kb) {
         fill16(n[kb], 0.0f);
 #pragma unroll
         for (int g = 0; g < H; ++g) {
           if (g + 1 < H) GR::rows(kt, at, 32 * kb, g + 1, f[cur ^ 1]);
-          else if (kb == 0) GR::rows(kt, at, 32, 0, f[cur ^ 1]);
+          else if (kb + 1 < NB) GR::rows(kt, at, 32 * (kb + 1), 0, f[cur ^ 1]);
           else GR::cols(vt, at, 0, 0, f[cur ^ 1]);
           raise<12 / H>(s, (kb * H + g) * (12 / H), sl2, m, l);
 #pragma unroll
@@ -73,23 +72,24 @@ struct Step {
       }
     } else {
       GR::cols(vt, at, 0, 0, f[0]);
-      raise<24>(s, 0, sl2, m, l);
+      raise<12 * NB>(s, 0, sl2, m, l);
     }
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
+    for (int kb = 0; kb < NB; ++kb) {
       frag p[GR::NP];
 #pragma unroll
       for (int j = 0; j < GR::NP; ++j) p[j] = pack<T>(s[kb], j * EPL);
 #pragma unroll
       for (int g = 0; g < H; ++g) {
         if (g + 1 < H) GR::cols(vt, at, 32 * kb, g + 1, f[cur ^ 1]);
-        else if (kb == 0) GR::cols(vt, at, 32, 0, f[cur ^ 1]);
-        if (kb == 0) {
-          raise<8 / H>(s, 24 + g * (8 / H), sl2, m, l);
+        else if (kb + 1 < NB) GR::cols(vt, at, 32 * (kb + 1), 0, f[cur ^ 1]);
+        if (kb < NB / 2) {
+          raise<8 / H>(s, 12 * NB + (kb * H + g) * (8 / H), sl2, m, l);
         } else if constexpr (NEXT) {
-          if (g == 0) top = fmaxf(n[0][0], n[1][0]);
+          const floatx16 &x = n[2 * (kb - NB / 2)], &y = n[2 * (kb - NB / 2) + 1];
+          if (kb == NB / 2 && g == 0) top = x[0];
 #pragma unroll
-          for (int i = g * (16 / H); i < (g + 1) * (16 / H); ++i) top = fmaxf(fmaxf(top, n[0][i]), n[1][i]);
+          for (int i = g * (16 / H); i < (g + 1) * (16 / H); ++i) top = fmaxf(fmaxf(top, x[i]), y[i]);
         }
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
@@ -101,16 +101,19 @@ struct Step {
       }
     }
     if constexpr (NEXT) {
-      s[0] = n[0];
-      s[1] = n[1];
+#pragma unroll
+      for (int kb = 0; kb < NB; ++kb) s[kb] = n[kb];
     }
   }
 };
 
-__device__ __forceinline__ float largest(const floatx16 (&s)[2]) {
-  float x = fmaxf(s[0][0], s[1][0]);
+template <int NB>
+__device__ __forceinline__ float largest(const floatx16 (&s)[NB]) {
+  float x = s[0][0];
 #pragma unroll
-  for (int i = 1; i < 16; ++i) x = fmaxf(fmaxf(x, s[0][i]), s[1][i]);
+  for (int kb = 0; kb < NB; kb += 2)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x = fmaxf(fmaxf(x, s[kb][i]), s[kb + 1][i]);
   return x;
 }
 
@@ -118,12 +121,12 @@ __device__ __forceinline__ float largest(const floatx16 (&s)[2]) {
 // maximum passed it by more than 2^8: sums and O are relative to m, exact for any
 // m near the maximum, so they are rescaled (one multiplication an element)
 // only then, which after the first few steps is rare.
-template <int DB>
-__device__ __forceinline__ void settle(floatx16 (&s)[2], float top, int key0, const Row& row, float sl2,
+template <int NB, int DB>
+__device__ __forceinline__ void settle(floatx16 (&s)[NB], float top, int key0, const Row& row, float sl2,
                                        floatx16 (&o)[DB], float& m, float& l, int lane) {
-  if (key0 + kKeys > row.all) {
+  if (key0 + 32 * NB > row.all) {
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+    for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         if (key0 + 32 * kb + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= row.lim) s[kb][i] = -INFINITY;
@@ -141,13 +144,13 @@ __device__ __forceinline__ void settle(floatx16 (&s)[2], float top, int key0, co
   }
 }
 
-template <typename T, int DP>
+template <typename T, int DP, int NB>
 __device__ __forceinline__ void fwd_tile(const Args& a, const RowItem& it, int kvh, const char* __restrict__ K,
                                          const char* __restrict__ V, char* lds) {
   typedef Tile<T, DP> TL;
-  typedef Step<T, DP> ST;
+  typedef Step<T, DP, NB> ST;
   typedef typename Elt<T>::frag frag;
-  constexpr int NW = 4, ES = sizeof(T), TB = TL::bytes(kKeys), DB = DP / 32;
+  constexpr int NW = 4, ES = sizeof(T), KT = 32 * NB, TB = TL::bytes(KT), DB = DP / 32;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
   const int D = a.D;
   const float sl2 = a.scale * kLog2e;
@@ -156,15 +159,15 @@ __device__ __forceinline__ void fwd_tile(const Args& a, const RowItem& it, int k
   const int head = kvh * a.G + row.g;
 
   const At<T, DP> here(lane);
-  const RowStream<T, DP, NW, kKeys> ks(a.k.row, D, wave, lane), vs(a.v.row, D, wave, lane);
-  const int k_len = it.off + it.q_len, steps = (it.k_end - it.k_begin + kKeys - 1) / kKeys;
+  const RowStream<T, DP, NW, KT> ks(a.k.row, D, wave, lane), vs(a.v.row, D, wave, lane);
+  const int k_len = it.off + it.q_len, steps = (it.k_end - it.k_begin + KT - 1) / KT;
   // keys in buffers 0 and 1, values in 2 and 3, step s in buffer s & 1
   auto keys = [&](int s) {
-    const int key = it.k_begin + s * kKeys;
+    const int key = it.k_begin + s * KT;
     ks.issue(K, (int64_t)it.k_start + key, k_len - key, lds + (s & 1) * TB, wave);
   };
   auto values = [&](int s) {
-    const int key = it.k_begin + s * kKeys;
+    const int key = it.k_begin + s * KT;
     vs.issue(V, (int64_t)it.k_start + key, k_len - key, lds + (2 + (s & 1)) * TB, wave);
   };
   if (steps > 0) keys(0);
@@ -182,15 +185,15 @@ __device__ __forceinline__ void fwd_tile(const Args& a, const RowItem& it, int k
     tiles_landed();
     values(0);
     if (steps > 1) keys(1);
-    floatx16 s[2];
+    floatx16 s[NB];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
+    for (int kb = 0; kb < NB; ++kb) {
       fill16(s[kb], 0.0f);
 #pragma unroll
       for (int q = 0; q < TL::STEPS; ++q)
         s[kb] = Elt<T>::mma(TL::row(lds, here.row, 32 * kb, q), qf[q], s[kb]);
     }
-    settle<DB>(s, largest(s), it.k_begin, row, sl2, o, m, l, lane);
+    settle(s, largest(s), it.k_begin, row, sl2, o, m, l, lane);
     float top = 0.0f;
     // one step with another to follow; its buffers are known at compile time, so
     // that the LDS addresses of all fragments are a few registers plus immediate
@@ -205,7 +208,7 @@ __device__ __forceinline__ void fwd_tile(const Args& a, const RowItem& it, int k
         values(st + 1);
         if (st + 2 < steps) keys(st + 2);
       });
-      settle<DB>(s, top, it.k_begin + (st + 1) * kKeys, row, sl2, o, m, l, lane);
+      settle(s, top, it.k_begin + (st + 1) * KT, row, sl2, o, m, l, lane);
     };
     int st = 0;
     while (st < steps - 1) {
@@ -248,13 +251,13 @@ __device__ __forceinline__ void fwd_tile(const Args& a, const RowItem& it, int k
 
 // Two waves a SIMD (256 registers a wave) where the tiles allow it; fp32 of
 // width 128 needs the registers of one.
-template <typename T, int DP>
+template <typename T, int DP, int NB>
 __global__ __launch_bounds__(256, sizeof(T) * DP > 256 ? 1 : 2) void fwd_kernel(Args a) {
-  __shared__ __attribute__((aligned(16))) char lds[4 * Tile<T, DP>::bytes(kKeys)];
+  __shared__ __attribute__((aligned(16))) char lds[4 * Tile<T, DP>::bytes(32 * NB)];
   const int kvh = blockIdx.x % a.kv_heads;
   const RowItem it = static_cast<const RowItem*>(a.items)[blockIdx.x / a.kv_heads];
-  fwd_tile<T, DP>(a, it, kvh, static_cast<const char*>(a.k.p) + (int64_t)kvh * a.k.head * (int)sizeof(T),
-                  static_cast<const char*>(a.v.p) + (int64_t)kvh * a.v.head * (int)sizeof(T), lds);
+  fwd_tile<T, DP, NB>(a, it, kvh, static_cast<const char*>(a.k.p) + (int64_t)kvh * a.k.head * (int)sizeof(T),
+                      static_cast<const char*>(a.v.p) + (int64_t)kvh * a.v.head * (int)sizeof(T), lds);
 }
 
 // Joins the partial results of one tile: with each part's lse, its weight is
@@ -345,10 +348,14 @@ __global__ __launch_bounds__(256) void join_kernel(Args a, const JoinItem* items
 hipError_t launch_forward(const Args& a, hipStream_t st) {
   const dim3 grid((unsigned)(a.n_items * a.kv_heads));
   note_launch("attn_fwd", st);
-  if (a.dtype == 1 && a.D <= 64) fwd_kernel<bf16, 64><<<grid, 256, 0, st>>>(a);
-  else if (a.dtype == 1) fwd_kernel<bf16, 128><<<grid, 256, 0, st>>>(a);
-  else if (a.D <= 64) fwd_kernel<float, 64><<<grid, 256, 0, st>>>(a);
-  else fwd_kernel<float, 128><<<grid, 256, 0, st>>>(a);
+  // steps of 64 keys; bf16 of width 64, whose tiles are small, has steps of 128 and
+  // half the barriers (3500 and 900 tokens, 16 heads over 8: 44.6 us, 48.6 with
+  // 64), unless tiles are cut into parts of few steps (1500 tokens: 26.0 and 23.5)
+  if (a.dtype == 1 && a.D <= 64 && !a.cut) fwd_kernel<bf16, 64, 4><<<grid, 256, 0, st>>>(a);
+  else if (a.dtype == 1 && a.D <= 64) fwd_kernel<bf16, 64, 2><<<grid, 256, 0, st>>>(a);
+  else if (a.dtype == 1) fwd_kernel<bf16, 128, 2><<<grid, 256, 0, st>>>(a);
+  else if (a.D <= 64) fwd_kernel<float, 64, 2><<<grid, 256, 0, st>>>(a);
+  else fwd_kernel<float, 128, 2><<<grid, 256, 0, st>>>(a);
   return hipGetLastError();
 }
 
