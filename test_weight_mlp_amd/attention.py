@@ -71,27 +71,31 @@ _pack_heads = struct.Struct("Pqq").pack  # ipttt_heads: data, row_stride, head_s
 
 def _heads(t: torch.Tensor, shape, dtype: torch.dtype, what: str) -> bytes:
     """The ipttt_heads of a [rows, heads, head_dim] device tensor."""
-    row, head, one = t.stride() if t.dim() == 3 else (0, 0, 0)
-    if t.shape != shape or t.dtype is not dtype or one != 1 or not t.is_cuda:
-        raise ValueError(f"{what} must be a {list(shape)} {dtype} device tensor with a contiguous last dimension, not "
-                         f"{list(t.shape)} {t.dtype} of strides {t.stride()} on {t.device}")
-    return _pack_heads(t.data_ptr(), row, head)
+    if t.shape == shape and t.dtype is dtype and t.is_cuda:
+        row, head, one = t.stride()
+        if one == 1:
+            return _pack_heads(t.data_ptr(), row, head)
+    raise ValueError(f"{what} must be a {list(shape)} {dtype} device tensor with a contiguous last dimension, not "
+                     f"{list(t.shape)} {t.dtype} of strides {t.stride()} on {t.device}")
 
 
 def _flat(t: torch.Tensor, shape, dtype: torch.dtype, what: str) -> int:
-    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{what} must be a contiguous {list(shape)} {dtype} device tensor, not {list(t.shape)} "
-                         f"{t.dtype} on {t.device}")
-    return t.data_ptr()
+    if t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{what} must be a contiguous {list(shape)} {dtype} device tensor, not {list(t.shape)} "
+                     f"{t.dtype} on {t.device}")
 
 
 def _ws(ws: Optional[torch.Tensor]):
     return (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
 
 
+_current = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream() without its wrapper object
+
+
 def _on(stream, t: torch.Tensor) -> int:
     """The given stream, or the current one of the tensor's device."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+    return _current(t.get_device()) if stream is None else stream.cuda_stream
 
 
 # ------------------------------------------------------- norm and rotation
@@ -131,13 +135,16 @@ def ipttt_qk_norm_rope(p: QKProblem, q, k, w_q, w_k, positions, table, q_out, k_
     dt = _DTYPES[p.dtype]
     if (v is None) != (v_out is None):
         raise ValueError("v and v_out go together")
-    _check(_lib().ipttt_qk_norm_rope(
+    status = (_bound or _lib()).ipttt_qk_norm_rope(
         p.ref, _heads(q, p.q_shape, dt, "q"), _heads(k, p.k_shape, dt, "k"), _flat(w_q, p.w_shape, dt, "w_q"),
         _flat(w_k, p.w_shape, dt, "w_k"), _flat(positions, p.pos_shape, torch.int32, "positions"),
         _flat(table, p.table_shape, torch.float32, "table"), _heads(q_out, p.q_shape, dt, "q_out"),
         _heads(k_out, p.out_shape, dt, "k_out"), None if v is None else _heads(v, p.k_shape, dt, "v"),
         None if v is None else _heads(v_out, p.out_shape, dt, "v_out"),
-        None if rows is None else _flat(rows, p.pos_shape, torch.int32, "rows"), _on(stream, q)), "ipttt_qk_norm_rope")
+        None if rows is None else _flat(rows, p.pos_shape, torch.int32, "rows"),
+        _on(stream, q))
+    if status:
+        _check(status, "ipttt_qk_norm_rope")
 
 
 def ipttt_qk_backward_workspace_bytes(p: QKProblem) -> int:
@@ -160,13 +167,15 @@ def ipttt_qk_norm_rope_backward(p: QKProblem, q, k, w_q, w_k, positions, table, 
                                 stream=None):
     dt, f32 = _DTYPES[p.dtype], torch.float32
     w, wn = _ws(ws)
-    _check(_lib().ipttt_qk_norm_rope_backward(
+    status = (_bound or _lib()).ipttt_qk_norm_rope_backward(
         p.ref, _heads(q, p.q_shape, dt, "q"), _heads(k, p.k_shape, dt, "k"), _flat(w_q, p.w_shape, dt, "w_q"),
         _flat(w_k, p.w_shape, dt, "w_k"), _flat(positions, p.pos_shape, torch.int32, "positions"),
         _flat(table, p.table_shape, f32, "table"), _heads(dq_out, p.q_shape, dt, "dq_out"),
         _heads(dk_out, p.k_shape, dt, "dk_out"), _heads(dq, p.q_shape, dt, "dq"), _heads(dk, p.k_shape, dt, "dk"),
-        _flat(dw_q, p.w_shape, f32, "dw_q"), _flat(dw_k, p.w_shape, f32, "dw_k"), w, wn, _on(stream, q)),
-        "ipttt_qk_norm_rope_backward")
+        _flat(dw_q, p.w_shape, f32, "dw_q"), _flat(dw_k, p.w_shape, f32, "dw_k"), w, wn,
+        _on(stream, q))
+    if status:
+        _check(status, "ipttt_qk_norm_rope_backward")
 
 
 # --------------------------------------------------------------- attention
@@ -234,18 +243,24 @@ class AttentionBuffers:
 def ipttt_attention(plan: AttentionPlan, q, k, v, o, lse, ws=None, stream=None):
     dt = _DTYPES[plan.dtype]
     w, wn = _ws(ws)
-    _check(_lib().ipttt_attention(
+    status = (_bound or _lib()).ipttt_attention(
         plan.ref, plan.dev, plan.scale, _heads(q, plan.q_shape, dt, "q"), _heads(k, plan.k_shape, dt, "k"),
         _heads(v, plan.k_shape, dt, "v"), _heads(o, plan.q_shape, dt, "o"),
-        _flat(lse, plan.lse_shape, torch.float32, "lse"), w, wn, _on(stream, q)), "ipttt_attention")
+        _flat(lse, plan.lse_shape, torch.float32, "lse"), w, wn,
+        _on(stream, q))
+    if status:
+        _check(status, "ipttt_attention")
 
 
 def ipttt_attention_backward(plan: AttentionPlan, q, k, v, o, lse, dO, dq, dk, dv, ws, stream=None):
     dt = _DTYPES[plan.dtype]
     w, wn = _ws(ws)
-    _check(_lib().ipttt_attention_backward(
+    status = (_bound or _lib()).ipttt_attention_backward(
         plan.ref, plan.dev, plan.scale, _heads(q, plan.q_shape, dt, "q"), _heads(k, plan.k_shape, dt, "k"),
         _heads(v, plan.k_shape, dt, "v"), _heads(o, plan.q_shape, dt, "o"),
         _flat(lse, plan.lse_shape, torch.float32, "lse"), _heads(dO, plan.q_shape, dt, "dO"),
         _heads(dq, plan.q_shape, dt, "dq"), _heads(dk, plan.k_shape, dt, "dk"), _heads(dv, plan.k_shape, dt, "dv"), w,
-        wn, _on(stream, q)), "ipttt_attention_backward")
+        wn,
+        _on(stream, q))
+    if status:
+        _check(status, "ipttt_attention_backward")

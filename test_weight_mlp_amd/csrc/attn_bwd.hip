@@ -150,6 +150,10 @@ __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kv
     constexpr int B = decltype(odd)::value;
     constexpr int NB = KT / 32;
     tiles_landed();
+    if (it.k_begin + st * KT >= row.any) {  // no row of this wave sees these keys
+      if (st + 1 < steps) load(st + 1, B ^ 1);
+      return;
+    }
     const char *kt = lds + 2 * B * TB, *vt = kt + TB;
     frag f[2][4], p[NB][GR::NP];
     floatx16 s[NB], dp[NB];

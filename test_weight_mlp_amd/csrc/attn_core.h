@@ -302,7 +302,7 @@ struct Row {
   int r, t, g;      // flat row, query, head of the group
   bool live;
   int lim;          // it sees keys below lim
-  int all;          // every row of the wave sees the keys below all
+  int all, any;     // every row of the wave sees the keys below all, none those from any on
   int t0;           // the wave's first query
 
   __device__ __forceinline__ Row(const RowItem& it, int G, int wave, int lane) {
@@ -315,6 +315,8 @@ struct Row {
     live = r < n_rows;
     lim = live ? min(it.off + t + 1, it.k_end) : 0;
     all = __builtin_amdgcn_readfirstlane(min(it.off + rm.t0 + 1, it.k_end));
+    any = __builtin_amdgcn_readfirstlane(
+        r0 < n_rows ? max(0, min(it.off + min(r0 + 31, n_rows - 1) / G + 1, it.k_end)) : 0);
   }
 };
 

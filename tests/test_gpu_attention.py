@@ -91,6 +91,9 @@ SHAPES = [
     (16, 8, 24, [4, 0, 6], [0, 5, 6]),               # no keys; no queries
     (3, 3, 104, [256], [256]),
     (8, 1, 64, [900, 3], [900, 3]),                  # dK, dV summed from several parts
+    (128, 1, 32, [3, 41], [3, 90]),                  # a token's heads fill several tiles
+    (2, 2, 128, [1, 300], [40, 300]),                # few rows over few keys beside many
+    (4, 1, 128, [600], [600]),                       # delta from the keys and from O
 ]
 
 
