@@ -1,15 +1,16 @@
 """The attention half of a block: binding of the per-head norm and position
 rotation of queries and keys, and of causal attention over packed sequences.
 
-Like the rest of the binding, these functions only marshal arguments.  Tensors
-of heads are [rows, heads, head_dim] with any row and head strides that are
-multiples of 8 (slices of a fused projection, caches of either order).
+Like the rest of the binding, these functions only marshal arguments, the
+launching ones through a small native module that checks every tensor's shape,
+type, device and strides (csrc/marshal.cpp).  Tensors of heads are [rows, heads,
+head_dim] with any row and head strides that are multiples of 8 (slices of a
+fused projection, caches of either order).
 """
 from __future__ import annotations
 
 import ctypes
 import math
-import struct
 from typing import Optional, Sequence
 
 import numpy as np
@@ -34,6 +35,7 @@ class _CAttnProblem(ctypes.Structure):
 
 
 _bound = None
+_calls = None
 
 
 def _lib() -> ctypes.CDLL:
@@ -42,12 +44,12 @@ def _lib() -> ctypes.CDLL:
     if _bound is None:
         lib = library()
         vp, f32, i32, sz = ctypes.c_void_p, ctypes.c_float, ctypes.c_int, ctypes.c_size_t
-        H = ctypes.c_char_p  # ipttt_heads, packed by _heads
+        H = ctypes.c_char_p  # ipttt_heads, packed
         Q, A = ctypes.POINTER(_CQKProblem), ctypes.POINTER(_CAttnProblem)
         sigs = {
             "ipttt_qk_norm_rope": (i32, [Q, H, H, vp, vp, vp, vp, H, H, H, H, vp, vp]),
-            "ipttt_qk_backward_workspace_bytes": (sz, [Q]),
             "ipttt_qk_norm_rope_backward": (i32, [Q, H, H, vp, vp, vp, vp, H, H, H, H, vp, vp, vp, sz, vp]),
+            "ipttt_qk_backward_workspace_bytes": (sz, [Q]),
             "ipttt_attn_validate": (i32, [A]),
             "ipttt_attn_plan_bytes": (sz, [A]),
             "ipttt_attn_plan": (i32, [A, vp, sz]),
@@ -63,31 +65,22 @@ def _lib() -> ctypes.CDLL:
     return _bound
 
 
-# Argument marshalling is most of a single-token call's time, so it looks at
-# each tensor once, in as few attribute reads as the checks need.
-
-_pack_heads = struct.Struct("Pqq").pack  # ipttt_heads: data, row_stride, head_stride
-
-
-def _heads(t: torch.Tensor, shape, dtype: torch.dtype, what: str) -> bytes:
-    """The ipttt_heads of a [rows, heads, head_dim] device tensor."""
-    if t.shape == shape and t.dtype is dtype and t.is_cuda:
-        row, head, one = t.stride()
-        if one == 1:
-            return _pack_heads(t.data_ptr(), row, head)
-    raise ValueError(f"{what} must be a {list(shape)} {dtype} device tensor with a contiguous last dimension, not "
-                     f"{list(t.shape)} {t.dtype} of strides {t.stride()} on {t.device}")
-
-
-def _flat(t: torch.Tensor, shape, dtype: torch.dtype, what: str) -> int:
-    if t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous():
-        return t.data_ptr()
-    raise ValueError(f"{what} must be a contiguous {list(shape)} {dtype} device tensor, not {list(t.shape)} "
-                     f"{t.dtype} on {t.device}")
-
-
-def _ws(ws: Optional[torch.Tensor]):
-    return (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
+def _native():
+    """The marshalling module, bound to the library's launching entry points; it
+    checks the tensors of a call and makes it."""
+    global _calls
+    if _calls is None:
+        lib = _lib()
+        try:
+            from . import _marshal
+        except ImportError as e:
+            raise RuntimeError("the binding's _marshal.so is missing: build it with "
+                               "`python -m test_weight_mlp_amd.build`") from e
+        _marshal.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
+                        for n in ("ipttt_qk_norm_rope", "ipttt_qk_norm_rope_backward", "ipttt_attention",
+                                  "ipttt_attention_backward")))
+        _calls = _marshal
+    return _calls
 
 
 _current = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream() without its wrapper object
@@ -95,7 +88,9 @@ _current = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream() wit
 
 def _on(stream, t: torch.Tensor) -> int:
     """The given stream, or the current one of the tensor's device."""
-    return _current(t.get_device()) if stream is None else stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return _current(t.get_device()) if t.is_cuda else 0
 
 
 # ------------------------------------------------------- norm and rotation
@@ -118,10 +113,7 @@ class QKProblem:
         self.out_rows = tokens if out_rows is None else out_rows
         self._c = _CQKProblem(tokens, heads, kv_heads, head_dim, table_rows, self.out_rows, dtype, eps)
         self.ref = ctypes.byref(self._c)
-        # the shapes that the calls check their tensors against
-        self.q_shape, self.k_shape = (tokens, heads, head_dim), (tokens, kv_heads, head_dim)
-        self.out_shape = (self.out_rows, kv_heads, head_dim)
-        self.w_shape, self.pos_shape, self.table_shape = (head_dim,), (tokens,), (table_rows, head_dim)
+        self.address = ctypes.addressof(self._c)
 
     @property
     def torch_dtype(self) -> torch.dtype:
@@ -132,17 +124,10 @@ def ipttt_qk_norm_rope(p: QKProblem, q, k, w_q, w_k, positions, table, q_out, k_
                        stream=None):
     """Norms and rotates q and k into q_out and k_out; with ``rows`` the keys (and
     v, if given) go to those rows of k_out (and v_out).  q_out may be q."""
-    dt = _DTYPES[p.dtype]
     if (v is None) != (v_out is None):
         raise ValueError("v and v_out go together")
-    status = (_bound or _lib()).ipttt_qk_norm_rope(
-        p.ref, _heads(q, p.q_shape, dt, "q"), _heads(k, p.k_shape, dt, "k"), _flat(w_q, p.w_shape, dt, "w_q"),
-        _flat(w_k, p.w_shape, dt, "w_k"), _flat(positions, p.pos_shape, torch.int32, "positions"),
-        _flat(table, p.table_shape, torch.float32, "table"), _heads(q_out, p.q_shape, dt, "q_out"),
-        _heads(k_out, p.out_shape, dt, "k_out"), None if v is None else _heads(v, p.k_shape, dt, "v"),
-        None if v is None else _heads(v_out, p.out_shape, dt, "v_out"),
-        None if rows is None else _flat(rows, p.pos_shape, torch.int32, "rows"),
-        _on(stream, q))
+    status = (_calls or _native()).qk(p.address, q, k, w_q, w_k, positions, table, q_out, k_out, v, v_out, rows,
+                                      _on(stream, q))
     if status:
         _check(status, "ipttt_qk_norm_rope")
 
@@ -165,15 +150,8 @@ class QKGrads:
 
 def ipttt_qk_norm_rope_backward(p: QKProblem, q, k, w_q, w_k, positions, table, dq_out, dk_out, dq, dk, dw_q, dw_k, ws,
                                 stream=None):
-    dt, f32 = _DTYPES[p.dtype], torch.float32
-    w, wn = _ws(ws)
-    status = (_bound or _lib()).ipttt_qk_norm_rope_backward(
-        p.ref, _heads(q, p.q_shape, dt, "q"), _heads(k, p.k_shape, dt, "k"), _flat(w_q, p.w_shape, dt, "w_q"),
-        _flat(w_k, p.w_shape, dt, "w_k"), _flat(positions, p.pos_shape, torch.int32, "positions"),
-        _flat(table, p.table_shape, f32, "table"), _heads(dq_out, p.q_shape, dt, "dq_out"),
-        _heads(dk_out, p.k_shape, dt, "dk_out"), _heads(dq, p.q_shape, dt, "dq"), _heads(dk, p.k_shape, dt, "dk"),
-        _flat(dw_q, p.w_shape, f32, "dw_q"), _flat(dw_k, p.w_shape, f32, "dw_k"), w, wn,
-        _on(stream, q))
+    status = (_calls or _native()).qk_backward(p.address, q, k, w_q, w_k, positions, table, dq_out, dk_out, dq, dk,
+                                               dw_q, dw_k, ws, _on(stream, q))
     if status:
         _check(status, "ipttt_qk_norm_rope_backward")
 
@@ -203,13 +181,12 @@ class AttentionPlan:
         self.q_rows = ends[0] if q_rows is None else q_rows
         self.k_rows = ends[1] if k_rows is None else k_rows
         self.scale = 1.0 / math.sqrt(head_dim) if scale is None else float(scale)
-        # the shapes that the calls check their tensors against
-        self.q_shape, self.k_shape = (self.q_rows, heads, head_dim), (self.k_rows, kv_heads, head_dim)
-        self.lse_shape = (self.q_rows, heads)
         P = ctypes.POINTER(ctypes.c_int64)
         c = _CAttnProblem(ql.size, heads, kv_heads, head_dim, self.q_rows, self.k_rows, dtype,
                           *(x.ctypes.data_as(P) for x in arrays))
         lib, ref = _lib(), ctypes.byref(c)
+        self._c, self._arrays = c, arrays  # the calls read the sizes
+        self.address = ctypes.addressof(c)
         _check(lib.ipttt_attn_validate(ref), "ipttt_attn_validate")
         n = int(lib.ipttt_attn_plan_bytes(ref))
         self._host = np.empty((n + 7) // 8, dtype=np.int64)
@@ -230,9 +207,10 @@ class AttentionBuffers:
     the backward too (one workspace serves both calls in turn)."""
 
     def __init__(self, plan: AttentionPlan, grads: bool = False, device="cuda"):
-        dt, q, k = plan.torch_dtype, plan.q_shape, plan.k_shape
+        dt, d = plan.torch_dtype, plan.head_dim
+        q, k = (plan.q_rows, plan.heads, d), (plan.k_rows, plan.kv_heads, d)
         self.o = torch.empty(q, dtype=dt, device=device)
-        self.lse = torch.empty(plan.lse_shape, dtype=torch.float32, device=device)
+        self.lse = torch.empty(q[:2], dtype=torch.float32, device=device)
         need = max(plan.workspace_bytes, plan.backward_workspace_bytes if grads else 0)
         self.ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
         self.dq = torch.empty(q, dtype=dt, device=device) if grads else None
@@ -241,26 +219,14 @@ class AttentionBuffers:
 
 
 def ipttt_attention(plan: AttentionPlan, q, k, v, o, lse, ws=None, stream=None):
-    dt = _DTYPES[plan.dtype]
-    w, wn = _ws(ws)
-    status = (_bound or _lib()).ipttt_attention(
-        plan.ref, plan.dev, plan.scale, _heads(q, plan.q_shape, dt, "q"), _heads(k, plan.k_shape, dt, "k"),
-        _heads(v, plan.k_shape, dt, "v"), _heads(o, plan.q_shape, dt, "o"),
-        _flat(lse, plan.lse_shape, torch.float32, "lse"), w, wn,
-        _on(stream, q))
+    status = (_calls or _native()).attention(plan.address, plan.ref, plan.dev, plan.scale, q, k, v, o, lse, ws,
+                                             _on(stream, q))
     if status:
         _check(status, "ipttt_attention")
 
 
 def ipttt_attention_backward(plan: AttentionPlan, q, k, v, o, lse, dO, dq, dk, dv, ws, stream=None):
-    dt = _DTYPES[plan.dtype]
-    w, wn = _ws(ws)
-    status = (_bound or _lib()).ipttt_attention_backward(
-        plan.ref, plan.dev, plan.scale, _heads(q, plan.q_shape, dt, "q"), _heads(k, plan.k_shape, dt, "k"),
-        _heads(v, plan.k_shape, dt, "v"), _heads(o, plan.q_shape, dt, "o"),
-        _flat(lse, plan.lse_shape, torch.float32, "lse"), _heads(dO, plan.q_shape, dt, "dO"),
-        _heads(dq, plan.q_shape, dt, "dq"), _heads(dk, plan.k_shape, dt, "dk"), _heads(dv, plan.k_shape, dt, "dv"), w,
-        wn,
-        _on(stream, q))
+    status = (_calls or _native()).attention_backward(plan.address, plan.ref, plan.dev, plan.scale, q, k, v, o, lse,
+                                                      dO, dq, dk, dv, ws, _on(stream, q))
     if status:
         _check(status, "ipttt_attention_backward")

@@ -68,7 +68,11 @@ def build(jobs: int = 8, verbose: bool = False, sanitize: bool = False) -> str:
     lib = SAN_LIB if sanitize else LIB
     os.makedirs(SAN_OBJDIR if sanitize else OBJDIR, exist_ok=True)
     with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, jobs)) as ex:
+        # the sanitized copy is loaded by the same marshalling module
+        marshal = None if sanitize else ex.submit(build_marshal, verbose)
         objs = list(ex.map(lambda src: _compile(src, sanitize), SOURCES))
+        if marshal is not None:
+            marshal.result()
     tmp = lib + ".tmp"
     cmd = [hipcc(), "-shared", "-fPIC", "--offload-arch=gfx950"] + (SANITIZE if sanitize else []) + \
         ["-o", tmp] + objs
@@ -79,6 +83,29 @@ def build(jobs: int = 8, verbose: bool = False, sanitize: bool = False) -> str:
     if verbose:
         print(f"built {lib}")
     return lib
+
+
+def build_marshal(verbose: bool = False) -> str:
+    """The binding's argument marshalling: host code only, against torch's
+    headers, for the interpreter that runs this."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+
+    out = os.path.join(HERE, "_marshal.so")
+    libs = [p for p in library_paths() if os.path.isdir(p)]
+    cmd = [shutil.which("g++") or "c++", "-O2", "-fPIC", "-shared", "-std=c++17", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f"-I{sysconfig.get_paths()['include']}"] + \
+        [f"-isystem{p}" for p in include_paths()] + [os.path.join(CSRC, "marshal.cpp"), "-o", out + ".tmp"] + \
+        [f"-L{p}" for p in libs] + ["-ltorch_python", "-ltorch_cpu", "-lc10"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{res.stderr}")
+    os.replace(out + ".tmp", out)
+    if verbose:
+        print(f"built {out}")
+    return out
 
 
 def sanitizer_runtime() -> str:

@@ -3,6 +3,7 @@ finite differences, the plan's tiles against the definition of what each query
 sees, and every refusal before anything is launched."""
 import ctypes
 import os
+import struct
 
 import numpy as np
 import pytest
@@ -210,7 +211,7 @@ def test_plan_buffer_is_checked():
 
 
 def _heads(data=256, row=256, head=64):
-    return at._pack_heads(data or 0, row, head)
+    return struct.pack("Pqq", data or 0, row, head)
 
 
 @needs_lib
@@ -280,11 +281,23 @@ def test_qk_refuses_before_any_launch():
     assert back(dq=_heads(4096, row=512)) == 8
 
 
+@needs_lib
 def test_binding_checks_tensors():
     import torch
-    x = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
-    for t, rows in ((x, 3), (x.float(), 3), (x, 4)):
-        with pytest.raises(ValueError):
-            at._heads(t, (rows, 4, 64), torch.bfloat16, "q")    # not on a device, another type, another shape
+    T, H, KV, D, N = 3, 4, 2, 64, 5
+    p = ip.QKProblem(T, H, KV, D, table_rows=N)
+
+    def qk(**bad):
+        a = dict(q=torch.zeros(T, H, D), k=torch.zeros(T, KV, D), w_q=torch.zeros(D), w_k=torch.zeros(D),
+                 positions=torch.zeros(T, dtype=torch.int32), table=torch.zeros(N, D), q_out=torch.zeros(T, H, D),
+                 k_out=torch.zeros(T, KV, D))
+        a = {n: x.bfloat16() if n not in ("positions", "table") else x for n, x in a.items()}
+        a.update(bad)
+        ip.ipttt_qk_norm_rope(p, **a)
+
+    with pytest.raises(ValueError, match=r"^q must be a \[3, 4, 64\] BFloat16 device tensor"):   # not on a device
+        qk()
+    with pytest.raises(ValueError, match="go together"):
+        qk(v=torch.zeros(T, KV, D))
     with pytest.raises(ValueError):
         ip.AttentionPlan(4, 2, 64, [1, 2], [1], device="cpu")

@@ -448,3 +448,42 @@ def test_norm_rope_position_outside_the_table_is_nan():
     torch.cuda.synchronize()
     for t in (qo, ko):
         assert bool(torch.isnan(t[1:3]).all()) and bool(torch.isfinite(t[[0, 3]]).all())
+
+
+# ------------------------------------------------------------------ binding
+
+def _without(t, how):
+    """t with one thing about it made wrong."""
+    return {"shape": lambda: t[:-1], "type": lambda: t.double(), "host": lambda: t.cpu(), "kind": lambda: [0.0],
+            "rank": lambda: t[None], "strides": lambda: torch.stack([t, t], -1)[..., 0]}[how]()
+
+
+@pytest.mark.parametrize("how", ["shape", "type", "host", "kind", "rank", "strides"])
+def test_binding_refuses_tensors(how):
+    """Every tensor of every call is checked: nothing is launched, and the message
+    names the tensor."""
+    T, H, KV, D, bf, dev = 4, 4, 2, 64, torch.bfloat16, "cuda"
+    z = lambda *s, t=bf: torch.zeros(s, dtype=t, device=dev)
+    p = ip.QKProblem(T, H, KV, D, table_rows=6)
+    plan = ip.AttentionPlan(H, KV, D, [T], [T])
+    base = dict(q=z(T, H, D), k=z(T, KV, D), w_q=z(D), w_k=z(D), positions=z(T, t=torch.int32),
+                table=z(6, D, t=torch.float32))
+    qk = dict(base, q_out=z(T, H, D), k_out=z(T, KV, D), v=z(T, KV, D), v_out=z(T, KV, D),
+              rows=torch.arange(T, dtype=torch.int32, device=dev))
+    g = ip.QKGrads(p)
+    back = dict(base, dq_out=z(T, H, D), dk_out=z(T, KV, D), dq=g.dq, dk=g.dk, dw_q=g.dw_q, dw_k=g.dw_k, ws=g.ws)
+    fwd = dict(q=z(T, H, D), k=z(T, KV, D), v=z(T, KV, D), o=z(T, H, D), lse=z(T, H, t=torch.float32))
+    b = ip.AttentionBuffers(plan, grads=True)
+    bwd = dict(fwd, dO=z(T, H, D), dq=b.dq, dk=b.dk, dv=b.dv, ws=b.ws)
+    here = torch.cuda.current_stream()
+    for call, args in ((lambda **a: ip.ipttt_qk_norm_rope(p, **a, stream=here), qk),
+                       (lambda **a: ip.ipttt_qk_norm_rope_backward(p, **a, stream=here), back),
+                       (lambda **a: ip.ipttt_attention(plan, **a, stream=here), fwd),
+                       (lambda **a: ip.ipttt_attention_backward(plan, **a, stream=here), bwd)):
+        call(**args)
+        for name, t in args.items():
+            if t is None or (name == "ws" and how in ("shape", "type", "rank")):   # any memory of enough bytes will do
+                continue
+            with pytest.raises(TypeError if how == "kind" else ValueError, match=rf"^{name} must be"):
+                call(**dict(args, **{name: _without(t, how)}))
+    torch.cuda.synchronize()
