@@ -76,7 +76,7 @@ struct Args {
   bool cut;               // tiles of the forward are cut into parts
   View q, k, v, o, dO, dq, dk, dv;
   float *lse;             // [q rows, heads]
-  float *nlse, *ndelta;   // same: -lse / scale (-inf on rows that see nothing), -delta
+  float *nlse, *ndelta;   // same: what is added to the scores (-inf on rows that see nothing), -delta
   float *part_o, *part_lse, *part_dq;
 };
 

@@ -24,15 +24,37 @@ namespace {
 // 256 keys, is 0.0049, 0.0027, 0.0025 with O and 0.0024, 0.0024, 0.0023 without.
 // Over whole sequences of 1k to 8k the bound of 512 keeps dQ within 1.5 times the
 // error of rounding it alone (1.41 to 1.43 without this term; bound 256: 1.51).
-constexpr int kExactDelta = 512;
+// fp32: where one probability is near 1, dP - delta is what dP's own rounding
+// leaves unless delta was made of the same dP and of P's that add up to 1 (sequences
+// of 9 tokens: dQ 1.0 times a plain fp32 form's error, 1.6 with O; of 120: 1.12 and
+// 1.18; one of 300 and one of 30 tokens, forward and backward: 53.6 us and 48.7).
+template <typename T>
+constexpr int kExactDelta = sizeof(T) == 2 ? 512 : 64;
 
-// -lse / scale and -delta of one tile of 128 flat rows, 32 a wave.
+// Where lse and delta are taken off.  bf16: the accumulators start at -lse / scale
+// and -delta, which costs no instruction.  fp32: after the products; sums that start
+// ten times as large as the score round ten times as coarsely at every step (dQ's
+// error against 64 bits, 2300 tokens of width 128: 1.1e-6, and 1.9e-6 from -lse /
+// scale; a plain fp32 form's 0.9e-6).
+template <typename T>
+struct Shift {
+  static constexpr bool kLate = sizeof(T) == 4;
+  // of a row, from its lse
+  static __device__ __forceinline__ float of(float lse, float scale) { return kLate ? -lse * kLog2e : -lse / scale; }
+  // P and dS of one element, from what the accumulators hold
+  static __device__ __forceinline__ float p(float s, float sl2, float shift) {
+    return __builtin_amdgcn_exp2f(kLate ? fmaf(s, sl2, shift) : s * sl2);
+  }
+  static __device__ __forceinline__ float ds(float p, float dp, float ndelta) { return p * (kLate ? dp + ndelta : dp); }
+};
+
+// The shift (Shift::of) and -delta of one tile of 128 flat rows, 32 a wave.
 template <typename T, int DP>
 __device__ __forceinline__ void delta_tile(const Args& a, const RowItem& it, int kvh, const char* __restrict__ K,
                                            const char* __restrict__ V, char* lds) {
   typedef Tile<T, DP> TL;
   typedef typename Elt<T>::frag frag;
-  constexpr int NW = 4, TB = TL::bytes(kKeys), EPL = Elt<T>::EPL;
+  constexpr int NW = 4, KT = sizeof(T) == 2 ? kKeys : kKeys / 2, TB = TL::bytes(KT), EPL = Elt<T>::EPL;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
   const int D = a.D;
   const Row row(it, a.G, wave, lane);
@@ -40,31 +62,32 @@ __device__ __forceinline__ void delta_tile(const Args& a, const RowItem& it, int
   float nlse = -INFINITY;
   if (row.live) {
     const float x = a.lse[at];
-    if (x != -INFINITY) nlse = -x / a.scale;
+    if (x != -INFINITY) nlse = Shift<T>::of(x, a.scale);
   }
   frag df[TL::STEPS];
   row_frags<T, DP>(a.dO, it, row, kvh, a.G, D, h, df);
   float delta = 0.0f;
-  if (sizeof(T) == 2 && it.k_end <= kExactDelta) {
+  if (it.k_end <= kExactDelta<T>) {
     frag qf[TL::STEPS];
     row_frags<T, DP>(a.q, it, row, kvh, a.G, D, h, qf);
     const float sl2 = a.scale * kLog2e;
     const At<T, DP> here(lane);
-    const RowStream<T, DP, NW, kKeys> ks(a.k.row, D, wave, lane), vs(a.v.row, D, wave, lane);
+    const RowStream<T, DP, NW, KT> ks(a.k.row, D, wave, lane), vs(a.v.row, D, wave, lane);
     auto load = [&](int key0, char* tile) {
       const int left = it.off + it.q_len - key0;
       ks.issue(K, (int64_t)it.k_start + key0, left, tile, wave);
       vs.issue(V, (int64_t)it.k_start + key0, left, tile + TB, wave);
     };
+    float l = 0.0f;
     if (it.k_end > 0) load(0, lds);
-    for (int key0 = 0, odd = 0; key0 < it.k_end; key0 += kKeys, odd ^= 1) {
+    for (int key0 = 0, odd = 0; key0 < it.k_end; key0 += KT, odd ^= 1) {
       const char* tile = lds + odd * 2 * TB;
       tiles_landed();
-      if (key0 + kKeys < it.k_end) load(key0 + kKeys, lds + (odd ^ 1) * 2 * TB);
-      floatx16 x[2], dp[2];
+      if (key0 + KT < it.k_end) load(key0 + KT, lds + (odd ^ 1) * 2 * TB);
+      floatx16 x[KT / 32], dp[KT / 32];
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        fill16(x[kb], nlse);
+      for (int kb = 0; kb < KT / 32; ++kb) {
+        fill16(x[kb], Shift<T>::kLate ? 0.0f : nlse);
         fill16(dp[kb], 0.0f);
 #pragma unroll
         for (int q = 0; q < TL::STEPS; ++q) {
@@ -73,12 +96,19 @@ __device__ __forceinline__ void delta_tile(const Args& a, const RowItem& it, int
         }
       }
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+      for (int kb = 0; kb < KT / 32; ++kb)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float p = __builtin_amdgcn_exp2f(x[kb][i] * sl2);
-          if (key0 + 32 * kb + 8 * (i >> 2) + 4 * h + (i & 3) < row.lim) delta = fmaf(p, dp[kb][i], delta);
+          const float p = Shift<T>::p(x[kb][i], sl2, nlse);
+          if (key0 + 32 * kb + 8 * (i >> 2) + 4 * h + (i & 3) < row.lim) {
+            delta = fmaf(p, dp[kb][i], delta);
+            l += p;
+          }
         }
+    }
+    if constexpr (Shift<T>::kLate) {  // P's sum is 1 only within lse's rounding; bf16's P are rounded anyhow
+      l = half_sum(l);
+      if (l > 0.0f) delta /= l;
     }
   } else {
     frag of[TL::STEPS];
@@ -97,7 +127,7 @@ __device__ __forceinline__ void delta_tile(const Args& a, const RowItem& it, int
 
 template <typename T, int DP>
 __global__ __launch_bounds__(256) void delta_kernel(Args a) {
-  __shared__ __attribute__((aligned(16))) char lds[sizeof(T) == 2 ? 4 * Tile<T, DP>::bytes(kKeys) : 16];
+  __shared__ __attribute__((aligned(16))) char lds[4 * Tile<T, DP>::bytes(sizeof(T) == 2 ? kKeys : kKeys / 2)];
   const int kvh = blockIdx.x % a.kv_heads;
   const RowItem it = static_cast<const RowItem*>(a.items)[blockIdx.x / a.kv_heads];
   delta_tile<T, DP>(a, it, kvh, static_cast<const char*>(a.k.p) + (int64_t)kvh * a.k.head * (int)sizeof(T),
@@ -106,8 +136,7 @@ __global__ __launch_bounds__(256) void delta_kernel(Args a) {
 
 // dQ of one tile of 128 flat rows, 32 a wave: over the keys the rows see,
 // S^T = K Q^T and dP^T = V dO^T, then dQ^T += K^T dS^T with K read transposed.
-// The scores' accumulators start at -lse / scale, dP's at -delta: what comes out
-// of the products is ready for the exponential and for dS = P (dP - delta).
+// bf16: what comes out of the products is ready for the exponential and for dS.
 template <typename T, int DP>
 __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kvh, const char* __restrict__ K,
                                         const char* __restrict__ V, char* lds) {
@@ -162,7 +191,7 @@ __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kv
     // dS of block b from its P and dP - delta
     auto grad = [&](int b) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[b][i] *= dp[b][i];
+      for (int i = 0; i < 16; ++i) s[b][i] = Shift<T>::ds(s[b][i], dp[b][i], ndelta);
       // a softmax over one key has no gradient: exactly 0, whatever rounding
       // put between dP and delta
       if (b == 0 && st == 0 && it.k_begin == 0 && row.all <= 1 && row.lim == 1) fill16(s[b], 0.0f);
@@ -171,8 +200,8 @@ __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kv
     };
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      start16(s[b], nlse);
-      start16(dp[b], ndelta);
+      start16(s[b], Shift<T>::kLate ? 0.0f : nlse);
+      start16(dp[b], Shift<T>::kLate ? 0.0f : ndelta);
 #pragma unroll
       for (int g = 0; g < H; ++g) {
         if (g + 1 < H) GR::rows(kt, here, 32 * b, g + 1, f[cur ^ 1]);
@@ -196,7 +225,7 @@ __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kv
         else if (b + 1 < NB) GR::rows(kt, here, 32 * (b + 1), 0, f[cur ^ 1]);
         else GR::cols(kt, here, 0, 0, f[cur ^ 1]);
 #pragma unroll
-        for (int i = g * (16 / H); i < (g + 1) * (16 / H); ++i) s[b][i] = __builtin_amdgcn_exp2f(s[b][i] * sl2);
+        for (int i = g * (16 / H); i < (g + 1) * (16 / H); ++i) s[b][i] = Shift<T>::p(s[b][i], sl2, nlse);
 #pragma unroll
         for (int x = 0; x < 4; ++x) dp[b] = Elt<T>::mma(f[cur][x], df[4 * g + x], dp[b]);
         cur ^= 1;
@@ -260,7 +289,7 @@ template <typename T, int DP>
 struct KeyTile {
   typedef Tile<T, DP> TL;
   static constexpr int RT = kBwdRows, TB = TL::bytes(RT), VB = TL::bytes(kBwdKeys);
-  static constexpr int STAT = VB + 4 * TB;           // [buffer][-lse / scale, -delta][row]
+  static constexpr int STAT = VB + 4 * TB;           // [buffer][shift, -delta][row]
   static constexpr int LDS = STAT + 2 * 2 * RT * 4;
 };
 
@@ -341,7 +370,7 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, (lds_ptr_t)(qt + blk * TL::PITCH), 16, ok ? oq : kOob, 0, 0, 0);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (lds_ptr_t)(qt + TB + blk * TL::PITCH), 16, ok ? od : kOob, 0, 0, 0);
     }
-    if (wave < 2) {  // -lse / scale by wave 0, -delta by wave 1, 32 lanes each
+    if (wave < 2) {  // the shift by wave 0, -delta by wave 1, 32 lanes each
       const __amdgpu_buffer_rsrc_t rs = rsrc_of((wave == 0 ? nlse : ndelta) + row * a.heads, kMaxBytes);
       int t, g;
       rm.of(lane & 31, &t, &g);
@@ -371,9 +400,14 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
     frag f[2][4];
     int cur = 0;
     GR::rows(qt, here, 0, 0, f[0]);
-    floatx16 s, dp;
-    row_stats(stat, h, s);
-    row_stats(stat + RT, h, dp);
+    floatx16 shift, ndelta;
+    row_stats(stat, h, shift);
+    row_stats(stat + RT, h, ndelta);
+    floatx16 s = shift, dp = ndelta;
+    if constexpr (Shift<T>::kLate) {
+      fill16(s, 0.0f);
+      fill16(dp, 0.0f);
+    }
     auto pair = [&](int g, frag(&x)[4]) {  // two fragments of dO, two of V
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -403,7 +437,7 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
       else GR::cols(ot, here, 0, 0, f[cur ^ 1]);
       constexpr int EX = 16 / (2 * H);
 #pragma unroll
-      for (int i = g * EX; i < (g + 1) * EX; ++i) s[i] = __builtin_amdgcn_exp2f(s[i] * sl2);
+      for (int i = g * EX; i < (g + 1) * EX; ++i) s[i] = Shift<T>::p(s[i], sl2, shift[i]);
 #pragma unroll
       for (int x = 0; x < 2; ++x) dp = Elt<T>::mma(f[cur][x], f[cur][2 + x], dp);
       cur ^= 1;
@@ -418,7 +452,7 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
       else GR::cols(qt, here, 0, 0, f[cur ^ 1]);
 #pragma unroll
       for (int i = g * (16 / H); i < (g + 1) * (16 / H); ++i)
-        dp[i] *= s[i];
+        dp[i] = Shift<T>::ds(s[i], dp[i], ndelta[i]);
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int y = 4 * g + x;

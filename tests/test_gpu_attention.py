@@ -450,6 +450,45 @@ def test_norm_rope_position_outside_the_table_is_nan():
         assert bool(torch.isnan(t[1:3]).all()) and bool(torch.isfinite(t[[0, 3]]).all())
 
 
+@pytest.mark.parametrize("heads,kv,dim,lens", [(6, 6, 80, [17, 3]), (32, 8, 128, [9]), (16, 8, 64, [40, 5]),
+                                               (8, 2, 128, [120]), (16, 8, 64, [300, 30]), (8, 1, 96, [700])])
+def test_fp32_gradients_are_as_near_as_the_plain_form(heads, kv, dim, lens):
+    """fp32 gradients, against the definition in 64 bits, are no more than twice as
+    far off (in the Frobenius norm) as the formulas in 32-bit torch operations: the
+    same roundings in another order differ by less, one rounding at a larger
+    magnitude by more."""
+    plan = ip.AttentionPlan(heads, kv, dim, lens, lens, dtype=ip.IPTTT_F32)
+    gen = torch.Generator(device="cuda").manual_seed(sum(lens) + dim)
+    n, G = sum(lens), heads // kv
+    q, do = (torch.randn(n, heads, dim, device="cuda", generator=gen) for _ in "ab")
+    k, v = (torch.randn(n, kv, dim, device="cuda", generator=gen) for _ in "ab")
+    b = ip.AttentionBuffers(plan, grads=True)
+    ip.ipttt_attention(plan, q, k, v, b.o, b.lse, b.ws)
+    ip.ipttt_attention_backward(plan, q, k, v, b.o, b.lse, do, b.dq, b.dk, b.dv, b.ws)
+
+    def plain(dtype):
+        dq, dk, dv = torch.zeros_like(q, dtype=dtype), torch.zeros_like(k, dtype=dtype), torch.zeros_like(v, dtype=dtype)
+        t0 = 0
+        for length in lens:
+            at = slice(t0, t0 + length)
+            t0 += length
+            hidden = torch.ones(length, length, dtype=torch.bool, device="cuda").triu(1)
+            for head in range(heads):
+                x, y, z, d = (t[at, i].to(dtype) for t, i in ((q, head), (k, head // G), (v, head // G), (do, head)))
+                w = torch.softmax((x @ y.T * plan.scale).masked_fill(hidden, -float("inf")), -1)
+                dw = d @ z.T
+                ds = w * (dw - (w * dw).sum(-1, keepdim=True)) * plan.scale
+                dq[at, head] = ds @ y
+                dk[at, head // G] += ds.T @ x
+                dv[at, head // G] += w.T @ d
+        return dq, dk, dv
+
+    for name, got, near, want in zip(("dq", "dk", "dv"), (b.dq, b.dk, b.dv), plain(torch.float32), plain(torch.float64)):
+        ours, theirs = ((t.double() - want).norm().item() for t in (got, near))
+        print(f"{name} {ours / want.norm().item():.2e} plain {theirs / want.norm().item():.2e}")
+        assert ours <= 2 * theirs, name
+
+
 # ------------------------------------------------------------------ binding
 
 def _without(t, how):
