@@ -84,7 +84,7 @@ __device__ __forceinline__ void few_tile(const Args& a, const RowItem& it, int k
     for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
     top = half_max(top) * sl2;
     if (__any(top > m + 8.0f)) {
-      const float mn = fmaxf(m, top), c = __builtin_amdgcn_exp2f(m - mn);
+      const float mn = top > m + 8.0f ? top : m, c = __builtin_amdgcn_exp2f(m - mn);
       m = mn;
       l *= c;
 #pragma unroll

@@ -120,7 +120,8 @@ __device__ __forceinline__ float largest(const floatx16 (&s)[NB]) {
 // Masks a step's scores (whose largest is top) and moves m up if a row's
 // maximum passed it by more than 2^8: sums and O are relative to m, exact for any
 // m near the maximum, so they are rescaled (one multiplication an element)
-// only then, which after the first few steps is rare.
+// only then, which after the first few steps is rare.  A row's own scores decide:
+// its result does not depend on the other rows of its wave.
 template <int NB, int DB>
 __device__ __forceinline__ void settle(floatx16 (&s)[NB], float top, int key0, const Row& row, float sl2,
                                        floatx16 (&o)[DB], float& m, float& l, int lane) {
@@ -134,7 +135,7 @@ __device__ __forceinline__ void settle(floatx16 (&s)[NB], float top, int key0, c
   }
   const float x = half_max(top) * sl2;
   if (__any(x > m + 8.0f)) {
-    const float mn = fmaxf(m, x), c = __builtin_amdgcn_exp2f(m - mn);
+    const float mn = x > m + 8.0f ? x : m, c = __builtin_amdgcn_exp2f(m - mn);
     m = mn;
     l *= c;
 #pragma unroll
