@@ -183,7 +183,7 @@ class AttentionPlan:
         self.scale = 1.0 / math.sqrt(head_dim) if scale is None else float(scale)
         P = ctypes.POINTER(ctypes.c_int64)
         c = _CAttnProblem(ql.size, heads, kv_heads, head_dim, self.q_rows, self.k_rows, dtype,
-                          *(x.ctypes.data_as(P) for x in arrays))
+                          *(P.from_buffer(ctypes.c_void_p(x.ctypes.data)) for x in arrays))
         lib, ref = _lib(), ctypes.byref(c)
         self._c, self._arrays = c, arrays  # the calls read the sizes
         self.address = ctypes.addressof(c)

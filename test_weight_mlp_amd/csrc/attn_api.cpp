@@ -97,8 +97,9 @@ int64_t key_steps(const ipttt_attn_problem* p, int64_t i, int64_t k0) {
   return div_up(p->q_len[i] * (p->heads / p->kv_heads) - key_rows(p, i, k0), kBwdRows);
 }
 
-// Workgroups that run at once: two a CU.
-constexpr int64_t kGroups = 512;
+constexpr int64_t kCus = 256;
+// Workgroups that run at once: two a CU (one, of fp32 tiles wider than 64).
+constexpr int64_t kGroups = 2 * kCus;
 
 // How far the tiles are cut into parts.
 struct Cut {
@@ -116,14 +117,80 @@ bool few_rows(const ipttt_attn_problem* p, const Cut& cut, int64_t i) {
   return fits_few(p, i) && !(cut.rows && p->k_len[i] <= 4 * kKeys);
 }
 
-// Forward: where there are fewer tiles than workgroups that run at once, they
-// share the keys of all tiles evenly; a part is at least a few steps long, so that
-// its join costs little beside it (fp32 steps take longer, and beside them a join is
-// cheap enough to cut a call's longest tiles however many tiles there are: 2000 and
-// 3000 tokens, 16 heads over 8 of width 64: 278 us uncut, 247; bf16, 2500 tokens: 62
-// uncut, 74 cut).  Few rows: only
-// reading matters, so parts are short enough that four rounds of workgroups even
-// out, but at least two blocks of 32 keys for each of a workgroup's two waves.
+// Whether the workgroups of a forward call are alone on their CUs.
+bool alone(const ipttt_attn_problem* p) { return p->dtype == IPTTT_F32 && p->head_dim > 64; }
+// Whether a call's workgroups all start at once, two on some CUs.  The second then
+// comes to a CU in the order of the first, so the shortest should meet the longest.
+bool folded(const ipttt_attn_problem* p, int64_t groups) { return !alone(p) && kCus < groups && groups <= kGroups; }
+
+// The most steps (of kKeys keys) of a part of a forward tile of many rows; kMaxInt
+// leaves every tile whole.  Two workgroups on a CU take about as long as one of both
+// lengths, so a call takes as long as the CU with the most steps, the longest
+// parts handed out first; a lone bf16 workgroup a tenth longer.  Of n-ths of the
+// longest tile and even shares of all work, the part is the one for which that ends
+// first, with some steps' time for each part's start and for a join, if any: 4 and
+// 12, fp32 (whose steps take longer) 1/2 and 3/2.  Calls of two tiles a CU and more (fp32: four) stay whole.  Over
+// 62 shapes of 32 to 900 tiles that is some 2 % above the best part of a sweep;
+// cutting wherever a workgroup had less than an even share of 512: 10 % (bf16) and 6 %
+// (fp32).  Heads 32 over 8 of width 128, 1000 tokens: whole 22 us, cut in shares 31;
+// 100 tokens over 16000: whole 240, cut 46.
+int64_t forward_part(const ipttt_attn_problem* p, const Cut& cut) {
+  const bool f32 = p->dtype == IPTTT_F32;
+  constexpr int64_t kMost = 4 * kCus;
+  const int64_t G = p->heads / p->kv_heads, copies = p->kv_heads;
+  const int64_t start = f32 ? 1 : 8, join = f32 ? 3 : 24, least = f32 ? 2 : 4;  // start and join in half steps
+  const int64_t whole = f32 ? kMost : kGroups, limit = f32 ? kMost : 3 * kCus;
+  const auto tiles = [&](auto&& f) {
+    for (int64_t i = 0; i < p->n_seqs; ++i) {
+      if (few_rows(p, cut, i)) continue;
+      for (int64_t r0 = 0; r0 < p->q_len[i] * G; r0 += kRows)
+        if (!f(div_up(tile_keys(p, i, r0, kRows), kKeys))) return;
+    }
+  };
+  int64_t longest = 0, work = 0, n = 0;
+  tiles([&](int64_t steps) {
+    longest = std::max(longest, steps);
+    work += steps * copies;
+    return (n += copies) < whole;
+  });
+  if (n >= whole) return kMaxInt;
+  int64_t best = INT64_MAX, part = kMaxInt;
+  for (int64_t nth : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128, 192, 256, -1, -2}) {
+    const int64_t most = nth > 0 ? std::max<int64_t>(1, div_up(longest, nth)) : div_up(work, -nth * kCus);
+    if (nth != 1 && (most < least || most >= longest)) continue;
+    int64_t size[kMost], load[kCus] = {}, sum = 0;
+    bool fits = true;
+    n = 0;  // parts of one key head
+    tiles([&](int64_t steps) {
+      for (; fits; steps -= most) {
+        fits = (n + 1) * copies <= limit;
+        if (fits) sum += size[n++] = start + 2 * std::min(steps, most);
+        if (steps <= most) break;
+      }
+      return fits;
+    });
+    if (!fits) continue;
+    std::sort(size, size + n, [](int64_t x, int64_t y) { return x > y; });
+    const int64_t total = n * copies, more = nth == 1 ? 0 : join;
+    if (n == 0 || std::max(sum * copies / kCus, size[0]) + more >= best) continue;  // it cannot be the one
+    for (int64_t i = 0; i < total;) {
+      std::sort(load, load + kCus);
+      for (int64_t j = 0; j < kCus && i < total; ++j, ++i) load[j] += size[i / copies];
+    }
+    int64_t time = *std::max_element(load, load + kCus);
+    // beyond two a CU the second comes to a CU in the order of the first
+    if (!alone(p) && total > kGroups) time = std::max(time, size[0] + size[kCus / copies]);
+    if (!f32 && total <= kCus) time += time / 10;
+    if (time + more >= best) continue;
+    best = time + more;
+    part = nth == 1 ? kMaxInt : most;
+  }
+  return part;
+}
+
+// Few rows: only reading matters, so parts are short enough that four rounds of
+// workgroups even out, but at least two blocks of 32 keys for each of a workgroup's
+// two waves.
 // Backward: the first keys of a causal sequence meet all its rows and the last
 // almost none, and a call's last workgroup ends it, so no tile of keys is longer
 // than what a workgroup gets on average (8k tokens, 32 heads over 8 of width 128:
@@ -136,25 +203,21 @@ Cut cut_of(const ipttt_attn_problem* p) {
   const int64_t G = p->heads / p->kv_heads;
   Cut c = {};
   for (int64_t i = 0; i < p->n_seqs; ++i) c.rows = c.rows || !fits_few(p, i);
-  int64_t tiles = 0, keys = 0, few = 0, bwd_tiles = 0, work = 0;
+  int64_t few = 0, bwd_tiles = 0, work = 0;
   for (int64_t i = 0; i < p->n_seqs; ++i) {
     if (few_rows(p, c, i)) few += p->k_len[i];
     for (int64_t r0 = 0; r0 < p->q_len[i] * G; r0 += kRows) {
       const int64_t n = tile_keys(p, i, r0, kRows);
       ++bwd_tiles;
       work += 3 * div_up(n, kKeys);
-      if (few_rows(p, c, i)) continue;
-      ++tiles;
-      keys += n;
     }
     for (int64_t k0 = 0; k0 < p->k_len[i]; k0 += kBwdKeys) {
       ++bwd_tiles;
       work += 2 * key_steps(p, i, k0);
     }
   }
-  c.keys = !f32 && tiles * p->kv_heads >= kGroups
-               ? kMaxInt
-               : div_up(std::max(least, div_up(keys * p->kv_heads, kGroups)), kKeys) * kKeys;
+  const int64_t part = forward_part(p, c);
+  c.keys = part == kMaxInt ? kMaxInt : part * kKeys;
   c.few = div_up(std::max(least_few, div_up(few * p->kv_heads, 4 * kGroups)), 64) * 64;
   const int64_t each = div_up(work * p->kv_heads, kGroups);
   c.steps = std::max(least_steps, div_up(each, 2));
@@ -478,6 +541,8 @@ ipttt_status ipttt_attn_plan(const ipttt_attn_problem* p, void* plan, size_t pla
     return x.q_start != y.q_start ? x.q_start < y.q_start : x.r0 != y.r0 ? x.r0 < y.r0 : x.k_begin < y.k_begin;
   };
   std::sort(rows - s.rows, rows, longer);
+  // (3900 tokens, 16 heads over 8 of width 64: 49.4 us without, 47.4; fp32 351 and 258)
+  if (folded(p, s.rows * p->kv_heads)) std::reverse(rows - s.rows + kCus / p->kv_heads, rows);
   std::sort(few - s.few, few, longer);
   std::sort(dq - s.dq, dq, longer);
   std::sort(key - s.key, key, [](const KeyItem& x, const KeyItem& y) {
