@@ -195,7 +195,9 @@ int64_t forward_part(const ipttt_attn_problem* p, const Cut& cut) {
 // almost none, and a call's last workgroup ends it, so no tile of keys is longer
 // than what a workgroup gets on average (8k tokens, 32 heads over 8 of width 128:
 // 1.70 ms uncut, 1.19 ms cut and joined); where workgroups would stay idle, tiles
-// of rows are cut alike.  A step of rows is 128 x 64 x 3 products, one of keys
+// of rows are cut alike, and those of keys in parts of 1.5 shares, which leaves fewer
+// (bf16, 1000 tokens: 66 us, 77 in even shares; 4000 tokens, whose tiles fill the
+// CUs: 513 and 462; fp32: even shares everywhere).  A step of rows is 128 x 64 x 3 products, one of keys
 // 32 x 128 x 4: three to two.
 Cut cut_of(const ipttt_attn_problem* p) {
   const bool f32 = p->dtype == IPTTT_F32;
@@ -220,8 +222,9 @@ Cut cut_of(const ipttt_attn_problem* p) {
   c.keys = part == kMaxInt ? kMaxInt : part * kKeys;
   c.few = div_up(std::max(least_few, div_up(few * p->kv_heads, 4 * kGroups)), 64) * 64;
   const int64_t each = div_up(work * p->kv_heads, kGroups);
-  c.steps = std::max(least_steps, div_up(each, 2));
-  c.dq = bwd_tiles * p->kv_heads >= kGroups ? kMaxInt : std::max(least, div_up(each, 3) * kKeys);
+  const bool some = bwd_tiles * p->kv_heads < kGroups;
+  c.steps = std::max(least_steps, div_up(some && !f32 ? 3 * each : 2 * each, 4));
+  c.dq = !some ? kMaxInt : std::max(least, div_up(each, 3) * kKeys);
   return c;
 }
 
