@@ -188,9 +188,33 @@ int64_t forward_part(const ipttt_attn_problem* p, const Cut& cut) {
   return part;
 }
 
-// Few rows: only reading matters, so parts are short enough that four rounds of
-// workgroups even out, but at least two blocks of 32 keys for each of a workgroup's
-// two waves.
+// The most keys of a part of few rows: a multiple of 64, a block of 32 for each of a
+// workgroup's two waves.  Only reading matters, and a second workgroup on a CU reads
+// no sooner than the first: the shortest parts that are no more than the CUs (one
+// token over 16000 keys, 8 key heads of width 128: 21.2 us in parts of 512, 32.8 of
+// 128).  A long sequence's are at least 128, as a join is longer for each (4000 keys
+// of one head: 10.8 us, 13.0 of 64).  Where that takes parts of more than 1024,
+// shares of 2048 workgroups, whose ends even out, but at least 512 keys (16 tokens
+// over 3000, 8 key heads of width 64: 26.3 us, 29.2 of 1024, 28.2 of 192).
+int64_t few_part(const ipttt_attn_problem* p, const Cut& cut) {
+  int64_t keys = 0, longest = 0;
+  for (int64_t i = 0; i < p->n_seqs; ++i) {
+    if (!few_rows(p, cut, i)) continue;
+    keys += p->k_len[i];
+    longest = std::max(longest, p->k_len[i]);
+  }
+  int64_t most = longest > 2048 ? 128 : 64;
+  const auto fits = [&] {
+    int64_t n = 0;
+    for (int64_t i = 0; i < p->n_seqs; ++i)
+      if (few_rows(p, cut, i)) n += div_up(p->k_len[i], most);
+    return n * p->kv_heads <= kCus;
+  };
+  while (most <= 1024 && !fits()) most += 64;
+  if (most > 1024) most = std::max<int64_t>(512, div_up(div_up(keys * p->kv_heads, 4 * kGroups), 64) * 64);
+  return most;
+}
+
 // Backward: the first keys of a causal sequence meet all its rows and the last
 // almost none, and a call's last workgroup ends it, so no tile of keys is longer
 // than what a workgroup gets on average (8k tokens, 32 heads over 8 of width 128:
@@ -201,13 +225,12 @@ int64_t forward_part(const ipttt_attn_problem* p, const Cut& cut) {
 // 32 x 128 x 4: three to two.
 Cut cut_of(const ipttt_attn_problem* p) {
   const bool f32 = p->dtype == IPTTT_F32;
-  const int64_t least = (f32 ? 2 : 4) * kKeys, least_few = 128, least_steps = f32 ? 4 : 8;
+  const int64_t least = (f32 ? 2 : 4) * kKeys, least_steps = f32 ? 4 : 8;
   const int64_t G = p->heads / p->kv_heads;
   Cut c = {};
   for (int64_t i = 0; i < p->n_seqs; ++i) c.rows = c.rows || !fits_few(p, i);
-  int64_t few = 0, bwd_tiles = 0, work = 0;
+  int64_t bwd_tiles = 0, work = 0;
   for (int64_t i = 0; i < p->n_seqs; ++i) {
-    if (few_rows(p, c, i)) few += p->k_len[i];
     for (int64_t r0 = 0; r0 < p->q_len[i] * G; r0 += kRows) {
       const int64_t n = tile_keys(p, i, r0, kRows);
       ++bwd_tiles;
@@ -220,7 +243,7 @@ Cut cut_of(const ipttt_attn_problem* p) {
   }
   const int64_t part = forward_part(p, c);
   c.keys = part == kMaxInt ? kMaxInt : part * kKeys;
-  c.few = div_up(std::max(least_few, div_up(few * p->kv_heads, 4 * kGroups)), 64) * 64;
+  c.few = few_part(p, c);
   const int64_t each = div_up(work * p->kv_heads, kGroups);
   const bool some = bwd_tiles * p->kv_heads < kGroups;
   c.steps = std::max(least_steps, div_up(some && !f32 ? 3 * each : 2 * each, 4));
