@@ -17,19 +17,25 @@ namespace ipttt {
 namespace attn {
 namespace {
 
-// Rows that see at most this many keys get delta = sum_j P dP from the keys
+// Rows that see at most so many keys get delta = sum_j P dP from the keys
 // themselves (one pass more over them); the others from the forward's O.  In
 // bf16, O's rounding (2^-9 of it) goes into delta, and it is not small beside dP
 // while O averages few values: dQ's error against 64 bits, random data of 2, 64 and
 // 256 keys, is 0.0049, 0.0027, 0.0025 with O and 0.0024, 0.0024, 0.0023 without.
-// Over whole sequences of 1k to 8k the bound of 512 keeps dQ within 1.5 times the
-// error of rounding it alone (1.41 to 1.43 without this term; bound 256: 1.51).
+// Over whole sequences these bounds keep dQ within 1.5 times the error of rounding it
+// alone, 1.41 to 1.45 of which are dS's and its own rounding (sequences of 333 to 1999
+// tokens of width 64: 1.50 with a bound of 512, 1.46 of 1024, 1.45 of 2048; 1500 of
+// width 128: 1.48 of 512, 1.45 of 1024), and this part short beside the rest (the same
+// sequences, forward and backward: 107, 115 and 129 us).  Narrow heads average fewer
+// roundings in delta and need more.
 // fp32: where one probability is near 1, dP - delta is what dP's own rounding
 // leaves unless delta was made of the same dP and of P's that add up to 1 (sequences
 // of 9 tokens: dQ 1.0 times a plain fp32 form's error, 1.6 with O; of 120: 1.12 and
 // 1.18; one of 300 and one of 30 tokens, forward and backward: 53.6 us and 48.7).
 template <typename T>
-constexpr int kExactDelta = sizeof(T) == 2 ? 512 : 64;
+__device__ __forceinline__ int exact_delta_keys(int D) {
+  return sizeof(T) == 4 ? 64 : max(768, 73728 / D);
+}
 
 // Where lse and delta are taken off.  bf16: the accumulators start at -lse / scale
 // and -delta, which costs no instruction.  fp32: after the products; sums that start
@@ -67,7 +73,7 @@ __device__ __forceinline__ void delta_tile(const Args& a, const RowItem& it, int
   frag df[TL::STEPS];
   row_frags<T, DP>(a.dO, it, row, kvh, a.G, D, h, df);
   float delta = 0.0f;
-  if (it.k_end <= kExactDelta<T>) {
+  if (it.k_end <= exact_delta_keys<T>(D)) {
     frag qf[TL::STEPS];
     row_frags<T, DP>(a.q, it, row, kvh, a.G, D, h, qf);
     const float sl2 = a.scale * kLog2e;
