@@ -133,7 +133,7 @@ __device__ __forceinline__ void delta_tile(const Args& a, const RowItem& it, int
 
 // Bound by reading O and dO once (8192 tokens, 32 heads of width 128: 26 us, 5.1 TB/s),
 // where rows see few keys by the products (4 sequences of 333 to 1999 tokens, 16
-// heads over 8 of width 64: 15 us).
+// heads over 8 of width 64: 24 us).
 template <typename T, int DP>
 __global__ __launch_bounds__(256) void delta_kernel(Args a) {
   __shared__ __attribute__((aligned(16))) char lds[4 * Tile<T, DP>::bytes(sizeof(T) == 2 ? kKeys : kKeys / 2)];
