@@ -26,7 +26,7 @@ namespace {
 // alone, 1.41 to 1.45 of which are dS's and its own rounding (sequences of 333 to 1999
 // tokens of width 64: 1.50 with a bound of 512, 1.46 of 1024, 1.45 of 2048; 1500 of
 // width 128: 1.48 of 512, 1.45 of 1024), and this part short beside the rest (the same
-// sequences, forward and backward: 107, 115 and 129 us).  Narrow heads average fewer
+// sequences, forward and backward: 107, 114 and 129 us).  Narrow heads average fewer
 // roundings in delta and need more.
 // fp32: where one probability is near 1, dP - delta is what dP's own rounding
 // leaves unless delta was made of the same dP and of P's that add up to 1 (sequences
@@ -84,7 +84,7 @@ __device__ __forceinline__ void delta_tile(const Args& a, const RowItem& it, int
       ks.issue(K, (int64_t)it.k_start + key0, left, tile, wave);
       vs.issue(V, (int64_t)it.k_start + key0, left, tile + TB, wave);
     };
-    float l = 0.0f;
+    float l = 0.0f, sum[4] = {};
     if (it.k_end > 0) load(0, lds);
     for (int key0 = 0, odd = 0; key0 < it.k_end; key0 += KT, odd ^= 1) {
       const char* tile = lds + odd * 2 * TB;
@@ -101,17 +101,23 @@ __device__ __forceinline__ void delta_tile(const Args& a, const RowItem& it, int
           dp[kb] = Elt<T>::mma(TL::row(tile + TB, here.row, 32 * kb, q), df[q], dp[kb]);
         }
       }
+      if (key0 + KT > row.all) {
+#pragma unroll
+        for (int kb = 0; kb < KT / 32; ++kb)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (key0 + 32 * kb + 8 * (i >> 2) + 4 * h + (i & 3) >= row.lim) x[kb][i] = -INFINITY;
+      }
 #pragma unroll
       for (int kb = 0; kb < KT / 32; ++kb)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const float p = Shift<T>::p(x[kb][i], sl2, nlse);
-          if (key0 + 32 * kb + 8 * (i >> 2) + 4 * h + (i & 3) < row.lim) {
-            delta = fmaf(p, dp[kb][i], delta);
-            l += p;
-          }
+          sum[i & 3] = fmaf(p, dp[kb][i], sum[i & 3]);
+          l += p;
         }
     }
+    delta = (sum[0] + sum[1]) + (sum[2] + sum[3]);
     if constexpr (Shift<T>::kLate) {  // P's sum is 1 only within lse's rounding; bf16's P are rounded anyhow
       l = half_sum(l);
       if (l > 0.0f) delta /= l;
@@ -131,9 +137,9 @@ __device__ __forceinline__ void delta_tile(const Args& a, const RowItem& it, int
   }
 }
 
-// Bound by reading O and dO once (8192 tokens, 32 heads of width 128: 26 us, 5.1 TB/s),
+// Bound by reading O and dO once (8192 tokens, 32 heads of width 128: 29 us, 4.6 TB/s),
 // where rows see few keys by the products (4 sequences of 333 to 1999 tokens, 16
-// heads over 8 of width 64: 24 us).
+// heads over 8 of width 64: 22 us).
 template <typename T, int DP>
 __global__ __launch_bounds__(256) void delta_kernel(Args a) {
   __shared__ __attribute__((aligned(16))) char lds[4 * Tile<T, DP>::bytes(sizeof(T) == 2 ? kKeys : kKeys / 2)];
