@@ -58,7 +58,7 @@ struct PlanHeader {
   int32_t n_tiles, o_tiles;  // tiles of rows, uncut
   int32_t n_dq_join, o_dq_join, dq_parts;
   int32_t rows_cut;          // whether tiles of many rows are cut into parts
-  int32_t pad;
+  int32_t longest;           // most keys of a sequence
 };
 static_assert(sizeof(PlanHeader) == 128, "plan header");
 constexpr int32_t kMagic = 0x41545031;
@@ -74,6 +74,7 @@ struct Args {
   const void *items, *dq_items;  // device
   int n_items, n_dq;
   bool cut;               // tiles of the forward are cut into parts
+  bool twice;             // P and dS of the backward in two terms
   View q, k, v, o, dO, dq, dk, dv;
   float *lse;             // [q rows, heads]
   float *nlse, *ndelta;   // same: what is added to the scores (-inf on rows that see nothing), -delta

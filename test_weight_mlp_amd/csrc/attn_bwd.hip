@@ -152,7 +152,7 @@ __global__ __launch_bounds__(256) void delta_kernel(Args a) {
 // dQ of one tile of 128 flat rows, 32 a wave: over the keys the rows see,
 // S^T = K Q^T and dP^T = V dO^T, then dQ^T += K^T dS^T with K read transposed.
 // bf16: what comes out of the products is ready for the exponential and for dS.
-template <typename T, int DP>
+template <typename T, int DP, bool TWICE>
 __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kvh, const char* __restrict__ K,
                                         const char* __restrict__ V, char* lds) {
   typedef Tile<T, DP> TL;
@@ -199,7 +199,7 @@ __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kv
       return;
     }
     const char *kt = lds + 2 * B * TB, *vt = kt + TB;
-    frag f[2][4], p[NB][GR::NP];
+    frag f[2][4], p[NB][GR::NP], p2[NB][GR::NP];
     floatx16 s[NB], dp[NB];
     int cur = 0;
     GR::rows(kt, here, 0, 0, f[0]);
@@ -211,7 +211,10 @@ __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kv
       // put between dP and delta
       if (b == 0 && st == 0 && it.k_begin == 0 && row.all <= 1 && row.lim == 1) fill16(s[b], 0.0f);
 #pragma unroll
-      for (int j = 0; j < GR::NP; ++j) p[b][j] = pack<T>(s[b], j * EPL);
+      for (int j = 0; j < GR::NP; ++j) {
+        p[b][j] = pack<T>(s[b], j * EPL);
+        if constexpr (TWICE) p2[b][j] = rest<T>(s[b], j * EPL, p[b][j]);
+      }
     };
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -258,6 +261,7 @@ __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kv
         for (int x = 0; x < 4; ++x) {
           const int y = 4 * g + x;
           acc[y % DB] = Elt<T>::mma(f[cur][x], p[b][y / DB], acc[y % DB]);
+          if constexpr (TWICE) acc[y % DB] = Elt<T>::mma(f[cur][x], p2[b][y / DB], acc[y % DB]);
         }
         if (b + 1 < NB && g == 0) grad(b + 1);
         cur ^= 1;
@@ -318,7 +322,7 @@ __device__ __forceinline__ void row_stats(const float* x, int h, floatx16& c) {
   }
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool TWICE>
 __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int kvh, const char* __restrict__ Q,
                                          const char* __restrict__ dO, const float* __restrict__ nlse,
                                          const float* __restrict__ ndelta, const char* __restrict__ K,
@@ -458,9 +462,12 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
       cur ^= 1;
       __builtin_amdgcn_sched_barrier(0);
     }
-    frag p[GR::NP], d[GR::NP];
+    frag p[GR::NP], d[GR::NP], p2[GR::NP], d2[GR::NP];
 #pragma unroll
-    for (int j = 0; j < GR::NP; ++j) p[j] = pack<T>(s, j * EPL);
+    for (int j = 0; j < GR::NP; ++j) {
+      p[j] = pack<T>(s, j * EPL);
+      if constexpr (TWICE) p2[j] = rest<T>(s, j * EPL, p[j]);
+    }
 #pragma unroll
     for (int g = 0; g < H; ++g) {
       if (g + 1 < H) GR::cols(ot, here, 0, g + 1, f[cur ^ 1]);
@@ -472,6 +479,7 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
       for (int x = 0; x < 4; ++x) {
         const int y = 4 * g + x;
         dv[y % DB] = Elt<T>::mma(f[cur][x], p[y / DB], dv[y % DB]);
+        if constexpr (TWICE) dv[y % DB] = Elt<T>::mma(f[cur][x], p2[y / DB], dv[y % DB]);
       }
       cur ^= 1;
       __builtin_amdgcn_sched_barrier(0);
@@ -483,7 +491,10 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
         if (r0 + 8 * (i >> 2) + 4 * h + (i & 3) < one_row) dp[i] = 0.0f;
     }
 #pragma unroll
-    for (int j = 0; j < GR::NP; ++j) d[j] = pack<T>(dp, j * EPL);
+    for (int j = 0; j < GR::NP; ++j) {
+      d[j] = pack<T>(dp, j * EPL);
+      if constexpr (TWICE) d2[j] = rest<T>(dp, j * EPL, d[j]);
+    }
 #pragma unroll
     for (int g = 0; g < H; ++g) {
       if (g + 1 < H) GR::cols(qt, here, 0, g + 1, f[cur ^ 1]);
@@ -491,6 +502,7 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
       for (int x = 0; x < 4; ++x) {
         const int y = 4 * g + x;
         dk[y % DB] = Elt<T>::mma(f[cur][x], d[y / DB], dk[y % DB]);
+        if constexpr (TWICE) dk[y % DB] = Elt<T>::mma(f[cur][x], d2[y / DB], dk[y % DB]);
       }
       cur ^= 1;
       __builtin_amdgcn_sched_barrier(0);
@@ -537,8 +549,9 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
 // Bound by the matrix cores at the clock that the card's power allows: 8192 tokens,
 // 32 heads over 8 of width 128: 1.70 ms, 1.13 PFLOP/s of its seven products, matrix
 // cores 57 % busy at 1.88 GHz.
-template <typename T, int DP>
-__global__ __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2) void bwd_kernel(Args a) {
+// TWICE: P and dS go into the products as two bf16 each, 16 bits in all.
+template <typename T, int DP, bool TWICE = false>
+__global__ __launch_bounds__(256, sizeof(T) == 4 || TWICE ? 1 : 2) void bwd_kernel(Args a) {
   constexpr int ES = sizeof(T), DQ = 4 * Tile<T, DP>::bytes(ES == 2 ? kKeys : kKeys / 2);
   __shared__ __attribute__((aligned(16))) char lds[KeyTile<T, DP>::LDS > DQ ? KeyTile<T, DP>::LDS : DQ];
   const int kvh = blockIdx.x % a.kv_heads, i = blockIdx.x / a.kv_heads;
@@ -546,10 +559,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2) void bwd_kernel(Args a
   const char* V = static_cast<const char*>(a.v.p) + (int64_t)kvh * a.v.head * ES;
   if (i < a.n_items) {
     const int64_t q = (int64_t)kvh * a.G;
-    dkv_tile<T, DP>(a, static_cast<const KeyItem*>(a.items)[i], kvh, static_cast<const char*>(a.q.p) + q * a.q.head * ES,
+    dkv_tile<T, DP, TWICE>(a, static_cast<const KeyItem*>(a.items)[i], kvh, static_cast<const char*>(a.q.p) + q * a.q.head * ES,
                     static_cast<const char*>(a.dO.p) + q * a.dO.head * ES, a.nlse + q, a.ndelta + q, K, V, lds);
   } else {
-    dq_tile<T, DP>(a, static_cast<const RowItem*>(a.dq_items)[i - a.n_items], kvh, K, V, lds);
+    dq_tile<T, DP, TWICE>(a, static_cast<const RowItem*>(a.dq_items)[i - a.n_items], kvh, K, V, lds);
   }
 }
 
@@ -611,7 +624,9 @@ hipError_t launch_delta(const Args& a, hipStream_t st) {
 hipError_t launch_backward(const Args& a, hipStream_t st) {
   const dim3 grid((unsigned)((a.n_items + a.n_dq) * a.kv_heads));
   note_launch("attn_bwd", st);
-  if (a.dtype == 1 && a.D <= 64) bwd_kernel<bf16, 64><<<grid, 256, 0, st>>>(a);
+  if (a.twice && a.D <= 64) bwd_kernel<bf16, 64, true><<<grid, 256, 0, st>>>(a);
+  else if (a.twice) bwd_kernel<bf16, 128, true><<<grid, 256, 0, st>>>(a);
+  else if (a.dtype == 1 && a.D <= 64) bwd_kernel<bf16, 64><<<grid, 256, 0, st>>>(a);
   else if (a.dtype == 1) bwd_kernel<bf16, 128><<<grid, 256, 0, st>>>(a);
   else if (a.D <= 64) bwd_kernel<float, 64><<<grid, 256, 0, st>>>(a);
   else bwd_kernel<float, 128><<<grid, 256, 0, st>>>(a);

@@ -229,6 +229,15 @@ struct RowStream {
   }
 };
 
+// What that rounding left of them, rounded in turn.
+template <typename T>
+__device__ __forceinline__ typename Elt<T>::frag rest(const floatx16& x, int i0, const typename Elt<T>::frag& p) {
+  typename Elt<T>::frag r;
+#pragma unroll
+  for (int i = 0; i < Elt<T>::EPL; ++i) r[i] = (T)(x[i0 + i] - (float)p[i]);
+  return r;
+}
+
 // Waits until at most N of this wave's vector-memory operations are pending.
 template <int N>
 __device__ __forceinline__ void loads_pending() {

@@ -489,6 +489,26 @@ def test_fp32_gradients_are_as_near_as_the_plain_form(heads, kv, dim, lens):
         assert ours <= 2 * theirs, name
 
 
+@pytest.mark.parametrize("heads,kv,dim,lens", [(2, 1, 32, [3]), (32, 8, 128, [9]), (16, 8, 64, [2, 5, 1]), (5, 5, 64, [30]),
+                                               (8, 1, 128, [4, 32]), (6, 6, 80, [12])])
+def test_bf16_gradients_of_short_sequences(heads, kv, dim, lens):
+    """Few probabilities do not average their roundings, so calls of short sequences
+    round P and dS to 16 bits: what is left, in the Frobenius norm, is the gradients'
+    own rounding to bf16, here within a quarter of it."""
+    q, k, v, do = draw(BF16, heads, kv, dim, lens, lens, seed=sum(lens))
+    plan = ip.AttentionPlan(heads, kv, dim, lens, lens)
+    b = ip.AttentionBuffers(plan, grads=True)
+    ip.ipttt_attention(plan, q, k, v, b.o, b.lse, b.ws)
+    ip.ipttt_attention_backward(plan, q, k, v, b.o, b.lse, do, b.dq, b.dk, b.dv, b.ws)
+    torch.cuda.synchronize()
+    want = oa.attention_backward(*(np64(t) for t in (q, k, v, do)), seqs_of(lens, lens), plan.scale)
+    for name, got, w in zip(("dq", "dk", "dv"), (b.dq, b.dk, b.dv), want):
+        own = np64(torch.from_numpy(w).to(torch.bfloat16)) - w
+        ratio = np.linalg.norm(np64(got) - w) / np.linalg.norm(own)
+        print(f"{name} {ratio:.3f}")
+        assert ratio <= 1.25, name
+
+
 # ------------------------------------------------------------------ binding
 
 def _without(t, how):
