@@ -8,7 +8,7 @@
 // for each other until their results are joined at the end; ranges of one tile
 // are joined by the join kernel.  32 sequences' next tokens over up to 16000 keys, 8
 // key heads of width 128 (949 MB): 171 us, 5.5 TB/s; one over 4097 keys, where the
-// chain of one load after the other counts: 6.3 us.  Four waves a workgroup: equal.
+// chain of one load after the other counts: 7.1 us.  Four waves a workgroup: equal.
 #include "attn_core.h"
 #include "attn.h"
 #include "launch.h"
