@@ -129,11 +129,11 @@ bool folded(const ipttt_attn_problem* p, int64_t groups) { return !alone(p) && k
 // parts handed out first; a lone bf16 workgroup a tenth longer.  Of n-ths of the
 // longest tile and even shares of all work, the part is the one for which that ends
 // first, with some steps' time for each part's start and for a join, if any: 4 and
-// 12, fp32 (whose steps take longer) 1/2 and 3/2.  Calls of two tiles a CU and more (fp32: four) stay whole.  Over
-// 62 shapes of 32 to 900 tiles that is some 2 % above the best part of a sweep;
-// cutting wherever a workgroup had less than an even share of 512: 10 % (bf16) and 6 %
-// (fp32).  Heads 32 over 8 of width 128, 1000 tokens: whole 22 us, cut in shares 31;
-// 100 tokens over 16000: whole 240, cut 46.
+// 12, fp32 (whose steps take longer) 1/2 and 3/2.  Calls of two tiles a CU and more
+// (fp32: four) stay whole.  Over 62 shapes of 32 to 900 tiles that is some 2 % above
+// the best part of a sweep; cutting wherever a workgroup had less than an even share
+// of 512: 10 % (bf16) and 6 % (fp32).  Heads 32 over 8 of width 128, 1000 tokens: whole
+// 22 us, cut in shares 31; 100 tokens over 16000: whole 240, cut 46.
 int64_t forward_part(const ipttt_attn_problem* p, const Cut& cut) {
   const bool f32 = p->dtype == IPTTT_F32;
   constexpr int64_t kMost = 4 * kCus;
