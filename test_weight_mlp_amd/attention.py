@@ -193,7 +193,6 @@ class AttentionPlan:
         self.ref = self._host.ctypes.data
         _check(lib.ipttt_attn_plan(ref, self.ref, n), "ipttt_attn_plan")
         self.table = torch.from_numpy(self._host).to(device)
-        self.dev = self.table.data_ptr()
         self.workspace_bytes = int(lib.ipttt_attn_workspace_bytes(self.ref))
         self.backward_workspace_bytes = int(lib.ipttt_attn_backward_workspace_bytes(self.ref))
 
@@ -219,14 +218,14 @@ class AttentionBuffers:
 
 
 def ipttt_attention(plan: AttentionPlan, q, k, v, o, lse, ws=None, stream=None):
-    status = (_calls or _native()).attention(plan.address, plan.ref, plan.dev, plan.scale, q, k, v, o, lse, ws,
+    status = (_calls or _native()).attention(plan.address, plan.ref, plan.scale, plan.table, q, k, v, o, lse, ws,
                                              _on(stream, q))
     if status:
         _check(status, "ipttt_attention")
 
 
 def ipttt_attention_backward(plan: AttentionPlan, q, k, v, o, lse, dO, dq, dk, dv, ws, stream=None):
-    status = (_calls or _native()).attention_backward(plan.address, plan.ref, plan.dev, plan.scale, q, k, v, o, lse,
+    status = (_calls or _native()).attention_backward(plan.address, plan.ref, plan.scale, plan.table, q, k, v, o, lse,
                                                       dO, dq, dk, dv, ws, _on(stream, q))
     if status:
         _check(status, "ipttt_attention_backward")

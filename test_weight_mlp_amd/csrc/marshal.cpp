@@ -77,6 +77,20 @@ class Reader {
     }
     return flat(what, a, 0, type);
   }
+  // the plan's copy on the device
+  const void* plan_table() {
+    const at::Tensor* t = next("the plan's table");
+    if (t == nullptr) return nullptr;
+    if (!t->is_cuda() || !t->is_contiguous()) {
+      PyErr_SetString(PyExc_ValueError,
+                      c10::str("the plan's table must be a contiguous device tensor, not on ", t->device(),
+                               ": build the plan with the device of the call's tensors")
+                          .c_str());
+      ok_ = false;
+      return nullptr;
+    }
+    return t->data_ptr();
+  }
   // a workspace: None or any contiguous device tensor
   void* workspace(size_t* bytes) {
     *bytes = 0;
@@ -207,15 +221,16 @@ PyObject* qk_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// attention(problem address, plan address, device plan, scale, q, k, v, o, lse, ws, stream)
+// attention(problem address, plan address, scale, plan table, q, k, v, o, lse, ws, stream)
 PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     if (!arity(n, 11, reinterpret_cast<const void*>(g_attn))) return nullptr;
     const ipttt_attn_problem* p = pointer<const ipttt_attn_problem>(a[0]);
-    const void *plan = pointer<void>(a[1]), *dev = pointer<void>(a[2]);
-    const float scale = (float)PyFloat_AsDouble(a[3]);
+    const void* plan = pointer<void>(a[1]);
+    const float scale = (float)PyFloat_AsDouble(a[2]);
     if (p == nullptr || PyErr_Occurred() != nullptr) return nullptr;
-    Reader r(a + 4, p->dtype);
+    Reader r(a + 3, p->dtype);
+    const void* dev = r.plan_table();
     ipttt_heads q, k, v, o;
     r.heads("q", p->q_rows, p->heads, p->head_dim, &q);
     r.heads("k", p->k_rows, p->kv_heads, p->head_dim, &k);
@@ -232,15 +247,16 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// attention_backward(problem address, plan address, device plan, scale, q, k, v, o, lse, dO, dq, dk, dv, ws, stream)
+// attention_backward(problem address, plan address, scale, plan table, q, k, v, o, lse, dO, dq, dk, dv, ws, stream)
 PyObject* attention_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     if (!arity(n, 15, reinterpret_cast<const void*>(g_attn_bwd))) return nullptr;
     const ipttt_attn_problem* p = pointer<const ipttt_attn_problem>(a[0]);
-    const void *plan = pointer<void>(a[1]), *dev = pointer<void>(a[2]);
-    const float scale = (float)PyFloat_AsDouble(a[3]);
+    const void* plan = pointer<void>(a[1]);
+    const float scale = (float)PyFloat_AsDouble(a[2]);
     if (p == nullptr || PyErr_Occurred() != nullptr) return nullptr;
-    Reader r(a + 4, p->dtype);
+    Reader r(a + 3, p->dtype);
+    const void* dev = r.plan_table();
     ipttt_heads q, k, v, o, dO, dq, dk, dv;
     r.heads("q", p->q_rows, p->heads, p->head_dim, &q);
     r.heads("k", p->k_rows, p->kv_heads, p->head_dim, &k);
