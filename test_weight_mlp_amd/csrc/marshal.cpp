@@ -32,7 +32,8 @@ const at::Tensor* tensor(PyObject* o, const char* what) {
 }
 
 // The arguments of one call, read in order; ok() is false, with a Python error
-// set, once one of them did not fit.
+// set, once one of them did not fit.  All tensors of a call are on the device of
+// its first.
 class Reader {
  public:
   Reader(PyObject* const* args, int32_t dtype) : args_(args), dtype_(dtype) {}
@@ -47,6 +48,7 @@ class Reader {
       fail(*t, what, " device tensor with a contiguous last dimension", {rows, heads, dim}, type_of(dtype_));
       return;
     }
+    if (!here(*t, what)) return;
     *h = ipttt_heads{t->data_ptr(), t->stride(0), t->stride(1)};
   }
   // the same, or None
@@ -68,7 +70,7 @@ class Reader {
       fail(*t, what, " contiguous device tensor", {shape, b == 0 ? 1u : 2u}, type);
       return nullptr;
     }
-    return t->data_ptr();
+    return here(*t, what) ? t->data_ptr() : nullptr;
   }
   void* maybe_flat(const char* what, int64_t a, at::ScalarType type) {
     if (!ok_ || *args_ == Py_None) {
@@ -89,7 +91,7 @@ class Reader {
       ok_ = false;
       return nullptr;
     }
-    return t->data_ptr();
+    return here(*t, "the plan's table") ? t->data_ptr() : nullptr;
   }
   // a workspace: None or any contiguous device tensor
   void* workspace(size_t* bytes) {
@@ -105,6 +107,7 @@ class Reader {
       ok_ = false;
       return nullptr;
     }
+    if (!here(*t, "ws")) return nullptr;
     *bytes = t->nbytes();
     return t->data_ptr();
   }
@@ -117,6 +120,16 @@ class Reader {
     ok_ = t != nullptr;
     return t;
   }
+  bool here(const at::Tensor& t, const char* what) {
+    const auto device = t.get_device();
+    if (device_ < 0) device_ = device;
+    if (device == device_) return true;
+    PyErr_SetString(PyExc_ValueError,
+                    c10::str(what, " must be on device ", (int)device_, " like the call's first tensor, not on ", t.device())
+                        .c_str());
+    ok_ = false;
+    return false;
+  }
   void fail(const at::Tensor& t, const char* what, const char* kind, at::IntArrayRef shape, at::ScalarType type) {
     PyErr_SetString(PyExc_ValueError,
                     c10::str(what, " must be a ", shape, " ", type, kind, ", not ", t.sizes(), " ", t.scalar_type(),
@@ -126,6 +139,7 @@ class Reader {
   }
   PyObject* const* args_;
   int32_t dtype_;
+  int64_t device_ = -1;
   bool ok_ = true;
 };
 

@@ -4,6 +4,7 @@ import os
 
 import pytest
 import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
 
 import test_weight_mlp_amd as ip
 
@@ -22,3 +23,42 @@ def test_binding_refuses_a_plan_that_is_not_on_the_device():
         ip.ipttt_attention(plan, q, k, k, b.o, b.lse, b.ws)
     with pytest.raises(ValueError, match="^the plan's table must be a contiguous device tensor"):
         ip.ipttt_attention_backward(plan, q, k, k, b.o, b.lse, q, b.dq, b.dk, b.dv, b.ws)
+
+
+class _Stream:
+    cuda_stream = 0
+
+
+def _calls(device):
+    """Every launching call with its tensors on a device that need not be there:
+    tensors without memory, whose null pointers the C entries refuse."""
+    T, H, KV, D = 4, 4, 2, 64
+    p = ip.QKProblem(T, H, KV, D, table_rows=6)
+    plan = ip.AttentionPlan(H, KV, D, [T], [T], device="cpu")
+    with FakeTensorMode():
+        def z(*s, t=torch.bfloat16):
+            return torch.zeros(s, dtype=t, device=device)
+
+        f32, i32, u8 = torch.float32, torch.int32, torch.uint8
+        table = torch.zeros(plan.table.shape, dtype=plan.table.dtype, device=device)
+        base = dict(q=z(T, H, D), k=z(T, KV, D), w_q=z(D), w_k=z(D), positions=z(T, t=i32), table=z(6, D, t=f32))
+        qk = dict(base, q_out=z(T, H, D), k_out=z(T, KV, D), v=z(T, KV, D), v_out=z(T, KV, D), rows=z(T, t=i32))
+        back = dict(base, dq_out=z(T, H, D), dk_out=z(T, KV, D), dq=z(T, H, D), dk=z(T, KV, D), dw_q=z(D, t=f32),
+                    dw_k=z(D, t=f32), ws=z(1 << 20, t=u8))
+        fwd = dict(q=z(T, H, D), k=z(T, KV, D), v=z(T, KV, D), o=z(T, H, D), lse=z(T, H, t=f32), ws=z(1 << 20, t=u8))
+        bwd = dict(fwd, dO=z(T, H, D), dq=z(T, H, D), dk=z(T, KV, D), dv=z(T, KV, D))
+    plan.table = table
+    return [(lambda a: ip.ipttt_qk_norm_rope(p, **a, stream=_Stream), qk),
+            (lambda a: ip.ipttt_qk_norm_rope_backward(p, **a, stream=_Stream), back),
+            (lambda a: ip.ipttt_attention(plan, **a, stream=_Stream), fwd),
+            (lambda a: ip.ipttt_attention_backward(plan, **a, stream=_Stream), bwd)]
+
+
+@needs_lib
+@pytest.mark.filterwarnings("ignore")
+def test_binding_refuses_tensors_of_two_devices():
+    for (call, args), (_, others) in zip(_calls("cuda:0"), _calls("cuda:1")):
+        for name in args:
+            first = "k" if name == "q" and "w_q" in args else name     # the call's first tensor is not the odd one
+            with pytest.raises(ValueError, match=rf"^{first} must be on device"):
+                call(dict(args, **{name: others[name]}))
