@@ -407,7 +407,8 @@ typedef struct {
  *             that token t's key goes to.  A row outside [0, out_rows) drops
  *             that token's key; rows given twice get one of the two.
  *   v, v_out  NULL, or v [tokens, kv_heads, D] copied to the same rows of
- *             v_out [out_rows, kv_heads, D]
+ *             v_out [out_rows, kv_heads, D]; v_out may be v (same data and strides,
+ *             no rows)
  * One launch. */
 ipttt_status ipttt_qk_norm_rope(const ipttt_qk_problem *p, const ipttt_heads *q, const ipttt_heads *k,
                                 const void *w_q, const void *w_k, const int32_t *positions,

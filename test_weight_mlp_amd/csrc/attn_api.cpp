@@ -493,6 +493,7 @@ ipttt_status ipttt_qk_norm_rope(const ipttt_qk_problem* p, const ipttt_heads* q,
   // an output over its input has to be that input, row for row
   if (a.q_out.p == a.q.p && !same(a.q_out, a.q)) return IPTTT_ERR_ARG;
   if (a.k_out.p == a.k.p && (rows != nullptr || !same(a.k_out, a.k))) return IPTTT_ERR_ARG;
+  if (v != nullptr && a.v_out.p == a.v.p && (rows != nullptr || !same(a.v_out, a.v))) return IPTTT_ERR_ARG;
   a.rows = rows;
   return hip_status(ipttt::launch_qk(a, static_cast<hipStream_t>(stream)));
 }

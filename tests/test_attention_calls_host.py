@@ -1,12 +1,15 @@
 """Host checks of the attention half's calls and plans (no GPU): what the binding
 and the C entries refuse, and what a plan may not depend on."""
+import ctypes
 import os
+import struct
 
 import pytest
 import torch
 from torch._subclasses.fake_tensor import FakeTensorMode
 
 import test_weight_mlp_amd as ip
+from test_weight_mlp_amd import attention as at
 
 needs_lib = pytest.mark.skipif(not os.path.exists(ip.library_path), reason="libipttt.so not built")
 
@@ -62,3 +65,19 @@ def test_binding_refuses_tensors_of_two_devices():
             first = "k" if name == "q" and "w_q" in args else name     # the call's first tensor is not the odd one
             with pytest.raises(ValueError, match=rf"^{first} must be on device"):
                 call(dict(args, **{name: others[name]}))
+
+
+def _heads(data, row=128, head=64):
+    return struct.pack("Pqq", data, row, head)
+
+
+@needs_lib
+@pytest.mark.parametrize("v_out,rows", [(_heads(4096), 256), (_heads(4096, row=256), None),
+                                        (_heads(4096, head=192), None)], ids=["rows", "row stride", "head stride"])
+def test_values_over_themselves_are_refused_unless_row_for_row(v_out, rows):
+    """Other waves' rows are still to be read while this one's are written."""
+    c = at._CQKProblem(10, 4, 2, 64, 9, 10, ip.IPTTT_BF16, 1e-6)
+    ptr = ctypes.c_void_p
+    assert at._lib().ipttt_qk_norm_rope(ctypes.byref(c), _heads(256, row=256), _heads(512), ptr(256), ptr(256), ptr(256),
+                                        ptr(256), _heads(1024, row=256), _heads(2048), _heads(4096), v_out, ptr(rows),
+                                        None) == 8
