@@ -405,7 +405,8 @@ typedef struct {
  *   rows      NULL (token t's key goes to row t: out_rows >= tokens), or
  *             [tokens] int32 (device): the row of k_out, such as a cache's,
  *             that token t's key goes to.  A row outside [0, out_rows) drops
- *             that token's key; rows given twice get one of the two.
+ *             that token's key and value.  A row given twice is left with a
+ *             mix of the tokens' heads that may differ from run to run.
  *   v, v_out  NULL, or v [tokens, kv_heads, D] copied to the same rows of
  *             v_out [out_rows, kv_heads, D]; v_out may be v (same data and strides,
  *             no rows)
