@@ -112,9 +112,10 @@ struct Cut {
 
 // A sequence of few rows: the kernel for them reads the keys with every wave.
 // Over few keys it is worth no launch of its own beside the tiles of many rows.
+// One without queries (a pool's idle slot) has no rows and no part in the forward.
 bool fits_few(const ipttt_attn_problem* p, int64_t i) { return p->q_len[i] * (p->heads / p->kv_heads) <= kFewRows; }
 bool few_rows(const ipttt_attn_problem* p, const Cut& cut, int64_t i) {
-  return fits_few(p, i) && !(cut.rows && p->k_len[i] <= 4 * kKeys);
+  return p->q_len[i] > 0 && fits_few(p, i) && !(cut.rows && p->k_len[i] <= 4 * kKeys);
 }
 
 // Whether the workgroups of a forward call are alone on their CUs.
@@ -274,7 +275,7 @@ void walk(const ipttt_attn_problem* p, const Cut& cut, Rows&& rows, FewRows&& fe
                      (int32_t)slot});
     };
     const bool is_few = few_rows(p, cut, i);
-    if (p->q_len[i] > 0 && is_few) tile(0, tile_keys(p, i, 0, kFewRows), cut.few, 1, slots, few, join);
+    if (is_few) tile(0, tile_keys(p, i, 0, kFewRows), cut.few, 1, slots, few, join);
     for (int64_t r0 = 0; r0 < p->q_len[i] * G; r0 += kRows) {
       const int64_t n = tile_keys(p, i, r0, kRows);
       tiles(RowItem{qs, ql, (int32_t)r0, ks, off, 0, (int32_t)n, -1});

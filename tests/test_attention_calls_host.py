@@ -9,6 +9,7 @@ import torch
 from torch._subclasses.fake_tensor import FakeTensorMode
 
 import test_weight_mlp_amd as ip
+from test_attention_host import Plan
 from test_weight_mlp_amd import attention as at
 
 needs_lib = pytest.mark.skipif(not os.path.exists(ip.library_path), reason="libipttt.so not built")
@@ -81,3 +82,18 @@ def test_values_over_themselves_are_refused_unless_row_for_row(v_out, rows):
     assert at._lib().ipttt_qk_norm_rope(ctypes.byref(c), _heads(256, row=256), _heads(512), ptr(256), ptr(256), ptr(256),
                                         ptr(256), _heads(1024, row=256), _heads(2048), _heads(4096), v_out, ptr(rows),
                                         None) == 8
+
+
+def _beside_idle(ql, kl, dt):
+    """The plan of these sequences, and with a pool's idle slots after them."""
+    idle = 31
+    return (Plan(ip.AttentionPlan(32, 8, 128, q, k, dt, device="cpu"))
+            for q, k in ((ql, kl), (ql + [0] * idle, kl + [16000] * idle)))
+
+
+@needs_lib
+@pytest.mark.parametrize("dt", [ip.IPTTT_BF16, ip.IPTTT_F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("ql,kl", [([1], [4097]), ([1, 2, 1], [700, 5000, 64]), ([1, 900], [4000, 900])])
+def test_sequences_without_queries_do_not_change_the_forward_of_others(ql, kl, dt):
+    alone, beside = _beside_idle(ql, kl, dt)
+    assert beside.few == alone.few and beside.rows == alone.rows and beside.join == alone.join
