@@ -232,6 +232,7 @@ Cut cut_of(const ipttt_attn_problem* p) {
   for (int64_t i = 0; i < p->n_seqs; ++i) c.rows = c.rows || !fits_few(p, i);
   int64_t bwd_tiles = 0, work = 0;
   for (int64_t i = 0; i < p->n_seqs; ++i) {
+    if (p->q_len[i] == 0) continue;  // its keys' tiles only write zeros
     for (int64_t r0 = 0; r0 < p->q_len[i] * G; r0 += kRows) {
       const int64_t n = tile_keys(p, i, r0, kRows);
       ++bwd_tiles;

@@ -97,3 +97,14 @@ def _beside_idle(ql, kl, dt):
 def test_sequences_without_queries_do_not_change_the_forward_of_others(ql, kl, dt):
     alone, beside = _beside_idle(ql, kl, dt)
     assert beside.few == alone.few and beside.rows == alone.rows and beside.join == alone.join
+
+
+@needs_lib
+@pytest.mark.parametrize("dt", [ip.IPTTT_BF16, ip.IPTTT_F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("ql,kl", [([1000], [1000]), ([300, 41], [300, 90])])
+def test_sequences_without_queries_do_not_change_the_backward_of_others(ql, kl, dt):
+    """Their keys' tiles only write zeros, and fill no CU."""
+    alone, beside = _beside_idle(ql, kl, dt)
+    assert beside.dq == alone.dq and beside.dq_join == alone.dq_join and beside.key_join == alone.key_join
+    assert [x for x in beside.key if x["q_len"] > 0] == alone.key
+    assert len(beside.key) == len(alone.key) + 31 * 125
