@@ -366,8 +366,8 @@ ipttt_status ipttt_z_backward_saved(const ipttt_problem *p, const void *H, const
  * and key heads, and causal attention with grouped heads.  fp32 arithmetic
  * (fp32 data: fp32 matrix products), outputs rounded to dtype once; inside
  * the attention the probabilities and their gradients are rounded to dtype
- * (in the backward of short calls to 16 bits) once more, as operands of the
- * matrix cores. */
+ * once more, as operands of the matrix cores (in bf16's backward, for
+ * sequences of at most 32 keys, to 16 bits). */
 
 /* A [rows, heads, head_dim] tensor of dtype on the device: element (r, h, i)
  * at data[r * row_stride + h * head_stride + i].  Slices of a fused projection

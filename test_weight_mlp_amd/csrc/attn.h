@@ -15,6 +15,7 @@ constexpr int kFewRows = 32;    // most rows of a sequence that the kernel of fe
 constexpr int kPartRows = 32;   // rows of a slot of partial results (a forward tile takes kRows / kPartRows of them)
 constexpr int kBwdKeys = 128;   // keys of a dK, dV tile
 constexpr int kBwdRows = 32;    // rows of one step of it
+constexpr int kShortKeys = 32;  // most keys of a sequence whose bf16 gradients take P and dS in two terms
 
 // One forward (or dQ) tile: rows [r0, min(r0 + tile rows, q_len * G)) of one
 // sequence over keys [k_begin, k_end) of it.  Query t sees keys below off + t + 1.
@@ -58,7 +59,7 @@ struct PlanHeader {
   int32_t n_tiles, o_tiles;  // tiles of rows, uncut
   int32_t n_dq_join, o_dq_join, dq_parts;
   int32_t rows_cut;          // whether tiles of many rows are cut into parts
-  int32_t longest;           // most keys of a sequence
+  int32_t shorts;            // whether a sequence with queries has at most kShortKeys keys
 };
 static_assert(sizeof(PlanHeader) == 128, "plan header");
 constexpr int32_t kMagic = 0x41545031;
@@ -71,10 +72,10 @@ struct View {             // [rows, heads, D] with element strides
 struct Args {
   int dtype, heads, kv_heads, G, D;
   float scale;
+  bool shorts;            // sequences of at most kShortKeys keys are among those of the backward
   const void *items, *dq_items;  // device
   int n_items, n_dq;
   bool cut;               // tiles of the forward are cut into parts
-  bool twice;             // P and dS of the backward in two terms
   View q, k, v, o, dO, dq, dk, dv;
   float *lse;             // [q rows, heads]
   float *nlse, *ndelta;   // same: what is added to the scores (-inf on rows that see nothing), -delta

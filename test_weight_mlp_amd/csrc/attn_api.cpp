@@ -18,6 +18,7 @@ using ipttt::attn::kKeys;
 using ipttt::attn::kPartRows;
 using ipttt::attn::kMagic;
 using ipttt::attn::kRows;
+using ipttt::attn::kShortKeys;
 using ipttt::attn::PlanHeader;
 using ipttt::attn::RowItem;
 using ipttt::attn::View;
@@ -607,8 +608,8 @@ ipttt_status ipttt_attn_plan(const ipttt_attn_problem* p, void* plan, size_t pla
   h->o_few = (int32_t)s.o_few;
   h->join_rows = (int32_t)s.join_rows;
   h->rows_cut = s.rows_cut;
-  h->longest = 0;
-  for (int64_t i = 0; i < p->n_seqs; ++i) h->longest = std::max(h->longest, (int32_t)p->k_len[i]);
+  h->shorts = 0;
+  for (int64_t i = 0; i < p->n_seqs; ++i) h->shorts |= p->q_len[i] > 0 && p->k_len[i] <= kShortKeys;
   h->n_join = (int32_t)s.join;
   h->n_dq = (int32_t)s.dq;
   h->n_key = (int32_t)s.key;
@@ -706,13 +707,7 @@ ipttt_status ipttt_attention_backward(const void* plan, const void* plan_dev, fl
     a.n_items = h->n_key;
     a.dq_items = dev + h->o_dq;
     a.n_dq = h->n_dq;
-    // A few probabilities, each in many elements of a gradient, do not average their
-    // roundings (3 tokens: dQ 1.7 times the error of
-    // rounding it alone; in two terms 1.0).  Two terms cost a call of no more
-    // workgroups than CUs little (9 tokens, 32 heads over 8 of width 128, forward and
-    // backward: 16.1 and 17.1 us; 64 tokens, which do average them: 28.9 and 32.2).
-    a.twice = h->dtype == IPTTT_BF16 && h->longest <= 32 &&
-              ((int64_t)h->n_key + h->n_dq) * h->kv_heads <= kCus;
+    a.shorts = h->shorts != 0;
     IPTTT_TRY(hip_status(ipttt::attn::launch_backward(a, st)));
   }
   if (h->n_dq_join + h->n_key_join == 0) return IPTTT_OK;

@@ -37,6 +37,14 @@ __device__ __forceinline__ int exact_delta_keys(int D) {
   return sizeof(T) == 4 ? 64 : max(768, 73728 / D);
 }
 
+// Whether a sequence's P and dS go into bf16's products as two terms each, 16 bits in
+// all: a few probabilities, each in many elements of a gradient, do not average their
+// roundings (3 tokens: dQ 1.7 times the error of rounding it alone; in two terms 1.0).
+// The sequence's own keys decide, whatever it is packed with (forward and backward, 32
+// heads over 8 of width 128, in one term and two: 100 sequences of 9 tokens 44 and 45
+// us, 400 of 30 tokens 258 and 274).
+__device__ __forceinline__ bool short_keys(int k_len) { return k_len <= kShortKeys; }
+
 // Where lse and delta are taken off.  bf16: the accumulators start at -lse / scale
 // and -delta, which costs no instruction.  fp32: after the products; sums that start
 // ten times as large as the score round ten times as coarsely at every step (dQ's
@@ -152,7 +160,7 @@ __global__ __launch_bounds__(256) void delta_kernel(Args a) {
 // dQ of one tile of 128 flat rows, 32 a wave: over the keys the rows see,
 // S^T = K Q^T and dP^T = V dO^T, then dQ^T += K^T dS^T with K read transposed.
 // bf16: what comes out of the products is ready for the exponential and for dS.
-template <typename T, int DP, bool TWICE>
+template <typename T, int DP, bool SHORT, bool TWICE>
 __device__ __forceinline__ void dq_tile(const Args& a, const RowItem& it, int kvh, const char* __restrict__ K,
                                         const char* __restrict__ V, char* lds) {
   typedef Tile<T, DP> TL;
@@ -322,7 +330,7 @@ __device__ __forceinline__ void row_stats(const float* x, int h, floatx16& c) {
   }
 }
 
-template <typename T, int DP, bool TWICE>
+template <typename T, int DP, bool SHORT, bool TWICE>
 __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int kvh, const char* __restrict__ Q,
                                          const char* __restrict__ dO, const float* __restrict__ nlse,
                                          const float* __restrict__ ndelta, const char* __restrict__ K,
@@ -549,9 +557,12 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
 // Bound by the matrix cores at the clock that the card's power allows: 8192 tokens,
 // 32 heads over 8 of width 128: 1.70 ms, 1.13 PFLOP/s of its seven products, matrix
 // cores 57 % busy at 1.88 GHz.
-// TWICE: P and dS go into the products as two bf16 each, 16 bits in all.
-template <typename T, int DP, bool TWICE = false>
-__global__ __launch_bounds__(256, sizeof(T) == 4 || TWICE ? 1 : 2) void bwd_kernel(Args a) {
+// SHORT: sequences of few keys, whose P and dS go in two terms, are among them; at
+// width 128 both kinds of tile together do not fit a wave's registers (8192 tokens,
+// forward and backward: 2.10 ms, with a sequence of 12 beside them 2.14).  (Its tiles
+// have SHORT as a parameter too: hipcc's host pass takes one use of each.)
+template <typename T, int DP, bool SHORT = false>
+__global__ __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2) void bwd_kernel(Args a) {
   constexpr int ES = sizeof(T), DQ = 4 * Tile<T, DP>::bytes(ES == 2 ? kKeys : kKeys / 2);
   __shared__ __attribute__((aligned(16))) char lds[KeyTile<T, DP>::LDS > DQ ? KeyTile<T, DP>::LDS : DQ];
   const int kvh = blockIdx.x % a.kv_heads, i = blockIdx.x / a.kv_heads;
@@ -559,10 +570,25 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 || TWICE ? 1 : 2) void bwd_kern
   const char* V = static_cast<const char*>(a.v.p) + (int64_t)kvh * a.v.head * ES;
   if (i < a.n_items) {
     const int64_t q = (int64_t)kvh * a.G;
-    dkv_tile<T, DP, TWICE>(a, static_cast<const KeyItem*>(a.items)[i], kvh, static_cast<const char*>(a.q.p) + q * a.q.head * ES,
-                    static_cast<const char*>(a.dO.p) + q * a.dO.head * ES, a.nlse + q, a.ndelta + q, K, V, lds);
+    const char* Q = static_cast<const char*>(a.q.p) + q * a.q.head * ES;
+    const char* dO = static_cast<const char*>(a.dO.p) + q * a.dO.head * ES;
+    const KeyItem it = static_cast<const KeyItem*>(a.items)[i];
+    if constexpr (SHORT) {
+      if (short_keys(it.off + it.q_len)) {
+        dkv_tile<T, DP, SHORT, true>(a, it, kvh, Q, dO, a.nlse + q, a.ndelta + q, K, V, lds);
+        return;
+      }
+    }
+    dkv_tile<T, DP, SHORT, false>(a, it, kvh, Q, dO, a.nlse + q, a.ndelta + q, K, V, lds);
   } else {
-    dq_tile<T, DP, TWICE>(a, static_cast<const RowItem*>(a.dq_items)[i - a.n_items], kvh, K, V, lds);
+    const RowItem it = static_cast<const RowItem*>(a.dq_items)[i - a.n_items];
+    if constexpr (SHORT) {
+      if (short_keys(it.off + it.q_len)) {
+        dq_tile<T, DP, SHORT, true>(a, it, kvh, K, V, lds);
+        return;
+      }
+    }
+    dq_tile<T, DP, SHORT, false>(a, it, kvh, K, V, lds);
   }
 }
 
@@ -624,9 +650,9 @@ hipError_t launch_delta(const Args& a, hipStream_t st) {
 hipError_t launch_backward(const Args& a, hipStream_t st) {
   const dim3 grid((unsigned)((a.n_items + a.n_dq) * a.kv_heads));
   note_launch("attn_bwd", st);
-  if (a.twice && a.D <= 64) bwd_kernel<bf16, 64, true><<<grid, 256, 0, st>>>(a);
-  else if (a.twice) bwd_kernel<bf16, 128, true><<<grid, 256, 0, st>>>(a);
+  if (a.dtype == 1 && a.D <= 64 && a.shorts) bwd_kernel<bf16, 64, true><<<grid, 256, 0, st>>>(a);
   else if (a.dtype == 1 && a.D <= 64) bwd_kernel<bf16, 64><<<grid, 256, 0, st>>>(a);
+  else if (a.dtype == 1 && a.shorts) bwd_kernel<bf16, 128, true><<<grid, 256, 0, st>>>(a);
   else if (a.dtype == 1) bwd_kernel<bf16, 128><<<grid, 256, 0, st>>>(a);
   else if (a.D <= 64) bwd_kernel<float, 64><<<grid, 256, 0, st>>>(a);
   else bwd_kernel<float, 128><<<grid, 256, 0, st>>>(a);
