@@ -83,14 +83,12 @@ def _native():
     return _calls
 
 
-_current = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream() without its wrapper object
-
-
 def _on(stream, t: torch.Tensor) -> int:
     """The given stream, or the current one of the tensor's device."""
     if stream is not None:
         return stream.cuda_stream
-    return _current(t.get_device()) if t.is_cuda else 0
+    # torch.cuda.current_stream() without its wrapper object
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else 0
 
 
 # ------------------------------------------------------- norm and rotation

@@ -3,6 +3,8 @@ and the C entries refuse, and what a plan may not depend on."""
 import ctypes
 import os
 import struct
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -12,6 +14,7 @@ import test_weight_mlp_amd as ip
 from test_attention_host import Plan
 from test_weight_mlp_amd import attention as at
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 needs_lib = pytest.mark.skipif(not os.path.exists(ip.library_path), reason="libipttt.so not built")
 
 
@@ -108,3 +111,14 @@ def test_sequences_without_queries_do_not_change_the_backward_of_others(ql, kl, 
     assert beside.dq == alone.dq and beside.dq_join == alone.dq_join and beside.key_join == alone.key_join
     assert [x for x in beside.key if x["q_len"] > 0] == alone.key
     assert len(beside.key) == len(alone.key) + 31 * 125
+
+
+def test_package_imports_where_torch_has_no_raw_stream():
+    """Builds of torch without devices lack the name; it is looked up by the first
+    call on a device tensor."""
+    code = ("import torch\n"
+            "if hasattr(torch._C, '_cuda_getCurrentRawStream'): del torch._C._cuda_getCurrentRawStream\n"
+            "import test_weight_mlp_amd as ip\n"
+            "print(ip.Problem(1, 8, 64, 128, 8).rows, ip.AttentionPlan.__name__)\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT, timeout=100)
+    assert r.returncode == 0 and r.stdout.split() == ["1", "AttentionPlan"], r.stderr
