@@ -71,8 +71,6 @@ def build(jobs: int = 8, verbose: bool = False, sanitize: bool = False) -> str:
         # the sanitized copy is loaded by the same marshalling module
         marshal = None if sanitize else ex.submit(build_marshal, verbose)
         objs = list(ex.map(lambda src: _compile(src, sanitize), SOURCES))
-        if marshal is not None:
-            marshal.result()
     tmp = lib + ".tmp"
     cmd = [hipcc(), "-shared", "-fPIC", "--offload-arch=gfx950"] + (SANITIZE if sanitize else []) + \
         ["-o", tmp] + objs
@@ -82,6 +80,9 @@ def build(jobs: int = 8, verbose: bool = False, sanitize: bool = False) -> str:
     os.replace(tmp, lib)
     if verbose:
         print(f"built {lib}")
+    if marshal is not None and marshal.exception() is not None:
+        raise RuntimeError("libipttt.so is built and serves the layer; the attention half's marshalling module, which "
+                           f"also needs g++ and torch's headers, is not: {marshal.exception()}") from marshal.exception()
     return lib
 
 

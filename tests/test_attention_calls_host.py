@@ -122,3 +122,27 @@ def test_package_imports_where_torch_has_no_raw_stream():
             "print(ip.Problem(1, 8, 64, 128, 8).rows, ip.AttentionPlan.__name__)\n")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT, timeout=100)
     assert r.returncode == 0 and r.stdout.split() == ["1", "AttentionPlan"], r.stderr
+
+
+def test_library_is_linked_where_the_marshalling_module_cannot_be_built(monkeypatch, tmp_path):
+    """The layer needs only the library, which needs only hipcc; the missing half is
+    reported once that is there."""
+    from test_weight_mlp_amd import build as b
+    lib = tmp_path / "libipttt.so"
+    monkeypatch.setattr(b, "LIB", str(lib))
+    monkeypatch.setattr(b, "OBJDIR", str(tmp_path))
+    monkeypatch.setattr(b, "hipcc", lambda: "hipcc")
+    monkeypatch.setattr(b, "_compile", lambda src, sanitize=False: src)
+
+    def no_compiler(verbose=False):
+        raise FileNotFoundError("c++")
+
+    def link(cmd, **kw):
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(b, "build_marshal", no_compiler)
+    monkeypatch.setattr(b.subprocess, "run", link)
+    with pytest.raises(RuntimeError, match="libipttt.so is built.*attention"):
+        b.build(jobs=2)
+    assert lib.exists()
