@@ -386,7 +386,7 @@ typedef struct {
   int64_t kv_heads;    /* key (and value) heads, 1 .. 4096                       */
   int64_t head_dim;    /* D: multiple of 8, 8 .. 128                             */
   int64_t table_rows;  /* positions of the cos, sin table                        */
-  int64_t out_rows;    /* rows of k_out and v_out                                */
+  int64_t out_rows;    /* rows of k_out and v_out; 0: their data may be NULL     */
   int32_t dtype;       /* ipttt_dtype                                            */
   float eps;           /* added to the mean square; finite, >= 0                 */
 } ipttt_qk_problem;

@@ -430,8 +430,10 @@ ipttt_status check_qk(const ipttt_qk_problem* p) {
   return IPTTT_OK;
 }
 
-// Every address is 64-bit here: only the strides' own rules apply.
+// Every address is 64-bit here: only the strides' own rules apply.  A tensor of no
+// rows may be NULL.
 ipttt_status qk_view(const ipttt_qk_problem* p, const ipttt_heads* t, int64_t rows, int64_t heads, View* v) {
+  if (rows == 0) return IPTTT_OK;
   return check_heads(t, rows, heads, p->head_dim, p->dtype, 1, 1, v);
 }
 

@@ -7,7 +7,7 @@ import torch
 
 import test_weight_mlp_amd as ip
 from oracle import attention as oa
-from test_gpu_attention import BF16, draw, np64, seqs_of, starts
+from test_gpu_attention import BF16, draw, draw_qk, np64, seqs_of, starts
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +42,17 @@ def test_bf16_gradients_of_short_sequences_do_not_depend_on_their_company(heads,
         ratio = np.linalg.norm((np64(got) - w)[short]) / np.linalg.norm(own[short])
         print(f"{name} {ratio:.3f}")
         assert ratio <= 1.25, name
+
+
+def test_norm_rope_into_no_rows():
+    """A cache of no rows drops every key and value; the queries are as ever."""
+    n, hq, hk, d = 5, 4, 2, 64
+    q, k, v, w, table, pos, _ = draw_qk(BF16, n, hq, hk, d)
+    none, at = torch.empty(0, hk, d, dtype=q.dtype, device="cuda"), torch.zeros(n, dtype=torch.int32, device="cuda")
+    out, want = (torch.empty(n, hq, d, dtype=q.dtype, device="cuda") for _ in "ab")
+    ip.ipttt_qk_norm_rope(ip.QKProblem(n, hq, hk, d, BF16, table_rows=5000), q, k, w[0], w[1], pos, table, want,
+                          torch.empty(n, hk, d, dtype=q.dtype, device="cuda"))
+    ip.ipttt_qk_norm_rope(ip.QKProblem(n, hq, hk, d, BF16, table_rows=5000, out_rows=0), q, k, w[0], w[1], pos, table, out,
+                          none, v=v, v_out=none, rows=at)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
