@@ -146,3 +146,17 @@ def test_library_is_linked_where_the_marshalling_module_cannot_be_built(monkeypa
     with pytest.raises(RuntimeError, match="libipttt.so is built.*attention"):
         b.build(jobs=2)
     assert lib.exists()
+
+
+@needs_lib
+@pytest.mark.parametrize("heads,kv,dim,ql,kl,dt", [(32, 8, 64, [1800], [1800], ip.IPTTT_BF16),
+                                                   (16, 8, 64, [3900], [3900], ip.IPTTT_F32),
+                                                   (16, 8, 64, [300, 700], [4000, 700], ip.IPTTT_BF16)])
+def test_calls_of_two_workgroups_a_cu_fold_their_order(heads, kv, dim, ql, kl, dt):
+    """257 to 512 workgroups start together, the later ones second on a CU: the
+    longest tiles come first, then the others from the shortest."""
+    pl = Plan(ip.AttentionPlan(heads, kv, dim, ql, kl, dt, device="cpu"))
+    assert 256 < len(pl.rows) * kv <= 512
+    keys = [x["k_end"] - x["k_begin"] for x in pl.rows]
+    first, second = keys[:256 // kv], keys[256 // kv:]
+    assert first == sorted(first, reverse=True) and second == sorted(second) and min(first) >= max(second)

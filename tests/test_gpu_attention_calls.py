@@ -7,7 +7,8 @@ import torch
 
 import test_weight_mlp_amd as ip
 from oracle import attention as oa
-from test_gpu_attention import BF16, draw, draw_qk, np64, seqs_of, starts
+from test_attention_host import Plan
+from test_gpu_attention import BF16, F32, check_forward, draw, draw_qk, np64, rel, seqs_of, starts
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +57,52 @@ def test_norm_rope_into_no_rows():
                           none, v=v, v_out=none, rows=at)
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+# heads, key heads, width, query and key lengths, and what the plan does with them:
+# a backward of 512 tiles and more (tiles of rows whole, those of keys cut), a forward
+# of two workgroups a CU (folded order), tiles of many rows cut at narrow widths
+REGIMES = [
+    (32, 8, 64, [1800], [1800], "many folded"),
+    (16, 16, 128, [2050], [2050], "many"),
+    (32, 8, 128, [700, 600, 500], [700, 600, 500], "many"),
+    (16, 8, 64, [300, 700], [4000, 700], "cut"),
+    (16, 8, 32, [300], [5000], "cut"),
+]
+# Rounding to bf16 is off by 1.7e-3 of a tensor's norm.  O is rounded once and made of
+# rounded P: sqrt(2) times that.  A gradient the same, of dS or P, and bf16's O goes
+# into delta of rows of many keys.  A quarter more than sqrt(2) times 1.7e-3.
+NEAR = {BF16: 3.0e-3, F32: 2e-5}
+
+
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("heads,kv,dim,ql,kl,regime", REGIMES)
+def test_regimes_of_large_calls(dt, heads, kv, dim, ql, kl, regime):
+    plan = ip.AttentionPlan(heads, kv, dim, ql, kl, dt)
+    pl = Plan(plan)
+    if "many" in regime:
+        assert pl.h["n_dq_join"] == 0 and pl.h["n_key_join"] > 0
+    if "folded" in regime:
+        assert 256 < len(pl.rows) * kv <= 512
+    if "cut" in regime:
+        assert any(x["part"] >= 0 for x in pl.rows)
+    q, k, v, do = draw(dt, heads, kv, dim, ql, kl, seed=21)
+    b = step(plan, q, k, v, do)
+    check_forward(dt, plan, q, k, v, ql, kl, b)
+    want = oa.attention_backward(*(np64(t) for t in (q, k, v, do)), seqs_of(ql, kl), plan.scale)
+    for name, got, w in zip(("dq", "dk", "dv"), (b.dq, b.dk, b.dv), want):
+        print(f"{name} {rel(np64(got), w):.2e}")
+        assert rel(np64(got), w) <= NEAR[dt], name
+
+
+@pytest.mark.parametrize("heads,kv,dim,lens", [(8, 2, 64, [40] * 12), (4, 1, 128, [64, 50, 33]), (8, 8, 64, [130, 48])])
+def test_delta_of_few_keys_does_not_take_the_rounding_of_o(heads, kv, dim, lens):
+    """dQ of bf16 sequences of 33 keys and more: dS's rounding and its own, sqrt(2)
+    times the latter, and a tenth more; with bf16's O in delta it is twice the latter."""
+    q, k, v, do = draw(BF16, heads, kv, dim, lens, lens, seed=22)
+    b = step(ip.AttentionPlan(heads, kv, dim, lens, lens), q, k, v, do)
+    want = oa.attention_backward(*(np64(t) for t in (q, k, v, do)), seqs_of(lens, lens), dim ** -0.5)[0]
+    own = np64(torch.from_numpy(want).to(torch.bfloat16)) - want
+    ratio = np.linalg.norm(np64(b.dq) - want) / np.linalg.norm(own)
+    print(f"dq {ratio:.3f}")
+    assert ratio <= 1.1 * 2 ** 0.5
