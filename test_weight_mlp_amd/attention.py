@@ -83,12 +83,16 @@ def _native():
     return _calls
 
 
-def _on(stream, t: torch.Tensor) -> int:
-    """The given stream, or the current one of the tensor's device."""
-    if stream is not None:
-        return stream.cuda_stream
+def _on(stream, q: torch.Tensor) -> int:
+    """The given stream, or the current one.  Kernels are launched on the current
+    device, so the tensors have to be there."""
+    if not getattr(q, "is_cuda", False):  # refused with the other arguments
+        return 0
+    at, current = q.get_device(), torch._C._cuda_getDevice()
+    if at != current:
+        raise ValueError(f"q is on device {at}, the current device is {current}: call under torch.cuda.device({at})")
     # torch.cuda.current_stream() without its wrapper object
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else 0
+    return torch._C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream
 
 
 # ------------------------------------------------------- norm and rotation

@@ -63,12 +63,23 @@ def _calls(device):
 
 @needs_lib
 @pytest.mark.filterwarnings("ignore")
-def test_binding_refuses_tensors_of_two_devices():
+def test_binding_refuses_tensors_of_two_devices(monkeypatch):
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
     for (call, args), (_, others) in zip(_calls("cuda:0"), _calls("cuda:1")):
         for name in args:
-            first = "k" if name == "q" and "w_q" in args else name     # the call's first tensor is not the odd one
-            with pytest.raises(ValueError, match=rf"^{first} must be on device"):
+            # q decides which device is the call's; in the norm it is the first tensor
+            what = "q is on device 1, the current device is 0" if name == "q" else f"{name} must be on device 0"
+            with pytest.raises(ValueError, match="^" + what):
                 call(dict(args, **{name: others[name]}))
+
+
+@needs_lib
+def test_binding_refuses_tensors_that_are_not_on_the_current_device(monkeypatch):
+    """Kernels go to the current device, where another one's memory need not be mapped."""
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    for call, args in _calls("cuda:1"):
+        with pytest.raises(ValueError, match="on device 1, the current device is 0"):
+            call(args)
 
 
 def _heads(data, row=128, head=64):
