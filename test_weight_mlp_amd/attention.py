@@ -163,7 +163,9 @@ def ipttt_qk_norm_rope_backward(p: QKProblem, q, k, w_q, w_k, positions, table, 
 class AttentionPlan:
     """Sequences of an attention call and the plan the library makes of them
     (ipttt_attn_problem, ipttt_attn_plan), on the host and the device; built
-    once for a step and used by every layer.  q_starts and k_starts default to
+    once for a step and used by every layer.  It holds the lengths: a decoded token
+    needs a new one (32 us for one sequence, 79 for 32, 374 for 256 of 8000 keys, with
+    the copy to the device, which waits for it).  q_starts and k_starts default to
     sequences packed one after the other; scale defaults to head_dim^-1/2."""
 
     def __init__(self, heads: int, kv_heads: int, head_dim: int, q_lens: Sequence[int], k_lens: Sequence[int],

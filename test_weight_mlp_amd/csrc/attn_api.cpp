@@ -219,11 +219,12 @@ int64_t few_part(const ipttt_attn_problem* p, const Cut& cut) {
 
 // Backward: the first keys of a causal sequence meet all its rows and the last
 // almost none, and a call's last workgroup ends it, so no tile of keys is longer
-// than what a workgroup gets on average (8k tokens, 32 heads over 8 of width 128:
-// 1.70 ms uncut, 1.19 ms cut and joined); where workgroups would stay idle, tiles
-// of rows are cut alike, and those of keys in parts of 1.5 shares, which leaves fewer
-// (bf16, 1000 tokens: 66 us, 77 in even shares; 4000 tokens, whose tiles fill the
-// CUs: 513 and 462; fp32: even shares everywhere).  A step of rows is 128 x 64 x 3 products, one of keys
+// than what a workgroup gets on average (32 heads over 8 of width 128, forward and
+// backward: 2500 tokens 415 us uncut, 268 cut and joined; 4000: 740 and 564; 8192 and
+// more: equal); where workgroups would stay idle, tiles of rows are cut alike, and
+// those of keys in parts of 1.5 shares, which leaves fewer (bf16, 1000 tokens: 88 us,
+// 95 in even shares; 4000 tokens, whose tiles fill the CUs: 600 and 563; fp32: even
+// shares everywhere).  A step of rows is 128 x 64 x 3 products, one of keys
 // 32 x 128 x 4: three to two.
 Cut cut_of(const ipttt_attn_problem* p) {
   const bool f32 = p->dtype == IPTTT_F32;

@@ -26,12 +26,12 @@ namespace {
 // alone, 1.41 to 1.45 of which are dS's and its own rounding (sequences of 333 to 1999
 // tokens of width 64: 1.50 with a bound of 512, 1.46 of 1024, 1.45 of 2048; 1500 of
 // width 128: 1.48 of 512, 1.45 of 1024), and this part short beside the rest (the same
-// sequences, forward and backward: 107, 114 and 129 us).  Narrow heads average fewer
+// sequences, forward and backward: 97, 102 and 114 us).  Narrow heads average fewer
 // roundings in delta and need more.
 // fp32: where one probability is near 1, dP - delta is what dP's own rounding
 // leaves unless delta was made of the same dP and of P's that add up to 1 (sequences
 // of 9 tokens: dQ 1.0 times a plain fp32 form's error, 1.6 with O; of 120: 1.12 and
-// 1.18; one of 300 and one of 30 tokens, forward and backward: 53.6 us and 48.7).
+// 1.18; one of 300 and one of 30 tokens, forward and backward: 52.6 us and 47.8).
 template <typename T>
 __device__ __forceinline__ int exact_delta_keys(int D) {
   return sizeof(T) == 4 ? 64 : max(768, 73728 / D);
@@ -41,8 +41,8 @@ __device__ __forceinline__ int exact_delta_keys(int D) {
 // all: a few probabilities, each in many elements of a gradient, do not average their
 // roundings (3 tokens: dQ 1.7 times the error of rounding it alone; in two terms 1.0).
 // The sequence's own keys decide, whatever it is packed with (forward and backward, 32
-// heads over 8 of width 128, in one term and two: 100 sequences of 9 tokens 44 and 45
-// us, 400 of 30 tokens 258 and 274).
+// heads over 8 of width 128, in one term and two: 9 tokens 15.5 and 16.7 us, 100
+// sequences of 9 tokens 41 and 45, 400 of 30 tokens 243 and 277).
 __device__ __forceinline__ bool short_keys(int k_len) { return k_len <= kShortKeys; }
 
 // Where lse and delta are taken off.  bf16: the accumulators start at -lse / scale
@@ -147,7 +147,7 @@ __device__ __forceinline__ void delta_tile(const Args& a, const RowItem& it, int
 
 // Bound by reading O and dO once (8192 tokens, 32 heads of width 128: 29 us, 4.6 TB/s),
 // where rows see few keys by the products (4 sequences of 333 to 1999 tokens, 16
-// heads over 8 of width 64: 22 us).
+// heads over 8 of width 64: 21 us).
 template <typename T, int DP>
 __global__ __launch_bounds__(256) void delta_kernel(Args a) {
   __shared__ __attribute__((aligned(16))) char lds[4 * Tile<T, DP>::bytes(sizeof(T) == 2 ? kKeys : kKeys / 2)];
@@ -554,13 +554,13 @@ __device__ __forceinline__ void dkv_tile(const Args& a, const KeyItem& it, int k
 }
 
 // The tiles of keys (longest first), then those of rows.  bf16: two waves a SIMD.
-// Bound by the matrix cores at the clock that the card's power allows: 8192 tokens,
-// 32 heads over 8 of width 128: 1.70 ms, 1.13 PFLOP/s of its seven products, matrix
-// cores 57 % busy at 1.88 GHz.
+// Bound by the matrix cores at the clock that the card's power allows, and by what
+// keeps them waiting: 8192 tokens, 32 heads over 8 of width 128: 1.61 ms, 1.19 PFLOP/s
+// of its seven products, matrix cores 65 % busy at 1.77 GHz.
 // SHORT: sequences of few keys, whose P and dS go in two terms, are among them; at
-// width 128 both kinds of tile together do not fit a wave's registers (8192 tokens,
-// forward and backward: 2.10 ms, with a sequence of 12 beside them 2.14).  (Its tiles
-// have SHORT as a parameter too: hipcc's host pass takes one use of each.)
+// width 128 both kinds of tile together do not fit a wave's registers (8180 tokens
+// beside 12, forward and backward: 2.16 ms, 2.13 with one kind).  Its tiles have SHORT
+// as a parameter too: hipcc's host pass takes one use of each.
 template <typename T, int DP, bool SHORT = false>
 __global__ __launch_bounds__(256, sizeof(T) == 4 ? 1 : 2) void bwd_kernel(Args a) {
   constexpr int ES = sizeof(T), DQ = 4 * Tile<T, DP>::bytes(ES == 2 ? kKeys : kKeys / 2);

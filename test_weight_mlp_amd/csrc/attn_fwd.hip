@@ -252,10 +252,11 @@ __device__ __forceinline__ void fwd_tile(const Args& a, const RowItem& it, int k
 
 // Two waves a SIMD (256 registers a wave) where the tiles allow it; fp32 of
 // width 128 needs the registers of one.  Bound by the matrix cores at the clock
-// that the card's power allows: 32 heads over 8 of width 128, one sequence of 32768
-// tokens 7.7 ms, 1.14 PFLOP/s of what the mask leaves, matrix cores 65 % busy at
-// 1.67 GHz; of 8192 tokens 0.50 ms, 1.09 PFLOP/s.  (256 rows a tile with 8 waves:
-// equal at 32768, slower below.)
+// that the card's power allows, and by what keeps them waiting a third of the time:
+// 32 heads over 8 of width 128, one sequence of 32768 tokens 7.7 ms, 1.14 PFLOP/s of
+// what the mask leaves, matrix cores 65 % busy at 1.68 GHz (on zeros 67 % at 2.38
+// GHz); of 8192 tokens 0.50 ms, 1.09 PFLOP/s.  (256 rows a tile with 8 waves: equal
+// at 32768, slower below.)
 template <typename T, int DP, int NB>
 __global__ __launch_bounds__(256, sizeof(T) * DP > 256 ? 1 : 2) void fwd_kernel(Args a) {
   __shared__ __attribute__((aligned(16))) char lds[4 * Tile<T, DP>::bytes(32 * NB)];
@@ -269,8 +270,8 @@ __global__ __launch_bounds__(256, sizeof(T) * DP > 256 ? 1 : 2) void fwd_kernel(
 // e^(lse_i - lse), lse = log sum e^(lse_i); parts in slot order, eight parts'
 // loads in flight.  A tile of many rows: a thread takes four columns of one row.
 // One of few rows, which has many parts: a wave takes one row, two columns a
-// lane, and its lanes hold the weights of 64 parts (one token over 4097 keys, 33
-// parts: 4.3 us, 5.2 as the other kind).
+// lane, and its lanes hold the weights of 64 parts (one token over 4097 keys, 22
+// parts: 3.2 us; with 33 parts 4.3, and 5.2 as the other kind).
 template <typename T>
 __device__ __forceinline__ void join_many(const Args& a, const JoinItem& it, int kvh) {
   const int G = a.G, D = a.D, quads = D / 4, per = 256 / quads;
