@@ -106,3 +106,22 @@ def test_delta_of_few_keys_does_not_take_the_rounding_of_o(heads, kv, dim, lens)
     ratio = np.linalg.norm(np64(b.dq) - want) / np.linalg.norm(own)
     print(f"dq {ratio:.3f}")
     assert ratio <= 1.1 * 2 ** 0.5
+
+
+def test_graph_replays_of_short_and_long_sequences_equal_the_eager_calls():
+    heads, kv, dim, lens = 8, 2, 128, [9, 300, 1, 32]
+    q, k, v, do = draw(BF16, heads, kv, dim, lens, lens, seed=30)
+    plan = ip.AttentionPlan(heads, kv, dim, lens, lens)
+    b = step(plan, q, k, v, do)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ip.ipttt_attention(plan, q, k, v, b.o, b.lse, b.ws)
+        ip.ipttt_attention_backward(plan, q, k, v, b.o, b.lse, do, b.dq, b.dk, b.dv, b.ws)
+    for seed in (31, 32, 33):
+        for dst, src in zip((q, k, v, do), draw(BF16, heads, kv, dim, lens, lens, seed=seed)):
+            dst.copy_(src)
+        g.replay()
+        torch.cuda.synchronize()
+        want = step(plan, q, k, v, do)
+        for x in ("o", "lse", "dq", "dk", "dv"):
+            assert torch.equal(getattr(b, x), getattr(want, x)), x
