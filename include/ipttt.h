@@ -359,6 +359,27 @@ ipttt_status ipttt_z_backward_saved(const ipttt_problem *p, const void *H, const
                                     float *dW_gate, float *dW_up, void *ws, size_t ws_bytes,
                                     void *stream);
 
+/* ipttt_z_save and ipttt_z_backward_saved with G and U kept in 8 bits, about half
+ * the bytes (2.125 d_ff a token instead of 4 d_ff).  Of each token the values of
+ * 64 neighbouring features (rounded to bf16, from feature 0 on, the last block
+ * short where d_ff is no multiple of 64) share the scale s = max|g| / 127 (float)
+ * and are held as the integers round(127 g / max|g|): a value is off by at most half
+ * of 1/127 of the largest beside it, and no token's values depend on another token.
+ * A block whose largest value is below 2^-100 is kept as zeros; one that holds
+ * an infinity or a NaN comes back as NaN.
+ *   kept  ipttt_saved8_bytes(p) bytes (0 for an invalid problem and for fp32
+ *         data), 256-byte aligned; the bytes are opaque
+ * bf16 data only (IPTTT_ERR_DTYPE).  kept_bytes too small: IPTTT_ERR_WORKSPACE.
+ * Z is ipttt_z's; the gradients are those of ipttt_z_backward_saved for the
+ * values that were kept. */
+size_t ipttt_saved8_bytes(const ipttt_problem *p);
+ipttt_status ipttt_z_save8(const ipttt_problem *p, const void *H, const void *W_gate, const void *W_up,
+                           void *Z, void *kept, size_t kept_bytes, void *stream);
+ipttt_status ipttt_z_backward_saved8(const ipttt_problem *p, const void *H, const void *W_gate,
+                                     const void *W_up, const void *kept, size_t kept_bytes,
+                                     const void *dZ, void *dH, float *dW_gate, float *dW_up, void *ws,
+                                     size_t ws_bytes, void *stream);
+
 /* ---------------------------------------------------------- attention half
  *
  * The other half of a block around the layer, over the same packed documents,
@@ -498,6 +519,101 @@ ipttt_status ipttt_attention_backward(const void *plan, const void *plan_dev, fl
                                       const ipttt_heads *dq, const ipttt_heads *dk, const ipttt_heads *dv,
                                       void *ws, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------- the rest of the block
+ *
+ * What stands around the two halves: the norm in front of each, and the
+ * projections of the attention half with the residual sum.  fp32 arithmetic
+ * (fp32 data: fp32 matrix products), every output rounded once. */
+
+/* A [rows, columns] tensor of dtype on the device: element (r, i) at
+ * data[r * row_stride + i], such as columns of a wider tensor.  row_stride counts
+ * elements, is a multiple of 8, at least the columns and at most 2^22 (not used
+ * for a tensor of one row).  data is 16-byte aligned. */
+typedef struct {
+  void *data;
+  int64_t row_stride;
+} ipttt_rows;
+
+typedef enum { IPTTT_NORM_RMS = 0, IPTTT_NORM_LAYER = 1 } ipttt_norm_kind;
+
+typedef struct {
+  int64_t rows;   /* 1 .. 2^26 - 4                                          */
+  int64_t dim;    /* multiple of 8, 8 .. 16384                              */
+  int32_t dtype;  /* ipttt_dtype                                            */
+  int32_t kind;   /* ipttt_norm_kind                                        */
+  float eps;      /* added to the mean square; finite, >= 0                 */
+} ipttt_norm_problem;
+
+/* Norm of each row: with mu = mean(x) (IPTTT_NORM_LAYER) or 0 (IPTTT_NORM_RMS),
+ * r = 1 / sqrt(mean((x - mu)^2) + eps) and xn = (x - mu) r,
+ *   y = xn w + b.
+ *   x [rows, dim], y [rows, dim] out; y may be x (same data and stride)
+ *   w, b [dim] (dtype), either NULL: left out
+ * The mean is subtracted before the squares are summed, so a row's mean may be
+ * far larger than its spread.  One launch. */
+ipttt_status ipttt_norm(const ipttt_norm_problem *p, const ipttt_rows *x, const void *w, const void *b,
+                        const ipttt_rows *y, void *stream);
+
+/* Its gradients from the cotangent dy of y: with u = dy w,
+ *   dx = r (u - mean(u) [layer only] - xn mean(u xn)) + dres
+ *   dw = sum over rows of dy xn,   db = sum over rows of dy.
+ *   x, w         as in the forward (which saves nothing)
+ *   dy [rows, dim]
+ *   dres         NULL, or [rows, dim]: the cotangent that reaches x past the
+ *                norm, such as the residual stream's
+ *   dx [rows, dim] out; may be dy or dres (same data and stride)
+ *   dw, db [dim] float out, either NULL: not wanted; summed in a fixed order
+ * ws: ipttt_norm_backward_workspace_bytes(p), 256-byte aligned; may be NULL
+ * where dw and db are. */
+size_t ipttt_norm_backward_workspace_bytes(const ipttt_norm_problem *p);
+ipttt_status ipttt_norm_backward(const ipttt_norm_problem *p, const ipttt_rows *x, const void *w,
+                                 const ipttt_rows *dy, const ipttt_rows *dres, const ipttt_rows *dx,
+                                 float *dw, float *db, void *ws, size_t ws_bytes, void *stream);
+
+/* What a projection's epilogue applies: nothing, v sigmoid(v), or v times the
+ * normal distribution function (the exact GELU). */
+typedef enum { IPTTT_ACT_NONE = 0, IPTTT_ACT_SILU = 1, IPTTT_ACT_GELU = 2 } ipttt_act;
+
+typedef struct {
+  int64_t rows;        /* m: 1 .. 2^26 - 4                                       */
+  int64_t in_dim;      /* k: multiple of 8, 8 .. 2^20                            */
+  int64_t out_dim;     /* n: multiple of 8, 8 .. 2^20                            */
+  int32_t dtype;       /* ipttt_dtype of x, W, b, res, y, pre, dy and dx          */
+  int32_t act;         /* ipttt_act                                              */
+  int32_t grad_dtype;  /* ipttt_dtype of dW: IPTTT_F32, or dtype                 */
+} ipttt_linear_problem;
+
+/* Projection with its epilogue:
+ *   pre = x W^T + b,   y = act(pre) + res.
+ *   x [m, k], W [n, k] contiguous, b [n] or NULL
+ *   res [m, n] or NULL: added after the activation; may be y (same data and
+ *              stride), nothing else may overlap an output
+ *   y   [m, n] out
+ *   pre [m, n] out or NULL: what ipttt_linear_backward needs of an activation,
+ *              rounded to dtype (y is computed from the unrounded one)
+ * ws: ipttt_linear_workspace_bytes(p) (0: none, ws may be NULL), 256-byte
+ * aligned. */
+size_t ipttt_linear_workspace_bytes(const ipttt_linear_problem *p);
+ipttt_status ipttt_linear(const ipttt_linear_problem *p, const ipttt_rows *x, const void *W, const void *b,
+                          const ipttt_rows *res, const ipttt_rows *y, const ipttt_rows *pre, void *ws,
+                          size_t ws_bytes, void *stream);
+
+/* Its gradients from the cotangent dy of y (which is also that of res): with
+ * dp = dy act'(pre),
+ *   dx = dp W,   dW = dp^T x,   db = sum over rows of dp.
+ *   x, W    as in the forward
+ *   pre     [m, n] as the forward kept it; not read (NULL) without activation
+ *   dy      [m, n]
+ *   dx      [m, k] out, dW [n, k] out (grad_dtype), db [n] float out; each NULL:
+ *           not wanted
+ * With an activation dp is rounded to dtype, as an operand of the matrix cores
+ * (db sums the unrounded values).  Sums run in a fixed order.
+ * ws: ipttt_linear_backward_workspace_bytes(p), 256-byte aligned. */
+size_t ipttt_linear_backward_workspace_bytes(const ipttt_linear_problem *p);
+ipttt_status ipttt_linear_backward(const ipttt_linear_problem *p, const ipttt_rows *x, const void *W,
+                                   const ipttt_rows *pre, const ipttt_rows *dy, const ipttt_rows *dx,
+                                   void *dW, float *db, void *ws, size_t ws_bytes, void *stream);
+
 /* ---- measurement aid (not a step of the method) --------------------------
  *
  * When a hook is set, every entry point calls hook(kernel, stream, user) on
@@ -505,7 +621,8 @@ ipttt_status ipttt_attention_backward(const void *plan, const void *plan_dev, fl
  * small kernels) on `stream`, with a short name: "gated_z", "segments",
  * "target_prep", "conv", "target_gemm", "gram_v", "gram", "alpha",
  * "scale_rows", "scan", "apply", and the backward's "rscan_fast", "nt",
- * "tn_fast", ..., the attention half's "qk", "attn_fwd", "attn_join", ...  A
+ * "tn_fast", ..., the attention half's "qk", "attn_fwd", "attn_join", ..., the
+ * rest of the block's "norm", "linear", ...  A
  * profiler records a stream event in the hook and times each kernel between
  * consecutive events on the stream's own timeline.  The hook must not call
  * back into the library.  NULL (the default) disables it.  The setting is

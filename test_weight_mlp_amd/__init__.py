@@ -29,6 +29,11 @@ __all__ = [
     "IPTTT_NOALLOC_SCRATCH_BYTES", "ipttt_set_launch_hook",
     "QKProblem", "QKGrads", "ipttt_qk_backward_workspace_bytes", "ipttt_qk_norm_rope", "ipttt_qk_norm_rope_backward",
     "AttentionPlan", "AttentionBuffers", "ipttt_attention", "ipttt_attention_backward", "rotation_table",
+    "ipttt_saved8_bytes", "ipttt_z_save8", "ipttt_z_backward_saved8",
+    "IPTTT_NORM_RMS", "IPTTT_NORM_LAYER", "IPTTT_ACT_NONE", "IPTTT_ACT_SILU", "IPTTT_ACT_GELU",
+    "NormProblem", "NormGrads", "ipttt_norm", "ipttt_norm_backward", "ipttt_norm_backward_workspace_bytes",
+    "LinearProblem", "LinearGrads", "ipttt_linear", "ipttt_linear_workspace_bytes", "linear_workspace",
+    "ipttt_linear_backward", "ipttt_linear_backward_workspace_bytes",
 ]
 
 IPTTT_F32 = 0
@@ -112,6 +117,9 @@ def library() -> ctypes.CDLL:
             "ipttt_saved_bytes": (sz, [P]),
             "ipttt_z_save": (i32, [P, vp, vp, vp, vp, vp, vp]),
             "ipttt_z_backward_saved": (i32, [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+            "ipttt_saved8_bytes": (sz, [P]),
+            "ipttt_z_save8": (i32, [P, vp, vp, vp, vp, vp, sz, vp]),
+            "ipttt_z_backward_saved8": (i32, [P, vp, vp, vp, vp, sz, vp, vp, vp, vp, vp, sz, vp]),
             "ipttt_scan_apply_save": (i32, [P, vp, vp, vp, vp, f32, vp, vp, sz, vp, sz, vp]),
             "ipttt_scan_apply_backward_saved": (i32, [P, vp, vp, vp, f32, f32, vp, vp, sz, vp, vp, vp, vp, vp,
                                                       sz, vp]),
@@ -201,6 +209,10 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _nbytes(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
 def _stream(stream=None):
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
@@ -248,6 +260,15 @@ def ipttt_z_save(p: Problem, H, W_gate, W_up, Z, GU, stream=None):
            "ipttt_z_save")
 
 
+def ipttt_saved8_bytes(p: Problem) -> int:
+    return int(library().ipttt_saved8_bytes(p.ref))
+
+
+def ipttt_z_save8(p: Problem, H, W_gate, W_up, Z, kept, stream=None):
+    _check(library().ipttt_z_save8(p.ref, _ptr(H), _ptr(W_gate), _ptr(W_up), _ptr(Z), _ptr(kept), _nbytes(kept),
+                                   _stream(stream)), "ipttt_z_save8")
+
+
 def ipttt_target(p: Problem, X0, conv_w, W_target, V, ws, stream=None):
     _check(library().ipttt_target(p.ref, _ptr(X0), _ptr(conv_w), _ptr(W_target), _ptr(V),
                                   _ptr(ws), ws.numel(), _stream(stream)), "ipttt_target")
@@ -290,9 +311,12 @@ class Buffers:
     """Device buffers of one forward: outputs, intermediates and workspace;
     with ``save``, also what the backward can reuse: ``GU`` (the products
     before the gate) and ``saved`` (the chunk weights; None where the shape
-    keeps none)."""
+    keeps none).  With ``keep8`` too (bf16 data) the products are kept in 8 bits,
+    in ``GU8``, about half the bytes of ``GU``."""
 
-    def __init__(self, p: Problem, device="cuda", want_dW: bool = False, save: bool = False):
+    def __init__(self, p: Problem, device="cuda", want_dW: bool = False, save: bool = False, keep8: bool = False):
+        if keep8 and (not save or p.dtype != IPTTT_BF16):
+            raise ValueError("keep8 is for bf16 data and goes with save")
         dt = p.torch_dtype
         n, d, f = p.tokens, p.d_model, p.d_ff
         self.Z = torch.empty((n, f), dtype=dt, device=device)
@@ -304,11 +328,12 @@ class Buffers:
         self.ws = torch.empty(ipttt_workspace_bytes(p), dtype=torch.uint8, device=device)
         nsave = ipttt_saved_bytes(p) if save else 0
         self.saved = torch.empty(nsave, dtype=torch.uint8, device=device) if nsave > 0 else None
-        self.GU = torch.empty((2, n, f), dtype=dt, device=device) if save else None
+        self.GU = torch.empty((2, n, f), dtype=dt, device=device) if save and not keep8 else None
+        self.GU8 = torch.empty(ipttt_saved8_bytes(p), dtype=torch.uint8, device=device) if keep8 else None
 
 
-def allocate(p: Problem, device="cuda", want_dW: bool = False, save: bool = False) -> Buffers:
-    return Buffers(p, device, want_dW, save)
+def allocate(p: Problem, device="cuda", want_dW: bool = False, save: bool = False, keep8: bool = False) -> Buffers:
+    return Buffers(p, device, want_dW, save, keep8)
 
 
 def forward(p: Problem, H, X0, W_gate, W_up, W_down, conv_w, W_target, eta: float, tau: float,
@@ -323,11 +348,14 @@ def forward(p: Problem, H, X0, W_gate, W_up, W_down, conv_w, W_target, eta: floa
     each row's open document at its end; S_out may be S_in.  Otherwise, when
     ``buf.saved`` is set (``allocate(..., save=True)``), the last step is
     ipttt_scan_apply_save, which leaves the state ``backward`` reuses there;
-    with ``buf.GU`` set, the first step is ipttt_z_save."""
+    with ``buf.GU`` set, the first step is ipttt_z_save, with ``buf.GU8``
+    ipttt_z_save8."""
     if buf is None:
         buf = Buffers(p, H.device)
     if buf.GU is not None:
         ipttt_z_save(p, H, W_gate, W_up, buf.Z, buf.GU, stream)
+    elif buf.GU8 is not None:
+        ipttt_z_save8(p, H, W_gate, W_up, buf.Z, buf.GU8, stream)
     else:
         ipttt_z(p, H, W_gate, W_up, buf.Z, stream)
     ipttt_target(p, X0, conv_w, W_target, buf.V, buf.ws, stream)
@@ -379,6 +407,12 @@ def ipttt_z_backward_saved(p: Problem, H, W_gate, W_up, GU, dZ, dH, dW_gate, dW_
                                             _stream(stream)), "ipttt_z_backward_saved")
 
 
+def ipttt_z_backward_saved8(p: Problem, H, W_gate, W_up, kept, dZ, dH, dW_gate, dW_up, ws, stream=None):
+    _check(library().ipttt_z_backward_saved8(p.ref, _ptr(H), _ptr(W_gate), _ptr(W_up), _ptr(kept), _nbytes(kept),
+                                             _ptr(dZ), _ptr(dH), _ptr(dW_gate), _ptr(dW_up), _ptr(ws), ws.numel(),
+                                             _stream(stream)), "ipttt_z_backward_saved8")
+
+
 class Grads:
     """Device buffers of one backward: the input gradients, dZ, dV and the
     backward workspace."""
@@ -406,7 +440,8 @@ def backward(p: Problem, buf: Buffers, H, X0, W_gate, W_up, W_down, conv_w, W_ta
     """The layer's backward after ``forward(p, ..., buf)``: ipttt_scan_apply_backward ->
     ipttt_target_backward -> ipttt_z_backward on one stream, from the forward's Z and V
     (and, when the forward saved them, its clip scales and chunk weights:
-    ipttt_scan_apply_backward_saved; its G and U: ipttt_z_backward_saved)."""
+    ipttt_scan_apply_backward_saved; its G and U: ipttt_z_backward_saved, or in 8 bits
+    ipttt_z_backward_saved8)."""
     if grads is None:
         grads = Grads(p, H.device)
     g = grads
@@ -418,6 +453,8 @@ def backward(p: Problem, buf: Buffers, H, X0, W_gate, W_up, W_down, conv_w, W_ta
     ipttt_target_backward(p, X0, conv_w, W_target, g.dV, g.dX0, g.dconv_w, g.dW_target, g.ws, stream)
     if buf.GU is not None:
         ipttt_z_backward_saved(p, H, W_gate, W_up, buf.GU, g.dZ, g.dH, g.dW_gate, g.dW_up, g.ws, stream)
+    elif buf.GU8 is not None:
+        ipttt_z_backward_saved8(p, H, W_gate, W_up, buf.GU8, g.dZ, g.dH, g.dW_gate, g.dW_up, g.ws, stream)
     else:
         ipttt_z_backward(p, H, W_gate, W_up, g.dZ, g.dH, g.dW_gate, g.dW_up, g.ws, stream)
     return g
@@ -426,3 +463,7 @@ def backward(p: Problem, buf: Buffers, H, X0, W_gate, W_up, W_down, conv_w, W_ta
 from .attention import (AttentionBuffers, AttentionPlan, QKGrads, QKProblem, ipttt_attention,  # noqa: E402
                         ipttt_attention_backward, ipttt_qk_backward_workspace_bytes, ipttt_qk_norm_rope,
                         ipttt_qk_norm_rope_backward, rotation_table)
+from .block import (IPTTT_ACT_GELU, IPTTT_ACT_NONE, IPTTT_ACT_SILU, IPTTT_NORM_LAYER, IPTTT_NORM_RMS,  # noqa: E402
+                    LinearGrads, LinearProblem, NormGrads, NormProblem, ipttt_linear, ipttt_linear_backward,
+                    ipttt_linear_backward_workspace_bytes, ipttt_linear_workspace_bytes, ipttt_norm,
+                    ipttt_norm_backward, ipttt_norm_backward_workspace_bytes, linear_workspace)

@@ -87,6 +87,29 @@ ipttt_status check_problem(const ipttt_problem* q, Prob* p) {
   return IPTTT_OK;
 }
 
+// G and U in 8 bits: integers of G, of U, scales of G, of U, each region
+// 256-byte aligned.
+struct Keep8Layout {
+  ipttt::Keep8 k;
+  size_t bytes;
+};
+Keep8Layout keep8_layout(const Prob& p, void* kept) {
+  const size_t n = align256((size_t)p.M * p.f), m = align256((size_t)p.M * ((p.f + 63) / 64) * sizeof(float));
+  uint8_t* base = static_cast<uint8_t*>(kept);
+  Keep8Layout l;
+  l.bytes = 2 * n + 2 * m;
+  if (kept == nullptr) return l;
+  l.k = ipttt::Keep8{base, base + n, reinterpret_cast<float*>(base + 2 * n), reinterpret_cast<float*>(base + 2 * n + m)};
+  return l;
+}
+ipttt_status check_keep8(const Prob& p, const void* kept, size_t bytes, Keep8Layout* l) {
+  if (p.dtype != IPTTT_BF16) return IPTTT_ERR_DTYPE;
+  if (kept == nullptr) return IPTTT_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(kept) & 255) != 0) return IPTTT_ERR_ALIGN;
+  *l = keep8_layout(p, const_cast<void*>(kept));
+  return bytes < l->bytes ? IPTTT_ERR_WORKSPACE : IPTTT_OK;
+}
+
 // Workspace: per-token segment bytes | segment table | one region that each
 // call uses for itself:
 //   ipttt_target       W_target^T, tap-major conv weights, conv output Y
@@ -462,6 +485,24 @@ ipttt_status ipttt_z_save(const ipttt_problem* q, const void* H, const void* W_g
   if (!all_aligned(H, W_gate, W_up, Z, GU)) return IPTTT_ERR_ALIGN;
   (void)hipGetLastError();
   return hip_status(ipttt::launch_gated_z(p, H, W_gate, W_up, Z, GU, static_cast<hipStream_t>(stream)));
+}
+
+size_t ipttt_saved8_bytes(const ipttt_problem* q) {
+  Prob p;
+  return check_problem(q, &p) == IPTTT_OK && p.dtype == IPTTT_BF16 ? keep8_layout(p, nullptr).bytes : 0;
+}
+
+ipttt_status ipttt_z_save8(const ipttt_problem* q, const void* H, const void* W_gate, const void* W_up, void* Z,
+                           void* kept, size_t kept_bytes, void* stream) {
+  Prob p;
+  ipttt_status s = check_problem(q, &p);
+  if (s != IPTTT_OK) return s;
+  if (any_null(H, W_gate, W_up, Z)) return IPTTT_ERR_NULL;
+  if (!all_aligned(H, W_gate, W_up, Z)) return IPTTT_ERR_ALIGN;
+  Keep8Layout l;
+  if ((s = check_keep8(p, kept, kept_bytes, &l)) != IPTTT_OK) return s;
+  (void)hipGetLastError();
+  return hip_status(ipttt::launch_gated_z8(p, H, W_gate, W_up, Z, l.k, static_cast<hipStream_t>(stream)));
 }
 
 ipttt_status ipttt_target(const ipttt_problem* q, const void* X0, const void* conv_w,
@@ -946,10 +987,11 @@ ipttt_status ipttt_target_backward(const ipttt_problem* q, const void* X0, const
 
 namespace {
 
-// GU: the G and U the forward saved (ipttt_z_save), or NULL (recomputed).
+// GU: the G and U the forward saved (ipttt_z_save), or NULL (recomputed, or
+// read in 8 bits from k8).
 ipttt_status z_backward(const ipttt_problem* q, const void* H, const void* W_gate, const void* W_up, const void* GU,
-                        const void* dZ, void* dH, float* dW_gate, float* dW_up, void* ws, size_t ws_bytes,
-                        void* stream) {
+                        const ipttt::Keep8* k8, const void* dZ, void* dH, float* dW_gate, float* dW_up, void* ws,
+                        size_t ws_bytes, void* stream) {
   Prob p;
   BwdLayout l;
   ipttt_status s;
@@ -963,7 +1005,9 @@ ipttt_status z_backward(const ipttt_problem* q, const void* H, const void* W_gat
   char* c;
   if ((s = bwd_segments(q, p, ws, l, st, &segs, &table, &c)) != IPTTT_OK) return s;
   void *dG = c + l.dg, *dU = c + l.du;
-  if (GU != nullptr) {
+  if (k8 != nullptr) {
+    IPTTT_TRY(ipttt::launch_gated_grad8(p, *k8, dZ, dG, dU, st));
+  } else if (GU != nullptr) {
     IPTTT_TRY(ipttt::launch_gated_grad(p, GU, dZ, dG, dU, st));
   } else {
     IPTTT_TRY(ipttt::launch_gated_z_bwd(p, H, W_gate, W_up, dZ, dG, dU, st));
@@ -1018,14 +1062,25 @@ extern "C" {
 ipttt_status ipttt_z_backward(const ipttt_problem* q, const void* H, const void* W_gate, const void* W_up,
                               const void* dZ, void* dH, float* dW_gate, float* dW_up, void* ws, size_t ws_bytes,
                               void* stream) {
-  return z_backward(q, H, W_gate, W_up, nullptr, dZ, dH, dW_gate, dW_up, ws, ws_bytes, stream);
+  return z_backward(q, H, W_gate, W_up, nullptr, nullptr, dZ, dH, dW_gate, dW_up, ws, ws_bytes, stream);
 }
 
 ipttt_status ipttt_z_backward_saved(const ipttt_problem* q, const void* H, const void* W_gate, const void* W_up,
                                     const void* GU, const void* dZ, void* dH, float* dW_gate, float* dW_up, void* ws,
                                     size_t ws_bytes, void* stream) {
   if (GU == nullptr) return IPTTT_ERR_NULL;
-  return z_backward(q, H, W_gate, W_up, GU, dZ, dH, dW_gate, dW_up, ws, ws_bytes, stream);
+  return z_backward(q, H, W_gate, W_up, GU, nullptr, dZ, dH, dW_gate, dW_up, ws, ws_bytes, stream);
+}
+
+ipttt_status ipttt_z_backward_saved8(const ipttt_problem* q, const void* H, const void* W_gate, const void* W_up,
+                                     const void* kept, size_t kept_bytes, const void* dZ, void* dH, float* dW_gate,
+                                     float* dW_up, void* ws, size_t ws_bytes, void* stream) {
+  Prob p;
+  ipttt_status s = check_problem(q, &p);
+  if (s != IPTTT_OK) return s;
+  Keep8Layout l;
+  if ((s = check_keep8(p, kept, kept_bytes, &l)) != IPTTT_OK) return s;
+  return z_backward(q, H, W_gate, W_up, nullptr, &l.k, dZ, dH, dW_gate, dW_up, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -770,8 +770,19 @@ hipError_t launch_gated_z_bwd(const Prob& p, const void* H, const void* Wg, cons
   return hipGetLastError();
 }
 
-// dG = dZ * U * SiLU'(G), dU = dZ * SiLU(G) from the G and U the forward
-// saved (the same formulas as the recomputing kernels), 8 elements a thread.
+// dG = dZ * U * SiLU'(G), dU = dZ * SiLU(G) of 8 elements.
+__device__ __forceinline__ void gated_grad8(const float (&g)[8], const float (&u)[8], const float (&dz)[8],
+                                            float (&a)[8], float (&b)[8]) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const float s = 1.0f / (1.0f + __expf(-g[q]));
+    a[q] = dz[q] * u[q] * (s * (1.0f + g[q] * (1.0f - s)));
+    b[q] = dz[q] * g[q] * s;
+  }
+}
+
+// dG and dU from the G and U the forward saved (the same formulas as the
+// recomputing kernels), 8 elements a thread.
 template <typename T>
 __global__ __launch_bounds__(256) void gated_grad_kernel(const T* __restrict__ Gs, const T* __restrict__ Us,
                                                          const T* __restrict__ dZ, T* __restrict__ dG,
@@ -782,12 +793,25 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(const T* __restrict__ G
   load8(Gs + v * 8, g);
   load8(Us + v * 8, u);
   load8(dZ + v * 8, dz);
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const float s = 1.0f / (1.0f + __expf(-g[q]));
-    a[q] = dz[q] * u[q] * (s * (1.0f + g[q] * (1.0f - s)));
-    b[q] = dz[q] * g[q] * s;
-  }
+  gated_grad8(g, u, dz, a, b);
+  store8(dG + v * 8, a);
+  store8(dU + v * 8, b);
+}
+
+// The same from G and U in 8 bits: 8 elements of a row share a scale.
+__global__ __launch_bounds__(256) void gated_grad_keep8_kernel(Keep8 k, const bf16* __restrict__ dZ,
+                                                               bf16* __restrict__ dG, bf16* __restrict__ dU,
+                                                               int64_t n8, int f8) {
+  const int64_t v = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (v >= n8) return;
+  const int64_t row = v / f8;
+  const int blocks = (f8 * 8 + kKeep8 - 1) / kKeep8;
+  const int64_t at = row * blocks + (int)(v - row * f8) / (kKeep8 / 8);
+  float g[8], u[8], dz[8], a[8], b[8];
+  keep8_unpack(*reinterpret_cast<const u32x2*>(k.G + v * 8), k.sG[at], g);
+  keep8_unpack(*reinterpret_cast<const u32x2*>(k.U + v * 8), k.sU[at], u);
+  load8(dZ + v * 8, dz);
+  gated_grad8(g, u, dz, a, b);
   store8(dG + v * 8, a);
   store8(dU + v * 8, b);
 }
@@ -802,6 +826,14 @@ hipError_t launch_gated_grad(const Prob& p, const void* GU, const void* dZ, void
   else
     gated_grad_kernel<float><<<g, 256, 0, st>>>((const float*)GU, (const float*)GU + n, (const float*)dZ, (float*)dG,
                                                 (float*)dU, n8);
+  return hipGetLastError();
+}
+
+hipError_t launch_gated_grad8(const Prob& p, const Keep8& k, const void* dZ, void* dG, void* dU, hipStream_t st) {
+  note_launch("gated_grad8", st);
+  const int64_t n8 = p.M * p.f / 8;
+  gated_grad_keep8_kernel<<<(unsigned)((n8 + 255) / 256), 256, 0, st>>>(k, (const bf16*)dZ, (bf16*)dG, (bf16*)dU, n8,
+                                                                        p.f / 8);
   return hipGetLastError();
 }
 

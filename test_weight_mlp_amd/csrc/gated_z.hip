@@ -15,12 +15,18 @@
 
 namespace ipttt {
 
-// SAVE: also write G = H W_gate^T and U = H W_up^T (dtype) for the backward.
-template <typename T, bool SAVE>
+// What a Z kernel keeps of G = H W_gate^T and U = H W_up^T for the backward:
+// nothing, both in dtype, or both in 8 bits (bf16 data) with their scales.
+enum { KEEP_NONE = 0, KEEP_ALL = 1, KEEP_8 = 2 };
+struct Kept {
+  void *G, *U;
+  float *sG, *sU;
+};
+
+template <typename T, int KEEP>
 __global__ __launch_bounds__(kThreads) void gated_z_kernel(const T* __restrict__ H, const T* __restrict__ Wg,
                                                            const T* __restrict__ Wu, T* __restrict__ Z,
-                                                           T* __restrict__ Gs, T* __restrict__ Us, int64_t M, int d,
-                                                           int f) {
+                                                           Kept kept, int64_t M, int d, int f) {
   typedef Geo<T, 128, 128> G;
   constexpr int LDC = G::BN + G::VE;
   constexpr int kStage = (G::BM + 2 * G::BN) * G::LDK;
@@ -67,7 +73,7 @@ __global__ __launch_bounds__(kThreads) void gated_z_kernel(const T* __restrict__
 
   T* lC = lds;
   // which = 0: Z, 1: G, 2: U
-  auto emit = [&](int which, T* out) {
+  auto stage = [&](int which) {
 #pragma unroll
     for (int mb = 0; mb < G::MB; ++mb)
 #pragma unroll
@@ -80,14 +86,22 @@ __global__ __launch_bounds__(kThreads) void gated_z_kernel(const T* __restrict__
           lC[r * LDC + c] = from_f32<T>(which == 0 ? silu_f32(g) * u : which == 1 ? g : u);
         }
     __syncthreads();
-    store_tile_rows<T, G::BM, G::BN, LDC>(lC, out, m0, mrows, n0, nrows, f, tid);
   };
-  emit(0, Z);
-  if constexpr (SAVE) {
-    __syncthreads();
-    emit(1, Gs);
-    __syncthreads();
-    emit(2, Us);
+  stage(0);
+  store_tile_rows<T, G::BM, G::BN, LDC>(lC, Z, m0, mrows, n0, nrows, f, tid);
+  if constexpr (KEEP != KEEP_NONE) {
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      __syncthreads();
+      stage(1 + o);
+      void* to = o == 0 ? kept.G : kept.U;
+      if constexpr (KEEP == KEEP_8)
+        store_rows_keep8<G::BM, G::BN, kThreads>([&](int r, int c) { return lC + r * LDC + c; },
+                                                 static_cast<uint8_t*>(to), o == 0 ? kept.sG : kept.sU, m0, mrows, n0,
+                                                 nrows, f, tid);
+      else
+        store_tile_rows<T, G::BM, G::BN, LDC>(lC, static_cast<T*>(to), m0, mrows, n0, nrows, f, tid);
+    }
   }
 }
 
@@ -97,11 +111,10 @@ __global__ __launch_bounds__(kThreads) void gated_z_kernel(const T* __restrict__
 // stages it through LDS and writes Z rows with non-temporal stores.  The
 // tiles are grouped 4 token tiles at a time so that an XCD's workgroups share
 // H and weight panels in its L2.
-template <bool SAVE>
+template <int KEEP>
 __global__ __launch_bounds__(512) void gated_z_fast_kernel(const bf16* __restrict__ H, const bf16* __restrict__ Wg,
                                                          const bf16* __restrict__ Wu, bf16* __restrict__ Z,
-                                                         bf16* __restrict__ Gs, bf16* __restrict__ Us, int64_t M, int d,
-                                                         int f) {
+                                                         Kept kept, int64_t M, int d, int f) {
   using namespace pingpong;
   __shared__ __attribute__((aligned(1024))) bf16 lds[LDS_ELEMS];
   const int tid = threadIdx.x;
@@ -130,12 +143,18 @@ __global__ __launch_bounds__(512) void gated_z_fast_kernel(const bf16* __restric
     core::lds_barrier();
     store_rows_swz<BM, BN, LDR, 512, true>(stg, Z, mt, 0, mrows, nt, nrows, f, tid);
     core::lds_barrier();
-    if constexpr (SAVE) {
+    if constexpr (KEEP != KEEP_NONE) {
 #pragma unroll
       for (int o = 0; o < 2; ++o) {
         stage_wave(stg, [&](int mb, int nb, int j) { return acc[o][mb][nb][j]; });
         core::lds_barrier();
-        store_rows_swz<BM, BN, LDR, 512, true>(stg, o == 0 ? Gs : Us, mt, 0, mrows, nt, nrows, f, tid);
+        void* to = o == 0 ? kept.G : kept.U;
+        if constexpr (KEEP == KEEP_8)
+          store_rows_keep8<BM, BN, 512>([&](int r, int c) { return stg + swz_elem<LDR>(r, c); },
+                                        static_cast<uint8_t*>(to), o == 0 ? kept.sG : kept.sU, mt, mrows, nt, nrows, f,
+                                        tid);
+        else
+          store_rows_swz<BM, BN, LDR, 512, true>(stg, static_cast<bf16*>(to), mt, 0, mrows, nt, nrows, f, tid);
         core::lds_barrier();
       }
     }
@@ -143,12 +162,11 @@ __global__ __launch_bounds__(512) void gated_z_fast_kernel(const bf16* __restric
   pingpong::run(lds, tiles_m * tiles_n, operands, epilogue);
 }
 
-hipError_t launch_gated_z(const Prob& p, const void* H, const void* Wg, const void* Wu, void* Z, void* GU,
-                          hipStream_t st) {
-  const size_t e = p.dtype == 1 ? 2 : 4;
-  void* Gs = GU;
-  void* Us = GU != nullptr ? static_cast<char*>(GU) + (size_t)p.M * p.f * e : nullptr;
-  const bool save = GU != nullptr;
+namespace {
+
+template <int KEEP>
+hipError_t launch_kept(const Prob& p, const void* H, const void* Wg, const void* Wu, void* Z, const Kept& kept,
+                       hipStream_t st) {
   const int64_t tiles = ((p.M + 127) / 128) * ((p.f + 127) / 128);
   note_launch("gated_z", st);
   if (p.dtype == 1 && p.d % 64 == 0) {
@@ -158,28 +176,33 @@ hipError_t launch_gated_z(const Prob& p, const void* H, const void* Wg, const vo
       (void)hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
     const int64_t fast_tiles = ((p.M + 255) / 256) * ((p.f + 127) / 128);
     const int64_t g = std::min<int64_t>(std::max(8, cus / 8 * 8), (fast_tiles + 7) / 8 * 8);
-    if (save)
-      gated_z_fast_kernel<true><<<(unsigned)g, 512, 0, st>>>((const bf16*)H, (const bf16*)Wg, (const bf16*)Wu,
-                                                          (bf16*)Z, (bf16*)Gs, (bf16*)Us, p.M, p.d, p.f);
-    else
-      gated_z_fast_kernel<false><<<(unsigned)g, 512, 0, st>>>((const bf16*)H, (const bf16*)Wg, (const bf16*)Wu,
-                                                           (bf16*)Z, nullptr, nullptr, p.M, p.d, p.f);
+    gated_z_fast_kernel<KEEP><<<(unsigned)g, 512, 0, st>>>((const bf16*)H, (const bf16*)Wg, (const bf16*)Wu, (bf16*)Z,
+                                                         kept, p.M, p.d, p.f);
   } else if (p.dtype == 1) {
-    if (save)
-      gated_z_kernel<bf16, true><<<(unsigned)tiles, kThreads, 0, st>>>(
-          (const bf16*)H, (const bf16*)Wg, (const bf16*)Wu, (bf16*)Z, (bf16*)Gs, (bf16*)Us, p.M, p.d, p.f);
-    else
-      gated_z_kernel<bf16, false><<<(unsigned)tiles, kThreads, 0, st>>>(
-          (const bf16*)H, (const bf16*)Wg, (const bf16*)Wu, (bf16*)Z, nullptr, nullptr, p.M, p.d, p.f);
+    gated_z_kernel<bf16, KEEP><<<(unsigned)tiles, kThreads, 0, st>>>((const bf16*)H, (const bf16*)Wg, (const bf16*)Wu,
+                                                                     (bf16*)Z, kept, p.M, p.d, p.f);
+  } else if constexpr (KEEP == KEEP_8) {
+    return hipErrorInvalidValue;  // 8 bits are for bf16 data
   } else {
-    if (save)
-      gated_z_kernel<float, true><<<(unsigned)tiles, kThreads, 0, st>>>(
-          (const float*)H, (const float*)Wg, (const float*)Wu, (float*)Z, (float*)Gs, (float*)Us, p.M, p.d, p.f);
-    else
-      gated_z_kernel<float, false><<<(unsigned)tiles, kThreads, 0, st>>>(
-          (const float*)H, (const float*)Wg, (const float*)Wu, (float*)Z, nullptr, nullptr, p.M, p.d, p.f);
+    gated_z_kernel<float, KEEP><<<(unsigned)tiles, kThreads, 0, st>>>(
+        (const float*)H, (const float*)Wg, (const float*)Wu, (float*)Z, kept, p.M, p.d, p.f);
   }
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gated_z(const Prob& p, const void* H, const void* Wg, const void* Wu, void* Z, void* GU,
+                          hipStream_t st) {
+  if (GU == nullptr) return launch_kept<KEEP_NONE>(p, H, Wg, Wu, Z, Kept{}, st);
+  const size_t e = p.dtype == 1 ? 2 : 4;
+  return launch_kept<KEEP_ALL>(p, H, Wg, Wu, Z, Kept{GU, static_cast<char*>(GU) + (size_t)p.M * p.f * e, nullptr, nullptr},
+                               st);
+}
+
+hipError_t launch_gated_z8(const Prob& p, const void* H, const void* Wg, const void* Wu, void* Z, const Keep8& k,
+                           hipStream_t st) {
+  return launch_kept<KEEP_8>(p, H, Wg, Wu, Z, Kept{k.G, k.U, k.sG, k.sU}, st);
 }
 
 }  // namespace ipttt

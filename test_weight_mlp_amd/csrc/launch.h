@@ -51,6 +51,14 @@ hipError_t launch_segments(const Prob& p, const int64_t* starts, int64_t n_start
 // GU: NULL, or [2, M, f] dtype receiving G = H W_gate^T then U = H W_up^T.
 hipError_t launch_gated_z(const Prob& p, const void* H, const void* Wg, const void* Wu, void* Z, void* GU,
                           hipStream_t st);
+// G and U in 8 bits: integers [M, f] each and the scales [M, ceil(f / 64)] of
+// blocks of 64 (bf16 data only).
+struct Keep8 {
+  uint8_t *G, *U;
+  float *sG, *sU;
+};
+hipError_t launch_gated_z8(const Prob& p, const void* H, const void* Wg, const void* Wu, void* Z, const Keep8& k,
+                           hipStream_t st);
 // scratch: d*d + 5*d elements (transposed W_target and conv weights)
 hipError_t launch_target(const Prob& p, const void* X0, const void* convw, const void* Wt,
                          const uint8_t* segs, void* V, void* scratch, hipStream_t st);
@@ -207,6 +215,8 @@ hipError_t launch_gated_z_bwd(const Prob& p, const void* H, const void* Wg, cons
                               void* dU, hipStream_t st);
 // dG, dU from the saved G and U (GU as written by launch_gated_z), elementwise.
 hipError_t launch_gated_grad(const Prob& p, const void* GU, const void* dZ, void* dG, void* dU, hipStream_t st);
+// The same from G and U in 8 bits.
+hipError_t launch_gated_grad8(const Prob& p, const Keep8& k, const void* dZ, void* dG, void* dU, hipStream_t st);
 // dX0 and the conv weight-gradient partials (part: kConvParts * d * 5 floats)
 hipError_t launch_conv_bwd(const Prob& p, const float* dY, const void* X0, const void* convw, const uint8_t* segs,
                            void* dX0, float* part, hipStream_t st);

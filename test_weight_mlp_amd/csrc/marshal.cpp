@@ -1,5 +1,5 @@
-// Argument marshalling of the attention half's binding: tensors are checked
-// against the problem and handed to the C ABI.  A single token's norm and rotation
+// Argument marshalling of the binding of the attention half and of the rest of
+// the block: tensors are checked against the problem and handed to the C ABI.  A single token's norm and rotation
 // takes the device 3.5 us; looking at its eight tensors from Python took 5 us,
 // here it takes a fraction of one.
 //
@@ -22,6 +22,10 @@ decltype(&ipttt_qk_norm_rope) g_qk;
 decltype(&ipttt_qk_norm_rope_backward) g_qk_bwd;
 decltype(&ipttt_attention) g_attn;
 decltype(&ipttt_attention_backward) g_attn_bwd;
+decltype(&ipttt_norm) g_norm;
+decltype(&ipttt_norm_backward) g_norm_bwd;
+decltype(&ipttt_linear) g_linear;
+decltype(&ipttt_linear_backward) g_linear_bwd;
 
 at::ScalarType type_of(int32_t dtype) { return dtype == IPTTT_BF16 ? at::kBFloat16 : at::kFloat; }
 
@@ -60,6 +64,25 @@ class Reader {
     heads(what, rows, n, dim, h);
     return h;
   }
+  // [rows, columns] of the problem's type, any row stride
+  void rows(const char* what, int64_t rows, int64_t columns, ipttt_rows* r) {
+    const at::Tensor* t = next(what);
+    if (t == nullptr) return;
+    if (t->dim() != 2 || t->size(0) != rows || t->size(1) != columns || t->scalar_type() != type_of(dtype_) ||
+        !t->is_cuda() || t->stride(1) != 1) {
+      fail(*t, what, " device tensor with a contiguous last dimension", {rows, columns}, type_of(dtype_));
+      return;
+    }
+    if (here(*t, what)) *r = ipttt_rows{t->data_ptr(), t->stride(0)};
+  }
+  const ipttt_rows* maybe_rows(const char* what, int64_t n, int64_t columns, ipttt_rows* r) {
+    if (!ok_ || *args_ == Py_None) {
+      ++args_;
+      return nullptr;
+    }
+    rows(what, n, columns, r);
+    return r;
+  }
   // contiguous [a] (b = 0) or [a, b]
   void* flat(const char* what, int64_t a, int64_t b, at::ScalarType type) {
     const at::Tensor* t = next(what);
@@ -72,12 +95,12 @@ class Reader {
     }
     return here(*t, what) ? t->data_ptr() : nullptr;
   }
-  void* maybe_flat(const char* what, int64_t a, at::ScalarType type) {
+  void* maybe_flat(const char* what, int64_t a, at::ScalarType type, int64_t b = 0) {
     if (!ok_ || *args_ == Py_None) {
       ++args_;
       return nullptr;
     }
-    return flat(what, a, 0, type);
+    return flat(what, a, b, type);
   }
   // the plan's copy on the device
   const void* plan_table() {
@@ -292,20 +315,126 @@ PyObject* attention_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// bind(qk, qk_backward, attention, attention_backward): the entries' addresses
-PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
+// norm(problem address, x, w, b, y, stream)
+PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (!arity(n, 6, reinterpret_cast<const void*>(g_norm))) return nullptr;
+    const ipttt_norm_problem* p = pointer<const ipttt_norm_problem>(a[0]);
+    if (p == nullptr) return nullptr;
+    Reader r(a + 1, p->dtype);
+    ipttt_rows x, y;
+    r.rows("x", p->rows, p->dim, &x);
+    const void* w = r.maybe_flat("w", p->dim, type_of(p->dtype));
+    const void* b = r.maybe_flat("b", p->dim, type_of(p->dtype));
+    r.rows("y", p->rows, p->dim, &y);
+    if (!r.ok()) return nullptr;
+    void* stream = pointer<void>(a[5]);
+    return call([&] { return g_norm(p, &x, w, b, &y, stream); });
+  });
+}
+
+// norm_backward(problem address, x, w, dy, dres, dx, dw, db, ws, stream)
+PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (!arity(n, 10, reinterpret_cast<const void*>(g_norm_bwd))) return nullptr;
+    const ipttt_norm_problem* p = pointer<const ipttt_norm_problem>(a[0]);
+    if (p == nullptr) return nullptr;
+    Reader r(a + 1, p->dtype);
+    ipttt_rows x, dy, dres, dx;
+    r.rows("x", p->rows, p->dim, &x);
+    const void* w = r.maybe_flat("w", p->dim, type_of(p->dtype));
+    r.rows("dy", p->rows, p->dim, &dy);
+    const ipttt_rows* more = r.maybe_rows("dres", p->rows, p->dim, &dres);
+    r.rows("dx", p->rows, p->dim, &dx);
+    void* dw = r.maybe_flat("dw", p->dim, at::kFloat);
+    void* db = r.maybe_flat("db", p->dim, at::kFloat);
+    size_t bytes;
+    void* ws = r.workspace(&bytes);
+    if (!r.ok()) return nullptr;
+    void* stream = pointer<void>(a[9]);
+    return call([&] {
+      return g_norm_bwd(p, &x, w, &dy, more, &dx, static_cast<float*>(dw), static_cast<float*>(db), ws, bytes, stream);
+    });
+  });
+}
+
+// linear(problem address, x, W, b, res, y, pre, ws, stream)
+PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (!arity(n, 9, reinterpret_cast<const void*>(g_linear))) return nullptr;
+    const ipttt_linear_problem* p = pointer<const ipttt_linear_problem>(a[0]);
+    if (p == nullptr) return nullptr;
+    Reader r(a + 1, p->dtype);
+    ipttt_rows x, res, y, pre;
+    r.rows("x", p->rows, p->in_dim, &x);
+    const void* W = r.flat("W", p->out_dim, p->in_dim, type_of(p->dtype));
+    const void* b = r.maybe_flat("b", p->out_dim, type_of(p->dtype));
+    const ipttt_rows* more = r.maybe_rows("res", p->rows, p->out_dim, &res);
+    r.rows("y", p->rows, p->out_dim, &y);
+    const ipttt_rows* kept = r.maybe_rows("pre", p->rows, p->out_dim, &pre);
+    size_t bytes;
+    void* ws = r.workspace(&bytes);
+    if (!r.ok()) return nullptr;
+    void* stream = pointer<void>(a[8]);
+    return call([&] { return g_linear(p, &x, W, b, more, &y, kept, ws, bytes, stream); });
+  });
+}
+
+// linear_backward(problem address, x, W, pre, dy, dx, dW, db, ws, stream)
+PyObject* linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (!arity(n, 10, reinterpret_cast<const void*>(g_linear_bwd))) return nullptr;
+    const ipttt_linear_problem* p = pointer<const ipttt_linear_problem>(a[0]);
+    if (p == nullptr) return nullptr;
+    Reader r(a + 1, p->dtype);
+    ipttt_rows x, pre, dy, dx;
+    r.rows("x", p->rows, p->in_dim, &x);
+    const void* W = r.flat("W", p->out_dim, p->in_dim, type_of(p->dtype));
+    const ipttt_rows* kept = r.maybe_rows("pre", p->rows, p->out_dim, &pre);
+    r.rows("dy", p->rows, p->out_dim, &dy);
+    const ipttt_rows* to = r.maybe_rows("dx", p->rows, p->in_dim, &dx);
+    void* dW = r.maybe_flat("dW", p->out_dim, type_of(p->grad_dtype), p->in_dim);
+    void* db = r.maybe_flat("db", p->out_dim, at::kFloat);
+    size_t bytes;
+    void* ws = r.workspace(&bytes);
+    if (!r.ok()) return nullptr;
+    void* stream = pointer<void>(a[9]);
+    return call([&] {
+      return g_linear_bwd(p, &x, W, kept, &dy, to, dW, static_cast<float*>(db), ws, bytes, stream);
+    });
+  });
+}
+
+bool addresses(PyObject* const* a, Py_ssize_t n, void* (&f)[4]) {
   if (n != 4) {
     PyErr_SetString(PyExc_TypeError, "four addresses");
-    return nullptr;
+    return false;
   }
-  void* f[4];
   for (int i = 0; i < 4; ++i) {
     f[i] = pointer<void>(a[i]);
     if (f[i] == nullptr) {
       if (PyErr_Occurred() == nullptr) PyErr_SetString(PyExc_ValueError, "a null address");
-      return nullptr;
+      return false;
     }
   }
+  return true;
+}
+
+// bind_block(norm, norm_backward, linear, linear_backward): the entries' addresses
+PyObject* bind_block(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  void* f[4];
+  if (!addresses(a, n, f)) return nullptr;
+  g_norm = reinterpret_cast<decltype(g_norm)>(f[0]);
+  g_norm_bwd = reinterpret_cast<decltype(g_norm_bwd)>(f[1]);
+  g_linear = reinterpret_cast<decltype(g_linear)>(f[2]);
+  g_linear_bwd = reinterpret_cast<decltype(g_linear_bwd)>(f[3]);
+  Py_RETURN_NONE;
+}
+
+// bind(qk, qk_backward, attention, attention_backward): the entries' addresses
+PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  void* f[4];
+  if (!addresses(a, n, f)) return nullptr;
   g_qk = reinterpret_cast<decltype(g_qk)>(f[0]);
   g_qk_bwd = reinterpret_cast<decltype(g_qk_bwd)>(f[1]);
   g_attn = reinterpret_cast<decltype(g_attn)>(f[2]);
@@ -324,9 +453,14 @@ PyMethodDef g_methods[] = {
     {"qk_backward", fast<qk_backward>(), METH_FASTCALL, "ipttt_qk_norm_rope_backward"},
     {"attention", fast<attention>(), METH_FASTCALL, "ipttt_attention"},
     {"attention_backward", fast<attention_backward>(), METH_FASTCALL, "ipttt_attention_backward"},
+    {"bind_block", fast<bind_block>(), METH_FASTCALL, "the entries of the rest of the block, by address"},
+    {"norm", fast<norm>(), METH_FASTCALL, "ipttt_norm"},
+    {"norm_backward", fast<norm_backward>(), METH_FASTCALL, "ipttt_norm_backward"},
+    {"linear", fast<linear>(), METH_FASTCALL, "ipttt_linear"},
+    {"linear_backward", fast<linear_backward>(), METH_FASTCALL, "ipttt_linear_backward"},
     {nullptr, nullptr, 0, nullptr},
 };
-PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", "argument marshalling of the attention half", -1,
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", "argument marshalling of the block's calls", -1,
                         g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
