@@ -5,6 +5,7 @@
 #include "block.h"
 #include "common.h"
 #include "launch.h"
+#include "ring.h"
 
 #include <algorithm>
 #include <type_traits>
@@ -137,6 +138,223 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(GemmArgs g) {
       }
 }
 
+// --------------------------------------------------------------- bf16 tiles
+
+// How a product is cut: `whole` tiles over all of K, then the rest in `parts` of
+// `per` stages each, whose fp32 partial tiles a second launch joins.
+struct RingPlan {
+  int nw;                 // 8: tiles of 256 x 256, 4: of 128 x 128
+  int tiles_m, tiles_n, whole, split, parts, per, stages;
+};
+
+// One row's NJ neighbouring columns of a finished tile.
+template <int NJ>
+__device__ __forceinline__ void finish_row(const GemmArgs& g, int64_t m, int64_t n, const float (&bias)[NJ], float (&v)[NJ]) {
+  typedef bf16 vec __attribute__((ext_vector_type(NJ)));
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) v[j] += bias[j];
+  if (g.pre.p != nullptr) {
+    vec o;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) o[j] = (bf16)v[j];
+    *reinterpret_cast<vec*>(static_cast<bf16*>(g.pre.p) + m * g.pre.ld + n) = o;
+  }
+  if (g.act != IPTTT_ACT_NONE) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) v[j] = act_f32(g.act, v[j]);
+  }
+  if (g.res.p != nullptr) {
+    const vec r = *reinterpret_cast<const vec*>(static_cast<const bf16*>(g.res.p) + m * g.res.ld + n);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) v[j] += (float)r[j];
+  }
+  vec o;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) o[j] = (bf16)v[j];
+  *reinterpret_cast<vec*>(static_cast<bf16*>(g.c.p) + m * g.c.ld + n) = o;
+}
+
+// Finishes block row i of a tile at (m0, n0): this lane's four rows of it.  With B's
+// rows in the order of PERM (K contiguous) a lane has NJ neighbouring columns and
+// the whole epilogue; K-major products have none and store column by column.
+template <int NW, bool BK>
+__device__ __forceinline__ void finish_block(const GemmArgs& g, int64_t m0, int64_t n0, int i,
+                                             ring::f4 (&acc)[ring::Geo<NW>::NJ]) {
+  typedef ring::Geo<NW> G;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  const int64_t m = m0 + wm * G::WM + i * 16 + 4 * (lane >> 4);
+  if constexpr (!BK) {
+    const int64_t n = n0 + wn * G::WN + (lane & 15) * G::NJ;
+    if (n >= g.N) return;
+    float bias[G::NJ];
+#pragma unroll
+    for (int j = 0; j < G::NJ; ++j) bias[j] = g.bias != nullptr ? (float)static_cast<const bf16*>(g.bias)[n + j] : 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (m + e >= g.M) break;
+      float v[G::NJ];
+#pragma unroll
+      for (int j = 0; j < G::NJ; ++j) v[j] = acc[j][e];
+      finish_row<G::NJ>(g, m + e, n, bias, v);
+    }
+  } else {
+    const int64_t n = n0 + wn * G::WN + (lane & 15);
+    const int blocks = n < g.N ? (int)min((int64_t)G::NJ, (g.N - n + 15) / 16) : 0;
+    auto store = [&](auto* c) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (m + e >= g.M) break;
+        auto* row = c + (m + e) * g.c.ld + n;
+#pragma unroll
+        for (int j = 0; j < G::NJ; ++j)
+          if (j < blocks) row[j * 16] = from_f32<std::remove_pointer_t<decltype(c)>>(acc[j][e]);
+      }
+    };
+    if (g.c_f32) store(static_cast<float*>(g.c.p));
+    else store(static_cast<bf16*>(g.c.p));
+  }
+}
+
+// The tile of an item, and the part of it (-1: whole).
+__device__ __forceinline__ void ring_item(const RingPlan& p, int t, int64_t& m0, int64_t& n0, int& part) {
+  int tile = t;
+  part = -1;
+  if (t >= p.whole) {
+    tile = p.whole + (t - p.whole) / p.parts;
+    part = (t - p.whole) % p.parts;
+  }
+  int tm, tn;
+  // four rows of tiles walked together: an XCD's workgroups share both operands' panels
+  grouped_tile(tile, p.tiles_m, p.tiles_n, 4, tm, tn);
+  m0 = (int64_t)tm * p.nw * 32;
+  n0 = (int64_t)tn * p.nw * 32;
+}
+
+template <int NW, bool AK, bool BK>
+__device__ __forceinline__ void ring_product(const bf16* __restrict__ A, const bf16* __restrict__ B, const GemmArgs& g,
+                                             const RingPlan& p, char* lds) {
+  typedef ring::Geo<NW> G;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  auto stages = [&](int t, int& s0, int& n) {
+    s0 = 0;
+    n = p.stages;
+    if (t >= p.whole) {
+      s0 = (t - p.whole) % p.parts * p.per;
+      n = min(p.per, p.stages - s0);
+    }
+  };
+  auto open_a = [&](int t, ring::Loader<NW, AK>& l) {
+    int64_t m0, n0;
+    int part;
+    ring_item(p, t, m0, n0, part);
+    l.init(A + (AK ? m0 : m0 * g.a.ld), g.a.ld, g.M - m0, g.K, wave, lane, [](int r) { return r; });
+  };
+  auto open_b = [&](int t, ring::Loader<NW, BK>& l) {
+    int64_t m0, n0;
+    int part;
+    ring_item(p, t, m0, n0, part);
+    l.init(B + (BK ? n0 : n0 * g.b.ld), g.b.ld, g.N - n0, g.K, wave, lane, [](int r) { return ring::perm_row<NW>(r); });
+  };
+  auto epilogue = [&](int t, ring::f4 (&acc)[G::MI][G::NJ]) {
+    int64_t m0, n0;
+    int part;
+    ring_item(p, t, m0, n0, part);
+    if (part >= 0) {
+      ring::f4* to = reinterpret_cast<ring::f4*>(g.part) + (int64_t)(t - p.whole) * G::MI * G::NJ * G::NT + threadIdx.x;
+#pragma unroll
+      for (int i = 0; i < G::MI; ++i)
+#pragma unroll
+        for (int j = 0; j < G::NJ; ++j) to[(i * G::NJ + j) * G::NT] = acc[i][j];
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < G::MI; ++i) finish_block<NW, BK>(g, m0, n0, i, acc[i]);
+  };
+  ring::run<NW, AK, BK>(lds, p.whole, p.split * p.parts, stages, open_a, open_b, epilogue);
+}
+
+template <int NW, bool AK, bool BK>
+__global__ __launch_bounds__(ring::Geo<NW>::NT, ring::Geo<NW>::MAX_GROUPS) void ring_kernel(GemmArgs g, RingPlan p) {
+  __shared__ __attribute__((aligned(1024))) char lds[ring::Geo<NW>::LDS_BYTES];
+  ring_product<NW, AK, BK>(static_cast<const bf16*>(g.a.p), static_cast<const bf16*>(g.b.p), g, p, lds);
+}
+
+// Sums the parts of a split tile in order and finishes it; blockIdx.y takes a block
+// row of it.
+template <int NW, bool BK>
+__global__ __launch_bounds__(ring::Geo<NW>::NT) void ring_join_kernel(GemmArgs g, RingPlan p) {
+  typedef ring::Geo<NW> G;
+  const int i = blockIdx.y, t = p.whole + blockIdx.x * p.parts;
+  const ring::f4* from = reinterpret_cast<const ring::f4*>(g.part) +
+                         ((int64_t)blockIdx.x * p.parts * G::MI + i) * G::NJ * G::NT + threadIdx.x;
+  ring::f4 acc[G::NJ];
+#pragma unroll
+  for (int j = 0; j < G::NJ; ++j) acc[j] = from[j * G::NT];
+  for (int q = 1; q < p.parts; ++q) {
+    from += (int64_t)G::MI * G::NJ * G::NT;
+#pragma unroll
+    for (int j = 0; j < G::NJ; ++j) acc[j] += from[j * G::NT];
+  }
+  int64_t m0, n0;
+  int part;
+  ring_item(p, t, m0, n0, part);
+  finish_block<NW, BK>(g, m0, n0, i, acc);
+}
+
+constexpr int kCus = 256;
+
+// The cut for which an estimate of the product's time is least.
+RingPlan plan_ring(const GemmArgs& g) {
+  RingPlan best{};
+  double least = 1e300;
+  for (const int nw : {8, 4}) {
+    const int64_t w = nw * 32, tm = (g.M + w - 1) / w, tn = (g.N + w - 1) / w, tiles = tm * tn;
+    const int64_t groups = nw == 8 ? kCus : 2 * kCus;
+    const int stages = (int)((g.K + ring::KS - 1) / ring::KS);
+    const double stage = nw == 8 ? 1.6 : 1.0, lone = nw == 8 ? 1.2 : 0.7;   // us, on a full and a half empty device
+    auto consider = [&](int64_t whole, int parts) {
+      const int per = (stages + parts - 1) / parts;
+      parts = (stages + per - 1) / per;
+      const int64_t split = tiles - whole, items = split * parts;
+      const int64_t full = whole / groups;
+      double t = full * (stages * stage + 2.0);
+      const int64_t rest = whole % groups + items;
+      t += (double)((rest + groups - 1) / groups) * (per * (rest <= groups / 2 ? lone : stage) + 2.0);
+      if (parts > 1) t += 5.0 + (double)items * w * w * 8 / 4.0e6;
+      if (t >= least) return;
+      least = t;
+      best = RingPlan{nw, (int)tm, (int)tn, (int)(parts > 1 ? whole : tiles), (int)(parts > 1 ? split : 0), parts, per, stages};
+    };
+    consider(tiles, 1);
+    const int64_t whole = tiles / groups * groups, rem = tiles - whole;
+    if (rem > 0)
+      for (int64_t parts = 2; parts <= 32 && parts * 2 <= stages && rem * parts <= 2 * groups; ++parts) consider(whole, (int)parts);
+  }
+  return best;
+}
+
+template <int NW>
+hipError_t launch_ring(const GemmArgs& g, const RingPlan& p, hipStream_t st) {
+  typedef ring::Geo<NW> G;
+  const int64_t items = (int64_t)p.whole + (int64_t)p.split * p.parts;
+  const unsigned grid = (unsigned)std::min<int64_t>(kCus * G::MAX_GROUPS, (items + 7) / 8 * 8);
+  note_launch("linear", st);
+  if (!g.a_kmaj && !g.b_kmaj) ring_kernel<NW, false, false><<<grid, G::NT, 0, st>>>(g, p);
+  else if (!g.a_kmaj) ring_kernel<NW, false, true><<<grid, G::NT, 0, st>>>(g, p);
+  else ring_kernel<NW, true, true><<<grid, G::NT, 0, st>>>(g, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.split == 0) return e;
+  note_launch("linear_join", st);
+  const dim3 j((unsigned)p.split, G::MI);
+  if (!g.b_kmaj) ring_join_kernel<NW, false><<<j, G::NT, 0, st>>>(g, p);
+  else ring_join_kernel<NW, true><<<j, G::NT, 0, st>>>(g, p);
+  return hipGetLastError();
+}
+
+size_t ring_bytes(const RingPlan& p) {
+  return (size_t)p.split * p.parts * (p.nw * 32) * (p.nw * 32) * sizeof(float);
+}
+
 // ------------------------------------------------- the activation's gradient
 
 // A thread takes 8 columns of every eighth row of a strip of rows; the columns'
@@ -202,13 +420,16 @@ void launch_general(const GemmArgs& g, hipStream_t st) {
 
 }  // namespace
 
-size_t gemm_workspace(const GemmArgs&) { return 0; }
+size_t gemm_workspace(const GemmArgs& g) { return g.dtype == 1 ? ring_bytes(plan_ring(g)) : 0; }
 
 hipError_t launch_gemm(const GemmArgs& g, hipStream_t st) {
   if (g.a_kmaj && !g.b_kmaj) return hipErrorInvalidValue;  // no caller has such a product
+  if (g.dtype == 1) {
+    const RingPlan p = plan_ring(g);
+    return p.nw == 8 ? launch_ring<8>(g, p, st) : launch_ring<4>(g, p, st);
+  }
   note_launch("linear", st);
-  if (g.dtype == 1) launch_general<bf16>(g, st);
-  else launch_general<float>(g, st);
+  launch_general<float>(g, st);
   return hipGetLastError();
 }
 
