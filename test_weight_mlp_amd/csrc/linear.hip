@@ -243,17 +243,18 @@ __device__ __forceinline__ void ring_product(const bf16* __restrict__ A, const b
       n = min(p.per, p.stages - s0);
     }
   };
-  auto open_a = [&](int t, ring::Loader<NW, AK>& l) {
+  auto open_a = [&](int t, int s0, ring::Loader<NW, AK>& l) {
     int64_t m0, n0;
     int part;
     ring_item(p, t, m0, n0, part);
-    l.init(A + (AK ? m0 : m0 * g.a.ld), g.a.ld, g.M - m0, g.K, wave, lane, [](int r) { return r; });
+    l.init(A + (AK ? m0 : m0 * g.a.ld), g.a.ld, g.M - m0, g.K, s0, wave, lane, [](int r) { return r; });
   };
-  auto open_b = [&](int t, ring::Loader<NW, BK>& l) {
+  auto open_b = [&](int t, int s0, ring::Loader<NW, BK>& l) {
     int64_t m0, n0;
     int part;
     ring_item(p, t, m0, n0, part);
-    l.init(B + (BK ? n0 : n0 * g.b.ld), g.b.ld, g.N - n0, g.K, wave, lane, [](int r) { return ring::perm_row<NW>(r); });
+    l.init(B + (BK ? n0 : n0 * g.b.ld), g.b.ld, g.N - n0, g.K, s0, wave, lane,
+           [](int r) { return ring::perm_row<NW>(r); });
   };
   auto epilogue = [&](int t, ring::f4 (&acc)[G::MI][G::NJ]) {
     int64_t m0, n0;

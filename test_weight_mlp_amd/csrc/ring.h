@@ -31,6 +31,8 @@
 // of 128 x 128 instead of eight 1040.
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 #include "mfma_core.h"
 
@@ -54,65 +56,101 @@ struct Geo {
   static constexpr int MAX_GROUPS = NW == 8 ? 1 : 2;        // workgroups a CU
 };
 
-// Offsets past every buffer's end: such a load reads zeros.
-constexpr uint32_t kOut = 0xFFFFFFF0u;
+// Offsets past every buffer's end: such a load reads zeros.  (A tile's rows end
+// below 2^31: 255 strides of 2^22 elements, and K.)
+constexpr uint32_t kOut = 0x80000000u;
 
-// One operand's loads.  init(): p at the tile's first row (or column), n rows (or
-// columns) of it valid, K valid along k; stages count from k = 0.
+// One operand's loads.  issue() loads the stage that the cursor stands at, and
+// advance() moves it, so that the scalar work of a stage's addresses is done while
+// the fragment reads behind the loads are on their way.
 template <int NW, bool KMAJ>
 struct Loader {
   typedef Geo<NW> G;
   uint32_t voff[G::NL];
-  uint32_t chunk;        // rows: K element of this lane's pieces within a stage, by load (4 bits each, in 8s)
-  const char* base;
-  int64_t left, step;    // bytes valid from base on; bytes a stage
-  int K;                 // rows: valid k (K-major: unused)
+  uint32_t chunk;              // rows: K element of this lane's pieces within a stage, by load (4 bits each, in 8s)
+  __amdgpu_buffer_rsrc_t rs;   // rows: over the tile's rows, the stage's bytes into a row, and a row's valid bytes
+  uint32_t at, kbytes;
+  const char* base;            // K-major: the stage's first K row, the valid rows from it on, bytes a row
+  int krows;
+  uint32_t ldb, width;
 
-  // row(r): the operand's row that LDS row r holds
+  // p at the tile's first row (or column), n > 0 rows (or columns) of it valid, K
+  // valid along k; row(r): the operand's row that LDS row r holds
   template <class Row>
-  __device__ __forceinline__ void init(const bf16* p, int64_t ld, int64_t n, int64_t kvalid, int wave, int lane,
-                                       Row&& row) {
-    base = reinterpret_cast<const char*>(p);
-    const uint32_t ldb = (uint32_t)ld * 2u;
+  __device__ __forceinline__ void init(const bf16* p, int64_t ld, int64_t n, int64_t kvalid, int stage, int wave,
+                                       int lane, Row&& row) {
+    ldb = (uint32_t)ld * 2u;
+    const uint32_t here = (uint32_t)min(n, (int64_t)G::BM);
     if constexpr (!KMAJ) {
-      left = n > 0 ? (n - 1) * ld * 2 + kvalid * 2 : 0;
-      step = KS * 2;
-      K = (int)kvalid;
+      kbytes = (uint32_t)kvalid * 2u;
+      at = (uint32_t)stage * (KS * 2);
+      rs = core::make_operand(p, 0, (int64_t)(here - 1) * ldb + kbytes).rsrc;
       chunk = 0;
 #pragma unroll
       for (int j = 0; j < G::NL; ++j) {
         const int r = (wave * G::NL + j) * 8 + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
-        const int at = row(r);
-        voff[j] = at < n ? (uint32_t)at * ldb + (uint32_t)c * 16u : kOut;
+        const uint32_t from = (uint32_t)row(r);
+        voff[j] = from < here ? from * ldb + (uint32_t)c * 16u : kOut;
         chunk |= (uint32_t)c << (4 * j);
       }
     } else {
-      left = n > 0 ? (kvalid - 1) * ld * 2 + n * 2 : 0;
-      step = (int64_t)KS * ld * 2;
+      base = reinterpret_cast<const char*>(p) + (int64_t)stage * KS * ldb;
+      krows = (int)kvalid - stage * KS;
+      width = here * 2;
       constexpr int LPR = G::BM / 8, RPI = 64 / LPR;  // lanes a K row, K rows an instruction
 #pragma unroll
       for (int j = 0; j < G::NL; ++j) {
         const int r = (wave * G::NL + j) * RPI + lane / LPR, s = lane % LPR;
         const int u = (s >> 1) ^ (((r & 3) << 1) | ((r >> 3) & 1)), col = u * 16 + (s & 1) * 8;
-        voff[j] = col < n ? (uint32_t)r * ldb + (uint32_t)col * 2u : kOut;
+        voff[j] = (uint32_t)col < here ? (uint32_t)r * ldb + (uint32_t)col * 2u : kOut;
       }
     }
   }
-  __device__ __forceinline__ void issue(int s, char* slot, int wave) const {
-    const int64_t off = (int64_t)s * step;
-    const __amdgpu_buffer_rsrc_t rs = core::make_operand(base + off, 0, left - off).rsrc;
+  __device__ __forceinline__ void advance() {
+    if constexpr (!KMAJ) {
+      at += KS * 2;
+    } else {
+      base += (int64_t)KS * ldb;
+      krows -= KS;
+    }
+  }
+  // Tells the compiler that the cursor is the same in all lanes: it cannot see that
+  // after the branches that move a loader on to the next item.
+  __device__ __forceinline__ void uniform() {
+    if constexpr (!KMAJ) {
+      at = __builtin_amdgcn_readfirstlane(at);
+    } else {
+      const uint64_t p = reinterpret_cast<uint64_t>(base);
+      const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)p), hi = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32));
+      base = reinterpret_cast<const char*>((uint64_t)hi << 32 | lo);
+      krows = __builtin_amdgcn_readfirstlane(krows);
+    }
+  }
+  // last (a constant): the stage may be the last one, cut short by K
+  __device__ __forceinline__ void issue(char* slot, int wave, bool last) const {
     char* to = slot + wave * G::NL * 1024;
-    if (!KMAJ && (s + 1) * KS > K) {  // the last stage's pieces past K read as zero
+    if constexpr (!KMAJ) {
+      if (last && at + KS * 2 > kbytes) {  // pieces past K read as zero
+#pragma unroll
+        for (int j = 0; j < G::NL; ++j)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (core::lds_ptr_t)(to + j * 1024), 16,
+                                                   at + ((chunk >> (4 * j)) & 7) * 16 < kbytes ? voff[j] : kOut, at, 0,
+                                                   0);
+        return;
+      }
 #pragma unroll
       for (int j = 0; j < G::NL; ++j)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rs, (core::lds_ptr_t)(to + j * 1024), 16,
-            s * KS + (int)((chunk >> (4 * j)) & 7) * 8 < K ? voff[j] : kOut, 0, 0, 0);
-      return;
-    }
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (core::lds_ptr_t)(to + j * 1024), 16, voff[j], at, 0, 0);
+    } else {
+      // a resource over the stage's K rows, so that those past K read as zero
+      int end = 0x7FFFFFFF;
+      if (last && krows < KS) end = krows > 0 ? (int)((uint32_t)(krows - 1) * ldb + width) : 0;
+      const __amdgpu_buffer_rsrc_t r =
+          __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), (short)0, end, 0x00020000);
 #pragma unroll
-    for (int j = 0; j < G::NL; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (core::lds_ptr_t)(to + j * 1024), 16, voff[j], 0, 0, 0);
+      for (int j = 0; j < G::NL; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (core::lds_ptr_t)(to + j * 1024), 16, voff[j], 0, 0, 0);
+    }
   }
 };
 
@@ -183,8 +221,8 @@ struct Walk {
   }
 };
 
-// Walks the items.  stages(t) gives item t's first stage and their number (at least
-// one); open_a(t, loader) and open_b(t, loader) set its operands;
+// Walks the items.  stages(t, first, n) gives item t's first stage and their number
+// (at least one); open_a(t, first, loader) and open_b set its operands;
 // epilogue(t, acc) takes the finished tile: block (i, j), element e of a lane is
 // row wm * 64 + i * 16 + 4 * (lane / 16) + e and LDS row wn * WN + j * 16 + lane % 16
 // of B.  A and B are restrict so that the compiler tells the LDS reads apart from
@@ -204,55 +242,55 @@ __device__ __forceinline__ void run(char* lds, int n1, int n2, Stages&& stages, 
   Reader<NW, BK> rb;
   ra.init(wm * G::WM, lane);
   rb.init(wn * G::WN, lane);
-  auto m5 = [](int x) { return x >= NSLOT ? x - NSLOT : x; };
-  int sa = 0, ea = 0, sb = 0, eb = 0;  // the next stages to issue, and the items' ends
-  auto first = [&](const Walk& x, int& s, int& e) {
-    int n;
-    stages(x.t, s, n);
-    e = s + n;
+  // Stages left to issue of the items that the loaders stand at, and whether
+  // there is one.
+  int na = 0, nb = 0;
+  bool on_a = true, on_b = true;
+  auto enter_a = [&]() {
+    int s;
+    stages(wa.t, s, na);
+    open_a(wa.t, s, la);
   };
-  first(wa, sa, ea);
-  first(wb, sb, eb);
-  open_a(wa.t, la);
-  open_b(wb.t, lb);
-  int ia = 0, ib = 1;  // the slots they go to
-  auto issue_a = [&]() {
-    if (!wa.on()) return false;
-    la.issue(sa, lds + ia * G::SLOT, wave);
-    ia = m5(ia + 2);
-    if (++sa == ea) {
-      wa.next();
-      if (wa.on()) {
-        first(wa, sa, ea);
-        open_a(wa.t, la);
-      }
+  auto enter_b = [&]() {
+    int s;
+    stages(wb.t, s, nb);
+    open_b(wb.t, s, lb);
+  };
+  enter_a();
+  enter_b();
+  constexpr int RING = NSLOT * G::SLOT;
+  auto past = [](int x) { return x >= RING ? x - RING : x; };
+  int a = 0;  // where A of the stage to multiply lies; the slots after it: B, the next A, the next B, the A after
+  auto advance_a = [&]() {
+    if (--na > 0) {
+      la.advance();
+      return;
     }
-    return true;
+    wa.next();
+    on_a = wa.on();
+    if (on_a) enter_a();
   };
-  auto issue_b = [&]() {
-    if (!wb.on()) return;
-    lb.issue(sb, lds + ib * G::SLOT, wave);
-    ib = m5(ib + 2);
-    if (++sb == eb) {
-      wb.next();
-      if (wb.on()) {
-        first(wb, sb, eb);
-        open_b(wb.t, lb);
-      }
+  auto advance_b = [&]() {
+    if (--nb > 0) {
+      lb.advance();
+      return;
     }
+    wb.next();
+    on_b = wb.on();
+    if (on_b) enter_b();
   };
-  // all but the A part issued last have landed
-  bool more = false;
-  auto landed = [&]() {
+  la.issue(lds, wave, true);
+  advance_a();
+  lb.issue(lds + G::SLOT, wave, true);
+  advance_b();
+  bool more = on_a;  // whether the part issued last is an A that may still be on its way
+  if (on_a) {
+    la.issue(lds + 2 * G::SLOT, wave, true);
+    advance_a();
+  }
+  if constexpr (NW == 8) {
     if (more) core::wait_vmcnt<G::NL>();
     else core::wait_vmcnt<0>();
-  };
-  issue_a();
-  issue_b();
-  more = issue_a();
-  int a = 0;  // the slot of A of the stage to multiply
-  if constexpr (NW == 8) {
-    landed();
     core::lds_barrier();
   }
   for (; w.on(); w.next()) {
@@ -265,7 +303,7 @@ __device__ __forceinline__ void run(char* lds, int n1, int n2, Stages&& stages, 
     int s0, S;
     stages(w.t, s0, S);
     auto read = [&](int h) {
-      const char *pa = lds + a * G::SLOT, *pb = lds + m5(a + 1) * G::SLOT;
+      const char *pa = lds + a, *pb = lds + past(a + G::SLOT);
 #pragma unroll
       for (int i = 0; i < G::MI; ++i) fa[i] = ra.get(pa, i, h);
 #pragma unroll
@@ -278,52 +316,93 @@ __device__ __forceinline__ void run(char* lds, int n1, int n2, Stages&& stages, 
         for (int j = 0; j < G::NJ; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
     };
-    if constexpr (NW == 8) {
+    // One stage.  STEADY: the loaders stay in this item, short of its last stage, so
+    // that nothing is asked; otherwise they may be at its last stage, in the next
+    // item or done.
+    auto stage = [&](auto steady) {
+      constexpr bool STEADY = decltype(steady)::value;
+      auto landed = [&]() {  // all but the A issued last
+        if (STEADY || more) core::wait_vmcnt<G::NL>();
+        else core::wait_vmcnt<0>();
+      };
       auto phase_end = [&](bool wait) {
         __builtin_amdgcn_sched_barrier(0);
         if (wait) landed();
         core::lds_barrier();
         __builtin_amdgcn_sched_barrier(0);
       };
-      // Group 1 meets one barrier more before its phases, group 0 one after.  A
-      // wave's loads of stage s+1 have landed before the barrier ahead of group
-      // 0's first read of it (group 0: after its last products of stage s; group
-      // 1: after its last reads of it).
-      if (grp == 1) phase_end(false);
-      for (int s = 0; s < S; ++s) {
-        issue_b();
+      auto next_b = [&]() {
+        char* to = lds + past(a + 3 * G::SLOT);
+        if constexpr (STEADY) lb.issue(to, wave, false);
+        else if (on_b) lb.issue(to, wave, true);
         __builtin_amdgcn_sched_barrier(0);
+      };
+      auto next_a = [&]() {
+        char* to = lds + past(a + 4 * G::SLOT);
+        if constexpr (STEADY) {
+          la.issue(to, wave, false);
+        } else {
+          more = on_a;
+          if (on_a) la.issue(to, wave, true);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      auto step_b = [&]() {
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (STEADY) lb.advance();
+        else if (on_b) advance_b();
+      };
+      auto step_a = [&]() {
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (STEADY) la.advance();
+        else if (on_a) advance_a();
+      };
+      if constexpr (NW == 8) {
+        // A wave's loads of the next stage have landed before the barrier ahead of
+        // group 0's first read of it (group 0: after its last products of this
+        // stage; group 1: after its last reads of it).
+        next_b();
         read(0);
+        step_b();
         phase_end(false);
         multiply();
         phase_end(false);
-        more = issue_a();
-        __builtin_amdgcn_sched_barrier(0);
+        next_a();
         read(1);
+        step_a();
         phase_end(grp == 1);
         multiply();
         phase_end(grp == 0);
-        a = m5(a + 2);
-      }
-      if (grp == 0) phase_end(false);
-    } else {
-      for (int s = 0; s < S; ++s) {
-        // this wave's loads of stage s have landed, and every wave is done with
-        // stage s-1
-        landed();
-        core::lds_barrier();
-        __builtin_amdgcn_sched_barrier(0);
-        issue_b();
-        more = issue_a();
-        __builtin_amdgcn_sched_barrier(0);
+      } else {
+        // this wave's loads of the stage have landed, and every wave is done with
+        // the stage before
+        phase_end(true);
+        next_b();
+        next_a();
         read(0);
+        step_b();
+        step_a();
         multiply();
         read(1);
         multiply();
         __builtin_amdgcn_sched_barrier(0);
-        a = m5(a + 2);
       }
+      a = past(a + 2 * G::SLOT);
+    };
+    // Group 1 meets one barrier more before its phases, group 0 one after.
+    if (NW == 8 && grp == 1) core::lds_barrier();
+    int s = 0;
+    const int steady = S - 3;
+    if (steady > 0) {
+      la.uniform();
+      lb.uniform();
+      for (; s < steady; ++s) stage(std::true_type());
+      na -= steady;
+      nb -= steady;
     }
+    for (; s < S; ++s) stage(std::false_type());
+    if (NW == 8 && grp == 0) core::lds_barrier();
+    __builtin_amdgcn_sched_barrier(0);
     epilogue(w.t, acc);
   }
 }
