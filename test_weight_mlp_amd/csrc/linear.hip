@@ -38,107 +38,7 @@ __device__ __forceinline__ float slope_f32(int act, float v) {
   return 1.0f;
 }
 
-// Finishes element (m, n) of the product.
-template <typename T>
-__device__ __forceinline__ void finish(const GemmArgs& g, int64_t m, int n, float v) {
-  if (g.bias != nullptr) v += to_f32(static_cast<const T*>(g.bias)[n]);
-  if (g.pre.p != nullptr) static_cast<T*>(g.pre.p)[m * g.pre.ld + n] = from_f32<T>(v);
-  v = act_f32(g.act, v);
-  if (g.res.p != nullptr) v += to_f32(static_cast<const T*>(g.res.p)[m * g.res.ld + n]);
-  if (g.c_f32)
-    static_cast<float*>(g.c.p)[m * g.c.ld + n] = v;
-  else
-    static_cast<T*>(g.c.p)[m * g.c.ld + n] = from_f32<T>(v);
-}
-
-// ------------------------------------------------------------ general tiles
-
-// A [BK x 128] slice of a K-major operand (K rows of the matrix, 128 of its
-// columns) moved to the [128][LDK] LDS tile that stage_mma reads: 16-byte loads
-// along the columns, one element a row stored.  Columns >= ncols (a multiple of
-// the piece) and rows >= krows read as zero.
-template <typename T>
-struct KmajLoad {
-  static constexpr int VE = 16 / sizeof(T), BK = 128 / sizeof(T), VPR = 128 / VE, NV = BK * VPR / kThreads;
-  u32x4 v[NV];
-  __device__ __forceinline__ void load(const T* __restrict__ base, int64_t ld, int ncols, int64_t k0, int64_t krows,
-                                       int tid) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int idx = tid + j * kThreads;
-      const int k = idx / VPR, c = (idx % VPR) * VE;
-      v[j] = k0 + k < krows && c < ncols ? *reinterpret_cast<const u32x4*>(base + (k0 + k) * ld + c)
-                                         : u32x4{0u, 0u, 0u, 0u};
-    }
-  }
-  template <int LDK>
-  __device__ __forceinline__ void store(T* lds, int tid) const {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int idx = tid + j * kThreads;
-      const int k = idx / VPR, c = (idx % VPR) * VE;
-      const T* e = reinterpret_cast<const T*>(&v[j]);
-#pragma unroll
-      for (int q = 0; q < VE; ++q) lds[(c + q) * LDK + k] = e[q];
-    }
-  }
-};
-
-// One operand's slices: rows [0, n) of it from `base` on, K contiguous or major.
-template <typename T, bool KMAJ>
-struct Side {
-  typename std::conditional<KMAJ, KmajLoad<T>, TileLoad<T, 128>>::type t;
-  __device__ __forceinline__ void load(const T* base, int64_t ld, int n, int64_t k0, int64_t K, int tid) {
-    if constexpr (KMAJ) t.load(base, ld, n, k0, K, tid);
-    else t.load(base, ld, n, (int)k0, (int)K, tid);
-  }
-};
-
-// 128 x 128 tiles, 4 waves, one slice of each operand in LDS while the next is on
-// its way to registers.  Takes every size (multiples of 8) and both types.
-template <typename T, bool AK, bool BK>
-__global__ __launch_bounds__(kThreads) void gemm_kernel(GemmArgs g) {
-  typedef Geo<T, 128, 128> G;
-  __shared__ __attribute__((aligned(16))) T lds[(G::BM + G::BN) * G::LDK];
-  T *lA = lds, *lB = lds + G::BM * G::LDK;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave >> 1, wn = wave & 1;
-  const int tiles_m = (int)((g.M + 127) / 128), tiles_n = (int)((g.N + 127) / 128);
-  int tm, tn;
-  grouped_tile(xcd_remap(blockIdx.x, gridDim.x), tiles_m, tiles_n, 16, tm, tn);
-  const int64_t m0 = (int64_t)tm * 128, n0 = (int64_t)tn * 128;
-  const int mrows = (int)min((int64_t)128, g.M - m0), nrows = (int)min((int64_t)128, g.N - n0);
-  const T* A = static_cast<const T*>(g.a.p) + (AK ? m0 : m0 * g.a.ld);
-  const T* B = static_cast<const T*>(g.b.p) + (BK ? n0 : n0 * g.b.ld);
-  floatx16 acc[G::MB][G::NB];
-  zero_acc<G>(acc);
-  Side<T, AK> la;
-  Side<T, BK> lb;
-  la.load(A, g.a.ld, mrows, 0, g.K, tid);
-  lb.load(B, g.b.ld, nrows, 0, g.K, tid);
-  for (int64_t k0 = 0; k0 < g.K; k0 += G::BK) {
-    la.t.template store<G::LDK>(lA, tid);
-    lb.t.template store<G::LDK>(lB, tid);
-    __syncthreads();
-    if (k0 + G::BK < g.K) {
-      la.load(A, g.a.ld, mrows, k0 + G::BK, g.K, tid);
-      lb.load(B, g.b.ld, nrows, k0 + G::BK, g.K, tid);
-    }
-    stage_mma<T, G>(lA, lB, acc, wm, wn, lane);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int mb = 0; mb < G::MB; ++mb)
-#pragma unroll
-    for (int nb = 0; nb < G::NB; ++nb)
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int r = wm * G::WM + mb * 32 + acc_row(j, lane), c = wn * G::WN + nb * 32 + (lane & 31);
-        if (r < mrows && c < nrows) finish<T>(g, m0 + r, (int)n0 + c, acc[mb][nb][j]);
-      }
-}
-
-// --------------------------------------------------------------- bf16 tiles
+// -------------------------------------------------------------------- tiles
 
 // How a product is cut: `whole` tiles over all of K, then the rest in `parts` of
 // `per` stages each, whose fp32 partial tiles a second launch joins.
@@ -147,40 +47,63 @@ struct RingPlan {
   int tiles_m, tiles_n, whole, split, parts, per, stages;
 };
 
-// One row's NJ neighbouring columns of a finished tile.
-template <int NJ>
-__device__ __forceinline__ void finish_row(const GemmArgs& g, int64_t m, int64_t n, const float (&bias)[NJ], float (&v)[NJ]) {
-  typedef bf16 vec __attribute__((ext_vector_type(NJ)));
+// N neighbouring elements, 16-byte aligned (or less where they are fewer bytes).
+template <typename T, int N>
+struct Run {
+  typedef T type __attribute__((ext_vector_type(N), aligned(N * sizeof(T) < 16 ? N * sizeof(T) : 16)));
+};
+template <typename T, int N>
+using Vec = typename Run<T, N>::type;
+
+// One row's NJ neighbouring columns of a finished tile; res: the residual's.
+template <typename T, int NJ>
+__device__ __forceinline__ void finish_row(const GemmArgs& g, int64_t m, int64_t n, const float (&bias)[NJ],
+                                           const Vec<T, NJ>& res, float (&v)[NJ]) {
+  typedef Vec<T, NJ> vec;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) v[j] += bias[j];
   if (g.pre.p != nullptr) {
     vec o;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) o[j] = (bf16)v[j];
-    *reinterpret_cast<vec*>(static_cast<bf16*>(g.pre.p) + m * g.pre.ld + n) = o;
+    for (int j = 0; j < NJ; ++j) o[j] = (T)v[j];
+    *reinterpret_cast<vec*>(static_cast<T*>(g.pre.p) + m * g.pre.ld + n) = o;
   }
   if (g.act != IPTTT_ACT_NONE) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) v[j] = act_f32(g.act, v[j]);
   }
   if (g.res.p != nullptr) {
-    const vec r = *reinterpret_cast<const vec*>(static_cast<const bf16*>(g.res.p) + m * g.res.ld + n);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) v[j] += (float)r[j];
+    for (int j = 0; j < NJ; ++j) v[j] += (float)res[j];
   }
   vec o;
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) o[j] = (bf16)v[j];
-  *reinterpret_cast<vec*>(static_cast<bf16*>(g.c.p) + m * g.c.ld + n) = o;
+  for (int j = 0; j < NJ; ++j) o[j] = (T)v[j];
+  *reinterpret_cast<vec*>(static_cast<T*>(g.c.p) + m * g.c.ld + n) = o;
+}
+
+// The residual's rows of block row i of a tile at (m0, n0), loaded ahead.
+template <typename T, int NW>
+__device__ __forceinline__ void load_res(const GemmArgs& g, int64_t m0, int64_t n0, int i,
+                                         Vec<T, ring::Geo<T, NW>::NJ> (&res)[4]) {
+  typedef ring::Geo<T, NW> G;
+  if (g.res.p == nullptr) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  const int64_t m = m0 + wm * G::WM + i * 16 + 4 * (lane >> 4), n = n0 + wn * G::WN + (lane & 15) * G::NJ;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (n < g.N && m + e < g.M)
+      res[e] = *reinterpret_cast<const Vec<T, G::NJ>*>(static_cast<const T*>(g.res.p) + (m + e) * g.res.ld + n);
 }
 
 // Finishes block row i of a tile at (m0, n0): this lane's four rows of it.  With B's
 // rows in the order of PERM (K contiguous) a lane has NJ neighbouring columns and
 // the whole epilogue; K-major products have none and store column by column.
-template <int NW, bool BK>
+template <typename T, int NW, bool BK>
 __device__ __forceinline__ void finish_block(const GemmArgs& g, int64_t m0, int64_t n0, int i,
-                                             ring::f4 (&acc)[ring::Geo<NW>::NJ]) {
-  typedef ring::Geo<NW> G;
+                                             const Vec<T, ring::Geo<T, NW>::NJ> (&res)[4],
+                                             ring::f4 (&acc)[ring::Geo<T, NW>::NJ]) {
+  typedef ring::Geo<T, NW> G;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
   const int64_t m = m0 + wm * G::WM + i * 16 + 4 * (lane >> 4);
   if constexpr (!BK) {
@@ -188,14 +111,14 @@ __device__ __forceinline__ void finish_block(const GemmArgs& g, int64_t m0, int6
     if (n >= g.N) return;
     float bias[G::NJ];
 #pragma unroll
-    for (int j = 0; j < G::NJ; ++j) bias[j] = g.bias != nullptr ? (float)static_cast<const bf16*>(g.bias)[n + j] : 0.0f;
+    for (int j = 0; j < G::NJ; ++j) bias[j] = g.bias != nullptr ? (float)static_cast<const T*>(g.bias)[n + j] : 0.0f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (m + e >= g.M) break;
       float v[G::NJ];
 #pragma unroll
       for (int j = 0; j < G::NJ; ++j) v[j] = acc[j][e];
-      finish_row<G::NJ>(g, m + e, n, bias, v);
+      finish_row<T, G::NJ>(g, m + e, n, bias, res[e], v);
     }
   } else {
     const int64_t n = n0 + wn * G::WN + (lane & 15);
@@ -211,7 +134,7 @@ __device__ __forceinline__ void finish_block(const GemmArgs& g, int64_t m0, int6
       }
     };
     if (g.c_f32) store(static_cast<float*>(g.c.p));
-    else store(static_cast<bf16*>(g.c.p));
+    else store(static_cast<T*>(g.c.p));
   }
 }
 
@@ -230,10 +153,10 @@ __device__ __forceinline__ void ring_item(const RingPlan& p, int t, int64_t& m0,
   n0 = (int64_t)tn * p.nw * 32;
 }
 
-template <int NW, bool AK, bool BK>
-__device__ __forceinline__ void ring_product(const bf16* __restrict__ A, const bf16* __restrict__ B, const GemmArgs& g,
+template <typename T, int NW, bool AK, bool BK>
+__device__ __forceinline__ void ring_product(const T* __restrict__ A, const T* __restrict__ B, const GemmArgs& g,
                                              const RingPlan& p, char* lds) {
-  typedef ring::Geo<NW> G;
+  typedef ring::Geo<T, NW> G;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   auto stages = [&](int t, int& s0, int& n) {
     s0 = 0;
@@ -243,13 +166,13 @@ __device__ __forceinline__ void ring_product(const bf16* __restrict__ A, const b
       n = min(p.per, p.stages - s0);
     }
   };
-  auto open_a = [&](int t, int s0, ring::Loader<NW, AK>& l) {
+  auto open_a = [&](int t, int s0, ring::Loader<T, NW, AK>& l) {
     int64_t m0, n0;
     int part;
     ring_item(p, t, m0, n0, part);
     l.init(A + (AK ? m0 : m0 * g.a.ld), g.a.ld, g.M - m0, g.K, s0, wave, lane, [](int r) { return r; });
   };
-  auto open_b = [&](int t, int s0, ring::Loader<NW, BK>& l) {
+  auto open_b = [&](int t, int s0, ring::Loader<T, NW, BK>& l) {
     int64_t m0, n0;
     int part;
     ring_item(p, t, m0, n0, part);
@@ -268,24 +191,39 @@ __device__ __forceinline__ void ring_product(const bf16* __restrict__ A, const b
         for (int j = 0; j < G::NJ; ++j) to[(i * G::NJ + j) * G::NT] = acc[i][j];
       return;
     }
+    // the residual's loads two block rows at a time: waiting for each one's cost 26 us
+    // of 222 at 8192 x 2560 x 6144
 #pragma unroll
-    for (int i = 0; i < G::MI; ++i) finish_block<NW, BK>(g, m0, n0, i, acc[i]);
+    for (int i = 0; i < G::MI; i += 2) {
+      Vec<T, G::NJ> res[2][4];
+      if constexpr (!BK) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) load_res<T, NW>(g, m0, n0, i + q, res[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) finish_block<T, NW, BK>(g, m0, n0, i + q, res[q], acc[i + q]);
+    }
   };
-  ring::run<NW, AK, BK>(lds, p.whole, p.split * p.parts, stages, open_a, open_b, epilogue);
+  ring::run<T, NW, AK, BK>(lds, p.whole, p.split * p.parts, stages, open_a, open_b, epilogue);
 }
 
-template <int NW, bool AK, bool BK>
-__global__ __launch_bounds__(ring::Geo<NW>::NT, ring::Geo<NW>::MAX_GROUPS) void ring_kernel(GemmArgs g, RingPlan p) {
-  __shared__ __attribute__((aligned(1024))) char lds[ring::Geo<NW>::LDS_BYTES];
-  ring_product<NW, AK, BK>(static_cast<const bf16*>(g.a.p), static_cast<const bf16*>(g.b.p), g, p, lds);
+template <typename T, int NW, bool AK, bool BK>
+__global__ __launch_bounds__(NW * 64, NW == 8 ? 1 : 2) void ring_kernel(GemmArgs g, RingPlan p) {
+  __shared__ __attribute__((aligned(1024))) char lds[ring::Geo<T, NW>::LDS_BYTES];
+  ring_product<T, NW, AK, BK>(static_cast<const T*>(g.a.p), static_cast<const T*>(g.b.p), g, p, lds);
 }
 
 // Sums the parts of a split tile in order and finishes it; blockIdx.y takes a block
 // row of it.
-template <int NW, bool BK>
-__global__ __launch_bounds__(ring::Geo<NW>::NT) void ring_join_kernel(GemmArgs g, RingPlan p) {
-  typedef ring::Geo<NW> G;
+template <typename T, int NW, bool BK>
+__global__ __launch_bounds__(NW * 64) void ring_join_kernel(GemmArgs g, RingPlan p) {
+  typedef ring::Geo<T, NW> G;
   const int i = blockIdx.y, t = p.whole + blockIdx.x * p.parts;
+  int64_t m0, n0;
+  int part;
+  ring_item(p, t, m0, n0, part);
+  Vec<T, G::NJ> res[4];
+  if constexpr (!BK) load_res<T, NW>(g, m0, n0, i, res);
   const ring::f4* from = reinterpret_cast<const ring::f4*>(g.part) +
                          ((int64_t)blockIdx.x * p.parts * G::MI + i) * G::NJ * G::NT + threadIdx.x;
   ring::f4 acc[G::NJ];
@@ -296,10 +234,7 @@ __global__ __launch_bounds__(ring::Geo<NW>::NT) void ring_join_kernel(GemmArgs g
 #pragma unroll
     for (int j = 0; j < G::NJ; ++j) acc[j] += from[j * G::NT];
   }
-  int64_t m0, n0;
-  int part;
-  ring_item(p, t, m0, n0, part);
-  finish_block<NW, BK>(g, m0, n0, i, acc);
+  finish_block<T, NW, BK>(g, m0, n0, i, res, acc);
 }
 
 constexpr int kCus = 256;
@@ -311,8 +246,10 @@ RingPlan plan_ring(const GemmArgs& g) {
   for (const int nw : {8, 4}) {
     const int64_t w = nw * 32, tm = (g.M + w - 1) / w, tn = (g.N + w - 1) / w, tiles = tm * tn;
     const int64_t groups = nw == 8 ? kCus : 2 * kCus;
-    const int stages = (int)((g.K + ring::KS - 1) / ring::KS);
-    const double stage = nw == 8 ? 1.6 : 1.0, lone = nw == 8 ? 1.2 : 0.7;   // us, on a full and a half empty device
+    const int ks = g.dtype == 1 ? ring::kStage<bf16> : ring::kStage<float>, stages = (int)((g.K + ks - 1) / ks);
+    // us, on a full and a half empty device
+    const double stage = g.dtype != 1 ? (nw == 8 ? 7.5 : 3.8) : nw == 8 ? 1.5 : 1.0;
+    const double lone = g.dtype != 1 ? (nw == 8 ? 7.5 : 2.0) : nw == 8 ? 1.2 : 0.7;
     auto consider = [&](int64_t whole, int parts) {
       const int per = (stages + parts - 1) / parts;
       parts = (stages + per - 1) / per;
@@ -334,26 +271,112 @@ RingPlan plan_ring(const GemmArgs& g) {
   return best;
 }
 
-template <int NW>
+template <typename T, int NW>
 hipError_t launch_ring(const GemmArgs& g, const RingPlan& p, hipStream_t st) {
-  typedef ring::Geo<NW> G;
+  typedef ring::Geo<T, NW> G;
   const int64_t items = (int64_t)p.whole + (int64_t)p.split * p.parts;
   const unsigned grid = (unsigned)std::min<int64_t>(kCus * G::MAX_GROUPS, (items + 7) / 8 * 8);
   note_launch("linear", st);
-  if (!g.a_kmaj && !g.b_kmaj) ring_kernel<NW, false, false><<<grid, G::NT, 0, st>>>(g, p);
-  else if (!g.a_kmaj) ring_kernel<NW, false, true><<<grid, G::NT, 0, st>>>(g, p);
-  else ring_kernel<NW, true, true><<<grid, G::NT, 0, st>>>(g, p);
+  if (!g.a_kmaj && !g.b_kmaj) ring_kernel<T, NW, false, false><<<grid, G::NT, 0, st>>>(g, p);
+  else if (!g.a_kmaj) ring_kernel<T, NW, false, true><<<grid, G::NT, 0, st>>>(g, p);
+  else ring_kernel<T, NW, true, true><<<grid, G::NT, 0, st>>>(g, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.split == 0) return e;
   note_launch("linear_join", st);
   const dim3 j((unsigned)p.split, G::MI);
-  if (!g.b_kmaj) ring_join_kernel<NW, false><<<j, G::NT, 0, st>>>(g, p);
-  else ring_join_kernel<NW, true><<<j, G::NT, 0, st>>>(g, p);
+  if (!g.b_kmaj) ring_join_kernel<T, NW, false><<<j, G::NT, 0, st>>>(g, p);
+  else ring_join_kernel<T, NW, true><<<j, G::NT, 0, st>>>(g, p);
   return hipGetLastError();
 }
 
 size_t ring_bytes(const RingPlan& p) {
   return (size_t)p.split * p.parts * (p.nw * 32) * (p.nw * 32) * sizeof(float);
+}
+
+// ---------------------------------------------------------------- few rows
+
+// Up to 16 MT rows of x: the weights stream from HBM once, straight to the
+// fragments of 16x16 products (rows: 16 FB outputs, columns: rows of x), with all
+// their loads in flight; 16 waves take every 16th slice of K and are summed through
+// LDS.  A lane ends up with four neighbouring outputs of one row.
+template <typename T, int MT, int FB>
+__global__ __launch_bounds__(1024) void few_kernel(GemmArgs g) {
+  constexpr int W = 16;
+  typedef typename ring::Frag<T>::type frag;
+  constexpr int VE = 16 / sizeof(T), CK = 4 * VE;                              // K of a slice: 16 bytes a lane
+  constexpr int U = MT * FB == 4 ? 4 : 8;  // slices in flight
+  __shared__ ring::f4 red[W][MT * FB][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, kg = (lane >> 4) * VE;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * FB);
+  const T *a[FB], *b[MT];
+#pragma unroll
+  for (int f = 0; f < FB; ++f) a[f] = static_cast<const T*>(g.b.p) + min(n0 + f * 16 + r, g.N - 1) * g.b.ld + kg;
+#pragma unroll
+  for (int t = 0; t < MT; ++t) b[t] = static_cast<const T*>(g.a.p) + min((int64_t)(t * 16 + r), g.M - 1) * g.a.ld + kg;
+  ring::f4 acc[MT][FB];
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int f = 0; f < FB; ++f) acc[t][f] = ring::f4{0.0f, 0.0f, 0.0f, 0.0f};
+  const int K = (int)g.K;
+  for (int k0 = wave * CK; k0 < K; k0 += U * W * CK) {
+    frag fa[U][FB], fb[U][MT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * W * CK;
+      const bool on = k + kg < K;
+#pragma unroll
+      for (int f = 0; f < FB; ++f) fa[u][f] = on ? *reinterpret_cast<const frag*>(a[f] + k) : frag{};
+#pragma unroll
+      for (int t = 0; t < MT; ++t) fb[u][t] = on ? *reinterpret_cast<const frag*>(b[t] + k) : frag{};
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int f = 0; f < FB; ++f) acc[t][f] = ring::Frag<T>::mma(fa[u][f], fb[u][t], acc[t][f]);
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int f = 0; f < FB; ++f) red[wave][t * FB + f][lane] = acc[t][f];
+  __syncthreads();
+  for (int i = wave; i < MT * FB; i += W) {
+    ring::f4 v = red[0][i][lane];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += red[w][i][lane];
+    const int64_t m = i / FB * 16 + r, n = n0 + i % FB * 16 + 4 * (lane >> 4);
+    if (m >= g.M || n >= g.N) continue;
+    float bias[4], y[4];
+    Vec<T, 4> res = {};
+    if (g.res.p != nullptr) res = *reinterpret_cast<const Vec<T, 4>*>(static_cast<const T*>(g.res.p) + m * g.res.ld + n);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      bias[e] = g.bias != nullptr ? to_f32(static_cast<const T*>(g.bias)[n + e]) : 0.0f;
+      y[e] = v[e];
+    }
+    finish_row<T, 4>(g, m, n, bias, res, y);
+  }
+}
+
+// From 33 rows on the tiles take less: bf16, 2560 -> 6144 outputs, 16.6 us at 33 to 64 rows
+// (here with four blocks of rows 14.5 to 17.0), 9728 -> 2560 21.5 (42 to 53); fp32, 4096 ->
+// 2560, 36 (56 to 64).
+bool few_rows(const GemmArgs& g) { return g.M <= 32 && !g.a_kmaj && !g.b_kmaj; }
+
+// Two blocks of outputs a workgroup halve the rows' reads; they pay where there are
+// workgroups enough.
+template <typename T>
+void launch_few(const GemmArgs& g, hipStream_t st) {
+  note_launch("linear_few", st);
+  const auto groups = [&](int fb) { return (unsigned)((g.N + 16 * fb - 1) / (16 * fb)); };
+  const bool wide = groups(2) >= 192;
+  if (g.M <= 8) few_kernel<T, 1, 1><<<groups(1), 1024, 0, st>>>(g);
+  else if (g.M <= 16 && !wide) few_kernel<T, 1, 1><<<groups(1), 1024, 0, st>>>(g);
+  else if (g.M <= 16) few_kernel<T, 1, 2><<<groups(2), 1024, 0, st>>>(g);
+  else if (!wide) few_kernel<T, 2, 1><<<groups(1), 1024, 0, st>>>(g);
+  else few_kernel<T, 2, 2><<<groups(2), 1024, 0, st>>>(g);
 }
 
 // ------------------------------------------------- the activation's gradient
@@ -411,27 +434,20 @@ __global__ __launch_bounds__(256) void column_sum_kernel(const float* part, int 
 
 constexpr int kStrips = 256;  // most strips of rows of a column sum
 
-template <typename T>
-void launch_general(const GemmArgs& g, hipStream_t st) {
-  const unsigned tiles = (unsigned)(((g.M + 127) / 128) * ((g.N + 127) / 128));
-  if (!g.a_kmaj && !g.b_kmaj) gemm_kernel<T, false, false><<<tiles, kThreads, 0, st>>>(g);
-  else if (!g.a_kmaj) gemm_kernel<T, false, true><<<tiles, kThreads, 0, st>>>(g);
-  else gemm_kernel<T, true, true><<<tiles, kThreads, 0, st>>>(g);
-}
-
 }  // namespace
 
-size_t gemm_workspace(const GemmArgs& g) { return g.dtype == 1 ? ring_bytes(plan_ring(g)) : 0; }
+size_t gemm_workspace(const GemmArgs& g) { return few_rows(g) ? 0 : ring_bytes(plan_ring(g)); }
 
 hipError_t launch_gemm(const GemmArgs& g, hipStream_t st) {
   if (g.a_kmaj && !g.b_kmaj) return hipErrorInvalidValue;  // no caller has such a product
-  if (g.dtype == 1) {
-    const RingPlan p = plan_ring(g);
-    return p.nw == 8 ? launch_ring<8>(g, p, st) : launch_ring<4>(g, p, st);
+  if (few_rows(g)) {
+    if (g.dtype == 1) launch_few<bf16>(g, st);
+    else launch_few<float>(g, st);
+    return hipGetLastError();
   }
-  note_launch("linear", st);
-  launch_general<float>(g, st);
-  return hipGetLastError();
+  const RingPlan p = plan_ring(g);
+  if (g.dtype == 1) return p.nw == 8 ? launch_ring<bf16, 8>(g, p, st) : launch_ring<bf16, 4>(g, p, st);
+  return p.nw == 8 ? launch_ring<float, 8>(g, p, st) : launch_ring<float, 4>(g, p, st);
 }
 
 int act_grad_parts(int64_t rows, int64_t dim) {

@@ -39,16 +39,20 @@
 namespace ipttt {
 namespace ring {
 
-constexpr int KS = 64, NSLOT = 5;
+constexpr int NSLOT = 5;
 typedef float4_t f4;
 
-template <int NW>
+template <typename T>
+constexpr int kStage = 128 / (int)sizeof(T);  // K of a stage
+
+template <typename T, int NW>
 struct Geo {
+  static constexpr int KS = kStage<T>, ES = sizeof(T), VE = 16 / ES;
   static constexpr int BM = NW * 32, BN = NW * 32;          // 256 or 128
   static constexpr int WAVES_N = 2, WAVES_M = NW / 2;
   static constexpr int WM = 64, WN = BN / 2, MI = WM / 16, NJ = WN / 16;
   static_assert(BM == WAVES_M * WM, "wave grid");
-  static constexpr int SLOT = BM * KS * 2;                  // bytes
+  static constexpr int SLOT = BM * 128;                     // bytes
   static constexpr int LDS_BYTES = NSLOT * SLOT;
   static constexpr int NT = NW * 64;
   static constexpr int NL = 4;                              // load instructions a wave and part
@@ -60,12 +64,31 @@ struct Geo {
 // below 2^31: 255 strides of 2^22 elements, and K.)
 constexpr uint32_t kOut = 0x80000000u;
 
+// 16 bytes of an operand, and their products: bf16 32 of K; fp32 16 of K, element e of a
+// lane being K = 4 (lane / 16) + e in both operands.
+template <typename T> struct Frag;
+template <> struct Frag<bf16> {
+  typedef bf16x8 type;
+  static __device__ __forceinline__ f4 mma(type a, type b, f4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+};
+template <> struct Frag<float> {
+  typedef float4_t type;
+  static __device__ __forceinline__ f4 mma(type a, type b, f4 c) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+  }
+};
+
 // One operand's loads.  issue() loads the stage that the cursor stands at, and
 // advance() moves it, so that the scalar work of a stage's addresses is done while
 // the fragment reads behind the loads are on their way.
-template <int NW, bool KMAJ>
+template <typename T, int NW, bool KMAJ>
 struct Loader {
-  typedef Geo<NW> G;
+  typedef Geo<T, NW> G;
+  static constexpr int KS = G::KS;
   uint32_t voff[G::NL];
   uint32_t chunk;              // rows: K element of this lane's pieces within a stage, by load (4 bits each, in 8s)
   __amdgpu_buffer_rsrc_t rs;   // rows: over the tile's rows, the stage's bytes into a row, and a row's valid bytes
@@ -77,13 +100,13 @@ struct Loader {
   // p at the tile's first row (or column), n > 0 rows (or columns) of it valid, K
   // valid along k; row(r): the operand's row that LDS row r holds
   template <class Row>
-  __device__ __forceinline__ void init(const bf16* p, int64_t ld, int64_t n, int64_t kvalid, int stage, int wave,
+  __device__ __forceinline__ void init(const T* p, int64_t ld, int64_t n, int64_t kvalid, int stage, int wave,
                                        int lane, Row&& row) {
-    ldb = (uint32_t)ld * 2u;
+    ldb = (uint32_t)ld * G::ES;
     const uint32_t here = (uint32_t)min(n, (int64_t)G::BM);
     if constexpr (!KMAJ) {
-      kbytes = (uint32_t)kvalid * 2u;
-      at = (uint32_t)stage * (KS * 2);
+      kbytes = (uint32_t)kvalid * G::ES;
+      at = (uint32_t)stage * 128;
       rs = core::make_operand(p, 0, (int64_t)(here - 1) * ldb + kbytes).rsrc;
       chunk = 0;
 #pragma unroll
@@ -96,19 +119,20 @@ struct Loader {
     } else {
       base = reinterpret_cast<const char*>(p) + (int64_t)stage * KS * ldb;
       krows = (int)kvalid - stage * KS;
-      width = here * 2;
-      constexpr int LPR = G::BM / 8, RPI = 64 / LPR;  // lanes a K row, K rows an instruction
+      width = here * G::ES;
+      constexpr int LPR = G::BM / G::VE, RPI = 64 / LPR;  // lanes a K row, K rows an instruction
 #pragma unroll
       for (int j = 0; j < G::NL; ++j) {
         const int r = (wave * G::NL + j) * RPI + lane / LPR, s = lane % LPR;
-        const int u = (s >> 1) ^ (((r & 3) << 1) | ((r >> 3) & 1)), col = u * 16 + (s & 1) * 8;
-        voff[j] = (uint32_t)col < here ? (uint32_t)r * ldb + (uint32_t)col * 2u : kOut;
+        const int u = G::ES == 2 ? (s >> 1) ^ (((r & 3) << 1) | ((r >> 3) & 1)) : (s >> 2) ^ ((r >> 2) & 3);
+        const int col = u * 16 + (G::ES == 2 ? (s & 1) * 8 : (s & 3) * 4);
+        voff[j] = (uint32_t)col < here ? (uint32_t)r * ldb + (uint32_t)col * G::ES : kOut;
       }
     }
   }
   __device__ __forceinline__ void advance() {
     if constexpr (!KMAJ) {
-      at += KS * 2;
+      at += 128;
     } else {
       base += (int64_t)KS * ldb;
       krows -= KS;
@@ -130,7 +154,7 @@ struct Loader {
   __device__ __forceinline__ void issue(char* slot, int wave, bool last) const {
     char* to = slot + wave * G::NL * 1024;
     if constexpr (!KMAJ) {
-      if (last && at + KS * 2 > kbytes) {  // pieces past K read as zero
+      if (last && at + 128 > kbytes) {  // pieces past K read as zero
 #pragma unroll
         for (int j = 0; j < G::NL; ++j)
           __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (core::lds_ptr_t)(to + j * 1024), 16,
@@ -154,10 +178,11 @@ struct Loader {
   }
 };
 
-// Fragments of 16 rows x 32 K from a slot.
-template <int NW, bool KMAJ>
+// Fragments of 16 rows and half a stage's K from a slot.
+template <typename T, int NW, bool KMAJ>
 struct Reader {
-  typedef Geo<NW> G;
+  typedef Geo<T, NW> G;
+  typedef typename Frag<T>::type frag;
   int at, sw, unit;
   __device__ __forceinline__ void init(int row0, int lane) {
     if constexpr (!KMAJ) {
@@ -165,6 +190,10 @@ struct Reader {
       at = r * 128;
       sw = (r >> 1) & 7;
       unit = lane >> 4;
+    } else if constexpr (G::ES == 4) {
+      at = 4 * (lane >> 4) * G::BM * 4 + (lane & 15) * 4;
+      sw = lane >> 4;
+      unit = row0 >> 4;
     } else {
       const int kg = lane >> 4, r = (lane >> 2) & 3;
       at = (8 * kg + r) * G::BM * 2 + (lane & 3) * 8;
@@ -173,9 +202,15 @@ struct Reader {
     }
   }
   // block blk of 16 rows, half h of the stage's K
-  __device__ __forceinline__ bf16x8 get(const char* slot, int blk, int h) const {
+  __device__ __forceinline__ frag get(const char* slot, int blk, int h) const {
     if constexpr (!KMAJ) {
-      return *reinterpret_cast<const bf16x8*>(slot + at + blk * 16 * 128 + (((h * 4 + unit) ^ sw) << 4));
+      return *reinterpret_cast<const frag*>(slot + at + blk * 16 * 128 + (((h * 4 + unit) ^ sw) << 4));
+    } else if constexpr (G::ES == 4) {
+      const char* p = slot + at + h * 16 * G::BM * 4 + (((unit + blk) ^ sw) << 6);
+      frag x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = *reinterpret_cast<const float*>(p + e * G::BM * 4);
+      return x;
     } else {
       typedef __attribute__((address_space(3))) short4_t* lp4;
       const char* p = slot + at + h * 32 * G::BM * 2 + (((unit + blk) ^ sw) << 5);
@@ -189,7 +224,7 @@ struct Reader {
 // The order of B's rows with which a lane's NJ blocks are NJ neighbouring columns.
 template <int NW>
 __device__ __forceinline__ int perm_row(int r) {
-  constexpr int WN = Geo<NW>::WN, NJ = Geo<NW>::NJ;
+  constexpr int WN = Geo<bf16, NW>::WN, NJ = Geo<bf16, NW>::NJ;
   return r / WN * WN + (r & 15) * NJ + (r % WN >> 4);
 }
 
@@ -228,18 +263,18 @@ struct Walk {
 // of B.  A and B are restrict so that the compiler tells the LDS reads apart from
 // the direct loads and puts no wait for those in front of them; the ring's own
 // waits order them.
-template <int NW, bool AK, bool BK, class Stages, class OpenA, class OpenB, class Epilogue>
+template <typename T, int NW, bool AK, bool BK, class Stages, class OpenA, class OpenB, class Epilogue>
 __device__ __forceinline__ void run(char* lds, int n1, int n2, Stages&& stages, OpenA&& open_a, OpenB&& open_b,
                                     Epilogue&& epilogue) {
-  typedef Geo<NW> G;
+  typedef Geo<T, NW> G;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1, grp = NW == 8 ? wave >> 2 : 0;
   Walk w(n1, n2), wa = w, wb = w;
   if (!w.on()) return;
-  Loader<NW, AK> la;
-  Loader<NW, BK> lb;
-  Reader<NW, AK> ra;
-  Reader<NW, BK> rb;
+  Loader<T, NW, AK> la;
+  Loader<T, NW, BK> lb;
+  Reader<T, NW, AK> ra;
+  Reader<T, NW, BK> rb;
   ra.init(wm * G::WM, lane);
   rb.init(wn * G::WN, lane);
   // Stages left to issue of the items that the loaders stand at, and whether
@@ -299,7 +334,7 @@ __device__ __forceinline__ void run(char* lds, int n1, int n2, Stages&& stages, 
     for (int i = 0; i < G::MI; ++i)
 #pragma unroll
       for (int j = 0; j < G::NJ; ++j) acc[i][j] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-    bf16x8 fa[G::MI], fb[G::NJ];
+    typename Frag<T>::type fa[G::MI], fb[G::NJ];
     int s0, S;
     stages(w.t, s0, S);
     auto read = [&](int h) {
@@ -313,8 +348,7 @@ __device__ __forceinline__ void run(char* lds, int n1, int n2, Stages&& stages, 
 #pragma unroll
       for (int i = 0; i < G::MI; ++i)
 #pragma unroll
-        for (int j = 0; j < G::NJ; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < G::NJ; ++j) acc[i][j] = Frag<T>::mma(fa[i], fb[j], acc[i][j]);
     };
     // One stage.  STEADY: the loaders stay in this item, short of its last stage, so
     // that nothing is asked; otherwise they may be at its last stage, in the next
