@@ -7,9 +7,11 @@
 #include <cstring>
 
 #include "../../include/ipttt.h"
+#include "block.h"
 #include "launch.h"
 
 using ipttt::Prob;
+using ipttt::Rows;
 
 namespace {
 // The caller's launch hook (a measurement aid), process-wide.
@@ -218,6 +220,30 @@ Layout layout(const Prob& p, Passes ps = {0, 0}) {
 //   target_backward: tap-major conv weights | Y | dY (fp32) | Y^T, dV^T | conv
 //     partials (the 8-wave path keeps dW_target's token-slice partials in Y^T, dV^T)
 //   z_backward: dG, dU | W_gate^T, W_up^T | dG^T, dU^T, H^T
+// The products of the backward from 8 bits, without their tensors: dH = dG W_gate +
+// dU W_up, and dW_gate = dG^T H with dW_up = dU^T H.
+ipttt::GemmArgs keep8_dh(const Prob& p) {
+  ipttt::GemmArgs g{};
+  g.dtype = p.dtype;
+  g.M = p.M;
+  g.N = p.d;
+  g.K = p.f;
+  g.b_kmaj = 1;
+  g.two_pairs = 1;
+  return g;
+}
+ipttt::GemmArgs keep8_dw(const Prob& p) {
+  ipttt::GemmArgs g{};
+  g.dtype = p.dtype;
+  g.M = p.f;
+  g.N = p.d;
+  g.K = p.M;
+  g.a_kmaj = g.b_kmaj = 1;
+  g.c_f32 = 1;
+  g.two_products = 1;
+  return g;
+}
+
 struct BwdLayout {
   size_t table, call, total;
   // scan_apply_backward
@@ -225,7 +251,7 @@ struct BwdLayout {
   // target_backward
   size_t convt, y, dy, yt, dvt, cpart;
   // z_backward
-  size_t dg, du, wgt, wut, dgt, dut, ht;
+  size_t dg, du, wgt, wut, dgt, dut, ht, gpart;
   int64_t Mp;
 };
 
@@ -285,6 +311,8 @@ BwdLayout bwd_layout(const Prob& p) {
   l.dgt = take(tnfast ? 0 : (size_t)l.Mp * p.f * e);
   l.dut = take(tnfast ? 0 : (size_t)l.Mp * p.f * e);
   l.ht = take(tnfast ? 0 : (size_t)l.Mp * p.d * e);
+  l.gpart = take(p.dtype != IPTTT_BF16 ? 0
+                                       : std::max(ipttt::gemm_workspace(keep8_dh(p)), ipttt::gemm_workspace(keep8_dw(p))));
   const size_t zb = o;
   l.total = l.call + std::max(sa, std::max(tg, zb));
   return l;
@@ -1007,7 +1035,26 @@ ipttt_status z_backward(const ipttt_problem* q, const void* H, const void* W_gat
   void *dG = c + l.dg, *dU = c + l.du;
   if (k8 != nullptr) {
     IPTTT_TRY(ipttt::launch_gated_grad8(p, *k8, dZ, dG, dU, st));
-  } else if (GU != nullptr) {
+    // both products of dH summed in one, both weight gradients in one launch
+    ipttt::GemmArgs g = keep8_dh(p);
+    g.a = Rows{dG, p.f};
+    g.a2 = Rows{dU, p.f};
+    g.b = Rows{const_cast<void*>(W_gate), p.d};
+    g.b2 = Rows{const_cast<void*>(W_up), p.d};
+    g.c = Rows{dH, p.d};
+    g.part = reinterpret_cast<float*>(c + l.gpart);
+    IPTTT_TRY(ipttt::launch_gemm(g, st));
+    ipttt::GemmArgs w = keep8_dw(p);
+    w.a = Rows{dG, p.f};
+    w.a2 = Rows{dU, p.f};
+    w.b = Rows{const_cast<void*>(H), p.d};
+    w.c = Rows{dW_gate, p.d};
+    w.c2 = Rows{dW_up, p.d};
+    w.part = reinterpret_cast<float*>(c + l.gpart);
+    IPTTT_TRY(ipttt::launch_gemm(w, st));
+    return IPTTT_OK;
+  }
+  if (GU != nullptr) {
     IPTTT_TRY(ipttt::launch_gated_grad(p, GU, dZ, dG, dU, st));
   } else {
     IPTTT_TRY(ipttt::launch_gated_z_bwd(p, H, W_gate, W_up, dZ, dG, dU, st));

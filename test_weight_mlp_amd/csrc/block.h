@@ -28,7 +28,8 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t st);
 int norm_parts(int dtype, int64_t rows, int dim);
 hipError_t launch_norm_backward(const NormArgs& a, hipStream_t st);
 
-// C[m, n] = sum_k A[m, k] B[n, k] with the projection's epilogue.  A and B are
+// C[m, n] = sum_k A[m, k] B[n, k] with the projection's epilogue (which takes K
+// contiguous in B).  A and B are
 // row-major with K contiguous, or (a_kmaj, b_kmaj) K-major: A[m, k] at
 // a.p[k * a.ld + m].
 struct GemmArgs {
@@ -36,6 +37,10 @@ struct GemmArgs {
   int64_t M, N, K;
   Rows a, b, c;
   int a_kmaj, b_kmaj;
+  // A second pair of operands of the same sizes and strides, C = A B + A2 B2, or a
+  // second product, C = A B and C2 = A2 B, in one launch.
+  int two_pairs, two_products;
+  Rows a2, b2, c2;
   int c_f32;              // C is float (else dtype)
   int act;                // ipttt_act
   const void* bias;       // [N] dtype, or NULL

@@ -150,13 +150,14 @@ __device__ __forceinline__ void store_rows_swz(const bf16* rowT, bf16* __restric
 
 // ------------------------------------------------------- values kept in 8 bits
 
-// kKeep8 neighbouring values of a row share a scale; a thread holds 8 of them, so
-// the eight lanes of a block are consecutive.  Values v = q s with s = max|v| / 127
-// and q = round(127 v / max) to even, an integer in [-127, 127].  The quotient of
-// bf16 values meets ties exactly (v = max / 2 is one), so it is divided exactly:
-// scaled by a power of two so that max is in [2, 4), the numerator is exact in
-// fp32, and the reciprocal's quotient is corrected by its own remainder.  Blocks
-// below 2^-100 are zeros; one with an infinity or a NaN gets a NaN scale.
+// kKeep8 neighbouring values of a row share a scale: v = q s with s = max|v| / 127 and
+// q = round(127 v / max), an integer in [-127, 127], ties away from zero.  The
+// quotient of bf16 values is either a tie exactly (v = max / 2 is one) or 2^-16 of its
+// size away from any; multiplying by 127 / max made 2^-21 too large therefore decides
+// every value, with two operations each.  (Dividing exactly, with the largest taken of
+// the rounded values, a Z call that keeps 8 bits took 1306 instead of 1192 us at
+// 16384 x 2560 x 9728.)  Blocks below 2^-100 are zeros; one with an infinity or a NaN
+// gets a NaN scale.
 constexpr int kKeep8 = 64;
 
 template <int CTRL>
@@ -164,54 +165,36 @@ __device__ __forceinline__ uint32_t dpp_max(uint32_t x) {
   return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, true));
 }
 
-// The packed integers of 8 bf16 values, and their block's scale (in all 8 lanes).
-__device__ __forceinline__ u32x2 keep8_pack(u32x4 raw, float* scale) {
-  // |v| of non-negative floats orders like its bits, NaN above infinity
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) top = max(top, max(raw[i] & 0x7FFFu, (raw[i] >> 16) & 0x7FFFu));
-  top = dpp_max<0xB1>(top);   // quad_perm 1 0 3 2
-  top = dpp_max<0x4E>(top);   // quad_perm 2 3 0 1
-  top = dpp_max<0x141>(top);  // row_half_mirror: the other quad of the eight
-  const float m = __builtin_bit_cast(float, top << 16);
-  const bool none = m < 0x1p-100f, bad = top >= 0x7F80u;
-  *scale = bad ? __builtin_nanf("") : none ? 0.0f : m / 127.0f;
-  const float sc = none || bad ? 0.0f : __builtin_bit_cast(float, (255u - (top >> 7)) << 23);
-  const float den = none || bad ? 2.0f : m * sc, rcp = 1.0f / den, num = 127.0f * sc;
-  u32x2 q = {0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t h = i & 1 ? raw[i >> 1] & 0xFFFF0000u : raw[i >> 1] << 16;
-    const float v = bad ? 0.0f : __builtin_bit_cast(float, h) * num;
-    float t = v * rcp;
-    t = fmaf(fmaf(-t, den, v), rcp, t);
-    q[i >> 2] |= ((uint32_t)(int)rintf(t) & 0xFFu) << (8 * (i & 3));
+struct Keep8Scale {
+  float scale, inv;
+  bool bad;
+  // most: the block's largest |v| before its rounding to bf16 (rounding keeps the
+  // order), as fp32 bits, which order like the values, NaN above infinity
+  __device__ __forceinline__ explicit Keep8Scale(uint32_t most) {
+    const float m = (float)(bf16)__builtin_bit_cast(float, most);
+    bad = !(m < __builtin_inff());
+    const bool none = m < 0x1p-100f;
+    scale = bad ? __builtin_nanf("") : none ? 0.0f : m * (1.0f / 127.0f);
+    // (128 / max: neither a denormal number nor an infinity)
+    inv = none || bad ? 0.0f : __builtin_amdgcn_rcpf(m * 0x1p-7f) * (0.9921875f * (1.0f + 0x1p-21f));
   }
-  return q;
-}
+  // the bytes of N bf16 values: adding 1.5 2^23 rounds to the integer and leaves it in
+  // the low bits
+  template <int N>
+  __device__ __forceinline__ uint32_t bytes(const bf16 (&v)[N]) const {
+    uint32_t b[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) b[j] = __builtin_bit_cast(uint32_t, fmaf((float)v[j], inv, 12582912.0f));
+    uint32_t q = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u);
+    if constexpr (N == 4) q |= __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
+    static_assert(N == 2 || N == 4, "bytes of a word");
+    return bad ? 0u : q;
+  }
+};
 
 __device__ __forceinline__ void keep8_unpack(u32x2 q, float scale, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = (float)(int8_t)(q[i >> 2] >> (8 * (i & 3))) * scale;
-}
-
-// Rows [0, hi) of a staged tile (at(r, c): its 8 values from column c on) to
-// q[(m0 + r) * F + n0 + c] and scales[(m0 + r) * blocks + (n0 + c) / kKeep8].  The
-// tile starts at a whole block; columns from nrows on hold zeros.
-template <int BM, int BN, int NT, class At>
-__device__ __forceinline__ void store_rows_keep8(At&& at, uint8_t* __restrict__ q, float* __restrict__ scales,
-                                                 int64_t m0, int hi, int n0, int nrows, int F, int tid) {
-  constexpr int VPR = BN / 8;
-  static_assert(BM * VPR % NT == 0 && BN % kKeep8 == 0, "whole blocks in every step");
-  const int blocks = (F + kKeep8 - 1) / kKeep8;
-  for (int v = tid; v < BM * VPR; v += NT) {
-    const int r = v / VPR, c = (v - r * VPR) * 8;
-    float scale;
-    const u32x2 x = keep8_pack(*reinterpret_cast<const u32x4*>(at(r, c)), &scale);
-    if (r >= hi || c >= nrows) continue;
-    __builtin_nontemporal_store(x, reinterpret_cast<u32x2*>(q + (m0 + r) * (int64_t)F + n0 + c));
-    if (c % kKeep8 == 0) scales[(m0 + r) * (int64_t)blocks + (n0 + c) / kKeep8] = scale;
-  }
 }
 
 }  // namespace ipttt

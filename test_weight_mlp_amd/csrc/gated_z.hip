@@ -2,16 +2,17 @@
 // MLP (lijianxiong.blog "In-Place Test-Time Training", 方法 > 原地自适应 and
 // 高效的块状更新机制; phi = SiLU).
 //
-// One workgroup computes a 128-token x 128-feature tile of Z: the same H tile
-// is multiplied by the gate and the up tiles (a dual GEMM, K = d_model), both
-// products stay in fp32 registers, and the epilogue applies SiLU(g) * u before
-// rounding once to the output type.  Z is written row-major.
+// One workgroup computes a tile of Z: the same H tile is multiplied by the gate and
+// the up tiles (a dual GEMM, K = d_model), both products stay in fp32 registers, and
+// the epilogue applies SiLU(g) * u before rounding once to the output type.  Z is
+// written row-major.
 #include <algorithm>
+#include <type_traits>
 
 #include "epilogue.h"
 #include "launch.h"
 #include "mfma_core.h"
-#include "pingpong.h"
+#include "ring.h"
 
 namespace ipttt {
 
@@ -23,6 +24,7 @@ struct Kept {
   float *sG, *sU;
 };
 
+// fp32 data: 128 x 128 tiles of 4 waves.
 template <typename T, int KEEP>
 __global__ __launch_bounds__(kThreads) void gated_z_kernel(const T* __restrict__ H, const T* __restrict__ Wg,
                                                            const T* __restrict__ Wu, T* __restrict__ Z,
@@ -94,96 +96,186 @@ __global__ __launch_bounds__(kThreads) void gated_z_kernel(const T* __restrict__
     for (int o = 0; o < 2; ++o) {
       __syncthreads();
       stage(1 + o);
-      void* to = o == 0 ? kept.G : kept.U;
-      if constexpr (KEEP == KEEP_8)
-        store_rows_keep8<G::BM, G::BN, kThreads>([&](int r, int c) { return lC + r * LDC + c; },
-                                                 static_cast<uint8_t*>(to), o == 0 ? kept.sG : kept.sU, m0, mrows, n0,
-                                                 nrows, f, tid);
-      else
-        store_tile_rows<T, G::BM, G::BN, LDC>(lC, static_cast<T*>(to), m0, mrows, n0, nrows, f, tid);
+      store_tile_rows<T, G::BM, G::BN, LDC>(lC, static_cast<T*>(o == 0 ? kept.G : kept.U), m0, mrows, n0, nrows, f, tid);
     }
   }
 }
 
-// bf16 fast path (d_model a multiple of 64): 256 tokens x 128 features per
-// tile on the persistent ping-pong core (pingpong.h), the gate and up tiles
-// of W against the same H tile; the epilogue forms SiLU(g) * u in fp32,
-// stages it through LDS and writes Z rows with non-temporal stores.  The
-// tiles are grouped 4 token tiles at a time so that an XCD's workgroups share
-// H and weight panels in its L2.
-template <int KEEP>
-__global__ __launch_bounds__(512) void gated_z_fast_kernel(const bf16* __restrict__ H, const bf16* __restrict__ Wg,
-                                                         const bf16* __restrict__ Wu, bf16* __restrict__ Z,
-                                                         Kept kept, int64_t M, int d, int f) {
-  using namespace pingpong;
-  __shared__ __attribute__((aligned(1024))) bf16 lds[LDS_ELEMS];
-  const int tid = threadIdx.x;
-  const int tiles_m = (int)((M + BM - 1) / BM), tiles_n = (f + BN - 1) / BN;
-  auto origin = [&](int tt, int64_t& m0, int& n0) {
+// bf16: NW * 32 tokens x NW * 16 features a tile on the ring (ring.h), the B rows of a
+// stage being the tile's rows of W_gate and of W_up in the order that gives a lane
+// NW / 2 neighbouring features of both products: SiLU(g) * u is formed and stored
+// straight from the accumulators.  The tiles are grouped 4 token tiles at a time so
+// that an XCD's workgroups share H and weight panels in its L2.
+template <int NW, int KEEP>
+__device__ __forceinline__ void gated_z_tiles(const bf16* __restrict__ H, const bf16* __restrict__ Wg,
+                                              const bf16* __restrict__ Wu, bf16* Z, const Kept& kept, int64_t M, int d,
+                                              int f, char* lds) {
+  typedef ring::Geo<bf16, NW> G;
+  constexpr int BF = G::BN / 2, WF = G::WN / 2, NF = G::NJ / 2;  // features of a tile, a wave, a lane
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int tiles_m = (int)((M + G::BM - 1) / G::BM), tiles_n = (f + BF - 1) / BF;
+  auto origin = [&](int t, int64_t& m0, int& n0) {
     int tm, tn;
-    grouped_tile(tt, tiles_m, tiles_n, 4, tm, tn);
-    m0 = (int64_t)tm * BM;
-    n0 = tn * BN;
+    grouped_tile(t, tiles_m, tiles_n, 4, tm, tn);
+    m0 = (int64_t)tm * G::BM;
+    n0 = tn * BF;
   };
-  auto operands = [&](int tt, core::Operand& oa, core::Operand (&ob)[2], bool&, int& S) {
+  auto stages = [&](int, int, int& s0, int& n) {
+    s0 = 0;
+    n = (d + G::KS - 1) / G::KS;
+  };
+  auto open_a = [&](int t, int, int, ring::Loader<bf16, NW, false>& l) {
     int64_t m0;
     int n0;
-    origin(tt, m0, n0);
-    S = d / KS;
-    oa = core::make_operand(H + m0 * d, (int64_t)d * 2, (M - m0) * d * 2);
-    ob[0] = core::make_operand(Wg + (int64_t)n0 * d, (int64_t)d * 2, (int64_t)(f - n0) * d * 2);
-    ob[1] = core::make_operand(Wu + (int64_t)n0 * d, (int64_t)d * 2, (int64_t)(f - n0) * d * 2);
+    origin(t, m0, n0);
+    l.init(H + m0 * d, d, M - m0, d, 0, wave, lane, [](int r) { return r; });
   };
-  auto epilogue = [&](int tt, floatx16 (&acc)[2][2][2], bf16* stg) {
-    int64_t mt;
-    int nt;
-    origin(tt, mt, nt);
-    const int mrows = (int)min((int64_t)BM, M - mt), nrows = min(BN, f - nt);
-    stage_wave(stg, [&](int mb, int nb, int j) { return silu_f32(acc[0][mb][nb][j]) * acc[1][mb][nb][j]; });
-    core::lds_barrier();
-    store_rows_swz<BM, BN, LDR, 512, true>(stg, Z, mt, 0, mrows, nt, nrows, f, tid);
-    core::lds_barrier();
-    if constexpr (KEEP != KEEP_NONE) {
+  // LDS row r: block j of 16 rows of a wave's columns, the first half of the blocks of
+  // W_gate, the second of W_up; a wave's loads (32 rows) are of one of them
+  const bf16* W = wave * 32 % G::WN < WF ? Wg : Wu;
+  auto open_b = [&](int t, int, int, ring::Loader<bf16, NW, false>& l) {
+    int64_t m0;
+    int n0;
+    origin(t, m0, n0);
+    l.init(W + (int64_t)n0 * d, d, f - n0, d, 0, wave, lane,
+           [](int r) { return r / G::WN * WF + (r & 15) * NF + (r % WF >> 4); });
+  };
+  auto epilogue = [&](int t, ring::f4 (&acc)[G::MI][G::NJ], auto&& idle) {
+    typedef bf16 vec __attribute__((ext_vector_type(NF)));
+    int64_t m0;
+    int n0;
+    origin(t, m0, n0);
+    const int n = n0 + wn * WF + (lane & 15) * NF;
+    // 8 bits: the largest of a row's block of 64 features, this wave's 64 or (NW = 4) its
+    // 32 and those of the wave beside it, exchanged through the idle slots
+    auto largest = [&](int o, int i, int e) {
+      uint32_t x = 0;
 #pragma unroll
-      for (int o = 0; o < 2; ++o) {
-        stage_wave(stg, [&](int mb, int nb, int j) { return acc[o][mb][nb][j]; });
-        core::lds_barrier();
-        void* to = o == 0 ? kept.G : kept.U;
-        if constexpr (KEEP == KEEP_8)
-          store_rows_keep8<BM, BN, 512>([&](int r, int c) { return stg + swz_elem<LDR>(r, c); },
-                                        static_cast<uint8_t*>(to), o == 0 ? kept.sG : kept.sU, mt, mrows, nt, nrows, f,
-                                        tid);
-        else
-          store_rows_swz<BM, BN, LDR, 512, true>(stg, static_cast<bf16*>(to), mt, 0, mrows, nt, nrows, f, tid);
-        core::lds_barrier();
+      for (int j = 0; j < NF; ++j) {
+        // (of a vector's element itself the cast takes the vector's first)
+        const float v = acc[i][o * NF + j][e];
+        x = max(x, __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu);
       }
+      x = dpp_max<0xB1>(x);
+      x = dpp_max<0x4E>(x);
+      x = dpp_max<0x141>(x);
+      return dpp_max<0x140>(x);  // row_mirror: all 16 lanes
+    };
+    static_assert(KEEP != KEEP_8 || (kKeep8 == 64 && (WF == 64 || BF == 64)), "a block is a wave's features, or a tile's");
+    constexpr bool SHARE = KEEP == KEEP_8 && NW == 4;
+    uint32_t top[2][SHARE ? G::MI : 1][4];
+    if constexpr (SHARE) {
+      uint32_t* share = reinterpret_cast<uint32_t*>(idle(0));
+      auto at = [&](int w, int o, int i, int e) { return ((w * 2 + o) * G::MI + i) * 16 + 4 * (lane >> 4) + e; };
+      core::lds_barrier();  // every wave is done with the stage in it
+#pragma unroll
+      for (int o = 0; o < 2; ++o)
+#pragma unroll
+        for (int i = 0; i < G::MI; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            top[o][i][e] = largest(o, i, e);
+            if ((lane & 15) == 0) share[at(wave, o, i, e)] = top[o][i][e];
+          }
+      core::lds_barrier();
+#pragma unroll
+      for (int o = 0; o < 2; ++o)
+#pragma unroll
+        for (int i = 0; i < G::MI; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top[o][i][e] = max(top[o][i][e], share[at(wave ^ 1, o, i, e)]);
     }
+#pragma unroll
+    for (int i = 0; i < G::MI; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t m = m0 + wm * G::WM + i * 16 + 4 * (lane >> 4) + e;
+        uint32_t most[2] = {};
+        if constexpr (KEEP == KEEP_8) {  // (by all lanes)
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            if constexpr (SHARE) most[o] = top[o][i][e];
+            else most[o] = largest(o, i, e);
+          }
+        }
+        if (m >= M || n >= f) continue;
+        vec z, v[2];
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+          z[j] = (bf16)(silu_f32(acc[i][j][e]) * acc[i][NF + j][e]);
+          v[0][j] = (bf16)acc[i][j][e];
+          v[1][j] = (bf16)acc[i][NF + j][e];
+        }
+        const int64_t at = m * f + n;
+        __builtin_nontemporal_store(z, reinterpret_cast<vec*>(Z + at));
+        if constexpr (KEEP == KEEP_ALL) {
+          __builtin_nontemporal_store(v[0], reinterpret_cast<vec*>(static_cast<bf16*>(kept.G) + at));
+          __builtin_nontemporal_store(v[1], reinterpret_cast<vec*>(static_cast<bf16*>(kept.U) + at));
+        }
+        if constexpr (KEEP == KEEP_8) {
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            const Keep8Scale sc(most[o]);
+            bf16 x[NF];
+#pragma unroll
+            for (int j = 0; j < NF; ++j) x[j] = v[o][j];
+            const uint32_t q = sc.bytes(x);
+            uint8_t* to = static_cast<uint8_t*>(o == 0 ? kept.G : kept.U) + at;
+            if constexpr (NF == 4) __builtin_nontemporal_store(q, reinterpret_cast<uint32_t*>(to));
+            else __builtin_nontemporal_store((uint16_t)q, reinterpret_cast<uint16_t*>(to));
+            if (n % kKeep8 == 0) (o == 0 ? kept.sG : kept.sU)[m * ((f + kKeep8 - 1) / kKeep8) + n / kKeep8] = sc.scale;
+          }
+        }
+      }
   };
-  pingpong::run(lds, tiles_m * tiles_n, operands, epilogue);
+  ring::run<bf16, NW, false, false, 1>(lds, tiles_m * tiles_n, 0, stages, open_a, open_b, epilogue);
+}
+
+template <int NW, int KEEP>
+__global__ __launch_bounds__(NW * 64, NW == 8 ? 1 : 2) void gated_z_ring_kernel(const bf16* H, const bf16* Wg,
+                                                                              const bf16* Wu, bf16* Z, Kept kept,
+                                                                              int64_t M, int d, int f) {
+  __shared__ __attribute__((aligned(1024))) char lds[ring::Geo<bf16, NW>::LDS_BYTES];
+  gated_z_tiles<NW, KEEP>(H, Wg, Wu, Z, kept, M, d, f, lds);
 }
 
 namespace {
 
+// Whether tiles of 8 waves end sooner than those of 4, from the rounds that each
+// takes: a tile of 4 waves has a quarter of the products and, two on a CU, takes some
+// 0.31 of the time.
+bool wide_tiles(int64_t M, int f, int cus) {
+  const auto rounds = [&](int64_t nw, int64_t groups) {
+    return (((M + nw * 32 - 1) / (nw * 32)) * ((f + nw * 16 - 1) / (nw * 16)) + groups - 1) / groups;
+  };
+  return (double)rounds(8, cus) <= 0.62 * (double)rounds(4, 2 * cus);
+}
+
 template <int KEEP>
 hipError_t launch_kept(const Prob& p, const void* H, const void* Wg, const void* Wu, void* Z, const Kept& kept,
                        hipStream_t st) {
-  const int64_t tiles = ((p.M + 127) / 128) * ((p.f + 127) / 128);
   note_launch("gated_z", st);
-  if (p.dtype == 1 && p.d % 64 == 0) {
-    // one persistent workgroup per CU (the mapping needs a multiple of 8)
+  if (p.dtype == 1) {
+    const auto go = [&](auto nw, int cus) {
+      constexpr int NW = decltype(nw)::value;
+      const int64_t tiles = ((p.M + NW * 32 - 1) / (NW * 32)) * ((p.f + NW * 16 - 1) / (NW * 16));
+      const int64_t g = std::min<int64_t>(cus * (NW == 8 ? 1 : 2), (tiles + 7) / 8 * 8);
+      gated_z_ring_kernel<NW, KEEP><<<(unsigned)g, NW * 64, 0, st>>>((const bf16*)H, (const bf16*)Wg, (const bf16*)Wu,
+                                                                    (bf16*)Z, kept, p.M, p.d, p.f);
+    };
+    // one persistent workgroup of 8 waves a CU, or two of 4 (the walk needs a multiple
+    // of 8)
     int dev = 0, cus = 256;
     if (hipGetDevice(&dev) == hipSuccess)
       (void)hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
-    const int64_t fast_tiles = ((p.M + 255) / 256) * ((p.f + 127) / 128);
-    const int64_t g = std::min<int64_t>(std::max(8, cus / 8 * 8), (fast_tiles + 7) / 8 * 8);
-    gated_z_fast_kernel<KEEP><<<(unsigned)g, 512, 0, st>>>((const bf16*)H, (const bf16*)Wg, (const bf16*)Wu, (bf16*)Z,
-                                                         kept, p.M, p.d, p.f);
-  } else if (p.dtype == 1) {
-    gated_z_kernel<bf16, KEEP><<<(unsigned)tiles, kThreads, 0, st>>>((const bf16*)H, (const bf16*)Wg, (const bf16*)Wu,
-                                                                     (bf16*)Z, kept, p.M, p.d, p.f);
+    cus = std::max(8, cus / 8 * 8);
+    if (wide_tiles(p.M, p.f, cus)) go(std::integral_constant<int, 8>(), cus);
+    else go(std::integral_constant<int, 4>(), cus);
   } else if constexpr (KEEP == KEEP_8) {
     return hipErrorInvalidValue;  // 8 bits are for bf16 data
   } else {
+    const int64_t tiles = ((p.M + 127) / 128) * ((p.f + 127) / 128);
     gated_z_kernel<float, KEEP><<<(unsigned)tiles, kThreads, 0, st>>>(
         (const float*)H, (const float*)Wg, (const float*)Wu, (float*)Z, kept, p.M, p.d, p.f);
   }

@@ -44,7 +44,9 @@ __device__ __forceinline__ float slope_f32(int act, float v) {
 // `per` stages each, whose fp32 partial tiles a second launch joins.
 struct RingPlan {
   int nw;                 // 8: tiles of 256 x 256, 4: of 128 x 128
-  int tiles_m, tiles_n, whole, split, parts, per, stages;
+  int tiles_m, tiles_n;   // tiles_m: of both products, where there are two
+  int whole, split, parts, per;
+  int stages, legs;       // stages of a leg
 };
 
 // N neighbouring elements, 16-byte aligned (or less where they are fewer bytes).
@@ -100,7 +102,7 @@ __device__ __forceinline__ void load_res(const GemmArgs& g, int64_t m0, int64_t 
 // rows in the order of PERM (K contiguous) a lane has NJ neighbouring columns and
 // the whole epilogue; K-major products have none and store column by column.
 template <typename T, int NW, bool BK>
-__device__ __forceinline__ void finish_block(const GemmArgs& g, int64_t m0, int64_t n0, int i,
+__device__ __forceinline__ void finish_block(const GemmArgs& g, const Rows& c, int64_t m0, int64_t n0, int i,
                                              const Vec<T, ring::Geo<T, NW>::NJ> (&res)[4],
                                              ring::f4 (&acc)[ring::Geo<T, NW>::NJ]) {
   typedef ring::Geo<T, NW> G;
@@ -123,23 +125,25 @@ __device__ __forceinline__ void finish_block(const GemmArgs& g, int64_t m0, int6
   } else {
     const int64_t n = n0 + wn * G::WN + (lane & 15);
     const int blocks = n < g.N ? (int)min((int64_t)G::NJ, (g.N - n + 15) / 16) : 0;
-    auto store = [&](auto* c) {
+    auto store = [&](auto* to) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (m + e >= g.M) break;
-        auto* row = c + (m + e) * g.c.ld + n;
+        auto* row = to + (m + e) * c.ld + n;
 #pragma unroll
         for (int j = 0; j < G::NJ; ++j)
-          if (j < blocks) row[j * 16] = from_f32<std::remove_pointer_t<decltype(c)>>(acc[j][e]);
+          if (j < blocks) row[j * 16] = from_f32<std::remove_pointer_t<decltype(to)>>(acc[j][e]);
       }
     };
-    if (g.c_f32) store(static_cast<float*>(g.c.p));
-    else store(static_cast<T*>(g.c.p));
+    if (g.c_f32) store(static_cast<float*>(c.p));
+    else store(static_cast<T*>(c.p));
   }
 }
 
-// The tile of an item, and the part of it (-1: whole).
-__device__ __forceinline__ void ring_item(const RingPlan& p, int t, int64_t& m0, int64_t& n0, int& part) {
+// The tile of an item, and the part of it (-1: whole).  Of two products the second
+// has the second half of the tile rows.
+__device__ __forceinline__ bool ring_item(const GemmArgs& g, const RingPlan& p, int t, int64_t& m0, int64_t& n0,
+                                          int& part) {
   int tile = t;
   part = -1;
   if (t >= p.whole) {
@@ -149,40 +153,46 @@ __device__ __forceinline__ void ring_item(const RingPlan& p, int t, int64_t& m0,
   int tm, tn;
   // four rows of tiles walked together: an XCD's workgroups share both operands' panels
   grouped_tile(tile, p.tiles_m, p.tiles_n, 4, tm, tn);
-  m0 = (int64_t)tm * p.nw * 32;
+  const bool second = g.two_products && tm >= p.tiles_m / 2;
+  m0 = (int64_t)(second ? tm - p.tiles_m / 2 : tm) * p.nw * 32;
   n0 = (int64_t)tn * p.nw * 32;
+  return second;
 }
 
-template <typename T, int NW, bool AK, bool BK>
-__device__ __forceinline__ void ring_product(const T* __restrict__ A, const T* __restrict__ B, const GemmArgs& g,
-                                             const RingPlan& p, char* lds) {
+template <typename T, int NW, bool AK, bool BK, int LEGS>
+__device__ __forceinline__ void ring_product(const T* __restrict__ A, const T* __restrict__ B, const T* __restrict__ A2,
+                                             const T* __restrict__ B2, const GemmArgs& g, const RingPlan& p, char* lds) {
   typedef ring::Geo<T, NW> G;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  auto stages = [&](int t, int& s0, int& n) {
-    s0 = 0;
-    n = p.stages;
+  // an item's stages, counted through the legs, cut at the leg's ends
+  auto stages = [&](int t, int leg, int& s0, int& n) {
+    int from = 0, to = p.stages * LEGS;
     if (t >= p.whole) {
-      s0 = (t - p.whole) % p.parts * p.per;
-      n = min(p.per, p.stages - s0);
+      from = (t - p.whole) % p.parts * p.per;
+      to = min(to, from + p.per);
     }
+    s0 = max(0, from - leg * p.stages);
+    n = min(p.stages, to - leg * p.stages) - s0;
   };
-  auto open_a = [&](int t, int s0, ring::Loader<T, NW, AK>& l) {
+  auto open_a = [&](int t, int leg, int s0, ring::Loader<T, NW, AK>& l) {
     int64_t m0, n0;
     int part;
-    ring_item(p, t, m0, n0, part);
-    l.init(A + (AK ? m0 : m0 * g.a.ld), g.a.ld, g.M - m0, g.K, s0, wave, lane, [](int r) { return r; });
+    const bool second = ring_item(g, p, t, m0, n0, part);
+    const T* from = (LEGS > 1 && leg == 1) || second ? A2 : A;
+    l.init(from + (AK ? m0 : m0 * g.a.ld), g.a.ld, g.M - m0, g.K, s0, wave, lane, [](int r) { return r; });
   };
-  auto open_b = [&](int t, int s0, ring::Loader<T, NW, BK>& l) {
+  auto open_b = [&](int t, int leg, int s0, ring::Loader<T, NW, BK>& l) {
     int64_t m0, n0;
     int part;
-    ring_item(p, t, m0, n0, part);
-    l.init(B + (BK ? n0 : n0 * g.b.ld), g.b.ld, g.N - n0, g.K, s0, wave, lane,
+    ring_item(g, p, t, m0, n0, part);
+    const T* from = LEGS > 1 && leg == 1 ? B2 : B;
+    l.init(from + (BK ? n0 : n0 * g.b.ld), g.b.ld, g.N - n0, g.K, s0, wave, lane,
            [](int r) { return ring::perm_row<NW>(r); });
   };
-  auto epilogue = [&](int t, ring::f4 (&acc)[G::MI][G::NJ]) {
+  auto epilogue = [&](int t, ring::f4 (&acc)[G::MI][G::NJ], auto&&) {
     int64_t m0, n0;
     int part;
-    ring_item(p, t, m0, n0, part);
+    const Rows& c = ring_item(g, p, t, m0, n0, part) ? g.c2 : g.c;
     if (part >= 0) {
       ring::f4* to = reinterpret_cast<ring::f4*>(g.part) + (int64_t)(t - p.whole) * G::MI * G::NJ * G::NT + threadIdx.x;
 #pragma unroll
@@ -201,16 +211,17 @@ __device__ __forceinline__ void ring_product(const T* __restrict__ A, const T* _
         for (int q = 0; q < 2; ++q) load_res<T, NW>(g, m0, n0, i + q, res[q]);
       }
 #pragma unroll
-      for (int q = 0; q < 2; ++q) finish_block<T, NW, BK>(g, m0, n0, i + q, res[q], acc[i + q]);
+      for (int q = 0; q < 2; ++q) finish_block<T, NW, BK>(g, c, m0, n0, i + q, res[q], acc[i + q]);
     }
   };
-  ring::run<T, NW, AK, BK>(lds, p.whole, p.split * p.parts, stages, open_a, open_b, epilogue);
+  ring::run<T, NW, AK, BK, LEGS>(lds, p.whole, p.split * p.parts, stages, open_a, open_b, epilogue);
 }
 
-template <typename T, int NW, bool AK, bool BK>
+template <typename T, int NW, bool AK, bool BK, int LEGS = 1>
 __global__ __launch_bounds__(NW * 64, NW == 8 ? 1 : 2) void ring_kernel(GemmArgs g, RingPlan p) {
   __shared__ __attribute__((aligned(1024))) char lds[ring::Geo<T, NW>::LDS_BYTES];
-  ring_product<T, NW, AK, BK>(static_cast<const T*>(g.a.p), static_cast<const T*>(g.b.p), g, p, lds);
+  ring_product<T, NW, AK, BK, LEGS>(static_cast<const T*>(g.a.p), static_cast<const T*>(g.b.p),
+                                    static_cast<const T*>(g.a2.p), static_cast<const T*>(g.b2.p), g, p, lds);
 }
 
 // Sums the parts of a split tile in order and finishes it; blockIdx.y takes a block
@@ -221,7 +232,7 @@ __global__ __launch_bounds__(NW * 64) void ring_join_kernel(GemmArgs g, RingPlan
   const int i = blockIdx.y, t = p.whole + blockIdx.x * p.parts;
   int64_t m0, n0;
   int part;
-  ring_item(p, t, m0, n0, part);
+  const Rows& c = ring_item(g, p, t, m0, n0, part) ? g.c2 : g.c;
   Vec<T, G::NJ> res[4];
   if constexpr (!BK) load_res<T, NW>(g, m0, n0, i, res);
   const ring::f4* from = reinterpret_cast<const ring::f4*>(g.part) +
@@ -234,7 +245,7 @@ __global__ __launch_bounds__(NW * 64) void ring_join_kernel(GemmArgs g, RingPlan
 #pragma unroll
     for (int j = 0; j < G::NJ; ++j) acc[j] += from[j * G::NT];
   }
-  finish_block<T, NW, BK>(g, m0, n0, i, res, acc);
+  finish_block<T, NW, BK>(g, c, m0, n0, i, res, acc);
 }
 
 constexpr int kCus = 256;
@@ -244,9 +255,10 @@ RingPlan plan_ring(const GemmArgs& g) {
   RingPlan best{};
   double least = 1e300;
   for (const int nw : {8, 4}) {
-    const int64_t w = nw * 32, tm = (g.M + w - 1) / w, tn = (g.N + w - 1) / w, tiles = tm * tn;
+    const int64_t w = nw * 32, tm = (g.M + w - 1) / w * (g.two_products ? 2 : 1), tn = (g.N + w - 1) / w, tiles = tm * tn;
     const int64_t groups = nw == 8 ? kCus : 2 * kCus;
-    const int ks = g.dtype == 1 ? ring::kStage<bf16> : ring::kStage<float>, stages = (int)((g.K + ks - 1) / ks);
+    const int ks = g.dtype == 1 ? ring::kStage<bf16> : ring::kStage<float>, legs = g.two_pairs ? 2 : 1,
+              leg = (int)((g.K + ks - 1) / ks), stages = legs * leg;
     // us, on a full and a half empty device
     const double stage = g.dtype != 1 ? (nw == 8 ? 7.5 : 3.8) : nw == 8 ? 1.5 : 1.0;
     const double lone = g.dtype != 1 ? (nw == 8 ? 7.5 : 2.0) : nw == 8 ? 1.2 : 0.7;
@@ -261,7 +273,7 @@ RingPlan plan_ring(const GemmArgs& g) {
       if (parts > 1) t += 5.0 + (double)items * w * w * 8 / 4.0e6;
       if (t >= least) return;
       least = t;
-      best = RingPlan{nw, (int)tm, (int)tn, (int)(parts > 1 ? whole : tiles), (int)(parts > 1 ? split : 0), parts, per, stages};
+      best = RingPlan{nw, (int)tm, (int)tn, (int)(parts > 1 ? whole : tiles), (int)(parts > 1 ? split : 0), parts, per, leg, legs};
     };
     consider(tiles, 1);
     const int64_t whole = tiles / groups * groups, rem = tiles - whole;
@@ -278,7 +290,9 @@ hipError_t launch_ring(const GemmArgs& g, const RingPlan& p, hipStream_t st) {
   const unsigned grid = (unsigned)std::min<int64_t>(kCus * G::MAX_GROUPS, (items + 7) / 8 * 8);
   note_launch("linear", st);
   if (!g.a_kmaj && !g.b_kmaj) ring_kernel<T, NW, false, false><<<grid, G::NT, 0, st>>>(g, p);
-  else if (!g.a_kmaj) ring_kernel<T, NW, false, true><<<grid, G::NT, 0, st>>>(g, p);
+  else if (p.legs == 2) {
+    if constexpr (sizeof(T) == 2) ring_kernel<T, NW, false, true, 2><<<grid, G::NT, 0, st>>>(g, p);
+  } else if (!g.a_kmaj) ring_kernel<T, NW, false, true><<<grid, G::NT, 0, st>>>(g, p);
   else ring_kernel<T, NW, true, true><<<grid, G::NT, 0, st>>>(g, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.split == 0) return e;
@@ -439,7 +453,10 @@ constexpr int kStrips = 256;  // most strips of rows of a column sum
 size_t gemm_workspace(const GemmArgs& g) { return few_rows(g) ? 0 : ring_bytes(plan_ring(g)); }
 
 hipError_t launch_gemm(const GemmArgs& g, hipStream_t st) {
-  if (g.a_kmaj && !g.b_kmaj) return hipErrorInvalidValue;  // no caller has such a product
+  // products that no caller has
+  if (g.a_kmaj && !g.b_kmaj) return hipErrorInvalidValue;
+  if (g.two_pairs && (g.a_kmaj || !g.b_kmaj || g.two_products || g.dtype != 1)) return hipErrorInvalidValue;
+  if (g.two_products && (!g.a_kmaj || g.dtype != 1)) return hipErrorInvalidValue;
   if (few_rows(g)) {
     if (g.dtype == 1) launch_few<bf16>(g, st);
     else launch_few<float>(g, st);

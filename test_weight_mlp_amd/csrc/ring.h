@@ -256,14 +256,17 @@ struct Walk {
   }
 };
 
-// Walks the items.  stages(t, first, n) gives item t's first stage and their number
-// (at least one); open_a(t, first, loader) and open_b set its operands;
-// epilogue(t, acc) takes the finished tile: block (i, j), element e of a lane is
+// Walks the items.  An item is summed over LEGS legs, pairs of operands:
+// stages(t, leg, first, n) gives the first stage of one and their number (of some leg
+// at least one), open_a(t, leg, first, loader) and open_b set its operands.
+// epilogue(t, acc, idle) takes the finished tile, with idle two slots that nothing
+// reads or loads until the next barrier that all waves meet after it (waves may
+// still be reading them when it begins): block (i, j), element e of a lane is
 // row wm * 64 + i * 16 + 4 * (lane / 16) + e and LDS row wn * WN + j * 16 + lane % 16
 // of B.  A and B are restrict so that the compiler tells the LDS reads apart from
 // the direct loads and puts no wait for those in front of them; the ring's own
 // waits order them.
-template <typename T, int NW, bool AK, bool BK, class Stages, class OpenA, class OpenB, class Epilogue>
+template <typename T, int NW, bool AK, bool BK, int LEGS, class Stages, class OpenA, class OpenB, class Epilogue>
 __device__ __forceinline__ void run(char* lds, int n1, int n2, Stages&& stages, OpenA&& open_a, OpenB&& open_b,
                                     Epilogue&& epilogue) {
   typedef Geo<T, NW> G;
@@ -277,19 +280,38 @@ __device__ __forceinline__ void run(char* lds, int n1, int n2, Stages&& stages, 
   Reader<T, NW, BK> rb;
   ra.init(wm * G::WM, lane);
   rb.init(wn * G::WN, lane);
-  // Stages left to issue of the items that the loaders stand at, and whether
+  // The legs that the loaders stand at, their stages left to issue, and whether
   // there is one.
-  int na = 0, nb = 0;
+  int na = 0, nb = 0, leg_a = -1, leg_b = -1;
   bool on_a = true, on_b = true;
+  // to the next leg that has stages, of this item or the next
   auto enter_a = [&]() {
     int s;
-    stages(wa.t, s, na);
-    open_a(wa.t, s, la);
+    for (na = 0;;) {
+      if (++leg_a == LEGS) {
+        leg_a = 0;
+        wa.next();
+        on_a = wa.on();
+        if (!on_a) return;
+      }
+      stages(wa.t, leg_a, s, na);
+      if (LEGS == 1 || na > 0) break;
+    }
+    open_a(wa.t, leg_a, s, la);
   };
   auto enter_b = [&]() {
     int s;
-    stages(wb.t, s, nb);
-    open_b(wb.t, s, lb);
+    for (nb = 0;;) {
+      if (++leg_b == LEGS) {
+        leg_b = 0;
+        wb.next();
+        on_b = wb.on();
+        if (!on_b) return;
+      }
+      stages(wb.t, leg_b, s, nb);
+      if (LEGS == 1 || nb > 0) break;
+    }
+    open_b(wb.t, leg_b, s, lb);
   };
   enter_a();
   enter_b();
@@ -297,22 +319,12 @@ __device__ __forceinline__ void run(char* lds, int n1, int n2, Stages&& stages, 
   auto past = [](int x) { return x >= RING ? x - RING : x; };
   int a = 0;  // where A of the stage to multiply lies; the slots after it: B, the next A, the next B, the A after
   auto advance_a = [&]() {
-    if (--na > 0) {
-      la.advance();
-      return;
-    }
-    wa.next();
-    on_a = wa.on();
-    if (on_a) enter_a();
+    if (--na > 0) la.advance();
+    else enter_a();
   };
   auto advance_b = [&]() {
-    if (--nb > 0) {
-      lb.advance();
-      return;
-    }
-    wb.next();
-    on_b = wb.on();
-    if (on_b) enter_b();
+    if (--nb > 0) lb.advance();
+    else enter_b();
   };
   la.issue(lds, wave, true);
   advance_a();
@@ -335,8 +347,6 @@ __device__ __forceinline__ void run(char* lds, int n1, int n2, Stages&& stages, 
 #pragma unroll
       for (int j = 0; j < G::NJ; ++j) acc[i][j] = f4{0.0f, 0.0f, 0.0f, 0.0f};
     typename Frag<T>::type fa[G::MI], fb[G::NJ];
-    int s0, S;
-    stages(w.t, s0, S);
     auto read = [&](int h) {
       const char *pa = lds + a, *pb = lds + past(a + G::SLOT);
 #pragma unroll
@@ -425,19 +435,25 @@ __device__ __forceinline__ void run(char* lds, int n1, int n2, Stages&& stages, 
     };
     // Group 1 meets one barrier more before its phases, group 0 one after.
     if (NW == 8 && grp == 1) core::lds_barrier();
-    int s = 0;
-    const int steady = S - 3;
-    if (steady > 0) {
-      la.uniform();
-      lb.uniform();
-      for (; s < steady; ++s) stage(std::true_type());
-      na -= steady;
-      nb -= steady;
+#pragma unroll
+    for (int leg = 0; leg < LEGS; ++leg) {
+      int s0, S, s = 0;
+      stages(w.t, leg, s0, S);
+      // the loaders are up to two stages ahead, in this leg
+      const int steady = S - 3;
+      if (steady > 0) {
+        la.uniform();
+        lb.uniform();
+        for (; s < steady; ++s) stage(std::true_type());
+        na -= steady;
+        nb -= steady;
+      }
+      for (; s < S; ++s) stage(std::false_type());
     }
-    for (; s < S; ++s) stage(std::false_type());
     if (NW == 8 && grp == 0) core::lds_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    epilogue(w.t, acc);
+    // the stage multiplied last lies in the two slots before a
+    epilogue(w.t, acc, [&](int which) { return lds + past(a + (NSLOT - 2 + which) * G::SLOT); });
   }
 }
 

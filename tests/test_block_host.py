@@ -65,7 +65,7 @@ def test_activations_far_out():
 def test_kept_values():
     g = np.array([[127.0, -63.5, 1.4, 1.6, 0.0] + [0.0] * 60 + [2.54, 1.0]])
     k = ob.kept8(g)
-    assert k[0, :5].tolist() == [127.0, -64.0, 1.0, 2.0, 0.0]     # a tie goes to the even one
+    assert k[0, :5].tolist() == [127.0, -64.0, 1.0, 2.0, 0.0]     # a tie goes away from zero
     assert np.allclose(k[0, 64:], [0.0, 2.54, 1.0])               # the second block: multiples of 0.02
     assert not ob.kept8(np.zeros((2, 70))).any()
 
