@@ -1,7 +1,7 @@
 // Layer norm and RMS norm of rows, and their gradients.
 //
-// A row is held in the registers of one wave (or, wider rows, of a workgroup's
-// four), in 16-byte pieces a lane, so that it is read once: the mean, the squares
+// A row is held in the registers of one wave (or, wider rows, of several in a
+// workgroup), in 16-byte pieces a lane, so that it is read once: the mean, the squares
 // about it and the output come from the same registers.  All arithmetic is
 // fp32; the outputs are rounded once.
 #include "block.h"
@@ -31,12 +31,12 @@ __device__ __forceinline__ float wave_sum(float x) {
   return x;
 }
 
-// N sums over a row's lanes: the wave's, or (NW = 4) the workgroup's through LDS.
-// slot alternates between consecutive calls, so that one barrier a call is
-// enough: a wave that writes a slot again has passed the barrier of the call
-// between, which every wave meets after its reads of that slot.
+// N sums over a row's lanes: the wave's, or (NW > 1) those of NW neighbouring waves
+// through LDS, red[slot][wave].  slot alternates between consecutive calls, so that one
+// barrier a call is enough: a wave that writes a slot again has passed the barrier of
+// the call between, which every wave meets after its reads of that slot.
 template <int NW, int N>
-__device__ __forceinline__ void row_sum(float (&x)[N], float (*red)[4][N], int slot, int wave) {
+__device__ __forceinline__ void row_sum(float (&x)[N], float (*red)[8][N], int slot, int wave) {
 #pragma unroll
   for (int i = 0; i < N; ++i) x[i] = wave_sum(x[i]);
   if constexpr (NW > 1) {
@@ -45,8 +45,13 @@ __device__ __forceinline__ void row_sum(float (&x)[N], float (*red)[4][N], int s
       for (int i = 0; i < N; ++i) red[slot][wave][i] = x[i];
     }
     __syncthreads();
+    const int first = wave / NW * NW;
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = red[slot][0][i] + red[slot][1][i] + red[slot][2][i] + red[slot][3][i];
+    for (int i = 0; i < N; ++i) {
+      x[i] = red[slot][first][i];
+#pragma unroll
+      for (int q = 1; q < NW; ++q) x[i] += red[slot][first + q][i];
+    }
   }
 }
 
@@ -60,7 +65,7 @@ template <typename T, int NW, int IT>
 __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
   constexpr int V = Piece<T>::V, L = NW * 64;
   typedef typename Piece<T>::vec vec;
-  __shared__ float red[2][4][1];
+  __shared__ float red[2][8][1];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x % L;
   for (int64_t row = (int64_t)blockIdx.x * (4 / NW) + wave / NW; row < a.rows; row += (int64_t)gridDim.x * (4 / NW)) {
     const T* x = static_cast<const T*>(a.x.p) + row * a.x.ld;
@@ -111,35 +116,44 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
   }
 }
 
-// Rows of a grid's stride a wave (or workgroup); the weight gradients of a
-// lane's columns stay in registers until its last row, and each workgroup writes
-// one partial.
+// NW waves a row, 8 / NW rows a workgroup at a time.  The weight gradients of a lane's
+// columns stay in registers until its last row, and each workgroup writes one partial
+// (a lone one the result).  Bound by the memory: 16384 x 2560 in bf16 with dres 83 us
+// for 336 MB (4.0 TB/s), 32768 x 1024 58 us (4.6 TB/s).  Loading the next row's pieces
+// before the current row's sums gained nothing (84 and 59 us): with 16 waves resident
+// the others' loads fill the wait.
 template <typename T, int NW, int IT>
-__global__ __launch_bounds__(256, 1) void norm_bwd_kernel(NormArgs a) {
-  constexpr int V = Piece<T>::V, L = NW * 64;
+__global__ __launch_bounds__(512) void norm_bwd_kernel(NormArgs a) {
+  constexpr int V = Piece<T>::V, L = NW * 64, ROWS = 8 / NW;
   typedef typename Piece<T>::vec vec;
-  __shared__ float red[2][4][3];
-  __shared__ float red1[2][4][1];
-  __shared__ float sum[NW == 1 ? 4 : 1][NW == 1 ? IT * L * V : 1];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x % L;
+  __shared__ float red[2][8][3];
+  __shared__ float red1[2][8][1];
+  __shared__ float sum[NW < 8 ? ROWS : 1][NW < 8 ? IT * L * V : 1];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x % L, group = wave / NW;
   const bool grads = a.dw != nullptr || a.db != nullptr;
   float dw[IT][V], db[IT][V];
 #pragma unroll
   for (int i = 0; i < IT; ++i)
 #pragma unroll
     for (int e = 0; e < V; ++e) dw[i][e] = db[i][e] = 0.0f;
-  int slot = 0;
-  for (int64_t row = (int64_t)blockIdx.x * (4 / NW) + wave / NW; row < a.rows;
-       row += (int64_t)gridDim.x * (4 / NW), slot ^= 1) {
-    const T* xp = static_cast<const T*>(a.x.p) + row * a.x.ld;
-    const T* yp = static_cast<const T*>(a.dy.p) + row * a.dy.ld;
-    vec x[IT], dy[IT];
+  auto load = [&](const Rows& t, int64_t row, vec (&to)[IT]) {
+    const T* p = static_cast<const T*>(t.p) + row * t.ld;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
       const int c = (i * L + lane) * V;
-      x[i] = c < a.dim ? *reinterpret_cast<const vec*>(xp + c) : vec{};
-      dy[i] = c < a.dim ? *reinterpret_cast<const vec*>(yp + c) : vec{};
+      to[i] = c < a.dim && row < a.rows ? *reinterpret_cast<const vec*>(p + c) : vec{};
     }
+  };
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  vec x[IT], dy[IT];
+  load(a.x, (int64_t)blockIdx.x * ROWS + group, x);
+  load(a.dy, (int64_t)blockIdx.x * ROWS + group, dy);
+  int slot = 0;
+  // all groups make the same rounds (they meet in row_sum); rows past the end are zeros
+  for (int64_t first = (int64_t)blockIdx.x * ROWS; first < a.rows; first += step, slot ^= 1) {
+    const int64_t row = first + group;
+    vec more[IT];
+    if (a.dres.p != nullptr) load(a.dres, row, more);
     float mu[1] = {0.0f};
     if (a.center) {
 #pragma unroll
@@ -168,68 +182,71 @@ __global__ __launch_bounds__(256, 1) void norm_bwd_kernel(NormArgs a) {
     row_sum<NW>(s, red, slot, wave);
     const float n = (float)a.dim, r = rsqrtf(s[0] / n + a.eps);
     const float mean_u = a.center ? s[1] / n : 0.0f, along = s[2] / n * r * r;
-    const T* rp = a.dres.p != nullptr ? static_cast<const T*>(a.dres.p) + row * a.dres.ld : nullptr;
     T* op = static_cast<T*>(a.dx.p) + row * a.dx.ld;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
       const int c = (i * L + lane) * V;
-      if (c >= a.dim) continue;
-      vec w, more, o;
+      if (c >= a.dim || row >= a.rows) continue;
+      vec w, o;
       if (a.w != nullptr) w = *reinterpret_cast<const vec*>(static_cast<const T*>(a.w) + c);
-      if (rp != nullptr) more = *reinterpret_cast<const vec*>(rp + c);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float g = (float)dy[i][e], d = (float)x[i][e] - mu[0];
         const float u = a.w != nullptr ? g * (float)w[e] : g;
         float v = r * (u - mean_u - d * along);
-        if (rp != nullptr) v += (float)more[e];
+        if (a.dres.p != nullptr) v += (float)more[i][e];
         o[e] = (T)v;
         dw[i][e] = fmaf(g, d * r, dw[i][e]);
         db[i][e] += g;
       }
       *reinterpret_cast<vec*>(op + c) = o;
     }
+    load(a.x, row + step, x);
+    load(a.dy, row + step, dy);
   }
   if (!grads) return;
-  float* part = a.part + (int64_t)blockIdx.x * 2 * a.dim;
-  if constexpr (NW == 1) {
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
+  for (int which = 0; which < 2; ++which) {
+    float* to = which == 0 ? a.dw : a.db;
+    if (gridDim.x > 1) to = a.part + ((int64_t)blockIdx.x * 2 + which) * a.dim;
+    if constexpr (NW < 8) {
+      __syncthreads();
 #pragma unroll
       for (int i = 0; i < IT; ++i)
 #pragma unroll
-        for (int e = 0; e < V; ++e) sum[wave][(i * L + lane) * V + e] = which == 0 ? dw[i][e] : db[i][e];
+        for (int e = 0; e < V; ++e) sum[group][(i * L + lane) * V + e] = which == 0 ? dw[i][e] : db[i][e];
       __syncthreads();
-      for (int c = threadIdx.x; c < a.dim; c += 256) part[which * a.dim + c] = sum[0][c] + sum[1][c] + sum[2][c] + sum[3][c];
-      __syncthreads();
-    }
-  } else {
+      for (int c = threadIdx.x; c < a.dim && to != nullptr; c += 512) {
+        float t = sum[0][c];
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const int c = (i * L + lane) * V;
-      if (c >= a.dim) continue;
+        for (int q = 1; q < ROWS; ++q) t += sum[q][c];
+        to[c] = t;
+      }
+    } else {
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        part[c + e] = dw[i][e];
-        part[a.dim + c + e] = db[i][e];
+      for (int i = 0; i < IT; ++i) {
+        const int c = (i * L + lane) * V;
+        if (c >= a.dim || to == nullptr) continue;
+#pragma unroll
+        for (int e = 0; e < V; ++e) to[c + e] = which == 0 ? dw[i][e] : db[i][e];
       }
     }
   }
 }
 
-// dw and db: the partials of 32 columns a workgroup, eight threads a column, in a
-// fixed order.
-__global__ __launch_bounds__(256) void norm_sum_kernel(const float* part, int parts, int dim, float* dw, float* db) {
-  __shared__ float red[8][32];
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
+// dw and db: the partials of 16 columns a workgroup, 32 threads a column, in a fixed
+// order.
+__global__ __launch_bounds__(512) void norm_sum_kernel(const float* part, int parts, int dim, float* dw, float* db) {
+  __shared__ float red[32][17];
+  const int c = blockIdx.x * 16 + (threadIdx.x & 15), g = threadIdx.x >> 4;
   float x = 0.0f;
   if (c < 2 * dim)
-    for (int p = g; p < parts; p += 8) x += part[(int64_t)p * 2 * dim + c];
-  red[g][threadIdx.x & 31] = x;
+    for (int p = g; p < parts; p += 32) x += part[(int64_t)p * 2 * dim + c];
+  red[g][threadIdx.x & 15] = x;
   __syncthreads();
-  if (g != 0 || c >= 2 * dim) return;
+  if (threadIdx.x >= 16 || c >= 2 * dim) return;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) x += red[i][threadIdx.x & 31];
+  for (int i = 1; i < 32; ++i) x += red[i][threadIdx.x];
   float* out = c < dim ? dw : db;
   if (out != nullptr) out[c < dim ? c : c - dim] = x;
 }
@@ -265,7 +282,44 @@ void with_row(int dim, bool wave, F&& f) {
   else with_pieces<T, 4>(it, f);
 }
 
-constexpr int kNormParts = 512;
+// The gradient's waves a row: as few as hold it in kGradPieces 16-byte pieces a lane
+// (16384 x 2560 in bf16 83 us; one wave with 5 pieces, its registers spilled, 112;
+// 8192 x 2560 in fp32 74 with 4 waves and 3 pieces, 87 with 2 and 5).
+constexpr int kGradPieces = 3;
+int pieces_a_lane(int dtype, int nw, int dim) {
+  const int v = dtype == 1 ? 8 : 4;
+  return (dim + nw * 64 * v - 1) / (nw * 64 * v);
+}
+int grad_waves(int dtype, int dim) {
+  int nw = 1;
+  while (nw < 8 && pieces_a_lane(dtype, nw, dim) > kGradPieces) nw *= 2;
+  return nw;
+}
+
+template <typename T, int NW, typename F>
+void with_grad_pieces(int it, F&& f) {
+  constexpr int most = NW < 8 ? kGradPieces : 16384 / (8 * 64 * Piece<T>::V);
+  auto pick = [&](auto n) {
+    if constexpr (decltype(n)::value <= most) f(std::integral_constant<int, NW>(), n);
+  };
+  if (it <= 1) pick(std::integral_constant<int, 1>());
+  else if (it <= 2) pick(std::integral_constant<int, 2>());
+  else if (it <= 3) pick(std::integral_constant<int, 3>());
+  else if (it <= 4) pick(std::integral_constant<int, 4>());
+  else if (it <= 6) pick(std::integral_constant<int, 6>());
+  else pick(std::integral_constant<int, 8>());
+}
+
+template <typename T, typename F>
+void with_grad_row(int dtype, int dim, F&& f) {
+  const int nw = grad_waves(dtype, dim), it = pieces_a_lane(dtype, nw, dim);
+  switch (nw) {
+    case 1: return with_grad_pieces<T, 1>(it, f);
+    case 2: return with_grad_pieces<T, 2>(it, f);
+    case 4: return with_grad_pieces<T, 4>(it, f);
+    default: return with_grad_pieces<T, 8>(it, f);
+  }
+}
 
 }  // namespace
 
@@ -284,9 +338,13 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+// As many workgroups as are resident: two a compute unit while a row's pieces and their
+// gradients fit 128 registers a lane (16 elements in bf16, 12 in fp32), above that one:
+// 32768 x 1024 in bf16 58 us with 512 and 65 with 256, 16384 x 2560 89 and 83.
 int norm_parts(int dtype, int64_t rows, int dim) {
-  const bool wave = dtype == 1 ? one_wave<bf16>(dim) : one_wave<float>(dim);
-  return (int)std::min<int64_t>(kNormParts, wave ? (rows + 3) / 4 : rows);
+  const int nw = grad_waves(dtype, dim);
+  const int64_t groups = 8 / nw, most = pieces_a_lane(dtype, nw, dim) <= (dtype == 1 ? 2 : 3) ? 512 : 256;
+  return (int)std::min<int64_t>(most, (rows + groups - 1) / groups);
 }
 
 hipError_t launch_norm_backward(const NormArgs& a, hipStream_t st) {
@@ -294,16 +352,16 @@ hipError_t launch_norm_backward(const NormArgs& a, hipStream_t st) {
   note_launch("norm_bwd", st);
   auto go = [&](auto type) {
     typedef decltype(type) T;
-    with_row<T>(a.dim, one_wave<T>(a.dim), [&](auto nw, auto it) {
-      norm_bwd_kernel<T, decltype(nw)::value, decltype(it)::value><<<parts, 256, 0, st>>>(a);
+    with_grad_row<T>(a.dtype, a.dim, [&](auto nw, auto it) {
+      norm_bwd_kernel<T, decltype(nw)::value, decltype(it)::value><<<parts, 512, 0, st>>>(a);
     });
   };
   if (a.dtype == 1) go(bf16());
   else go(float());
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || (a.dw == nullptr && a.db == nullptr)) return e;
+  if (e != hipSuccess || parts == 1 || (a.dw == nullptr && a.db == nullptr)) return e;
   note_launch("norm_sum", st);
-  norm_sum_kernel<<<(2 * a.dim + 31) / 32, 256, 0, st>>>(a.part, parts, a.dim, a.dw, a.db);
+  norm_sum_kernel<<<(2 * a.dim + 15) / 16, 512, 0, st>>>(a.part, parts, a.dim, a.dw, a.db);
   return hipGetLastError();
 }
 
