@@ -5,15 +5,21 @@
 //
 // Operands go HBM/L2 -> LDS with direct loads into a ring of five slots, each the A
 // or the B part of a stage of 64 K: stage q's A in slot 2q % 5, its B in slot
-// (2q + 1) % 5.  While stage q is multiplied, B of stage q+1 and A of stage q+2 are
-// issued, into the slots that stage q-1 left, so that A has a stage and a half to
-// arrive, B a stage, and each memory phase issues four loads a wave.  The ring goes
-// on over the ends of a workgroup's tiles: the next one's first stages are in flight
-// while a tile is finished.
+// (2q + 1) % 5.  The ring goes on over the ends of a workgroup's tiles: the next one's
+// first stages are in flight while a tile is finished.
 //
 // 8 waves: two groups with one wave of each on every SIMD, one phase apart, so
 // that one reads fragments and issues loads while the other multiplies; a barrier
-// ends each phase.  4 waves: the CU's other workgroup fills the gaps.
+// ends each phase.  While stage q is multiplied, B of stage q+1 and A of stage q+2 are
+// issued, into the slots that stage q-1 left, so that A has a stage and a half to
+// arrive, B a stage, and each memory phase issues four loads a wave.
+// 4 waves: one barrier a stage, in its middle; each half is multiplied while the next
+// half's fragments are read and one part's four loads (A of stage q+2, B of stage q+2)
+// are issued, spread over the products.  A CU's loads take as long as its products
+// here (32 KB and 512 cycles a stage), so that eight loads issued at once left the
+// matrix units idle: a tile alone took 0.49 us a stage and now takes 0.36, 2049 x 2560 x
+// 2560 40.5 us and now 35.5.  A ring twice as deep, one workgroup a CU, gained nothing
+// (0.49): the loads' rate counts, not their latency.
 //
 // LDS layouts, both free of bank conflicts:
 //   rows     128-byte rows of 64 K; 16-byte chunk c of LDS row r at slot
@@ -39,7 +45,7 @@
 namespace ipttt {
 namespace ring {
 
-constexpr int NSLOT = 5;
+constexpr int SLOTS = 5;
 typedef float4_t f4;
 
 template <typename T>
@@ -53,11 +59,10 @@ struct Geo {
   static constexpr int WM = 64, WN = BN / 2, MI = WM / 16, NJ = WN / 16;
   static_assert(BM == WAVES_M * WM, "wave grid");
   static constexpr int SLOT = BM * 128;                     // bytes
-  static constexpr int LDS_BYTES = NSLOT * SLOT;
+  static constexpr int LDS_BYTES = SLOTS * SLOT;
   static constexpr int NT = NW * 64;
   static constexpr int NL = 4;                              // load instructions a wave and part
   static_assert(SLOT == NW * NL * 1024, "load split");
-  static constexpr int MAX_GROUPS = NW == 8 ? 1 : 2;        // workgroups a CU
 };
 
 // Offsets past every buffer's end: such a load reads zeros.  (A tile's rows end
@@ -150,31 +155,25 @@ struct Loader {
       krows = __builtin_amdgcn_readfirstlane(krows);
     }
   }
-  // last (a constant): the stage may be the last one, cut short by K
-  __device__ __forceinline__ void issue(char* slot, int wave, bool last) const {
-    char* to = slot + wave * G::NL * 1024;
+  // Load j of the stage's four.  last (a constant): the stage may be the last one, cut
+  // short by K, so that its pieces past K read as zero.
+  __device__ __forceinline__ void issue_one(char* slot, int wave, bool last, int j) const {
+    core::lds_ptr_t to = (core::lds_ptr_t)(slot + (wave * G::NL + j) * 1024);
     if constexpr (!KMAJ) {
-      if (last && at + 128 > kbytes) {  // pieces past K read as zero
-#pragma unroll
-        for (int j = 0; j < G::NL; ++j)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (core::lds_ptr_t)(to + j * 1024), 16,
-                                                   at + ((chunk >> (4 * j)) & 7) * 16 < kbytes ? voff[j] : kOut, at, 0,
-                                                   0);
-        return;
-      }
-#pragma unroll
-      for (int j = 0; j < G::NL; ++j)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (core::lds_ptr_t)(to + j * 1024), 16, voff[j], at, 0, 0);
+      const bool cut = last && at + ((chunk >> (4 * j)) & 7) * 16 >= kbytes;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, to, 16, cut ? kOut : voff[j], at, 0, 0);
     } else {
-      // a resource over the stage's K rows, so that those past K read as zero
+      // a resource over the stage's K rows
       int end = 0x7FFFFFFF;
       if (last && krows < KS) end = krows > 0 ? (int)((uint32_t)(krows - 1) * ldb + width) : 0;
       const __amdgpu_buffer_rsrc_t r =
           __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), (short)0, end, 0x00020000);
-#pragma unroll
-      for (int j = 0; j < G::NL; ++j)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (core::lds_ptr_t)(to + j * 1024), 16, voff[j], 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 16, voff[j], 0, 0, 0);
     }
+  }
+  __device__ __forceinline__ void issue(char* slot, int wave, bool last) const {
+#pragma unroll
+    for (int j = 0; j < G::NL; ++j) issue_one(slot, wave, last, j);
   }
 };
 
@@ -266,7 +265,7 @@ struct Walk {
 // of B.  A and B are restrict so that the compiler tells the LDS reads apart from
 // the direct loads and puts no wait for those in front of them; the ring's own
 // waits order them.
-template <typename T, int NW, bool AK, bool BK, int LEGS, class Stages, class OpenA, class OpenB, class Epilogue>
+template <typename T, int NW, bool AK, bool BK, int LEGS, bool HOLD, class Stages, class OpenA, class OpenB, class Epilogue>
 __device__ __forceinline__ void run(char* lds, int n1, int n2, Stages&& stages, OpenA&& open_a, OpenB&& open_b,
                                     Epilogue&& epilogue) {
   typedef Geo<T, NW> G;
@@ -315,7 +314,7 @@ __device__ __forceinline__ void run(char* lds, int n1, int n2, Stages&& stages, 
   };
   enter_a();
   enter_b();
-  constexpr int RING = NSLOT * G::SLOT;
+  constexpr int RING = G::LDS_BYTES;
   auto past = [](int x) { return x >= RING ? x - RING : x; };
   int a = 0;  // where A of the stage to multiply lies; the slots after it: B, the next A, the next B, the A after
   auto advance_a = [&]() {
@@ -326,44 +325,136 @@ __device__ __forceinline__ void run(char* lds, int n1, int n2, Stages&& stages, 
     if (--nb > 0) lb.advance();
     else enter_b();
   };
-  la.issue(lds, wave, true);
-  advance_a();
-  lb.issue(lds + G::SLOT, wave, true);
-  advance_b();
-  bool more = on_a;  // whether the part issued last is an A that may still be on its way
-  if (on_a) {
-    la.issue(lds + 2 * G::SLOT, wave, true);
-    advance_a();
-  }
+  bool more;  // whether every part up to the one issued last was there to issue
   if constexpr (NW == 8) {
+    la.issue(lds, wave, true);
+    advance_a();
+    lb.issue(lds + G::SLOT, wave, true);
+    advance_b();
+    more = on_a;
+    if (on_a) {
+      la.issue(lds + 2 * G::SLOT, wave, true);
+      advance_a();
+    }
     if (more) core::wait_vmcnt<G::NL>();
     else core::wait_vmcnt<0>();
-    core::lds_barrier();
+  } else {
+#pragma unroll
+    for (int p = 0; p < SLOTS - 1; ++p) {
+      more = p % 2 == 0 ? on_a : on_b;
+      if (!more) break;
+      if (p % 2 == 0) {
+        la.issue(lds + p * G::SLOT, wave, true);
+        advance_a();
+      } else {
+        lb.issue(lds + p * G::SLOT, wave, true);
+        advance_b();
+      }
+    }
+    if (more) core::wait_vmcnt<2 * G::NL>();
+    else core::wait_vmcnt<0>();
   }
+  core::lds_barrier();
+  // 4 waves: the fragments of the two halves; half 0 of a stage is read ahead of it
+  typename Frag<T>::type fa[NW == 8 ? 1 : 2][G::MI], fb[NW == 8 ? 1 : 2][G::NJ];
+  auto read = [&](int stage_at, int h, int to) {
+    const char *pa = lds + past(a + stage_at * G::SLOT), *pb = lds + past(a + (stage_at + 1) * G::SLOT);
+#pragma unroll
+    for (int i = 0; i < G::MI; ++i) fa[to][i] = ra.get(pa, i, h);
+#pragma unroll
+    for (int j = 0; j < G::NJ; ++j) fb[to][j] = rb.get(pb, j, h);
+  };
+  if constexpr (NW == 4) read(0, 0, 0);
   for (; w.on(); w.next()) {
     f4 acc[G::MI][G::NJ];
 #pragma unroll
     for (int i = 0; i < G::MI; ++i)
 #pragma unroll
       for (int j = 0; j < G::NJ; ++j) acc[i][j] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-    typename Frag<T>::type fa[G::MI], fb[G::NJ];
-    auto read = [&](int h) {
-      const char *pa = lds + a, *pb = lds + past(a + G::SLOT);
-#pragma unroll
-      for (int i = 0; i < G::MI; ++i) fa[i] = ra.get(pa, i, h);
-#pragma unroll
-      for (int j = 0; j < G::NJ; ++j) fb[j] = rb.get(pb, j, h);
-    };
-    auto multiply = [&]() {
+    auto multiply = [&](int from) {
 #pragma unroll
       for (int i = 0; i < G::MI; ++i)
 #pragma unroll
-        for (int j = 0; j < G::NJ; ++j) acc[i][j] = Frag<T>::mma(fa[i], fb[j], acc[i][j]);
+        for (int j = 0; j < G::NJ; ++j) acc[i][j] = Frag<T>::mma(fa[from][i], fb[from][j], acc[i][j]);
     };
-    // One stage.  STEADY: the loaders stay in this item, short of its last stage, so
-    // that nothing is asked; otherwise they may be at its last stage, in the next
-    // item or done.
-    auto stage = [&](auto steady) {
+    // A part's loads into the slot `to` slots behind the stage's A.  STEADY: the loaders
+    // stay in this item, short of its last stage, so that nothing is asked; otherwise
+    // they may be at its last stage, in the next item or done.
+    auto next_b = [&](auto steady, int to) {
+      constexpr bool STEADY = decltype(steady)::value;
+      if constexpr (STEADY) {
+        lb.issue(lds + past(a + to * G::SLOT), wave, false);
+      } else {
+        more = on_b;
+        if (on_b) lb.issue(lds + past(a + to * G::SLOT), wave, true);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto next_a = [&](auto steady, int to) {
+      constexpr bool STEADY = decltype(steady)::value;
+      if constexpr (STEADY) {
+        la.issue(lds + past(a + to * G::SLOT), wave, false);
+      } else {
+        more = on_a;
+        if (on_a) la.issue(lds + past(a + to * G::SLOT), wave, true);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto step_b = [&](auto steady) {
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (decltype(steady)::value) lb.advance();
+      else if (on_b) advance_b();
+    };
+    auto step_a = [&](auto steady) {
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (decltype(steady)::value) la.advance();
+      else if (on_a) advance_a();
+    };
+    // 4 waves: half h of the stage is multiplied while the other half's (h = 1: the next
+    // stage's first) fragments are read and one part's loads are issued, spread over the
+    // products: the loads of a CU take as long as its products.
+    auto window = [&](auto steady, auto half, bool hold) {
+      constexpr bool STEADY = decltype(steady)::value;
+      constexpr int H = decltype(half)::value;
+      // A to where B of the stage before lay, B to where this stage's A lay
+      constexpr int TO = H == 0 ? SLOTS - 1 : 0;
+      constexpr bool IS_A = H == 0;
+      if (!STEADY && !hold) {
+        if constexpr (IS_A) {
+          next_a(steady, TO);
+          step_a(steady);
+        } else {
+          next_b(steady, TO);
+          step_b(steady);
+        }
+      }
+      char* to = lds + past(a + TO * G::SLOT);
+      const char *pa = lds + past(a + 2 * H * G::SLOT), *pb = lds + past(a + (2 * H + 1) * G::SLOT);
+#pragma unroll
+      for (int i = 0; i < G::MI; ++i) {
+        if (STEADY) {
+          if constexpr (IS_A) la.issue_one(to, wave, false, i);
+          else lb.issue_one(to, wave, false, i);
+        }
+        if (i == 0) {
+#pragma unroll
+          for (int q = 0; q < G::MI; ++q) fa[1 - H][q] = ra.get(pa, q, 1 - H);
+        }
+        if (i == 1) {
+#pragma unroll
+          for (int q = 0; q < G::NJ; ++q) fb[1 - H][q] = rb.get(pb, q, 1 - H);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < G::NJ; ++j) acc[i][j] = Frag<T>::mma(fa[H][i], fb[H][j], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (STEADY) {
+        if constexpr (IS_A) la.advance();
+        else lb.advance();
+      }
+    };
+    auto stage = [&](auto steady, bool hold) {
       constexpr bool STEADY = decltype(steady)::value;
       auto landed = [&]() {  // all but the A issued last
         if (STEADY || more) core::wait_vmcnt<G::NL>();
@@ -375,64 +466,34 @@ __device__ __forceinline__ void run(char* lds, int n1, int n2, Stages&& stages, 
         core::lds_barrier();
         __builtin_amdgcn_sched_barrier(0);
       };
-      auto next_b = [&]() {
-        char* to = lds + past(a + 3 * G::SLOT);
-        if constexpr (STEADY) lb.issue(to, wave, false);
-        else if (on_b) lb.issue(to, wave, true);
-        __builtin_amdgcn_sched_barrier(0);
-      };
-      auto next_a = [&]() {
-        char* to = lds + past(a + 4 * G::SLOT);
-        if constexpr (STEADY) {
-          la.issue(to, wave, false);
-        } else {
-          more = on_a;
-          if (on_a) la.issue(to, wave, true);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      };
-      auto step_b = [&]() {
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (STEADY) lb.advance();
-        else if (on_b) advance_b();
-      };
-      auto step_a = [&]() {
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (STEADY) la.advance();
-        else if (on_a) advance_a();
-      };
       if constexpr (NW == 8) {
         // A wave's loads of the next stage have landed before the barrier ahead of
         // group 0's first read of it (group 0: after its last products of this
         // stage; group 1: after its last reads of it).
-        next_b();
-        read(0);
-        step_b();
+        next_b(steady, 3);
+        read(0, 0, 0);
+        step_b(steady);
         phase_end(false);
-        multiply();
+        multiply(0);
         phase_end(false);
-        next_a();
-        read(1);
-        step_a();
+        next_a(steady, 4);
+        read(0, 1, 0);
+        step_a(steady);
         phase_end(grp == 1);
-        multiply();
+        multiply(0);
         phase_end(grp == 0);
       } else {
-        // this wave's loads of the stage have landed, and every wave is done with
-        // the stage before
+        window(steady, std::integral_constant<int, 0>(), false);
+        // this wave's loads of the next stage have landed, and every wave has read
+        // this one
         phase_end(true);
-        next_b();
-        next_a();
-        read(0);
-        step_b();
-        step_a();
-        multiply();
-        read(1);
-        multiply();
-        __builtin_amdgcn_sched_barrier(0);
+        window(steady, std::integral_constant<int, 1>(), hold);
       }
-      a = past(a + 2 * G::SLOT);
+      if (!hold) a = past(a + 2 * G::SLOT);
     };
+    // (a wait that the compiler sees: scalar loads left over from the epilogue would have
+    // it wait for every LDS read in the loop)
+    if constexpr (NW == 4) __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
     // Group 1 meets one barrier more before its phases, group 0 one after.
     if (NW == 8 && grp == 1) core::lds_barrier();
 #pragma unroll
@@ -444,16 +505,28 @@ __device__ __forceinline__ void run(char* lds, int n1, int n2, Stages&& stages, 
       if (steady > 0) {
         la.uniform();
         lb.uniform();
-        for (; s < steady; ++s) stage(std::true_type());
+        for (; s < steady; ++s) stage(std::true_type(), false);
         na -= steady;
         nb -= steady;
       }
-      for (; s < S; ++s) stage(std::false_type());
+      const int rest = HOLD && leg == LEGS - 1 ? S - 1 : S;
+      for (; s < rest; ++s) stage(std::false_type(), false);
     }
+    if constexpr (HOLD) stage(std::false_type(), true);
     if (NW == 8 && grp == 0) core::lds_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    // the stage multiplied last lies in the two slots before a
-    epilogue(w.t, acc, [&](int which) { return lds + past(a + (NSLOT - 2 + which) * G::SLOT); });
+    if constexpr (NW == 8) {
+      // the stage multiplied last lies in the two slots before a
+      epilogue(w.t, acc, [&](int which) { return lds + past(a + (SLOTS - 2 + which) * G::SLOT); });
+    } else {
+      epilogue(w.t, acc, [&](int which) { return lds + past(a + which * G::SLOT); });
+      if constexpr (HOLD) {
+        core::lds_barrier();  // every wave is done with the idle slots
+        next_b(std::false_type(), 0);
+        step_b(std::false_type());
+        a = past(a + 2 * G::SLOT);
+      }
+    }
   }
 }
 
