@@ -1031,7 +1031,11 @@ ipttt_status z_backward(const ipttt_problem* q, const void* H, const void* W_gat
   uint8_t* segs;
   int32_t* table;
   char* c;
-  if ((s = bwd_segments(q, p, ws, l, st, &segs, &table, &c)) != IPTTT_OK) return s;
+  if (k8 == nullptr) {
+    if ((s = bwd_segments(q, p, ws, l, st, &segs, &table, &c)) != IPTTT_OK) return s;
+  } else {
+    c = static_cast<char*>(ws) + l.call;  // its products ask no segments
+  }
   void *dG = c + l.dg, *dU = c + l.du;
   if (k8 != nullptr) {
     IPTTT_TRY(ipttt::launch_gated_grad8(p, *k8, dZ, dG, dU, st));

@@ -68,6 +68,14 @@ def test_gradients_from_kept_values(t, d, f):
         assert rel(got, w) <= 1.5 * 2.0 ** -9 + 2.0 ** -10
 
 
+# tiles of 8 waves in the forward; the large launches of the gradients: dH of 8 waves and
+# of 4, with the last tiles cut along K, and the same of the weights' gradients
+@pytest.mark.parametrize("t, d, f", [(20000, 64, 640), (5000, 320, 1096), (3480, 4776, 464), (7248, 1088, 336),
+                                     (872, 1000, 8304), (752, 5424, 672)])
+def test_large_launches(t, d, f):
+    test_gradients_from_kept_values(t, d, f)
+
+
 @pytest.mark.parametrize("d, f", [(64, 64), (64, 192), (72, 72)])
 def test_kept_values_themselves(d, f):
     """H = rows of the unit matrix reads W's columns: G[t, j] = W_gate[j, t], exact in

@@ -118,6 +118,95 @@ def test_linear_backward(dt, m, k, n):
             assert all(bool((t == 5.0).all()) for j, t in enumerate((g.dx, g.dW, g.db)) if j != i)
 
 
+# (M, N, K) of a product of the large launches: in bf16 tiles of 8 waves in more than one
+# round, those with the last ones cut along K, and the same of 4 waves; in fp32 tiles of
+# 8 waves cut along K, those of 4 with the last ones cut, and in two rounds
+LARGE = [(BF16, 5432, 4048, 72), (BF16, 3296, 5064, 600), (BF16, 7216, 1144, 872), (BF16, 5384, 3096, 136),
+         (F32, 8368, 400, 2648), (F32, 8320, 904, 168), (F32, 5600, 3288, 72)]
+
+
+@pytest.mark.parametrize("which", ["y", "dx", "dW"])
+@pytest.mark.parametrize("dt, M, N, K", LARGE)
+def test_large_launches(dt, M, N, K, which):
+    """Each product in these sizes, in 64 bits on the device; bounds as above."""
+    m, k, n = {"y": (M, K, N), "dx": (M, N, K), "dW": (K, N, M)}[which]
+    x, W, b, res, dy = inputs(dt, m, k, n, seed=7)
+    p = ip.LinearProblem(m, k, n, dt, ip.IPTTT_ACT_SILU if which == "y" else ip.IPTTT_ACT_NONE, grad_dtype=dt)
+    X, V, G = (t.double() for t in (x, W, dy))
+    half = HALF[dt]
+
+    def near(got, want, bound):
+        assert bool(((got.double() - want).abs() <= bound).all())
+
+    if which == "y":
+        y, pre = forward(p, x, W, b, res, True)
+        mid = X @ V.T + b.double()
+        off = K * 2 * E32 * (X.abs() @ V.abs().T) + 2 * E32 * mid.abs()
+        near(pre, mid, off + half * mid.abs())
+        want = mid * torch.sigmoid(mid) + res.double()
+        near(y, want, 1.13 * off + 32 * E32 * (mid.abs() + want.abs()) + half * want.abs())
+        return
+    g = ip.LinearGrads(p)
+    for t in (g.dx, g.dW):
+        t.fill_(5.0)
+    if which == "dx":
+        ip.ipttt_linear_backward(p, x, W, dy, g.dx, None, None, g.ws)
+        want = G @ V
+        near(g.dx, want, K * 2 * E32 * (G.abs() @ V.abs()) + half * want.abs())
+    else:
+        ip.ipttt_linear_backward(p, x, W, dy, None, g.dW, g.db, g.ws)
+        want = G.T @ X
+        near(g.dW, want, K * 2 * E32 * (G.abs().T @ X.abs()) + half * want.abs())
+        near(g.db, G.sum(0), (K + 8) * E32 * G.abs().sum(0))
+
+
+def test_two_calls_at_once_and_two_graphs():
+    """Calls side by side on two streams, each with its own workspace, and two captured
+    graphs that share one, replayed in turn."""
+    shapes = [(1500, 256, 320), (700, 512, 256)]
+    made = []
+    for i, (m, k, n) in enumerate(shapes):
+        p = ip.LinearProblem(m, k, n, BF16, ip.IPTTT_ACT_SILU)
+        x, W, b, res, dy = inputs(BF16, m, k, n, seed=20 + i)
+        made.append((p, x, W, b, res, dy, torch.empty_like(res), torch.empty_like(res), ip.LinearGrads(p)))
+
+    def call(c, ws, gws, stream=None):
+        p, x, W, b, res, dy, y, pre, g = c
+        ip.ipttt_linear(p, x, W, y, b=b, res=res, pre=pre, ws=ws, stream=stream)
+        ip.ipttt_linear_backward(p, x, W, dy, g.dx, g.dW, g.db, gws, pre=pre, stream=stream)
+
+    own = [(ip.linear_workspace(c[0]), c[8].ws) for c in made]
+    outs = [(c[6], c[7], c[8].dx, c[8].dW, c[8].db) for c in made]
+    want = []
+    for c, w, o in zip(made, own, outs):
+        call(c, *w)
+        want.append([t.clone() for t in o])
+        for t in o:
+            t.zero_()
+    streams = [torch.cuda.Stream() for _ in made]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        for c, w, s in zip(made, own, streams):
+            call(c, *w, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, t) for w, o in zip(want, outs) for a, t in zip(w, o))
+    shared = torch.empty(max(t.numel() for w in own for t in w if t is not None), dtype=torch.uint8, device="cuda")
+    graphs = []
+    for c in made:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call(c, shared, shared)
+    for _ in range(3):
+        for g, w, o in zip(graphs, want, outs):
+            for t in o:
+                t.zero_()
+            shared.fill_(0xFF)
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, t) for a, t in zip(w, o))
+
+
 @pytest.mark.parametrize("m, k, n", [(3, 128, 192), (40, 192, 64), (300, 256, 512), (70, 72, 104)])
 def test_columns_of_wider_tensors_and_in_place(m, k, n):
     for dt in (BF16, F32):

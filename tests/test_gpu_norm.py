@@ -92,6 +92,13 @@ def test_norm_and_gradients(dt, kind, rows, dim):
         check_backward(p, x, ww, dy, more, g.dx, dw, db)
 
 
+# more rows than the gradient's launch has places, for one to eight waves a row
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("rows, dim", [(9001, 64), (4500, 1000), (2100, 2560), (1301, 4096), (700, 9728)])
+def test_several_rounds_of_rows(dt, rows, dim):
+    test_norm_and_gradients(dt, ip.IPTTT_NORM_LAYER, rows, dim)
+
+
 @pytest.mark.parametrize("rows, dim", [(5, 64), (37, 2560), (3, 4096)])
 def test_slices_of_wider_tensors_and_in_place(rows, dim):
     for dt in (BF16, F32):
