@@ -4,10 +4,12 @@ read in pieces, single tokens and a training step.
     x -> norm -> q, k, v -> per-head norm and rotation -> attention -> + x
       -> norm -> In-Place TTT layer -> +
 
-The projections are plain library products; the per-head norm and rotation,
-the attention and the layer run in libipttt.so.  What a program keeps: the
-rotation table, one attention plan for the sequences of a step (every layer of
-a model shares it) and, for serving, a cache of keys and values.
+All of it runs in libipttt.so: the norms (whose gradient adds the residual stream's),
+the projections (the second adds the residual stream in its epilogue), the per-head
+norm and rotation, the attention and the layer, which in bf16 keeps its gate and up
+products for the backward in 8 bits.  What a program keeps: the rotation table, one
+attention plan for the sequences of a step (every layer of a model shares it) and, for
+serving, a cache of keys and values.
 
     python examples/attention_block.py            # runs all four, prints agreement and times
 """
@@ -23,8 +25,58 @@ import test_weight_mlp_amd as ip  # noqa: E402
 ETA, TAU, EPS = 1e-3, 1e-5, 1e-6
 
 
-def norm(x):
-    return x * torch.rsqrt(x.float().square().mean(-1, keepdim=True) + EPS).to(x.dtype)
+def code(t):
+    return ip.IPTTT_BF16 if t.dtype == torch.bfloat16 else ip.IPTTT_F32
+
+
+class Norm(torch.autograd.Function):
+    """The RMS norm of x's rows times w (or None), and x itself for the residual stream:
+    the backward adds that stream's gradient to the norm's in the same pass."""
+
+    @staticmethod
+    def forward(ctx, x, w):
+        ctx.p = ip.NormProblem(*x.shape, code(x), ip.IPTTT_NORM_RMS, EPS)
+        ctx.save_for_backward(x, w)
+        ctx.set_materialize_grads(False)
+        y = torch.empty_like(x)
+        ip.ipttt_norm(ctx.p, x, w, None, y)
+        return y, x.view_as(x)
+
+    @staticmethod
+    def backward(ctx, dy, dres):
+        x, w = ctx.saved_tensors
+        if dy is None:
+            return dres, None
+        g = ip.NormGrads(ctx.p, device=x.device)
+        dw = None if w is None else g.dw
+        ip.ipttt_norm_backward(ctx.p, x, w, dy.contiguous(), g.dx, dw, None, g.ws,
+                               dres=None if dres is None else dres.contiguous())
+        return g.dx, None if w is None else dw.to(w.dtype)
+
+
+def norm(x, w=None):
+    return Norm.apply(x, w)[0]
+
+
+class Linear(torch.autograd.Function):
+    """x W^T + res (or None)."""
+
+    @staticmethod
+    def forward(ctx, x, W, res):
+        ctx.p = ip.LinearProblem(len(x), W.shape[1], W.shape[0], code(x), grad_dtype=code(x))
+        ctx.save_for_backward(x, W)
+        y = torch.empty(len(x), W.shape[0], dtype=x.dtype, device=x.device)
+        ip.ipttt_linear(ctx.p, x, W, y, res=res, ws=ip.linear_workspace(ctx.p, x.device))
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, W = ctx.saved_tensors
+        g = ip.LinearGrads(ctx.p, device=x.device)
+        dx, dW = (t if need else None for t, need in zip((g.dx, g.dW), ctx.needs_input_grad))
+        if dx is not None or dW is not None:
+            ip.ipttt_linear_backward(ctx.p, x, W, dy.contiguous(), dx, dW, None, g.ws)
+        return dx, dW, dy if ctx.needs_input_grad[2] else None
 
 
 def starts(lens):
@@ -68,8 +120,8 @@ class TTTLayer(torch.autograd.Function):
     """The In-Place TTT layer over one step's tokens."""
 
     @staticmethod
-    def forward(ctx, H, X0, W_gate, W_up, W_down, conv_w, W_target, p):
-        buf = ip.allocate(p, H.device, save=True)
+    def forward(ctx, H, X0, W_gate, W_up, W_down, conv_w, W_target, p, keep8):
+        buf = ip.allocate(p, H.device, save=True, keep8=keep8)
         ip.forward(p, H, X0, W_gate, W_up, W_down, conv_w, W_target, ETA, TAU, buf)
         ctx.save_for_backward(H, X0, W_gate, W_up, W_down, conv_w, W_target)
         ctx.p, ctx.buf = p, buf
@@ -80,7 +132,7 @@ class TTTLayer(torch.autograd.Function):
         t = ctx.saved_tensors
         g = ip.backward(ctx.p, ctx.buf, *t, ETA, TAU, dO.contiguous())
         return (g.dH, g.dX0) + tuple(x.to(w.dtype) for x, w in zip(
-            (g.dW_gate, g.dW_up, g.dW_down, g.dconv_w, g.dW_target), t[2:])) + (None,)
+            (g.dW_gate, g.dW_up, g.dW_down, g.dconv_w, g.dW_target), t[2:])) + (None, None)
 
 
 class Block:
@@ -98,23 +150,30 @@ class Block:
         self.W_o = w(d, heads * head_dim, var=1 / (heads * head_dim))
         self.w_q, self.w_k = 1 + w(head_dim, var=0.01), 1 + w(head_dim, var=0.01)
         self.ttt = [w(f, d, var=1 / d), w(f, d, var=1 / d), w(d, f, var=1 / f), w(d, 5, var=0.05), w(d, d, var=1 / d)]
+        self.w_in, self.w_mid = 1 + w(d, var=0.01), 1 + w(d, var=0.01)
+        self.keep8 = dtype == torch.bfloat16
         self.table = ip.rotation_table(positions, head_dim, 1e6)
 
     def weights(self):
-        return [self.W_qkv, self.W_o, self.w_q, self.w_k] + self.ttt
+        return [self.W_qkv, self.W_o, self.w_q, self.w_k] + self.ttt + [self.w_in, self.w_mid]
 
     def qk_problem(self, tokens, out_rows=None):
         return ip.QKProblem(tokens, self.hq, self.hk, self.D, self.code, EPS, self.table.shape[0], out_rows)
 
-    def prompt(self, x, docs):
-        """Packed documents; differentiable."""
+    def half(self, x, docs):
+        """Packed documents through the attention half; differentiable."""
         plan = ip.AttentionPlan(self.hq, self.hk, self.D, docs, docs, self.code)
         pos = torch.cat([torch.arange(n, dtype=torch.int32, device="cuda") for n in docs])
-        a = AttentionHalf.apply(norm(x) @ self.W_qkv.T, self.w_q, self.w_k, pos, self.table, plan,
+        n, stream = Norm.apply(x, self.w_in)
+        a = AttentionHalf.apply(Linear.apply(n, self.W_qkv, None), self.w_q, self.w_k, pos, self.table, plan,
                                 self.qk_problem(len(x)))
-        y = x + a @ self.W_o.T
+        return Linear.apply(a, self.W_o, stream)
+
+    def prompt(self, x, docs):
+        """Packed documents; differentiable."""
+        n, stream = Norm.apply(self.half(x, docs), self.w_mid)
         p = ip.Problem(1, len(x), self.d, self.f, self.chunk, self.code, starts(docs)).prepare_segments()
-        return y + TTTLayer.apply(norm(y), x, *self.ttt, p)
+        return stream + TTTLayer.apply(n, x, *self.ttt, p, self.keep8)
 
     def cache(self, rows):
         return Cache(self, rows)
@@ -125,16 +184,16 @@ class Block:
         (fold=False) tokens of a chunk that is not complete yet."""
         n, end = len(x), cache.end
         rows = torch.arange(end, end + n, dtype=torch.int32, device="cuda")
-        qkv = (norm(x) @ self.W_qkv.T).view(n, self.hq + 2 * self.hk, self.D)
+        qkv = Linear.apply(norm(x, self.w_in), self.W_qkv, None).view(n, self.hq + 2 * self.hk, self.D)
         q, k, v = qkv[:, :self.hq], qkv[:, self.hq:self.hq + self.hk], qkv[:, self.hq + self.hk:]
         ip.ipttt_qk_norm_rope(self.qk_problem(n, len(cache.k)), q, k, self.w_q, self.w_k, rows, self.table, q, cache.k,
                               v=v, v_out=cache.v, rows=rows)
         plan = ip.AttentionPlan(self.hq, self.hk, self.D, [n], [end + n], self.code, k_rows=len(cache.k))
         b = ip.AttentionBuffers(plan)
         ip.ipttt_attention(plan, q, cache.k, cache.v, b.o, b.lse, b.ws)
-        y = x + b.o.view(n, -1) @ self.W_o.T
+        y = Linear.apply(b.o.view(n, -1), self.W_o, x)
         p = ip.Problem(1, n, self.d, self.f, self.chunk, self.code, continues=[end > 0])
-        buf = ip.forward(p, norm(y), x, *self.ttt, ETA, TAU, carry=True, S_in=cache.S if end else None,
+        buf = ip.forward(p, norm(y, self.w_mid), x, *self.ttt, ETA, TAU, carry=True, S_in=cache.S if end else None,
                          S_out=cache.S if fold else None)
         cache.end += n
         return y + buf.O
