@@ -46,7 +46,7 @@ METRIC = "TTT-MLP layer tokens/s at 4B shape, 32k ctx, C=512; % of bf16 MFMA pea
 # Sources of each profiled kernel: a committed traffic summary counts only
 # while these files are unchanged.
 KERNEL_SOURCES = {
-    "gated_z_fast_kernel": ["gated_z.hip", "common.h", "epilogue.h", "launch.h", "mfma_core.h", "pingpong.h"],
+    "gated_z_ring_kernel": ["gated_z.hip", "common.h", "epilogue.h", "launch.h", "mfma_core.h", "ring.h"],
     "scan_fast_kernel": ["delta.hip", "common.h", "epilogue.h", "launch.h", "mfma_core.h"],
     "apply_fast_kernel": ["apply.hip", "common.h", "epilogue.h", "launch.h", "mfma_core.h"],
 }
@@ -310,7 +310,7 @@ def main(argv=None) -> int:
               "target_gemm": 2.0 * M * d * d if target != ip.IPTTT_TARGET_NO_PROJ else None,
               "conv": 10.0 * M * d if target != ip.IPTTT_TARGET_NO_CONV else None}
     fast = cfg.dtype == "bf16" and cfg.d_model % 64 == 0 and cfg.d_ff % 64 == 0
-    kernel_symbol = {"gated_z": "gated_z_fast_kernel" if fast else "gated_z_kernel",
+    kernel_symbol = {"gated_z": "gated_z_ring_kernel" if cfg.dtype == "bf16" else "gated_z_kernel",
                      "scan": "scan_fast_kernel" if fast else "scan_kernel",
                      "apply": "apply_fast_kernel" if fast else "apply_kernel",
                      "target_gemm": "target_fast_kernel" if fast else "target_kernel",

@@ -179,7 +179,7 @@ struct Keep8Scale {
     inv = none || bad ? 0.0f : __builtin_amdgcn_rcpf(m * 0x1p-7f) * (0.9921875f * (1.0f + 0x1p-21f));
   }
   // the bytes of N bf16 values: adding 1.5 2^23 rounds to the integer and leaves it in
-  // the low bits
+  // the low bits (0 for a bad block: of the sum itself, or of a NaN that comes from bf16)
   template <int N>
   __device__ __forceinline__ uint32_t bytes(const bf16 (&v)[N]) const {
     uint32_t b[N];
@@ -188,7 +188,7 @@ struct Keep8Scale {
     uint32_t q = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u);
     if constexpr (N == 4) q |= __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
     static_assert(N == 2 || N == 4, "bytes of a word");
-    return bad ? 0u : q;
+    return q;
   }
 };
 

@@ -186,6 +186,10 @@ __device__ __forceinline__ void gated_z_tiles(const bf16* __restrict__ H, const 
 #pragma unroll
           for (int e = 0; e < 4; ++e) top[o][i][e] = max(top[o][i][e], share[at(wave ^ 1, o, i, e)]);
     }
+    // the scales: of the 16 lanes of a row each takes one of the 16 rows that they share
+    // (2049 x 1024 x 4096 50 us; stored row by row by the first lane 54)
+    uint32_t mine[2] = {};
+    static_assert(G::MI * 4 == 16, "a scale a lane");
 #pragma unroll
     for (int i = 0; i < G::MI; ++i)
 #pragma unroll
@@ -197,6 +201,7 @@ __device__ __forceinline__ void gated_z_tiles(const bf16* __restrict__ H, const 
           for (int o = 0; o < 2; ++o) {
             if constexpr (SHARE) most[o] = top[o][i][e];
             else most[o] = largest(o, i, e);
+            if ((lane & 15) == i * 4 + e) mine[o] = most[o];
           }
         }
         if (m >= M || n >= f) continue;
@@ -224,10 +229,19 @@ __device__ __forceinline__ void gated_z_tiles(const bf16* __restrict__ H, const 
             uint8_t* to = static_cast<uint8_t*>(o == 0 ? kept.G : kept.U) + at;
             if constexpr (NF == 4) __builtin_nontemporal_store(q, reinterpret_cast<uint32_t*>(to));
             else __builtin_nontemporal_store((uint16_t)q, reinterpret_cast<uint16_t*>(to));
-            if (n % kKeep8 == 0) (o == 0 ? kept.sG : kept.sU)[m * ((f + kKeep8 - 1) / kKeep8) + n / kKeep8] = sc.scale;
           }
         }
       }
+    if constexpr (KEEP == KEEP_8) {
+      // (NW = 4: both waves of a block hold it, the first writes it)
+      const int n64 = n0 + wn * WF;
+      const int64_t m = m0 + wm * G::WM + (lane & 15) / 4 * 16 + 4 * (lane >> 4) + (lane & 3);
+      if (m < M && n64 < f && n64 % kKeep8 == 0) {
+        const int64_t at = m * ((f + kKeep8 - 1) / kKeep8) + n64 / kKeep8;
+        kept.sG[at] = Keep8Scale(mine[0]).scale;
+        kept.sU[at] = Keep8Scale(mine[1]).scale;
+      }
+    }
   };
   ring::run<bf16, NW, false, false, 1, KEEP == KEEP_8 && NW == 4>(lds, tiles_m * tiles_n, 0, stages, open_a, open_b, epilogue);
 }

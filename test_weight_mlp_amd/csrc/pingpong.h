@@ -1,10 +1,9 @@
 // Persistent ping-pong product core for gfx950: per tile, two NT products
 // that share their A operand, acc[o] = A[256 rows, K] * B_o[128 rows, K]^T
 // (o = 0, 1), with direct-to-LDS operand loads, 32x32x16 bf16 MFMAs and an
-// epilogue supplied by the kernel that uses it.  The gated MLP's Z kernel
-// takes B_0 = W_gate and B_1 = W_up rows of one 128-feature tile; the LM
-// target's GEMM takes the two 128-row halves of one 256-column tile of
-// W_target^T.
+// epilogue supplied by the kernel that uses it.  The LM target's GEMM takes the
+// two 128-row halves of one 256-column tile of W_target^T as B_0 and B_1, the
+// clip's Grams those of a 256-row tile of the other side.
 //
 // 256 rows x (128 + 128) columns per tile, 8 waves (two per SIMD), a wave
 // holding 64 x 64 of both products.  Operands move HBM/L2 -> LDS with

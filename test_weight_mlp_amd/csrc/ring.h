@@ -31,10 +31,11 @@
 // lane ends up with neighbouring columns of C and stores 16 bytes at once.
 //
 // Measured (one MI355X, TFLOP/s; both K contiguous, B K-major, both K-major):
-// 8192^3 1434, 1340, 1325; 8192 x 6144 x 2560 1339, 1256, 1213.  With two whole stages
-// instead of the ring 1283, 1341, 1332 and 1294, 1251, 1265; with 32x32x16 products
-// 1372 and 1271 (first only); both parts' loads issued in one phase 1354; four waves
-// of 128 x 128 instead of eight 1040.
+// 8192^3 1519, 1501, 1474; 8192 x 6144 x 2560 1418, 1292, 1399.  The steady loop without
+// branches made these of 1434, 1340, 1325 and 1339, 1256, 1213; next to those stood, with
+// two whole stages instead of the ring, 1283, 1341, 1332 and 1294, 1251, 1265; with
+// 32x32x16 products 1372 and 1271 (first only); both parts' loads issued in one phase
+// 1354; four waves of 128 x 128 instead of eight 1040.
 #pragma once
 
 #include <type_traits>
