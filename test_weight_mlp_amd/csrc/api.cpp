@@ -251,7 +251,7 @@ struct BwdLayout {
   // target_backward
   size_t convt, y, dy, yt, dvt, cpart;
   // z_backward
-  size_t dg, du, wgt, wut, dgt, dut, ht, gpart;
+  size_t dg, du, wgt, wut, dgt, dut, ht, gpart, gpart2;
   int64_t Mp;
 };
 
@@ -311,8 +311,8 @@ BwdLayout bwd_layout(const Prob& p) {
   l.dgt = take(tnfast ? 0 : (size_t)l.Mp * p.f * e);
   l.dut = take(tnfast ? 0 : (size_t)l.Mp * p.f * e);
   l.ht = take(tnfast ? 0 : (size_t)l.Mp * p.d * e);
-  l.gpart = take(p.dtype != IPTTT_BF16 ? 0
-                                       : std::max(ipttt::gemm_workspace(keep8_dh(p)), ipttt::gemm_workspace(keep8_dw(p))));
+  l.gpart = take(p.dtype != IPTTT_BF16 ? 0 : ipttt::gemm_workspace(keep8_dh(p)));
+  l.gpart2 = take(p.dtype != IPTTT_BF16 ? 0 : ipttt::gemm_workspace(keep8_dw(p)));
   const size_t zb = o;
   l.total = l.call + std::max(sa, std::max(tg, zb));
   return l;
@@ -1039,7 +1039,7 @@ ipttt_status z_backward(const ipttt_problem* q, const void* H, const void* W_gat
   void *dG = c + l.dg, *dU = c + l.du;
   if (k8 != nullptr) {
     IPTTT_TRY(ipttt::launch_gated_grad8(p, *k8, dZ, dG, dU, st));
-    // both products of dH summed in one, both weight gradients in one launch
+    // both products of dH summed in one, both weight gradients as one
     ipttt::GemmArgs g = keep8_dh(p);
     g.a = Rows{dG, p.f};
     g.a2 = Rows{dU, p.f};
@@ -1047,15 +1047,14 @@ ipttt_status z_backward(const ipttt_problem* q, const void* H, const void* W_gat
     g.b2 = Rows{const_cast<void*>(W_up), p.d};
     g.c = Rows{dH, p.d};
     g.part = reinterpret_cast<float*>(c + l.gpart);
-    IPTTT_TRY(ipttt::launch_gemm(g, st));
     ipttt::GemmArgs w = keep8_dw(p);
     w.a = Rows{dG, p.f};
     w.a2 = Rows{dU, p.f};
     w.b = Rows{const_cast<void*>(H), p.d};
     w.c = Rows{dW_gate, p.d};
     w.c2 = Rows{dW_up, p.d};
-    w.part = reinterpret_cast<float*>(c + l.gpart);
-    IPTTT_TRY(ipttt::launch_gemm(w, st));
+    w.part = reinterpret_cast<float*>(c + l.gpart2);
+    IPTTT_TRY(ipttt::launch_gemm_pair(g, w, st));
     return IPTTT_OK;
   }
   if (GU != nullptr) {

@@ -49,6 +49,10 @@ struct GemmArgs {
 };
 size_t gemm_workspace(const GemmArgs& g);
 hipError_t launch_gemm(const GemmArgs& g, hipStream_t st);
+// Two products that do not depend on each other, g with B K-major and h with both
+// (dx and dW of a projection), each with its own part: the same bits as one by one, in
+// one launch where both are of small tiles.
+hipError_t launch_gemm_pair(const GemmArgs& g, const GemmArgs& h, hipStream_t st);
 
 // dp = dy act'(pre) and db (each optional), in one pass over dy.
 struct ActGradArgs {

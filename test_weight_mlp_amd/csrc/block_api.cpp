@@ -127,18 +127,18 @@ GemmArgs dw_args(const ipttt_linear_problem* p) {
 }
 
 // The backward's workspace: dp (where there is an activation) | partial column
-// sums | partial products, of one product at a time.
+// sums | partial products of dx | of dW.
 struct BackwardLayout {
-  size_t dp, db, part, total;
+  size_t dp, db, part_x, part_w, total;
 };
 BackwardLayout backward_layout(const ipttt_linear_problem* p) {
   const size_t e = p->dtype == IPTTT_BF16 ? 2 : 4;
   BackwardLayout l;
   l.dp = 0;
   l.db = l.dp + (p->act != IPTTT_ACT_NONE ? align256((size_t)p->rows * (size_t)p->out_dim * e) : 0);
-  l.part = l.db + align256((size_t)ipttt::act_grad_parts(p->rows, p->out_dim) * (size_t)p->out_dim * sizeof(float));
-  const size_t a = ipttt::gemm_workspace(dx_args(p)), b = ipttt::gemm_workspace(dw_args(p));
-  l.total = l.part + align256(a > b ? a : b);
+  l.part_x = l.db + align256((size_t)ipttt::act_grad_parts(p->rows, p->out_dim) * (size_t)p->out_dim * sizeof(float));
+  l.part_w = l.part_x + align256(ipttt::gemm_workspace(dx_args(p)));
+  l.total = l.part_w + align256(ipttt::gemm_workspace(dw_args(p)));
   return l;
 }
 
@@ -260,23 +260,18 @@ ipttt_status ipttt_linear_backward(const ipttt_linear_problem* p, const ipttt_ro
     a.part = reinterpret_cast<float*>(base + l.db);
     IPTTT_TRY(hip_status(ipttt::launch_act_grad(a, st)));
   }
-  float* part = reinterpret_cast<float*>(base + l.part);
-  if (dxv.p != nullptr) {
-    GemmArgs g = dx_args(p);
-    g.a = dp;
-    g.b = Rows{const_cast<void*>(W), p->in_dim};
-    g.c = dxv;
-    g.part = part;
-    IPTTT_TRY(hip_status(ipttt::launch_gemm(g, st)));
-  }
-  if (dW != nullptr) {
-    GemmArgs g = dw_args(p);
-    g.a = dp;
-    g.b = xv;
-    g.c = Rows{dW, p->in_dim};
-    g.part = part;
-    IPTTT_TRY(hip_status(ipttt::launch_gemm(g, st)));
-  }
+  GemmArgs gx = dx_args(p), gw = dw_args(p);
+  gx.a = dp;
+  gx.b = Rows{const_cast<void*>(W), p->in_dim};
+  gx.c = dxv;
+  gx.part = reinterpret_cast<float*>(base + l.part_x);
+  gw.a = dp;
+  gw.b = xv;
+  gw.c = Rows{dW, p->in_dim};
+  gw.part = reinterpret_cast<float*>(base + l.part_w);
+  if (dxv.p != nullptr && dW != nullptr) return hip_status(ipttt::launch_gemm_pair(gx, gw, st));
+  if (dxv.p != nullptr) return hip_status(ipttt::launch_gemm(gx, st));
+  if (dW != nullptr) return hip_status(ipttt::launch_gemm(gw, st));
   return IPTTT_OK;
 }
 

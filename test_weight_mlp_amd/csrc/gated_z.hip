@@ -243,7 +243,7 @@ __device__ __forceinline__ void gated_z_tiles(const bf16* __restrict__ H, const 
       }
     }
   };
-  ring::run<bf16, NW, false, false, 1, KEEP == KEEP_8 && NW == 4>(lds, tiles_m * tiles_n, 0, stages, open_a, open_b, epilogue);
+  ring::run<bf16, NW, false, false, 1, KEEP == KEEP_8 && NW == 4>(lds, tiles_m * tiles_n, 0, 0, stages, open_a, open_b, epilogue);
 }
 
 template <int NW, int KEEP>

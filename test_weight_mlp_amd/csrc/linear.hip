@@ -110,14 +110,15 @@ __device__ __forceinline__ void finish_row(const GemmArgs& g, int64_t m, int64_t
 // Waits for x's loads here: left to a use in a branch they would have the compiler wait
 // in the next tile's loop, for the tile's loads behind them too.
 template <typename V>
-__device__ __forceinline__ void settle(V& x) {
+__device__ __forceinline__ V settled(V x) {
   if constexpr (sizeof(V) == 4) {
     asm volatile("" : "+v"(x));
+    return x;
   } else {
     typedef uint32_t words __attribute__((ext_vector_type(sizeof(V) / 4)));
     words w = __builtin_bit_cast(words, x);
     asm volatile("" : "+v"(w));
-    x = __builtin_bit_cast(V, w);
+    return __builtin_bit_cast(V, w);
   }
 }
 
@@ -152,7 +153,7 @@ __device__ __forceinline__ void finish_block(const GemmArgs& g, const Rows& c, i
 #pragma unroll
     for (int j = 0; j < G::NJ; ++j) bias[j] = g.bias != nullptr ? (float)static_cast<const T*>(g.bias)[n + j] : 0.0f;
 #pragma unroll
-    for (int j = 0; j < G::NJ; ++j) settle(bias[j]);
+    for (int j = 0; j < G::NJ; ++j) bias[j] = settled(bias[j]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (m + e >= g.M) break;
@@ -200,7 +201,8 @@ __device__ __forceinline__ bool ring_item(const GemmArgs& g, const RingPlan& p, 
 
 template <typename T, int NW, bool AK, bool BK, int LEGS>
 __device__ __forceinline__ void ring_product(const T* __restrict__ A, const T* __restrict__ B, const T* __restrict__ A2,
-                                             const T* __restrict__ B2, const GemmArgs& g, const RingPlan& p, char* lds) {
+                                             const T* __restrict__ B2, const GemmArgs& g, const RingPlan& p, int turn,
+                                             char* lds) {
   typedef ring::Geo<T, NW> G;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   // an item's stages, counted through the legs, cut at the leg's ends
@@ -249,20 +251,34 @@ __device__ __forceinline__ void ring_product(const T* __restrict__ A, const T* _
 #pragma unroll
         for (int q = 0; q < 2; ++q) load_res<T, NW>(g, m0, n0, i + q, res[q]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) settle(res[e / 4][e % 4]);
+        for (int e = 0; e < 8; ++e) res[e / 4][e % 4] = settled(res[e / 4][e % 4]);
       }
 #pragma unroll
       for (int q = 0; q < 2; ++q) finish_block<T, NW, BK>(g, c, m0, n0, i + q, res[q], acc[i + q]);
     }
   };
-  ring::run<T, NW, AK, BK, LEGS, false>(lds, p.whole, p.split * p.parts, stages, open_a, open_b, epilogue);
+  ring::run<T, NW, AK, BK, LEGS, false>(lds, p.whole, p.split * p.parts, turn, stages, open_a, open_b, epilogue);
 }
 
 template <typename T, int NW, bool AK, bool BK, int LEGS>
 __global__ __launch_bounds__(NW * 64, NW == 8 ? 1 : 2) void ring_kernel(GemmArgs g, RingPlan p) {
   __shared__ __attribute__((aligned(1024))) char lds[ring::Geo<T, NW>::LDS_BYTES];
   ring_product<T, NW, AK, BK, LEGS>(static_cast<const T*>(g.a.p), static_cast<const T*>(g.b.p),
-                                    static_cast<const T*>(g.a2.p), static_cast<const T*>(g.b2.p), g, p, lds);
+                                    static_cast<const T*>(g.a2.p), static_cast<const T*>(g.b2.p), g, p, 0, lds);
+}
+
+// Both gradients of a projection in one launch, tiles of 4 waves: a workgroup walks its
+// items of the first product, then of the second, the workgroups that the first one's
+// last round leaves without an item first.  (A wave may begin the second while others
+// finish the first: the slots that it loads are read only for products that are not
+// formed.)
+template <typename T, int LEGS>
+__global__ __launch_bounds__(256, 2) void ring_pair_kernel(GemmArgs g, RingPlan p, GemmArgs h, RingPlan q, int turn) {
+  __shared__ __attribute__((aligned(1024))) char lds[ring::Geo<T, 4>::LDS_BYTES];
+  ring_product<T, 4, false, true, LEGS>(static_cast<const T*>(g.a.p), static_cast<const T*>(g.b.p),
+                                        static_cast<const T*>(g.a2.p), static_cast<const T*>(g.b2.p), g, p, 0, lds);
+  ring_product<T, 4, true, true, 1>(static_cast<const T*>(h.a.p), static_cast<const T*>(h.b.p),
+                                    static_cast<const T*>(h.a2.p), static_cast<const T*>(h.b2.p), h, q, turn, lds);
 }
 
 // Sums the parts of a split tile in order and finishes it; blockIdx.y takes a block
@@ -327,24 +343,43 @@ RingPlan plan_ring(const GemmArgs& g) {
   return best;
 }
 
+int64_t ring_items(const RingPlan& p) { return (int64_t)p.whole + (int64_t)p.split * p.parts; }
+
+template <typename T, int NW>
+hipError_t launch_join(const GemmArgs& g, const RingPlan& p, hipStream_t st) {
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.split == 0) return e;
+  note_launch("linear_join", st);
+  typedef ring::Geo<T, NW> G;
+  const dim3 j((unsigned)p.split, G::MI);
+  if (!g.b_kmaj) ring_join_kernel<T, NW, false><<<j, G::NT, 0, st>>>(g, p);
+  else ring_join_kernel<T, NW, true><<<j, G::NT, 0, st>>>(g, p);
+  return hipGetLastError();
+}
+
 template <typename T, int NW>
 hipError_t launch_ring(const GemmArgs& g, const RingPlan& p, hipStream_t st) {
   typedef ring::Geo<T, NW> G;
-  const int64_t items = (int64_t)p.whole + (int64_t)p.split * p.parts;
-  const unsigned grid = (unsigned)std::min<int64_t>(kCus * (NW == 8 ? 1 : 2), (items + 7) / 8 * 8);
+  const unsigned grid = (unsigned)std::min<int64_t>(kCus * (NW == 8 ? 1 : 2), (ring_items(p) + 7) / 8 * 8);
   note_launch("linear", st);
   if (!g.a_kmaj && !g.b_kmaj) ring_kernel<T, NW, false, false, 1><<<grid, G::NT, 0, st>>>(g, p);
   else if (p.legs == 2) {
     if constexpr (sizeof(T) == 2) ring_kernel<T, NW, false, true, 2><<<grid, G::NT, 0, st>>>(g, p);
   } else if (!g.a_kmaj) ring_kernel<T, NW, false, true, 1><<<grid, G::NT, 0, st>>>(g, p);
   else ring_kernel<T, NW, true, true, 1><<<grid, G::NT, 0, st>>>(g, p);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.split == 0) return e;
-  note_launch("linear_join", st);
-  const dim3 j((unsigned)p.split, G::MI);
-  if (!g.b_kmaj) ring_join_kernel<T, NW, false><<<j, G::NT, 0, st>>>(g, p);
-  else ring_join_kernel<T, NW, true><<<j, G::NT, 0, st>>>(g, p);
-  return hipGetLastError();
+  return launch_join<T, NW>(g, p, st);
+}
+
+template <typename T, int LEGS>
+hipError_t launch_ring_pair(const GemmArgs& g, const RingPlan& p, const GemmArgs& h, const RingPlan& q,
+                            hipStream_t st) {
+  const unsigned grid = (unsigned)std::min<int64_t>(kCus * 2, (ring_items(p) + ring_items(q) + 7) / 8 * 8);
+  // the items an XCD's workgroups walk last in the first product
+  const int last = p.split > 0 ? p.split * p.parts : p.whole;
+  note_launch("linear_pair", st);
+  ring_pair_kernel<T, LEGS><<<grid, 256, 0, st>>>(g, p, h, q, (last + 7) / 8 % (int)(grid / 8));
+  const hipError_t e = launch_join<T, 4>(g, p, st);
+  return e != hipSuccess ? e : launch_join<T, 4>(h, q, st);
 }
 
 size_t ring_bytes(const RingPlan& p) {
@@ -528,6 +563,20 @@ hipError_t launch_gemm(const GemmArgs& g, hipStream_t st) {
   const RingPlan p = plan_ring(g);
   if (g.dtype == 1) return p.nw == 8 ? launch_ring<bf16, 8>(g, p, st) : launch_ring<bf16, 4>(g, p, st);
   return p.nw == 8 ? launch_ring<float, 8>(g, p, st) : launch_ring<float, 4>(g, p, st);
+}
+
+hipError_t launch_gemm_pair(const GemmArgs& g, const GemmArgs& h, hipStream_t st) {
+  const RingPlan p = plan_ring(g), q = plan_ring(h);
+  // Tiles of 4 waves together: 1999 x 1024 x 4096 in bf16 44.7 us, one after the other
+  // 55.5; 4096 x 1024 x 1024 30.0 and 41.7; 6000 x 1024 x 2048 in fp32, which fills the
+  // device twice each, 478 and 470.  Tiles of 8 waves, one workgroup a CU, fill the
+  // device by themselves.
+  if (p.nw != 4 || q.nw != 4 || g.a_kmaj || !g.b_kmaj || !h.a_kmaj || !h.b_kmaj || g.dtype != h.dtype) {
+    const hipError_t e = launch_gemm(g, st);
+    return e != hipSuccess ? e : launch_gemm(h, st);
+  }
+  if (g.dtype != 1) return g.two_pairs || h.two_products ? hipErrorInvalidValue : launch_ring_pair<float, 1>(g, p, h, q, st);
+  return g.two_pairs ? launch_ring_pair<bf16, 2>(g, p, h, q, st) : launch_ring_pair<bf16, 1>(g, p, h, q, st);
 }
 
 int act_grad_parts(int64_t rows, int64_t dim) {

@@ -233,10 +233,10 @@ __device__ __forceinline__ int perm_row(int r) {
 // contiguous range of either kind together.  Launches have a multiple of 8
 // workgroups.
 struct Walk {
-  int n1, n2, t, end, per;
+  int n1, n2, t, end, per, slot;
   bool second;
   __device__ __forceinline__ void range(int first, int n) {
-    const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3, r = (n + 7) >> 3;
+    const int xcd = blockIdx.x & 7, r = (n + 7) >> 3;
     end = first + min(n, (xcd + 1) * r);
     t = first + xcd * r + slot;
   }
@@ -245,7 +245,10 @@ struct Walk {
     second = true;
     range(n1, n2);
   }
-  __device__ __forceinline__ Walk(int a, int b) : n1(a), n2(b), per((int)gridDim.x >> 3), second(false) {
+  // turn: the workgroup of an XCD that begins
+  __device__ __forceinline__ Walk(int a, int b, int turn)
+      : n1(a), n2(b), per((int)gridDim.x >> 3), slot(((int)blockIdx.x >> 3) - turn), second(false) {
+    if (slot < 0) slot += per;
     range(0, n1);
     settle();
   }
@@ -256,7 +259,8 @@ struct Walk {
   }
 };
 
-// Walks the items.  An item is summed over LEGS legs, pairs of operands:
+// Walks the items, from the XCD's workgroup `turn` on (a launch may walk the items of
+// two products one after the other).  An item is summed over LEGS legs, pairs of operands:
 // stages(t, leg, first, n) gives the first stage of one and their number (of some leg
 // at least one), open_a(t, leg, first, loader) and open_b set its operands.
 // epilogue(t, acc, idle) takes the finished tile, with idle two slots that nothing
@@ -267,12 +271,12 @@ struct Walk {
 // the direct loads and puts no wait for those in front of them; the ring's own
 // waits order them.
 template <typename T, int NW, bool AK, bool BK, int LEGS, bool HOLD, class Stages, class OpenA, class OpenB, class Epilogue>
-__device__ __forceinline__ void run(char* lds, int n1, int n2, Stages&& stages, OpenA&& open_a, OpenB&& open_b,
+__device__ __forceinline__ void run(char* lds, int n1, int n2, int turn, Stages&& stages, OpenA&& open_a, OpenB&& open_b,
                                     Epilogue&& epilogue) {
   typedef Geo<T, NW> G;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1, grp = NW == 8 ? wave >> 2 : 0;
-  Walk w(n1, n2), wa = w, wb = w;
+  Walk w(n1, n2, turn), wa = w, wb = w;
   if (!w.on()) return;
   Loader<T, NW, AK> la;
   Loader<T, NW, BK> lb;
