@@ -392,6 +392,10 @@ size_t ring_bytes(const RingPlan& p) {
 // fragments of 16x16 products (rows: 16 FB outputs, columns: rows of x), with all
 // their loads in flight; 16 waves take every 16th slice of K and are summed through
 // LDS.  A lane ends up with four neighbouring outputs of one row.
+// Bound by the launch and the weights' way from HBM: one row 2560 -> 6144 in bf16 8.9 us
+// for 31 MB (3.5 TB/s), 32 rows 4096 -> 2560 12.9 us, where each of 160 workgroups reads
+// the 262 KB of x beside 131 KB of weights.  Two neighbouring slices a wave, so that it
+// reads whole lines, changed nothing (9.1 and 13.0).
 template <typename T, int MT, int FB>
 __global__ __launch_bounds__(1024) void few_kernel(GemmArgs g) {
   constexpr int W = 16;
@@ -453,10 +457,14 @@ __global__ __launch_bounds__(1024) void few_kernel(GemmArgs g) {
   }
 }
 
-// From 33 rows on the tiles take less: bf16, 2560 -> 6144 outputs, 16.6 us at 33 to 64 rows
-// (here with four blocks of rows 14.5 to 17.0), 9728 -> 2560 21.5 (42 to 53); fp32, 4096 ->
-// 2560, 36 (56 to 64).
-bool few_rows(const GemmArgs& g) { return g.M <= 32 && !g.a_kmaj && !g.b_kmaj; }
+// From 33 rows on the tiles take less: bf16, 2560 -> 6144 outputs, 16.1 us at 33 to 64 rows
+// (here with four blocks of rows 14.5 to 17.0), 9728 -> 2560 21.0 (42 to 53); fp32, 4096 ->
+// 2560, 35 (56 to 64).  From 17 rows on they do for large weights, which every workgroup's
+// reads of all of x hold up here: at 32 rows in bf16 2560 -> 9728 19.0 us (here 22.1),
+// 9728 -> 2560 21.0 (27.5), but 2560 -> 6144 16.1 (11.7); fp32 62 (61), 63 (74), 42 (31).
+bool few_rows(const GemmArgs& g) {
+  return (g.M <= 16 || (g.M <= 32 && g.N * g.K <= 20000000)) && !g.a_kmaj && !g.b_kmaj;
+}
 
 // Two blocks of outputs a workgroup halve the rows' reads; they pay where there are
 // workgroups enough.
