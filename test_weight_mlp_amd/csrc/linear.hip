@@ -66,7 +66,7 @@ __device__ __forceinline__ float slope_f32(int act, float v) {
 // How a product is cut: `whole` tiles over all of K, then the rest in `parts` of
 // `per` stages each, whose fp32 partial tiles a second launch joins.
 struct RingPlan {
-  int nw;                 // 8: tiles of 256 x 256, 4: of 128 x 128
+  int nw;                 // tiles of 32 nw x 32 nw
   int tiles_m, tiles_n;   // tiles_m: of both products, where there are two
   int whole, split, parts, per;
   int stages, legs;       // stages of a leg
@@ -261,7 +261,7 @@ __device__ __forceinline__ void ring_product(const T* __restrict__ A, const T* _
 }
 
 template <typename T, int NW, bool AK, bool BK, int LEGS>
-__global__ __launch_bounds__(NW * 64, NW == 8 ? 1 : 2) void ring_kernel(GemmArgs g, RingPlan p) {
+__global__ __launch_bounds__((ring::Geo<T, NW>::NT), (ring::Geo<T, NW>::GROUPS)) void ring_kernel(GemmArgs g, RingPlan p) {
   __shared__ __attribute__((aligned(1024))) char lds[ring::Geo<T, NW>::LDS_BYTES];
   ring_product<T, NW, AK, BK, LEGS>(static_cast<const T*>(g.a.p), static_cast<const T*>(g.b.p),
                                     static_cast<const T*>(g.a2.p), static_cast<const T*>(g.b2.p), g, p, 0, lds);
@@ -272,19 +272,19 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 1 : 2) void ring_kernel(GemmArgs
 // last round leaves without an item first.  (A wave may begin the second while others
 // finish the first: the slots that it loads are read only for products that are not
 // formed.)
-template <typename T, int LEGS>
-__global__ __launch_bounds__(256, 2) void ring_pair_kernel(GemmArgs g, RingPlan p, GemmArgs h, RingPlan q, int turn) {
-  __shared__ __attribute__((aligned(1024))) char lds[ring::Geo<T, 4>::LDS_BYTES];
-  ring_product<T, 4, false, true, LEGS>(static_cast<const T*>(g.a.p), static_cast<const T*>(g.b.p),
+template <typename T, int NW, int LEGS>
+__global__ __launch_bounds__(256, (ring::Geo<T, NW>::GROUPS)) void ring_pair_kernel(GemmArgs g, RingPlan p, GemmArgs h, RingPlan q, int turn) {
+  __shared__ __attribute__((aligned(1024))) char lds[ring::Geo<T, NW>::LDS_BYTES];
+  ring_product<T, NW, false, true, LEGS>(static_cast<const T*>(g.a.p), static_cast<const T*>(g.b.p),
                                         static_cast<const T*>(g.a2.p), static_cast<const T*>(g.b2.p), g, p, 0, lds);
-  ring_product<T, 4, true, true, 1>(static_cast<const T*>(h.a.p), static_cast<const T*>(h.b.p),
+  ring_product<T, NW, true, true, 1>(static_cast<const T*>(h.a.p), static_cast<const T*>(h.b.p),
                                     static_cast<const T*>(h.a2.p), static_cast<const T*>(h.b2.p), h, q, turn, lds);
 }
 
 // Sums the parts of a split tile in order and finishes it; blockIdx.y takes a block
 // row of it.
 template <typename T, int NW, bool BK>
-__global__ __launch_bounds__(NW * 64) void ring_join_kernel(GemmArgs g, RingPlan p) {
+__global__ __launch_bounds__((ring::Geo<T, NW>::NT)) void ring_join_kernel(GemmArgs g, RingPlan p) {
   typedef ring::Geo<T, NW> G;
   const int i = blockIdx.y, t = p.whole + blockIdx.x * p.parts;
   int64_t m0, n0;
@@ -311,29 +311,37 @@ constexpr int kCus = 256;
 RingPlan plan_ring(const GemmArgs& g) {
   RingPlan best{};
   double least = 1e300;
-  for (const int nw : {8, 4}) {
-    const int64_t w = nw * 32, tm = (g.M + w - 1) / w * (g.two_products ? 2 : 1), tn = (g.N + w - 1) / w, tiles = tm * tn;
-    const int64_t groups = nw == 8 ? kCus : 2 * kCus;
-    const int ks = g.dtype == 1 ? ring::kStage<bf16> : ring::kStage<float>, legs = g.two_pairs ? 2 : 1,
+  const bool h = g.dtype == 1;
+  // us of a stage, of a workgroup alone on its CU and on a full one, of an item beside its
+  // stages and of joining, fitted to some 1000 products of both types in all cuts (64 to
+  // 16384 rows): the cut so chosen takes 1 % longer than the best one on average
+  // (fp32: tiles of 128 x 128 instead took 19 % longer on average and up to 4 % less, at
+  // 8192 x 2560 x 2560, of 256 x 256 up to four times as long)
+  const struct Cost {
+    int nw;
+    double lone, full, item;
+  } costs[2][2] = {{{2, 0.55, 1.9, 2.0}}, {{8, 1.0, 1.4, 3.0}, {4, 0.5, 0.85, 2.0}}};
+  for (const Cost& c : costs[h]) {
+    if (c.nw == 0) continue;
+    const int64_t w = c.nw * 32, tm = (g.M + w - 1) / w * (g.two_products ? 2 : 1), tn = (g.N + w - 1) / w, tiles = tm * tn;
+    const int64_t most = 8 / c.nw, groups = most * kCus;
+    const int ks = h ? ring::kStage<bf16> : ring::kStage<float>, legs = g.two_pairs ? 2 : 1,
               leg = (int)((g.K + ks - 1) / ks), stages = legs * leg;
-    // us of a stage, on a full and a half empty device, of an item beside its stages and
-    // of joining, fitted to some 700 products of both types in all cuts (64 to 16384
-    // rows): the cut so chosen takes 1.2 % longer than the best one on average
-    const bool h = g.dtype == 1;
-    const double stage = nw == 8 ? (h ? 1.4 : 7.5) : (h ? 0.85 : 3.6), lone = nw == 8 ? (h ? 1.0 : 7.5) : (h ? 0.5 : 1.9);
-    const double item = nw == 8 ? (h ? 3.0 : 4.0) : 2.0, bytes = h ? 6.0e6 : 8.0e6;
     auto consider = [&](int64_t whole, int parts) {
       const int per = (stages + parts - 1) / parts;
       parts = (stages + per - 1) / per;
       const int64_t split = tiles - whole, items = split * parts;
-      const int64_t full = whole / groups;
-      double t = full * (stages * stage + item);
+      const int64_t rounds = whole / groups;
+      double t = rounds * (stages * c.full + c.item);
       const int64_t rest = whole % groups + items;
-      t += (double)((rest + groups - 1) / groups) * (per * (rest <= groups / 2 ? lone : stage) + item);
-      if (parts > 1) t += 4.0 + (double)items * w * w * 8 / bytes;
+      // 8 waves: a half empty device
+      const double share = most == 1 ? (rest > groups / 2 ? 1.0 : 0.0)
+                                     : (double)(std::min((rest + kCus - 1) / kCus, most) - 1) / (double)(most - 1);
+      t += (double)((rest + groups - 1) / groups) * (per * (c.lone + (c.full - c.lone) * share) + c.item);
+      if (parts > 1) t += 4.0 + (double)items * w * w * 8 / (h ? 6.0e6 : 8.0e6);
       if (t >= least) return;
       least = t;
-      best = RingPlan{nw, (int)tm, (int)tn, (int)(parts > 1 ? whole : tiles), (int)(parts > 1 ? split : 0), parts, per, leg, legs};
+      best = RingPlan{c.nw, (int)tm, (int)tn, (int)(parts > 1 ? whole : tiles), (int)(parts > 1 ? split : 0), parts, per, leg, legs};
     };
     consider(tiles, 1);
     const int64_t whole = tiles / groups * groups, rem = tiles - whole;
@@ -360,7 +368,7 @@ hipError_t launch_join(const GemmArgs& g, const RingPlan& p, hipStream_t st) {
 template <typename T, int NW>
 hipError_t launch_ring(const GemmArgs& g, const RingPlan& p, hipStream_t st) {
   typedef ring::Geo<T, NW> G;
-  const unsigned grid = (unsigned)std::min<int64_t>(kCus * (NW == 8 ? 1 : 2), (ring_items(p) + 7) / 8 * 8);
+  const unsigned grid = (unsigned)std::min<int64_t>(kCus * G::GROUPS, (ring_items(p) + 7) / 8 * 8);
   note_launch("linear", st);
   if (!g.a_kmaj && !g.b_kmaj) ring_kernel<T, NW, false, false, 1><<<grid, G::NT, 0, st>>>(g, p);
   else if (p.legs == 2) {
@@ -370,16 +378,16 @@ hipError_t launch_ring(const GemmArgs& g, const RingPlan& p, hipStream_t st) {
   return launch_join<T, NW>(g, p, st);
 }
 
-template <typename T, int LEGS>
+template <typename T, int NW, int LEGS>
 hipError_t launch_ring_pair(const GemmArgs& g, const RingPlan& p, const GemmArgs& h, const RingPlan& q,
                             hipStream_t st) {
-  const unsigned grid = (unsigned)std::min<int64_t>(kCus * 2, (ring_items(p) + ring_items(q) + 7) / 8 * 8);
+  const unsigned grid = (unsigned)std::min<int64_t>(kCus * ring::Geo<T, NW>::GROUPS, (ring_items(p) + ring_items(q) + 7) / 8 * 8);
   // the items an XCD's workgroups walk last in the first product
   const int last = p.split > 0 ? p.split * p.parts : p.whole;
   note_launch("linear_pair", st);
-  ring_pair_kernel<T, LEGS><<<grid, 256, 0, st>>>(g, p, h, q, (last + 7) / 8 % (int)(grid / 8));
-  const hipError_t e = launch_join<T, 4>(g, p, st);
-  return e != hipSuccess ? e : launch_join<T, 4>(h, q, st);
+  ring_pair_kernel<T, NW, LEGS><<<grid, 256, 0, st>>>(g, p, h, q, (last + 7) / 8 % (int)(grid / 8));
+  const hipError_t e = launch_join<T, NW>(g, p, st);
+  return e != hipSuccess ? e : launch_join<T, NW>(h, q, st);
 }
 
 size_t ring_bytes(const RingPlan& p) {
@@ -457,13 +465,17 @@ __global__ __launch_bounds__(1024) void few_kernel(GemmArgs g) {
   }
 }
 
-// From 33 rows on the tiles take less: bf16, 2560 -> 6144 outputs, 16.1 us at 33 to 64 rows
-// (here with four blocks of rows 14.5 to 17.0), 9728 -> 2560 21.0 (42 to 53); fp32, 4096 ->
-// 2560, 35 (56 to 64).  From 17 rows on they do for large weights, which every workgroup's
-// reads of all of x hold up here: at 32 rows in bf16 2560 -> 9728 19.0 us (here 22.1),
-// 9728 -> 2560 21.0 (27.5), but 2560 -> 6144 16.1 (11.7); fp32 62 (61), 63 (74), 42 (31).
+// Where the tiles take less: from 33 rows on (bf16, 2560 -> 6144 outputs, 16.1 us at 33 to
+// 64 rows, here with four blocks of rows 14.5 to 17.0; 9728 -> 2560 21.0 and 42 to 53), and
+// from 17 or 9 on for large weights, which every workgroup's reads of all of x hold up
+// here.  Us here and on the tiles: bf16, 32 rows, 2560 -> 6144 11.7 and 16.1, 2560 -> 9728
+// 22.1 and 18.9; fp32, 32 rows, 1024 -> 2048 10.9 and 12.7, 4096 -> 2560 28.7 and 22.8; 16
+// rows, 4096 -> 2560 18.2 and 22.8, 2560 -> 9728 46.0 and 34.3; 8 rows 34.8 and 34.3.
 bool few_rows(const GemmArgs& g) {
-  return (g.M <= 16 || (g.M <= 32 && g.N * g.K <= 20000000)) && !g.a_kmaj && !g.b_kmaj;
+  if (g.a_kmaj || g.b_kmaj) return false;
+  const bool h = g.dtype == 1;
+  const int64_t weights = g.N * g.K;
+  return g.M <= (h ? 16 : 8) || (g.M <= (h ? 32 : 16) && weights <= 20000000) || (g.M <= 32 && weights <= 4000000);
 }
 
 // Two blocks of outputs a workgroup halve the rows' reads; they pay where there are
@@ -570,7 +582,7 @@ hipError_t launch_gemm(const GemmArgs& g, hipStream_t st) {
   }
   const RingPlan p = plan_ring(g);
   if (g.dtype == 1) return p.nw == 8 ? launch_ring<bf16, 8>(g, p, st) : launch_ring<bf16, 4>(g, p, st);
-  return p.nw == 8 ? launch_ring<float, 8>(g, p, st) : launch_ring<float, 4>(g, p, st);
+  return launch_ring<float, 2>(g, p, st);
 }
 
 hipError_t launch_gemm_pair(const GemmArgs& g, const GemmArgs& h, hipStream_t st) {
@@ -579,12 +591,14 @@ hipError_t launch_gemm_pair(const GemmArgs& g, const GemmArgs& h, hipStream_t st
   // 55.5; 4096 x 1024 x 1024 30.0 and 41.7; 6000 x 1024 x 2048 in fp32, which fills the
   // device twice each, 478 and 470.  Tiles of 8 waves, one workgroup a CU, fill the
   // device by themselves.
-  if (p.nw != 4 || q.nw != 4 || g.a_kmaj || !g.b_kmaj || !h.a_kmaj || !h.b_kmaj || g.dtype != h.dtype) {
+  if (p.nw == 8 || p.nw != q.nw || g.a_kmaj || !g.b_kmaj || !h.a_kmaj || !h.b_kmaj || g.dtype != h.dtype) {
     const hipError_t e = launch_gemm(g, st);
     return e != hipSuccess ? e : launch_gemm(h, st);
   }
-  if (g.dtype != 1) return g.two_pairs || h.two_products ? hipErrorInvalidValue : launch_ring_pair<float, 1>(g, p, h, q, st);
-  return g.two_pairs ? launch_ring_pair<bf16, 2>(g, p, h, q, st) : launch_ring_pair<bf16, 1>(g, p, h, q, st);
+  if (g.dtype == 1)
+    return g.two_pairs ? launch_ring_pair<bf16, 4, 2>(g, p, h, q, st) : launch_ring_pair<bf16, 4, 1>(g, p, h, q, st);
+  if (g.two_pairs || h.two_products) return hipErrorInvalidValue;
+  return launch_ring_pair<float, 2, 1>(g, p, h, q, st);
 }
 
 int act_grad_parts(int64_t rows, int64_t dim) {

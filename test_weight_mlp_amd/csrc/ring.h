@@ -1,10 +1,12 @@
-// Persistent tile products for gfx950 in bf16, C[m, n] = sum_k A[m, k] B[n, k]: tiles
+// Persistent tile products for gfx950, C[m, n] = sum_k A[m, k] B[n, k].  In bf16 tiles
 // of 256 x 256 by 8 waves, or of 128 x 128 by 4 (two workgroups a CU), on
-// v_mfma_f32_16x16x32_bf16.  Either operand may lie with K contiguous or K-major
-// (A[m, k] at p[k * ld + m]).
+// v_mfma_f32_16x16x32_bf16; in fp32 of 64 x 64 by 4 (four workgroups a CU), on
+// v_mfma_f32_16x16x4_f32, whose products take 8 times as long for the same bytes, so
+// that small tiles cost nothing and spread evenly.  Either operand may lie with K
+// contiguous or K-major (A[m, k] at p[k * ld + m]).
 //
 // Operands go HBM/L2 -> LDS with direct loads into a ring of five slots, each the A
-// or the B part of a stage of 64 K: stage q's A in slot 2q % 5, its B in slot
+// or the B part of a stage of 128 bytes of K: stage q's A in slot 2q % 5, its B in slot
 // (2q + 1) % 5.  The ring goes on over the ends of a workgroup's tiles: the next one's
 // first stages are in flight while a tile is finished.
 //
@@ -14,19 +16,20 @@
 // issued, into the slots that stage q-1 left, so that A has a stage and a half to
 // arrive, B a stage, and each memory phase issues four loads a wave.
 // 4 waves: one barrier a stage, in its middle; each half is multiplied while the next
-// half's fragments are read and one part's four loads (A of stage q+2, B of stage q+2)
-// are issued, spread over the products.  A CU's loads take as long as its products
-// here (32 KB and 512 cycles a stage), so that eight loads issued at once left the
+// half's fragments are read and one part's loads (A of stage q+2, B of stage q+2) are
+// issued, spread over the products.  A CU's loads take as long as its products
+// here in bf16 (32 KB and 512 cycles a stage), so that eight loads issued at once left the
 // matrix units idle: a tile alone took 0.49 us a stage and now takes 0.36, 2049 x 2560 x
 // 2560 40.5 us and now 35.5.  A ring twice as deep, one workgroup a CU, gained nothing
 // (0.49): the loads' rate counts, not their latency.
 //
 // LDS layouts, both free of bank conflicts:
-//   rows     128-byte rows of 64 K; 16-byte chunk c of LDS row r at slot
+//   rows     128-byte rows; 16-byte chunk c of LDS row r at slot
 //            c ^ ((r >> 1) & 7).
-//   K-major  a row of the tile's width for each K; its 32-byte unit u (16 columns)
-//            at slot u ^ (2 (k & 3) + ((k >> 3) & 1)), read with the transposing
-//            LDS loads.
+//   K-major  a row of the tile's width for each K.  bf16: its 32-byte unit u (16
+//            columns) at slot u ^ (2 (k & 3) + ((k >> 3) & 1)), read with the
+//            transposing LDS loads; fp32: its 64-byte unit at slot u ^ ((k >> 2) & 3),
+//            read one element at a time.
 // LDS row r of B's rows need not hold row r of the tile: with the order of PERM a
 // lane ends up with neighbouring columns of C and stores 16 bytes at once.
 //
@@ -35,7 +38,8 @@
 // branches made these of 1434, 1340, 1325 and 1339, 1256, 1213; next to those stood, with
 // two whole stages instead of the ring, 1283, 1341, 1332 and 1294, 1251, 1265; with
 // 32x32x16 products 1372 and 1271 (first only); both parts' loads issued in one phase
-// 1354; four waves of 128 x 128 instead of eight 1040.
+// 1354; four waves of 128 x 128 instead of eight 1040.  fp32: 8192 x 6144 x 2560 139, 142,
+// 141, 1021 x 4096 x 1024 123.
 #pragma once
 
 #include <type_traits>
@@ -55,15 +59,16 @@ constexpr int kStage = 128 / (int)sizeof(T);  // K of a stage
 template <typename T, int NW>
 struct Geo {
   static constexpr int KS = kStage<T>, ES = sizeof(T), VE = 16 / ES;
-  static constexpr int BM = NW * 32, BN = NW * 32;          // 256 or 128
-  static constexpr int WAVES_N = 2, WAVES_M = NW / 2;
-  static constexpr int WM = 64, WN = BN / 2, MI = WM / 16, NJ = WN / 16;
-  static_assert(BM == WAVES_M * WM, "wave grid");
+  static constexpr int BM = NW * 32, BN = NW * 32;          // 256, 128 or (fp32) 64
+  static constexpr int WAVES = NW == 8 ? 8 : 4, WAVES_N = 2, WAVES_M = WAVES / 2;
+  static constexpr int WM = BM / WAVES_M, WN = BN / 2, MI = WM / 16, NJ = WN / 16;
   static constexpr int SLOT = BM * 128;                     // bytes
   static constexpr int LDS_BYTES = SLOTS * SLOT;
-  static constexpr int NT = NW * 64;
-  static constexpr int NL = 4;                              // load instructions a wave and part
-  static_assert(SLOT == NW * NL * 1024, "load split");
+  static constexpr int NT = WAVES * 64;
+  static constexpr int NL = SLOT / (WAVES * 1024);          // load instructions a wave and part
+  static constexpr int GROUPS = 8 / NW;                     // workgroups a CU
+  static_assert(NW == 8 || NW == 4 || (NW == 2 && ES == 4), "tiles");
+  static_assert(NW == 8 || NL == MI, "a load for each block row of products");
 };
 
 // Offsets past every buffer's end: such a load reads zeros.  (A tile's rows end
@@ -224,7 +229,7 @@ struct Reader {
 // The order of B's rows with which a lane's NJ blocks are NJ neighbouring columns.
 template <int NW>
 __device__ __forceinline__ int perm_row(int r) {
-  constexpr int WN = Geo<bf16, NW>::WN, NJ = Geo<bf16, NW>::NJ;
+  constexpr int WN = Geo<float, NW>::WN, NJ = Geo<float, NW>::NJ;
   return r / WN * WN + (r & 15) * NJ + (r % WN >> 4);
 }
 
@@ -369,7 +374,7 @@ __device__ __forceinline__ void run(char* lds, int n1, int n2, int turn, Stages&
 #pragma unroll
     for (int j = 0; j < G::NJ; ++j) fb[to][j] = rb.get(pb, j, h);
   };
-  if constexpr (NW == 4) read(0, 0, 0);
+  if constexpr (NW != 8) read(0, 0, 0);
   for (; w.on(); w.next()) {
     f4 acc[G::MI][G::NJ];
 #pragma unroll
@@ -498,7 +503,7 @@ __device__ __forceinline__ void run(char* lds, int n1, int n2, int turn, Stages&
     };
     // (a wait that the compiler sees: scalar loads left over from the epilogue would have
     // it wait for every LDS read in the loop)
-    if constexpr (NW == 4) __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    if constexpr (NW != 8) __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
     // Group 1 meets one barrier more before its phases, group 0 one after.
     if (NW == 8 && grp == 1) core::lds_barrier();
 #pragma unroll

@@ -119,10 +119,10 @@ def test_linear_backward(dt, m, k, n):
 
 
 # (M, N, K) of a product of the large launches: in bf16 tiles of 8 waves in more than one
-# round, those with the last ones cut along K, and the same of 4 waves; in fp32 tiles of
-# 8 waves cut along K, those of 4 with the last ones cut, and in two rounds
+# round, those with the last ones cut along K, and the same of 4 waves; in fp32 more than
+# one round of tiles, with the last ones cut and not
 LARGE = [(BF16, 5432, 4048, 72), (BF16, 3296, 5064, 600), (BF16, 7216, 1144, 872), (BF16, 5384, 3096, 136),
-         (F32, 8368, 400, 2648), (F32, 8320, 904, 168), (F32, 5600, 3288, 72)]
+         (F32, 8368, 400, 2648), (F32, 8320, 904, 168), (F32, 5456, 712, 312), (F32, 5600, 3288, 72)]
 
 
 @pytest.mark.parametrize("which", ["y", "dx", "dW"])
