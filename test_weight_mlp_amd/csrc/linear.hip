@@ -409,7 +409,7 @@ __global__ __launch_bounds__(1024) void few_kernel(GemmArgs g) {
   constexpr int W = 16;
   typedef typename ring::Frag<T>::type frag;
   constexpr int VE = 16 / sizeof(T), CK = 4 * VE;                              // K of a slice: 16 bytes a lane
-  constexpr int U = MT * FB == 4 ? 4 : 8;  // slices in flight
+  constexpr int U = MT * FB >= 3 ? 4 : 8;  // slices in flight
   __shared__ ring::f4 red[W][MT * FB][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, kg = (lane >> 4) * VE;
   const int64_t n0 = (int64_t)blockIdx.x * (16 * FB);
@@ -465,17 +465,19 @@ __global__ __launch_bounds__(1024) void few_kernel(GemmArgs g) {
   }
 }
 
-// Where the tiles take less: from 33 rows on (bf16, 2560 -> 6144 outputs, 16.1 us at 33 to
-// 64 rows, here with four blocks of rows 14.5 to 17.0; 9728 -> 2560 21.0 and 42 to 53), and
-// from 17 or 9 on for large weights, which every workgroup's reads of all of x hold up
-// here.  Us here and on the tiles: bf16, 32 rows, 2560 -> 6144 11.7 and 16.1, 2560 -> 9728
-// 22.1 and 18.9; fp32, 32 rows, 1024 -> 2048 10.9 and 12.7, 4096 -> 2560 28.7 and 22.8; 16
-// rows, 4096 -> 2560 18.2 and 22.8, 2560 -> 9728 46.0 and 34.3; 8 rows 34.8 and 34.3.
+// Where the tiles take less: from 65 rows on, and before that for large weights, which
+// every workgroup's reads of all of x hold up here (they grow with the rows and K; the
+// outputs cost little until there are more than 256 workgroups).  Us here and on the
+// tiles: bf16, 64 rows, 1024 -> 2048 6.9 and 11.7, 2560 -> 2560 13.8 and 16.5, 4096 -> 1024
+// 20.1 and 12.2, 2560 -> 6144 26.5 and 16.1; 32 rows, 2560 -> 6144 11.7 and 16.1, 2560 ->
+// 9728 22.1 and 18.9; fp32, 32 rows, 1024 -> 2048 10.9 and 12.7, 4096 -> 2560 28.7 and 22.8;
+// 16 rows, 4096 -> 2560 18.2 and 22.8, 2560 -> 9728 46.0 and 34.3; 8 rows 34.8 and 34.3.
 bool few_rows(const GemmArgs& g) {
   if (g.a_kmaj || g.b_kmaj) return false;
   const bool h = g.dtype == 1;
   const int64_t weights = g.N * g.K;
-  return g.M <= (h ? 16 : 8) || (g.M <= (h ? 32 : 16) && weights <= 20000000) || (g.M <= 32 && weights <= 4000000);
+  if (g.M > 32) return h && g.M <= 64 && g.K <= 2560 && g.N <= 4096;
+  return g.M <= (h ? 16 : 8) || (g.M <= (h ? 32 : 16) && weights <= 20000000) || weights <= 4000000;
 }
 
 // Two blocks of outputs a workgroup halve the rows' reads; they pay where there are
@@ -488,7 +490,12 @@ void launch_few(const GemmArgs& g, hipStream_t st) {
   if (g.M <= 8) few_kernel<T, 1, 1><<<groups(1), 1024, 0, st>>>(g);
   else if (g.M <= 16 && !wide) few_kernel<T, 1, 1><<<groups(1), 1024, 0, st>>>(g);
   else if (g.M <= 16) few_kernel<T, 1, 2><<<groups(2), 1024, 0, st>>>(g);
-  else if (!wide) few_kernel<T, 2, 1><<<groups(1), 1024, 0, st>>>(g);
+  else if (g.M > 32) {
+    if constexpr (sizeof(T) == 2) {
+      if (g.M > 48) few_kernel<T, 4, 1><<<groups(1), 1024, 0, st>>>(g);
+      else few_kernel<T, 3, 1><<<groups(1), 1024, 0, st>>>(g);
+    }
+  } else if (!wide) few_kernel<T, 2, 1><<<groups(1), 1024, 0, st>>>(g);
   else few_kernel<T, 2, 2><<<groups(2), 1024, 0, st>>>(g);
 }
 
