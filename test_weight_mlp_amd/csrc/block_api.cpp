@@ -178,6 +178,12 @@ ipttt_status ipttt_norm_backward(const ipttt_norm_problem* p, const ipttt_rows* 
   IPTTT_TRY(in_place(a.dx, a.x));
   IPTTT_TRY(in_place(a.dx, a.dy));
   IPTTT_TRY(in_place(a.dx, a.dres));
+  IPTTT_TRY(apart(dw, db));
+  for (const void* in : {static_cast<const void*>(a.x.p), w, static_cast<const void*>(a.dy.p),
+                         static_cast<const void*>(a.dres.p), static_cast<const void*>(a.dx.p)}) {
+    IPTTT_TRY(apart(dw, in));
+    IPTTT_TRY(apart(db, in));
+  }
   if (dw != nullptr || db != nullptr) IPTTT_TRY(workspace(ws, ws_bytes, norm_bytes(p)));
   a.w = w;
   a.dw = dw;

@@ -151,7 +151,8 @@ NORM_ARGS = bad_rows("x", 1, 64) + bad_rows("y", 4, 64) + [
 NORM_BACKWARD_ARGS = sum((bad_rows(n, i, 64) for n, i in (("x", 1), ("dy", 3), ("dres", 4), ("dx", 5))), []) + [
     (dict(x=None), NULL), (dict(dy=None), NULL), (dict(dx=None), NULL), (dict(w=at(2) + 8), ALIGN),
     (dict(dw=at(6) + 4), ALIGN), (dict(db=at(7) + 4), ALIGN), (dict(dx=rows(3, 72)), ARG), (dict(dx=rows(4, 72)), ARG),
-    (dict(dx=rows(1, 72)), ARG), (dict(ws=None), WORKSPACE), (dict(ws_bytes=64), WORKSPACE), (dict(ws=at(8) + 16), ALIGN)]
+    (dict(dx=rows(1, 72)), ARG), (dict(ws=None), WORKSPACE), (dict(ws_bytes=64), WORKSPACE), (dict(ws=at(8) + 16), ALIGN)] + [
+    (dict([(n, at(i))]), ARG) for n, other in (("dw", 7), ("db", 6)) for i in (1, 2, 3, 4, 5, other)]
 LINEAR_ARGS = bad_rows("x", 1, 64) + sum((bad_rows(n, i, 128) for n, i in (("res", 4), ("y", 5), ("pre", 6))), []) + [
     (dict(x=None), NULL), (dict(W=None), NULL), (dict(y=None), NULL), (dict(W=at(2) + 8), ALIGN), (dict(b=at(3) + 2), ALIGN),
     (dict(y=rows(1, 128)), ARG), (dict(y=rows(2, 128)), ARG), (dict(y=rows(3, 128)), ARG), (dict(y=rows(4, 136)), ARG),
