@@ -240,8 +240,14 @@ __global__ __launch_bounds__(512) void norm_sum_kernel(const float* part, int pa
   __shared__ float red[32][17];
   const int c = blockIdx.x * 16 + (threadIdx.x & 15), g = threadIdx.x >> 4;
   float x = 0.0f;
-  if (c < 2 * dim)
-    for (int p = g; p < parts; p += 32) x += part[(int64_t)p * 2 * dim + c];
+  // (8 loads at a time: 256 partials of 2048 sums 2.8 us, one load at a time 4.5)
+  for (int p = g; p < parts && c < 2 * dim; p += 32 * 8) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = p + 32 * u < parts ? part[(int64_t)(p + 32 * u) * 2 * dim + c] : 0.0f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) x += v[u];
+  }
   red[g][threadIdx.x & 15] = x;
   __syncthreads();
   if (threadIdx.x >= 16 || c >= 2 * dim) return;
