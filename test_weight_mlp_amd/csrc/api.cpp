@@ -311,8 +311,10 @@ BwdLayout bwd_layout(const Prob& p) {
   l.dgt = take(tnfast ? 0 : (size_t)l.Mp * p.f * e);
   l.dut = take(tnfast ? 0 : (size_t)l.Mp * p.f * e);
   l.ht = take(tnfast ? 0 : (size_t)l.Mp * p.d * e);
-  l.gpart = take(p.dtype != IPTTT_BF16 ? 0 : ipttt::gemm_workspace(keep8_dh(p)));
-  l.gpart2 = take(p.dtype != IPTTT_BF16 ? 0 : ipttt::gemm_workspace(keep8_dw(p)));
+  size_t gx = 0, gw = 0;
+  if (p.dtype == IPTTT_BF16) ipttt::gemm_pair_workspace(keep8_dh(p), keep8_dw(p), &gx, &gw);
+  l.gpart = take(gx);
+  l.gpart2 = take(gw);
   const size_t zb = o;
   l.total = l.call + std::max(sa, std::max(tg, zb));
   return l;

@@ -50,8 +50,9 @@ struct GemmArgs {
 size_t gemm_workspace(const GemmArgs& g);
 hipError_t launch_gemm(const GemmArgs& g, hipStream_t st);
 // Two products that do not depend on each other, g with B K-major and h with both
-// (dx and dW of a projection), each with its own part: the same bits as one by one, in
-// one launch where both are of small tiles.
+// (dx and dW of a projection), each with its own part: in one launch where both are of
+// small tiles.  One whose c is NULL is left out; the other has the same bits as with it.
+void gemm_pair_workspace(const GemmArgs& g, const GemmArgs& h, size_t* of_g, size_t* of_h);
 hipError_t launch_gemm_pair(const GemmArgs& g, const GemmArgs& h, hipStream_t st);
 
 // dp = dy act'(pre) and db (each optional), in one pass over dy.

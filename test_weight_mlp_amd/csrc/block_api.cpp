@@ -137,8 +137,10 @@ BackwardLayout backward_layout(const ipttt_linear_problem* p) {
   l.dp = 0;
   l.db = l.dp + (p->act != IPTTT_ACT_NONE ? align256((size_t)p->rows * (size_t)p->out_dim * e) : 0);
   l.part_x = l.db + align256((size_t)ipttt::act_grad_parts(p->rows, p->out_dim) * (size_t)p->out_dim * sizeof(float));
-  l.part_w = l.part_x + align256(ipttt::gemm_workspace(dx_args(p)));
-  l.total = l.part_w + align256(ipttt::gemm_workspace(dw_args(p)));
+  size_t x, w;
+  ipttt::gemm_pair_workspace(dx_args(p), dw_args(p), &x, &w);
+  l.part_w = l.part_x + align256(x);
+  l.total = l.part_w + align256(w);
   return l;
 }
 
@@ -275,10 +277,7 @@ ipttt_status ipttt_linear_backward(const ipttt_linear_problem* p, const ipttt_ro
   gw.b = xv;
   gw.c = Rows{dW, p->in_dim};
   gw.part = reinterpret_cast<float*>(base + l.part_w);
-  if (dxv.p != nullptr && dW != nullptr) return hip_status(ipttt::launch_gemm_pair(gx, gw, st));
-  if (dxv.p != nullptr) return hip_status(ipttt::launch_gemm(gx, st));
-  if (dW != nullptr) return hip_status(ipttt::launch_gemm(gw, st));
-  return IPTTT_OK;
+  return hip_status(ipttt::launch_gemm_pair(gx, gw, st));
 }
 
 }  // extern "C"

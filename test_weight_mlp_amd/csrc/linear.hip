@@ -314,22 +314,25 @@ __global__ __launch_bounds__((ring::Geo<T, NW>::NT)) void ring_join_kernel(GemmA
 
 constexpr int kCus = 256;
 
-// The cut for which an estimate of the product's time is least.
-RingPlan plan_ring(const GemmArgs& g) {
+// The cut for which an estimate of the product's time is least (in us); only: 0, or the
+// one tile size to take.
+RingPlan plan_ring(const GemmArgs& g, int only, double* us) {
   RingPlan best{};
   double least = 1e300;
   const bool h = g.dtype == 1;
   // us of a stage, of a workgroup alone on its CU and on a full one, of an item beside its
-  // stages and of joining, fitted to some 1000 products of both types in all cuts (64 to
-  // 16384 rows): the cut so chosen takes 1 % longer than the best one on average
-  // (fp32: tiles of 128 x 128 instead took 19 % longer on average and up to 4 % less, at
-  // 8192 x 2560 x 2560, of 256 x 256 up to four times as long)
+  // stages and of joining, fitted to some 1000 products of both types in all cuts (33 to
+  // 16384 rows): the cut so chosen takes 1 % longer than the best one on average.  In bf16
+  // small tiles are for few of them (512 x 1024 x 1024 8.4 us on 64 x 64, 13.0 on 128 x 128;
+  // 1999 x 1024 x 4096 21.0 on 128 x 128, 28 on 256 x 256); in fp32, where products take
+  // 16 times as long, 128 x 128 took 19 % longer than 64 x 64 on average and up to 4 % less
+  // (8192 x 2560 x 2560), 256 x 256 up to four times as long.
   const struct Cost {
     int nw;
     double lone, full, item;
-  } costs[2][2] = {{{2, 0.55, 1.9, 2.0}}, {{8, 1.0, 1.4, 3.0}, {4, 0.5, 0.85, 2.0}}};
+  } costs[2][3] = {{{2, 0.55, 1.9, 2.0}}, {{8, 1.3, 1.35, 4.5}, {4, 0.5, 0.95, 1.9}, {2, 0.3, 0.77, 1.2}}};
   for (const Cost& c : costs[h]) {
-    if (c.nw == 0) continue;
+    if (c.nw == 0 || (only != 0 && c.nw != only)) continue;
     const int64_t w = c.nw * 32, tm = (g.M + w - 1) / w * (g.two_products ? 2 : 1), tn = (g.N + w - 1) / w, tiles = tm * tn;
     const int64_t most = 8 / c.nw, groups = most * kCus;
     const int ks = h ? ring::kStage<bf16> : ring::kStage<float>, legs = g.two_pairs ? 2 : 1,
@@ -345,7 +348,7 @@ RingPlan plan_ring(const GemmArgs& g) {
       const double share = most == 1 ? (rest > groups / 2 ? 1.0 : 0.0)
                                      : (double)(std::min((rest + kCus - 1) / kCus, most) - 1) / (double)(most - 1);
       t += (double)((rest + groups - 1) / groups) * (per * (c.lone + (c.full - c.lone) * share) + c.item);
-      if (parts > 1) t += 4.0 + (double)items * w * w * 8 / (h ? 6.0e6 : 8.0e6);
+      if (parts > 1) t += (h ? 2.8 : 4.0) + (double)items * w * w * 8 / (h ? 5.2e6 : 8.0e6);
       if (t >= least) return;
       least = t;
       best = RingPlan{c.nw, (int)tm, (int)tn, (int)(parts > 1 ? whole : tiles), (int)(parts > 1 ? split : 0), parts, per, leg, legs};
@@ -354,6 +357,30 @@ RingPlan plan_ring(const GemmArgs& g) {
     const int64_t whole = tiles / groups * groups, rem = tiles - whole;
     if (rem > 0)
       for (int64_t parts = 2; parts <= 32 && parts * 2 <= stages && rem * parts <= 2 * groups; ++parts) consider(whole, (int)parts);
+  }
+  *us = least;
+  return best;
+}
+RingPlan plan_ring(const GemmArgs& g) {
+  double us;
+  return plan_ring(g, 0, &us);
+}
+
+// Both gradients of a projection: tiles of one size where neither's are of 8 waves, so
+// that one launch can take both.
+struct PairPlan {
+  RingPlan g, h;
+};
+PairPlan plan_pair(const GemmArgs& g, const GemmArgs& h) {
+  PairPlan best{plan_ring(g), plan_ring(h)};
+  if (best.g.nw == best.h.nw || best.g.nw == 8 || best.h.nw == 8) return best;
+  double least = 1e300;
+  for (const int nw : {4, 2}) {
+    double a, b;
+    const PairPlan p{plan_ring(g, nw, &a), plan_ring(h, nw, &b)};
+    if (a + b >= least) continue;
+    least = a + b;
+    best = p;
   }
   return best;
 }
@@ -584,33 +611,50 @@ constexpr int kStrips = 256;  // most strips of rows of a column sum
 
 size_t gemm_workspace(const GemmArgs& g) { return few_rows(g) ? 0 : ring_bytes(plan_ring(g)); }
 
-hipError_t launch_gemm(const GemmArgs& g, hipStream_t st) {
+namespace {
+
+hipError_t launch_plan(const GemmArgs& g, const RingPlan& p, hipStream_t st) {
   // products that no caller has
   if (g.a_kmaj && !g.b_kmaj) return hipErrorInvalidValue;
   if (g.two_pairs && (g.a_kmaj || !g.b_kmaj || g.two_products || g.dtype != 1)) return hipErrorInvalidValue;
   if (g.two_products && (!g.a_kmaj || g.dtype != 1)) return hipErrorInvalidValue;
-  if (few_rows(g)) {
-    if (g.dtype == 1) launch_few<bf16>(g, st);
-    else launch_few<float>(g, st);
-    return hipGetLastError();
-  }
-  const RingPlan p = plan_ring(g);
-  if (g.dtype == 1) return p.nw == 8 ? launch_ring<bf16, 8>(g, p, st) : launch_ring<bf16, 4>(g, p, st);
+  if (g.dtype == 1)
+    return p.nw == 8   ? launch_ring<bf16, 8>(g, p, st)
+           : p.nw == 4 ? launch_ring<bf16, 4>(g, p, st)
+                       : launch_ring<bf16, 2>(g, p, st);
   return launch_ring<float, 2>(g, p, st);
 }
 
+}  // namespace
+
+hipError_t launch_gemm(const GemmArgs& g, hipStream_t st) {
+  if (!few_rows(g)) return launch_plan(g, plan_ring(g), st);
+  if (g.dtype == 1) launch_few<bf16>(g, st);
+  else launch_few<float>(g, st);
+  return hipGetLastError();
+}
+
+void gemm_pair_workspace(const GemmArgs& g, const GemmArgs& h, size_t* of_g, size_t* of_h) {
+  const PairPlan p = plan_pair(g, h);
+  *of_g = ring_bytes(p.g);
+  *of_h = ring_bytes(p.h);
+}
+
 hipError_t launch_gemm_pair(const GemmArgs& g, const GemmArgs& h, hipStream_t st) {
-  const RingPlan p = plan_ring(g), q = plan_ring(h);
+  const auto [p, q] = plan_pair(g, h);
   // Tiles of 4 waves together: 1999 x 1024 x 4096 in bf16 44.7 us, one after the other
   // 55.5; 4096 x 1024 x 1024 30.0 and 41.7; 6000 x 1024 x 2048 in fp32, which fills the
   // device twice each, 478 and 470.  Tiles of 8 waves, one workgroup a CU, fill the
   // device by themselves.
-  if (p.nw == 8 || p.nw != q.nw || g.a_kmaj || !g.b_kmaj || !h.a_kmaj || !h.b_kmaj || g.dtype != h.dtype) {
-    const hipError_t e = launch_gemm(g, st);
-    return e != hipSuccess ? e : launch_gemm(h, st);
+  if (g.c.p == nullptr || h.c.p == nullptr || p.nw == 8 || p.nw != q.nw || g.a_kmaj || !g.b_kmaj || !h.a_kmaj ||
+      !h.b_kmaj || g.dtype != h.dtype) {
+    const hipError_t e = g.c.p != nullptr ? launch_plan(g, p, st) : hipSuccess;
+    return e != hipSuccess || h.c.p == nullptr ? e : launch_plan(h, q, st);
   }
-  if (g.dtype == 1)
+  if (g.dtype == 1 && p.nw == 4)
     return g.two_pairs ? launch_ring_pair<bf16, 4, 2>(g, p, h, q, st) : launch_ring_pair<bf16, 4, 1>(g, p, h, q, st);
+  if (g.dtype == 1)
+    return g.two_pairs ? launch_ring_pair<bf16, 2, 2>(g, p, h, q, st) : launch_ring_pair<bf16, 2, 1>(g, p, h, q, st);
   if (g.two_pairs || h.two_products) return hipErrorInvalidValue;
   return launch_ring_pair<float, 2, 1>(g, p, h, q, st);
 }

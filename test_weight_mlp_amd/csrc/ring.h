@@ -59,7 +59,7 @@ constexpr int kStage = 128 / (int)sizeof(T);  // K of a stage
 template <typename T, int NW>
 struct Geo {
   static constexpr int KS = kStage<T>, ES = sizeof(T), VE = 16 / ES;
-  static constexpr int BM = NW * 32, BN = NW * 32;          // 256, 128 or (fp32) 64
+  static constexpr int BM = NW * 32, BN = NW * 32;          // 256, 128 or 64
   static constexpr int WAVES = NW == 8 ? 8 : 4, WAVES_N = 2, WAVES_M = WAVES / 2;
   static constexpr int WM = BM / WAVES_M, WN = BN / 2, MI = WM / 16, NJ = WN / 16;
   static constexpr int SLOT = BM * 128;                     // bytes
@@ -67,7 +67,7 @@ struct Geo {
   static constexpr int NT = WAVES * 64;
   static constexpr int NL = SLOT / (WAVES * 1024);          // load instructions a wave and part
   static constexpr int GROUPS = 8 / NW;                     // workgroups a CU
-  static_assert(NW == 8 || NW == 4 || (NW == 2 && ES == 4), "tiles");
+  static_assert(NW == 8 || NW == 4 || NW == 2, "tiles");
   static_assert(NW == 8 || NL == MI, "a load for each block row of products");
 };
 
@@ -92,6 +92,13 @@ template <> struct Frag<float> {
     return c;
   }
 };
+
+// The exchange of the units of a K-major row in bf16, K = 8 kg + r or 8 kg + 4 + r: half a
+// wave reads r = 0 .. 3 of two kg at once.
+template <int NW>
+__device__ __forceinline__ int kmajor_swizzle(int r, int kg) {
+  return NW == 2 ? (r >> 1 & 1) | (kg & 1) << 1 : r << 1 | (kg & 1);
+}
 
 // One operand's loads.  issue() loads the stage that the cursor stands at, and
 // advance() moves it, so that the scalar work of a stage's addresses is done while
@@ -135,7 +142,7 @@ struct Loader {
 #pragma unroll
       for (int j = 0; j < G::NL; ++j) {
         const int r = (wave * G::NL + j) * RPI + lane / LPR, s = lane % LPR;
-        const int u = G::ES == 2 ? (s >> 1) ^ (((r & 3) << 1) | ((r >> 3) & 1)) : (s >> 2) ^ ((r >> 2) & 3);
+        const int u = G::ES == 2 ? (s >> 1) ^ kmajor_swizzle<NW>(r & 3, r >> 3) : (s >> 2) ^ ((r >> 2) & 3);
         const int col = u * 16 + (G::ES == 2 ? (s & 1) * 8 : (s & 3) * 4);
         voff[j] = (uint32_t)col < here ? (uint32_t)r * ldb + (uint32_t)col * G::ES : kOut;
       }
@@ -202,7 +209,7 @@ struct Reader {
     } else {
       const int kg = lane >> 4, r = (lane >> 2) & 3;
       at = (8 * kg + r) * G::BM * 2 + (lane & 3) * 8;
-      sw = (r << 1) | (kg & 1);
+      sw = kmajor_swizzle<NW>(r, kg);
       unit = row0 >> 4;
     }
   }
