@@ -502,15 +502,15 @@ __global__ __launch_bounds__(1024) void few_kernel(GemmArgs g) {
 // Where the tiles take less: from 65 rows on, and before that for large weights, which
 // every workgroup's reads of all of x hold up here (they grow with the rows and K; the
 // outputs cost little until there are more than 256 workgroups).  Us here and on the
-// tiles: bf16, 64 rows, 1024 -> 2048 6.9 and 11.7, 2560 -> 2560 13.8 and 16.5, 4096 -> 1024
-// 20.1 and 12.2, 2560 -> 6144 26.5 and 16.1; 32 rows, 2560 -> 6144 11.7 and 16.1, 2560 ->
-// 9728 22.1 and 18.9; fp32, 32 rows, 1024 -> 2048 10.9 and 12.7, 4096 -> 2560 28.7 and 22.8;
-// 16 rows, 4096 -> 2560 18.2 and 22.8, 2560 -> 9728 46.0 and 34.3; 8 rows 34.8 and 34.3.
+// tiles: bf16, 64 rows, 1024 -> 2048 6.9 and 8.0, 2560 -> 2560 13.9 and 11.6; 32 rows,
+// 2560 -> 6144 11.7 and 12.9, 2560 -> 9728 22.1 and 19.8; fp32, 32 rows, 1024 -> 2048 10.9
+// and 12.7, 4096 -> 2560 28.7 and 22.3; 16 rows, 4096 -> 2560 18.4 and 22.2, 2560 -> 9728
+// 46.0 and 33.8; 8 rows 34.7 and 33.8.
 bool few_rows(const GemmArgs& g) {
   if (g.a_kmaj || g.b_kmaj) return false;
   const bool h = g.dtype == 1;
   const int64_t weights = g.N * g.K;
-  if (g.M > 32) return h && g.M <= 64 && g.K <= 2560 && g.N <= 4096;
+  if (g.M > 32) return h && g.M <= 64 && g.K <= 1280 && g.N <= 4096;
   return g.M <= (h ? 16 : 8) || (g.M <= (h ? 32 : 16) && weights <= 20000000) || weights <= 4000000;
 }
 

@@ -68,10 +68,12 @@ def test_gradients_from_kept_values(t, d, f):
         assert rel(got, w) <= 1.5 * 2.0 ** -9 + 2.0 ** -10
 
 
-# tiles of 8 waves in the forward; the large launches of the gradients: dH of 8 waves and
-# of 4, with the last tiles cut along K, and the same of the weights' gradients
+# tiles of 8 waves in the forward; the large launches of the gradients: dH of 8 waves, of 4
+# and of small tiles, with the last tiles cut along K; the weights' gradients of 8 waves in
+# several rounds, with the last ones cut, and of 4
 @pytest.mark.parametrize("t, d, f", [(20000, 64, 640), (5000, 320, 1096), (3480, 4776, 464), (7248, 1088, 336),
-                                     (872, 1000, 8304), (752, 5424, 672)])
+                                     (3080, 1296, 744), (72, 3824, 4056), (856, 5600, 1520), (872, 1000, 8304),
+                                     (752, 5424, 672)])
 def test_large_launches(t, d, f):
     test_gradients_from_kept_values(t, d, f)
 

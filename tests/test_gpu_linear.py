@@ -118,11 +118,12 @@ def test_linear_backward(dt, m, k, n):
             assert all(bool((t == 5.0).all()) for j, t in enumerate((g.dx, g.dW, g.db)) if j != i)
 
 
-# (M, N, K) of a product of the large launches: in bf16 tiles of 8 waves in more than one
-# round, those with the last ones cut along K, and the same of 4 waves; in fp32 more than
-# one round of tiles, with the last ones cut and not
-LARGE = [(BF16, 5432, 4048, 72), (BF16, 3296, 5064, 600), (BF16, 7216, 1144, 872), (BF16, 5384, 3096, 136),
-         (F32, 8368, 400, 2648), (F32, 8320, 904, 168), (F32, 5456, 712, 312), (F32, 5600, 3288, 72)]
+# (M, N, K) of a product of the large launches: in bf16 tiles of each size in more than one
+# round, and those with the last ones cut along K; in fp32 the same
+LARGE = [(BF16, 5688, 5504, 80), (BF16, 6040, 2744, 840), (BF16, 5432, 4048, 72), (BF16, 3296, 5064, 600),
+         (BF16, 7216, 1144, 872), (BF16, 6560, 1176, 856), (BF16, 5384, 3096, 136), (BF16, 776, 5000, 1696),
+         (BF16, 4624, 1712, 80), (F32, 8368, 400, 2648), (F32, 8320, 904, 168), (F32, 5456, 712, 312),
+         (F32, 5600, 3288, 72)]
 
 
 @pytest.mark.parametrize("which", ["y", "dx", "dW"])
