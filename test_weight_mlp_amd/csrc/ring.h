@@ -1,8 +1,8 @@
-// Persistent tile products for gfx950, C[m, n] = sum_k A[m, k] B[n, k].  In bf16 tiles
-// of 256 x 256 by 8 waves, or of 128 x 128 by 4 (two workgroups a CU), on
-// v_mfma_f32_16x16x32_bf16; in fp32 of 64 x 64 by 4 (four workgroups a CU), on
-// v_mfma_f32_16x16x4_f32, whose products take 8 times as long for the same bytes, so
-// that small tiles cost nothing and spread evenly.  Either operand may lie with K
+// Persistent tile products for gfx950, C[m, n] = sum_k A[m, k] B[n, k]: tiles of 256 x
+// 256 by 8 waves, of 128 x 128 by 4 (two workgroups a CU) or of 64 x 64 by 4 (four), on
+// v_mfma_f32_16x16x32_bf16 or v_mfma_f32_16x16x4_f32.  The smaller the tile, the more
+// evenly a small product spreads and the more bytes it loads; in fp32, whose products take
+// 8 times as long for the same bytes, that costs nothing.  Either operand may lie with K
 // contiguous or K-major (A[m, k] at p[k * ld + m]).
 //
 // Operands go HBM/L2 -> LDS with direct loads into a ring of five slots, each the A
@@ -27,7 +27,7 @@
 //   rows     128-byte rows; 16-byte chunk c of LDS row r at slot
 //            c ^ ((r >> 1) & 7).
 //   K-major  a row of the tile's width for each K.  bf16: its 32-byte unit u (16
-//            columns) at slot u ^ (2 (k & 3) + ((k >> 3) & 1)), read with the
+//            columns) at slot u ^ kmajor_swizzle(k & 3, k >> 3), read with the
 //            transposing LDS loads; fp32: its 64-byte unit at slot u ^ ((k >> 2) & 3),
 //            read one element at a time.
 // LDS row r of B's rows need not hold row r of the tile: with the order of PERM a
@@ -94,7 +94,8 @@ template <> struct Frag<float> {
 };
 
 // The exchange of the units of a K-major row in bf16, K = 8 kg + r or 8 kg + 4 + r: half a
-// wave reads r = 0 .. 3 of two kg at once.
+// wave reads r = 0 .. 3 of two kg at once, one unit each, and those have to lie in
+// different banks (a row of 64 columns is half the banks' width, so that two K share one).
 template <int NW>
 __device__ __forceinline__ int kmajor_swizzle(int r, int kg) {
   return NW == 2 ? (r >> 1 & 1) | (kg & 1) << 1 : r << 1 | (kg & 1);
