@@ -1,7 +1,7 @@
 // Layer norm and RMS norm of rows, and their gradients.
 //
-// A row is held in the registers of one wave (or, wider rows, of several in a
-// workgroup), in 16-byte pieces a lane, so that it is read once: the mean, the squares
+// A row is held in the registers of one wave (narrow rows of 8 to 32 lanes, wide ones of
+// several waves), in 16-byte pieces a lane, so that it is read once: the mean, the squares
 // about it and the output come from the same registers.  All arithmetic is
 // fp32; the outputs are rounded once.
 #include "block.h"
@@ -19,26 +19,28 @@ __device__ __forceinline__ float dpp_add(float x) {
   return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, true));
 }
 
-// Sum over the wave, in all lanes: neighbours, pairs, half rows and rows of 16
-// lanes, then across the rows.
-__device__ __forceinline__ float wave_sum(float x) {
+// Sum over groups of L lanes (8 to 64), in all of them: neighbours, pairs, half rows and
+// rows of 16 lanes, then across the rows.
+template <int L>
+__device__ __forceinline__ float lane_sum(float x) {
   x = dpp_add<0xB1>(x);   // quad_perm 1 0 3 2
   x = dpp_add<0x4E>(x);   // quad_perm 2 3 0 1
   x = dpp_add<0x141>(x);  // row_half_mirror
-  x = dpp_add<0x140>(x);  // row_mirror
-  x += __shfl_xor(x, 16, 64);
-  x += __shfl_xor(x, 32, 64);
+  if constexpr (L >= 16) x = dpp_add<0x140>(x);  // row_mirror
+  if constexpr (L >= 32) x += __shfl_xor(x, 16, 64);
+  if constexpr (L >= 64) x += __shfl_xor(x, 32, 64);
   return x;
 }
 
-// N sums over a row's lanes: the wave's, or (NW > 1) those of NW neighbouring waves
-// through LDS, red[slot][wave].  slot alternates between consecutive calls, so that one
+// N sums over a row's L lanes: within the wave, or (L > 64) of neighbouring waves through
+// LDS, red[slot][wave].  slot alternates between consecutive calls, so that one
 // barrier a call is enough: a wave that writes a slot again has passed the barrier of
 // the call between, which every wave meets after its reads of that slot.
-template <int NW, int N>
+template <int L, int N>
 __device__ __forceinline__ void row_sum(float (&x)[N], float (*red)[8][N], int slot, int wave) {
+  constexpr int NW = L / 64;
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = wave_sum(x[i]);
+  for (int i = 0; i < N; ++i) x[i] = lane_sum<L < 64 ? L : 64>(x[i]);
   if constexpr (NW > 1) {
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
@@ -61,13 +63,14 @@ struct Piece {  // 16 bytes
   typedef T vec __attribute__((ext_vector_type(V)));
 };
 
-template <typename T, int NW, int IT>
+// L lanes a row, 256 / L rows a workgroup at a time.
+template <typename T, int L, int IT>
 __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
-  constexpr int V = Piece<T>::V, L = NW * 64;
+  constexpr int V = Piece<T>::V, ROWS = 256 / L;
   typedef typename Piece<T>::vec vec;
   __shared__ float red[2][8][1];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x % L;
-  for (int64_t row = (int64_t)blockIdx.x * (4 / NW) + wave / NW; row < a.rows; row += (int64_t)gridDim.x * (4 / NW)) {
+  for (int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / L; row < a.rows; row += (int64_t)gridDim.x * ROWS) {
     const T* x = static_cast<const T*>(a.x.p) + row * a.x.ld;
     vec raw[IT];
 #pragma unroll
@@ -81,7 +84,7 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
       for (int i = 0; i < IT; ++i)
 #pragma unroll
         for (int e = 0; e < V; ++e) mu[0] += (float)raw[i][e];
-      row_sum<NW>(mu, red, 0, wave);
+      row_sum<L>(mu, red, 0, wave);
       mu[0] /= (float)a.dim;
     }
 #pragma unroll
@@ -93,7 +96,7 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
         sq[0] = fmaf(d, d, sq[0]);
       }
     }
-    row_sum<NW>(sq, red, 1, wave);
+    row_sum<L>(sq, red, 1, wave);
     const float r = rsqrtf(sq[0] / (float)a.dim + a.eps);
     T* y = static_cast<T*>(a.y.p) + row * a.y.ld;
 #pragma unroll
@@ -112,24 +115,24 @@ __global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
       }
       *reinterpret_cast<vec*>(y + c) = o;
     }
-    if constexpr (NW > 1) __syncthreads();  // before the next row writes red
+    if constexpr (L > 64) __syncthreads();  // before the next row writes red
   }
 }
 
-// NW waves a row, 8 / NW rows a workgroup at a time.  The weight gradients of a lane's
+// L lanes a row, 512 / L rows a workgroup at a time.  The weight gradients of a lane's
 // columns stay in registers until its last row, and each workgroup writes one partial
 // (a lone one the result).  Bound by the memory: 16384 x 2560 in bf16 with dres 83 us
 // for 336 MB (4.0 TB/s), 32768 x 1024 58 us (4.6 TB/s).  Loading the next row's pieces
 // before the current row's sums gained nothing (84 and 59 us): with 16 waves resident
 // the others' loads fill the wait.
-template <typename T, int NW, int IT>
+template <typename T, int L, int IT>
 __global__ __launch_bounds__(512) void norm_bwd_kernel(NormArgs a) {
-  constexpr int V = Piece<T>::V, L = NW * 64, ROWS = 8 / NW;
+  constexpr int V = Piece<T>::V, ROWS = 512 / L;
   typedef typename Piece<T>::vec vec;
   __shared__ float red[2][8][3];
   __shared__ float red1[2][8][1];
-  __shared__ float sum[NW < 8 ? ROWS : 1][NW < 8 ? IT * L * V : 1];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x % L, group = wave / NW;
+  __shared__ float sum[L < 512 ? ROWS : 1][L < 512 ? IT * L * V : 1];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x % L, group = threadIdx.x / L;
   const bool grads = a.dw != nullptr || a.db != nullptr;
   float dw[IT][V], db[IT][V];
 #pragma unroll
@@ -160,7 +163,7 @@ __global__ __launch_bounds__(512) void norm_bwd_kernel(NormArgs a) {
       for (int i = 0; i < IT; ++i)
 #pragma unroll
         for (int e = 0; e < V; ++e) mu[0] += (float)x[i][e];
-      row_sum<NW>(mu, red1, slot, wave);
+      row_sum<L>(mu, red1, slot, wave);
       mu[0] /= (float)a.dim;
     }
     float s[3] = {0.0f, 0.0f, 0.0f};  // squares, u, u (x - mu)
@@ -179,7 +182,7 @@ __global__ __launch_bounds__(512) void norm_bwd_kernel(NormArgs a) {
         s[2] = fmaf(u, d, s[2]);
       }
     }
-    row_sum<NW>(s, red, slot, wave);
+    row_sum<L>(s, red, slot, wave);
     const float n = (float)a.dim, r = rsqrtf(s[0] / n + a.eps);
     const float mean_u = a.center ? s[1] / n : 0.0f, along = s[2] / n * r * r;
     T* op = static_cast<T*>(a.dx.p) + row * a.dx.ld;
@@ -209,7 +212,7 @@ __global__ __launch_bounds__(512) void norm_bwd_kernel(NormArgs a) {
   for (int which = 0; which < 2; ++which) {
     float* to = which == 0 ? a.dw : a.db;
     if (gridDim.x > 1) to = a.part + ((int64_t)blockIdx.x * 2 + which) * a.dim;
-    if constexpr (NW < 8) {
+    if constexpr (L < 512) {
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < IT; ++i)
@@ -260,12 +263,25 @@ __global__ __launch_bounds__(512) void norm_sum_kernel(const float* part, int pa
 // Rows of up to this many elements a lane go to one wave.
 constexpr int kWaveElems = 40;
 
-template <typename T, int NW, typename F>
-void with_pieces(int it, F&& f) {
-  constexpr int most = NW == 1 ? kWaveElems / Piece<T>::V : 16384 / 256 / Piece<T>::V;
+// Rows of up to 32 pieces share a wave: the lanes, 8, 16 or 32, that hold one (20000 x 64
+// in bf16 3.4 us and its gradient 7.7; with a wave a row 6.5 and 14.6).
+template <typename T, typename F>
+bool with_narrow_row(int dim, F&& f) {
+  const int pieces = (dim + Piece<T>::V - 1) / Piece<T>::V;
+  const std::integral_constant<int, 1> one;
+  if (pieces <= 8) f(std::integral_constant<int, 8>(), one);
+  else if (pieces <= 16) f(std::integral_constant<int, 16>(), one);
+  else if (pieces <= 32) f(std::integral_constant<int, 32>(), one);
+  return pieces <= 32;
+}
+
+template <typename T, int L, typename F>
+void with_pieces(int dim, F&& f) {
+  constexpr int V = Piece<T>::V, most = L == 64 ? kWaveElems / V : 16384 / 256 / V;
+  const int it = (dim + L * V - 1) / (L * V);
   auto pick = [&](auto n) {
     constexpr int N = decltype(n)::value;
-    if constexpr (N <= most) f(std::integral_constant<int, NW>(), n);
+    if constexpr (N <= most) f(std::integral_constant<int, L>(), n);
   };
   if (it <= 1) pick(std::integral_constant<int, 1>());
   else if (it <= 2) pick(std::integral_constant<int, 2>());
@@ -278,14 +294,11 @@ void with_pieces(int it, F&& f) {
   else pick(std::integral_constant<int, 16>());
 }
 
-template <typename T>
-bool one_wave(int dim) { return dim <= 64 * kWaveElems; }
-
 template <typename T, typename F>
-void with_row(int dim, bool wave, F&& f) {
-  const int V = Piece<T>::V, L = wave ? 64 : 256, it = (dim + L * V - 1) / (L * V);
-  if (wave) with_pieces<T, 1>(it, f);
-  else with_pieces<T, 4>(it, f);
+void with_row(int dim, F&& f) {
+  if (with_narrow_row<T>(dim, f)) return;
+  if (dim <= 64 * kWaveElems) with_pieces<T, 64>(dim, f);
+  else with_pieces<T, 256>(dim, f);
 }
 
 // The gradient's waves a row: as few as hold it in kGradPieces 16-byte pieces a lane
@@ -302,11 +315,11 @@ int grad_waves(int dtype, int dim) {
   return nw;
 }
 
-template <typename T, int NW, typename F>
+template <typename T, int L, typename F>
 void with_grad_pieces(int it, F&& f) {
-  constexpr int most = NW < 8 ? kGradPieces : 16384 / (8 * 64 * Piece<T>::V);
+  constexpr int most = L < 512 ? kGradPieces : 16384 / (512 * Piece<T>::V);
   auto pick = [&](auto n) {
-    if constexpr (decltype(n)::value <= most) f(std::integral_constant<int, NW>(), n);
+    if constexpr (decltype(n)::value <= most) f(std::integral_constant<int, L>(), n);
   };
   if (it <= 1) pick(std::integral_constant<int, 1>());
   else if (it <= 2) pick(std::integral_constant<int, 2>());
@@ -318,12 +331,13 @@ void with_grad_pieces(int it, F&& f) {
 
 template <typename T, typename F>
 void with_grad_row(int dtype, int dim, F&& f) {
+  if (with_narrow_row<T>(dim, f)) return;
   const int nw = grad_waves(dtype, dim), it = pieces_a_lane(dtype, nw, dim);
   switch (nw) {
-    case 1: return with_grad_pieces<T, 1>(it, f);
-    case 2: return with_grad_pieces<T, 2>(it, f);
-    case 4: return with_grad_pieces<T, 4>(it, f);
-    default: return with_grad_pieces<T, 8>(it, f);
+    case 1: return with_grad_pieces<T, 64>(it, f);
+    case 2: return with_grad_pieces<T, 128>(it, f);
+    case 4: return with_grad_pieces<T, 256>(it, f);
+    default: return with_grad_pieces<T, 512>(it, f);
   }
 }
 
@@ -333,10 +347,10 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t st) {
   note_launch("norm", st);
   auto go = [&](auto type) {
     typedef decltype(type) T;
-    with_row<T>(a.dim, one_wave<T>(a.dim), [&](auto nw, auto it) {
-      constexpr int NW = decltype(nw)::value;
-      const unsigned g = (unsigned)std::min<int64_t>((a.rows + 4 / NW - 1) / (4 / NW), 1 << 20);
-      norm_kernel<T, NW, decltype(it)::value><<<g, 256, 0, st>>>(a);
+    with_row<T>(a.dim, [&](auto lanes, auto it) {
+      constexpr int L = decltype(lanes)::value, ROWS = 256 / L;
+      const unsigned g = (unsigned)std::min<int64_t>((a.rows + ROWS - 1) / ROWS, 1 << 20);
+      norm_kernel<T, L, decltype(it)::value><<<g, 256, 0, st>>>(a);
     });
   };
   if (a.dtype == 1) go(bf16());
@@ -349,7 +363,11 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t st) {
 // 32768 x 1024 in bf16 58 us with 512 and 65 with 256, 16384 x 2560 89 and 83.
 int norm_parts(int dtype, int64_t rows, int dim) {
   const int nw = grad_waves(dtype, dim);
-  const int64_t groups = 8 / nw, most = pieces_a_lane(dtype, nw, dim) <= (dtype == 1 ? 2 : 3) ? 512 : 256;
+  int64_t groups = 8 / nw;
+  const auto narrow = [&](auto lanes, auto) { groups = 512 / decltype(lanes)::value; };
+  if (dtype == 1) with_narrow_row<bf16>(dim, narrow);
+  else with_narrow_row<float>(dim, narrow);
+  const int64_t most = pieces_a_lane(dtype, nw, dim) <= (dtype == 1 ? 2 : 3) ? 512 : 256;
   return (int)std::min<int64_t>(most, (rows + groups - 1) / groups);
 }
 
@@ -358,8 +376,8 @@ hipError_t launch_norm_backward(const NormArgs& a, hipStream_t st) {
   note_launch("norm_bwd", st);
   auto go = [&](auto type) {
     typedef decltype(type) T;
-    with_grad_row<T>(a.dtype, a.dim, [&](auto nw, auto it) {
-      norm_bwd_kernel<T, decltype(nw)::value, decltype(it)::value><<<parts, 512, 0, st>>>(a);
+    with_grad_row<T>(a.dtype, a.dim, [&](auto lanes, auto it) {
+      norm_bwd_kernel<T, decltype(lanes)::value, decltype(it)::value><<<parts, 512, 0, st>>>(a);
     });
   };
   if (a.dtype == 1) go(bf16());

@@ -92,6 +92,14 @@ def test_norm_and_gradients(dt, kind, rows, dim):
         check_backward(p, x, ww, dy, more, g.dx, dw, db)
 
 
+# rows that share a wave, at the edges of 8, 16 and 32 lanes, in a last workgroup that is not full
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("kind", [ip.IPTTT_NORM_RMS, ip.IPTTT_NORM_LAYER], ids=["rms", "layer"])
+@pytest.mark.parametrize("rows, dim", [(1, 64), (131, 8), (131, 32), (259, 40), (67, 128), (601, 136), (45, 256), (130, 264)])
+def test_narrow_rows(dt, kind, rows, dim):
+    test_norm_and_gradients(dt, kind, rows, dim)
+
+
 # more rows than the gradient's launch has places, for one to eight waves a row
 @pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("rows, dim", [(9001, 64), (4500, 1000), (2100, 2560), (1301, 4096), (700, 9728)])
