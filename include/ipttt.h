@@ -363,7 +363,7 @@ ipttt_status ipttt_z_backward_saved(const ipttt_problem *p, const void *H, const
  * the bytes (2.125 d_ff a token instead of 4 d_ff).  Of each token the values of
  * 64 neighbouring features (rounded to bf16, from feature 0 on, the last block
  * short where d_ff is no multiple of 64) share the scale s = max|g| / 127 (float)
- * and are held as the integers round(127 g / max|g|), ties away from zero: a value
+ * and are held as the integers nearest 127 g / max|g|, ties to the even one: a value
  * is off by at most half of 1/127 of the largest beside it, and no token's values
  * depend on another token.  A block whose largest value is below 2^-100 is kept as zeros; one that holds
  * an infinity or a NaN comes back as NaN.

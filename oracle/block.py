@@ -75,7 +75,7 @@ def kept8(g, block=64):
         b = g[:, c:c + block]
         top = np.abs(b).max(1, keepdims=True)
         top = np.where(top > 0, top, 1.0)
-        # bf16 values times 127 are exact, so ties are met exactly; they go away from zero
-        q = np.sign(b) * np.floor(np.abs(b) * 127.0 / top + 0.5)
+        # bf16 values times 127 are exact, so ties are met exactly; they go to the even integer
+        q = np.rint(b * 127.0 / top)
         out[:, c:c + block] = q * (top / 127.0)
     return out

@@ -151,13 +151,15 @@ __device__ __forceinline__ void store_rows_swz(const bf16* rowT, bf16* __restric
 // ------------------------------------------------------- values kept in 8 bits
 
 // kKeep8 neighbouring values of a row share a scale: v = q s with s = max|v| / 127 and
-// q = round(127 v / max), an integer in [-127, 127], ties away from zero.  The
-// quotient of bf16 values is either a tie exactly (v = max / 2 is one) or 2^-16 of its
-// size away from any; multiplying by 127 / max made 2^-21 too large therefore decides
-// every value, with two operations each.  (Dividing exactly, with the largest taken of
-// the rounded values, a Z call that keeps 8 bits took 1306 instead of 1192 us at
-// 16384 x 2560 x 9728.)  Blocks below 2^-100 are zeros; one with an infinity or a NaN
-// gets a NaN scale.
+// q the integer nearest 127 v / max, in [-127, 127], ties to the even one.  The quotient
+// of bf16 values is either a tie exactly or 2^-16 of its size away from any.  It is a tie,
+// 254 v = (2n + 1) max, only if the prime 127 divides 2n + 1 (v = max / 2, 63.5, which
+// goes to 64) or the largest's significand is 254.  There 127 / max is a power of two, and
+// the product rounds as the quotient does; for every other largest, multiplying by
+// 127 / max made 2^-21 too large decides every value and takes 63.5 up.  Two operations
+// a value.  (Dividing exactly, with the largest taken of the rounded values, a Z call that
+// keeps 8 bits took 1306 instead of 1192 us at 16384 x 2560 x 9728.)  Blocks below 2^-100
+// are zeros; one with an infinity or a NaN gets a NaN scale.
 constexpr int kKeep8 = 64;
 
 template <int CTRL>
@@ -177,6 +179,9 @@ struct Keep8Scale {
     scale = bad ? __builtin_nanf("") : none ? 0.0f : m * (1.0f / 127.0f);
     // (128 / max: neither a denormal number nor an infinity)
     inv = none || bad ? 0.0f : __builtin_amdgcn_rcpf(m * 0x1p-7f) * (0.9921875f * (1.0f + 0x1p-21f));
+    // (significand 254: the power of two just below)
+    if ((__builtin_bit_cast(uint32_t, m) & 0x7FFFFFu) == 0x7E0000u)
+      inv = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, inv) & 0x7F800000u);
   }
   // the bytes of N bf16 values: adding 1.5 2^23 rounds to the integer and leaves it in
   // the low bits (0 for a bad block: of the sum itself, or of a NaN that comes from bf16)

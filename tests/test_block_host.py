@@ -70,6 +70,12 @@ def test_kept_values():
     assert not ob.kept8(np.zeros((2, 70))).any()
 
 
+def test_kept_values_of_ties():
+    """Halves go to the even integer, as torch.round takes them."""
+    g = np.array([[127.0, 0.5, -0.5, 1.5, -2.5, 62.5, 63.5, -126.5] + [0.0] * 56])
+    assert ob.kept8(g)[0, :8].tolist() == [127.0, 0.0, 0.0, 2.0, -2.0, 62.0, 64.0, -126.0]
+
+
 # ------------------------------------------------------------ the C entries
 
 class Rows(ctypes.Structure):

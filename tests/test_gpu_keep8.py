@@ -227,3 +227,38 @@ def test_streams_and_graphs():
         got = [x.clone() for x in (Z, g.dH, g.dW_gate, g.dW_up)]
         both()
         assert all(torch.equal(a, b) for a, b in zip(got, (Z, g.dH, g.dW_gate, g.dW_up)))
+
+
+def unit_kept(W):
+    """The integers and scales of G = W^T [tokens = inputs, features], U = W^T beside it."""
+    f, d = W.shape
+    p = ip.Problem(1, d, d, f, 64)
+    Z = torch.empty(d, f, dtype=torch.bfloat16, device="cuda")
+    kept = torch.empty(ip.ipttt_saved8_bytes(p), dtype=torch.uint8, device="cuda")
+    ip.ipttt_z_save8(p, torch.eye(d).bfloat16().cuda(), W, W, Z, kept)
+    return kept_parts(kept, d, f)
+
+
+def nearest(W):
+    """The definition's integers of G = W^T."""
+    g = np64(W).T
+    top = np.repeat(np.abs(g).reshape(len(g), -1, 64).max(-1), 64, 1)
+    return np.rint(g * 127.0 / np.where(top > 0, top, 1.0))
+
+
+@pytest.mark.parametrize("d", [256, 4096])   # tiles of 4 and of 8 waves
+def test_every_integer_is_the_nearest_and_ties_are_even(d):
+    W = randn(generator(6), BF16, d, d)
+    half = torch.arange(64, device="cuda") + 0.5
+    n = d // 64
+    for t in range(128):       # token t: a largest of each significand, halves of its steps beside it
+        top = 1 + t / 128
+        step = 2.0 ** (t % 40 - 20)
+        block = W[64 * (t % n):64 * (t % n) + 64, t]
+        block.copy_((torch.where(half.long() % 3 == 0, -1, 1) * half * (top / 127 if t == 126 else top / 128) * step).bfloat16())
+        block[0], block[1], block[2] = top * step, top / 2 * step, -top / 2 * step
+    q, scale = unit_kept(W)
+    want = nearest(W)
+    assert np.isfinite(scale).all() and np.array_equal(q, want)
+    values = np64(W).T * 127 / np.repeat(np.abs(np64(W).T).reshape(d, -1, 64).max(-1), 64, 1)
+    assert (np.abs(values[126]) % 1 == 0.5).sum() >= 60    # the ties are there
