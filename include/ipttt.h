@@ -547,7 +547,8 @@ typedef struct {
 /* Norm of each row: with mu = mean(x) (IPTTT_NORM_LAYER) or 0 (IPTTT_NORM_RMS),
  * r = 1 / sqrt(mean((x - mu)^2) + eps) and xn = (x - mu) r,
  *   y = xn w + b.
- *   x [rows, dim], y [rows, dim] out; y may be x (same data and stride)
+ *   x [rows, dim], y [rows, dim] out; y may be x (same data and stride), nothing
+ *          else may overlap it
  *   w, b [dim] (dtype), either NULL: left out
  * The mean is subtracted before the squares are summed, so a row's mean may be
  * far larger than its spread.  One launch. */
@@ -561,7 +562,8 @@ ipttt_status ipttt_norm(const ipttt_norm_problem *p, const ipttt_rows *x, const 
  *   dy [rows, dim]
  *   dres         NULL, or [rows, dim]: the cotangent that reaches x past the
  *                norm, such as the residual stream's
- *   dx [rows, dim] out; may be dy or dres (same data and stride)
+ *   dx [rows, dim] out; may be x, dy or dres (same data and stride), nothing else
+ *                may overlap an output
  *   dw, db [dim] float out, either NULL: not wanted; summed in a fixed order
  * ws: ipttt_norm_backward_workspace_bytes(p), 256-byte aligned; may be NULL
  * where dw and db are. */

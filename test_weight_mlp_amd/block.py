@@ -131,7 +131,7 @@ class NormGrads:
 
 
 def ipttt_norm_backward(p: NormProblem, x, w, dy, dx, dw, db, ws, dres=None, stream=None):
-    """dx (plus dres), dw and db (either None) from the cotangent dy; dx may be dy or dres."""
+    """dx (plus dres), dw and db (either None) from the cotangent dy; dx may be x, dy or dres."""
     status = (_calls or _native()).norm_backward(p.address, x, w, dy, dres, dx, dw, db, ws, _on(stream, x))
     if status:
         _check(status, "ipttt_norm_backward")

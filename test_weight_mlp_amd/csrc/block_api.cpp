@@ -156,6 +156,8 @@ ipttt_status ipttt_norm(const ipttt_norm_problem* p, const ipttt_rows* x, const 
   IPTTT_TRY(view(y, p->rows, p->dim, false, &a.y));
   IPTTT_TRY(vectors(w, b));
   IPTTT_TRY(in_place(a.y, a.x));
+  IPTTT_TRY(apart(a.y.p, w));
+  IPTTT_TRY(apart(a.y.p, b));
   a.w = w;
   a.b = b;
   (void)hipGetLastError();
@@ -180,6 +182,7 @@ ipttt_status ipttt_norm_backward(const ipttt_norm_problem* p, const ipttt_rows* 
   IPTTT_TRY(in_place(a.dx, a.x));
   IPTTT_TRY(in_place(a.dx, a.dy));
   IPTTT_TRY(in_place(a.dx, a.dres));
+  IPTTT_TRY(apart(a.dx.p, w));
   IPTTT_TRY(apart(dw, db));
   for (const void* in : {static_cast<const void*>(a.x.p), w, static_cast<const void*>(a.dy.p),
                          static_cast<const void*>(a.dres.p), static_cast<const void*>(a.dx.p)}) {

@@ -180,6 +180,13 @@ def test_arguments_refused(call, args):
 
 
 @needs_lib
+@pytest.mark.parametrize("call, change", [(norm_call, dict(y=rows(2, 64))), (norm_call, dict(y=rows(3, 64))),
+                                          (norm_backward_call, dict(dx=rows(2, 64)))], ids=["y over w", "y over b", "dx over w"])
+def test_norm_outputs_over_a_weight_refused(call, change):
+    assert call(**change) == ARG
+
+
+@needs_lib
 def test_problem_pointer_may_not_be_null():
     L, r = bk._lib(), rows(1, 64)
     assert L.ipttt_norm(None, pack(r), None, None, pack(r), None) == NULL

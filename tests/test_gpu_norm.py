@@ -137,6 +137,23 @@ def test_slices_of_wider_tensors_and_in_place(rows, dim):
 
 
 @pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("rows, dim", [(5, 64), (2100, 320), (700, 2560), (300, 4096), (260, 9728)])
+def test_gradient_over_the_input(dt, rows, dim):
+    """dx over x, over columns of a wider tensor and over all of it; several rounds of rows."""
+    for kind in (ip.IPTTT_NORM_RMS, ip.IPTTT_NORM_LAYER):
+        p = ip.NormProblem(rows, dim, dt, kind, EPS)
+        x0, w, _, dy, dres = inputs(dt, rows, dim)
+        g, g2 = ip.NormGrads(p), ip.NormGrads(p)
+        ip.ipttt_norm_backward(p, x0, w, dy, g.dx, g.dw, g.db, g.ws, dres=dres)
+        x, x_kept = wide(dt, rows, dim, 32)
+        x.copy_(x0)
+        for over in (x, x0):
+            ip.ipttt_norm_backward(p, over, w, dy, over, g2.dw, g2.db, g2.ws, dres=dres)
+            assert torch.equal(over, g.dx) and torch.equal(g2.dw, g.dw) and torch.equal(g2.db, g.db)
+        assert x_kept()
+
+
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
 def test_rows_far_from_zero_and_rows_of_nothing(dt):
     """A mean a thousand times the spread; zeros; a constant row; tiny and huge rows."""
     dim = 512
