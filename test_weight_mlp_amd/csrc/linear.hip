@@ -541,7 +541,8 @@ void launch_few(const GemmArgs& g, hipStream_t st) {
 // time 13.3), 8192 x 6144 without an activation 17 us for 101 MB.
 template <typename T>
 __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a, int64_t strip) {
-  typedef T vec __attribute__((ext_vector_type(8)));
+  typedef Vec<T, 8> vec;
+  static_assert(alignof(vec) <= 16, "what the entries ask of a tensor");
   constexpr int U = 2;
   __shared__ float red[8][256];
   const int cg = threadIdx.x & 31, rg = threadIdx.x >> 5;

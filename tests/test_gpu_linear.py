@@ -231,6 +231,30 @@ def test_columns_of_wider_tensors_and_in_place(m, k, n):
         assert x_kept() and res_kept() and y_kept() and pre_kept() and dy_kept() and dx_kept()
 
 
+@pytest.mark.parametrize("m, k, n", [(3, 64, 72), (40, 192, 64), (300, 256, 520)])
+@pytest.mark.parametrize("kind", ["none", "gelu"])
+def test_tensors_that_start_at_16_bytes(m, k, n, kind):
+    """fp32 tensors whose rows of 8 elements start in the middle of 32 bytes."""
+    p = ip.LinearProblem(m, k, n, F32, ACTS[kind])
+    x0, W, b, pre0, dy0 = inputs(F32, m, k, n)
+
+    def placed(rows, cols, values=None):
+        t = torch.full((rows, cols + 8), 7.0, device="cuda")[:, 4:4 + cols]
+        assert t.data_ptr() % 32 == 16
+        return t if values is None else t.copy_(values)
+
+    x, dy, dx, y, res = placed(m, k, x0), placed(m, n, dy0), placed(m, k), placed(m, n), placed(m, n, pre0)
+    pre = placed(m, n, pre0) if kind != "none" else None
+    want, _ = forward(p, x0, W, b, pre0)
+    ip.ipttt_linear(p, x, W, y, b=b, res=res, ws=ip.linear_workspace(p))
+    assert torch.equal(y, want)
+    g, g2 = ip.LinearGrads(p), ip.LinearGrads(p)
+    ip.ipttt_linear_backward(p, x0, W, dy0, g.dx, g.dW, g.db, g.ws, pre=None if pre is None else pre0)
+    ip.ipttt_linear_backward(p, x, W, dy, dx, g2.dW, g2.db, g2.ws, pre=pre)
+    check_backward(p, kind, x, W, pre, dy, dx, g2.dW, g2.db)
+    assert torch.equal(dx, g.dx) and torch.equal(g2.dW, g.dW) and torch.equal(g2.db, g.db)
+
+
 @pytest.mark.parametrize("m", [1, 20, 100, 513])
 def test_rows_with_infinities_stay_their_own(m):
     k, n = 256, 320
