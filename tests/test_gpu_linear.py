@@ -292,6 +292,27 @@ def test_activations_of_extreme_values():
             within(g.dx, slope, 64 * E32 * (1 + np.minimum(np.abs(np64(x)), 100)) + 2 * HALF[dt] * np.abs(slope))
 
 
+@pytest.mark.parametrize("m", [2, 130])   # one pass over the weights; tiles
+def test_gelu_of_negative_values_keeps_their_bits(m):
+    """Relative to the value, through the unit matrix (exact).  The tail's polynomial is
+    off by 0.5 roundings, its evaluation by up to 8 (an emulation of the fp32 steps), the
+    reciprocal and the exponential by an ulp each (2 + 2), the product with v by one: 14,
+    bounded by 16.  The slope's second term, v times the density, is the larger: the tail's
+    and the density's errors, 16 and 8, add to less than 28 of their difference."""
+    g = generator(5)
+    v = -3 - 9 * torch.rand(m, 64, generator=g, device="cuda")
+    W = torch.eye(64, device="cuda")
+    p = ip.LinearProblem(m, 64, 64, F32, ACTS["gelu"])
+    y, pre = forward(p, v, W, keep=True)
+    want = ob.act("gelu", np64(v))
+    assert torch.equal(pre, v)
+    within(y, want, 16 * E32 * np.abs(want))
+    grads = ip.LinearGrads(p)
+    ip.ipttt_linear_backward(p, v, W, torch.ones_like(v), grads.dx, None, None, grads.ws, pre=pre)
+    slope = ob.slope("gelu", np64(v))
+    within(grads.dx, slope, 28 * E32 * np.abs(slope))
+
+
 @pytest.mark.parametrize("m", [1, 31, 200, 700])
 def test_a_row_does_not_depend_on_the_others(m):
     """The same row at other places of a call of the same size."""
