@@ -292,6 +292,44 @@ def test_activations_of_extreme_values():
             within(g.dx, slope, 64 * E32 * (1 + np.minimum(np.abs(np64(x)), 100)) + 2 * HALF[dt] * np.abs(slope))
 
 
+@pytest.mark.parametrize("dt", **IDS)
+@pytest.mark.parametrize("kind", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("m", [3, 100])   # one pass over the weights; tiles
+def test_infinite_and_nan_values_before_an_activation(m, kind, dt):
+    """Infinities and a NaN come in through the bias, and through pre in the gradient:
+    where the definition has a number or an infinity so has the call, where it has a NaN
+    (0 times an infinity) the call has one, and the other outputs are those without them."""
+    k = n = 64
+    x, W, b, pre, dy = inputs(dt, m, k, n)
+    p = ip.LinearProblem(m, k, n, dt, ACTS[kind], grad_dtype=dt)
+    clean, _ = forward(p, x, W, b)
+    odd = {3: float("inf"), 17: float("-inf"), 40: float("nan")}
+    for at, v in odd.items():
+        b[at] = v
+    y, kept = forward(p, x, W, b, keep=True)
+    rest = [i for i in range(n) if i not in odd]
+    assert torch.equal(y[:, rest], clean[:, rest])
+    with np.errstate(invalid="ignore", over="ignore"):
+        v = np.array(list(odd.values()))
+        act, slope = ob.act(kind, v), ob.slope(kind, v)
+    got, mid = np64(y)[:, list(odd)], np64(kept)[:, list(odd)]
+    assert np.array_equal(mid, np.broadcast_to(v, mid.shape), equal_nan=True)
+    assert np.array_equal(got, np.broadcast_to(act, got.shape), equal_nan=True)
+    g, g2 = ip.LinearGrads(p), ip.LinearGrads(p)
+    none = kind == "none"
+    ip.ipttt_linear_backward(p, x, W, dy, g.dx, g.dW, g.db, g.ws, pre=None if none else pre)
+    dirty = pre.clone()
+    dirty[m // 2, list(odd)] = torch.tensor(v, device="cuda").to(dirty.dtype)
+    ip.ipttt_linear_backward(p, x, W, dy, g2.dx, g2.dW, g2.db, g2.ws, pre=None if none else dirty)
+    others = [i for i in range(m) if none or i != m // 2]
+    assert torch.equal(g2.dx[others], g.dx[others]) and torch.equal(g2.dW[rest], g.dW[rest])
+    assert torch.equal(g2.db[rest], g.db[rest])
+    finite = [at for at, s in zip(odd, slope) if np.isfinite(s)]
+    bad = [at for at, s in zip(odd, slope) if not np.isfinite(s)]
+    assert g2.db[finite].isfinite().all() and g2.db[bad].isnan().all() and g2.dW[bad].isnan().all()
+    assert g2.dx[m // 2].isnan().all() if bad else g2.dx.isfinite().all()
+
+
 @pytest.mark.parametrize("m", [2, 130])   # one pass over the weights; tiles
 def test_gelu_of_negative_values_keeps_their_bits(m):
     """Relative to the value, through the unit matrix (exact).  The tail's polynomial is
