@@ -369,6 +369,7 @@ ipttt_status ipttt_z_backward_saved(const ipttt_problem *p, const void *H, const
  * an infinity or a NaN comes back as NaN.
  *   kept  ipttt_saved8_bytes(p) bytes (0 for an invalid problem and for fp32
  *         data), 256-byte aligned; the bytes are opaque
+ *   ws    as for the other backward calls; this one builds no segment table
  * bf16 data only (IPTTT_ERR_DTYPE).  kept_bytes too small: IPTTT_ERR_WORKSPACE.
  * Z is ipttt_z's; the gradients are those of ipttt_z_backward_saved for the
  * values that were kept. */

@@ -112,6 +112,48 @@ ipttt_status check_keep8(const Prob& p, const void* kept, size_t bytes, Keep8Lay
   return bytes < l->bytes ? IPTTT_ERR_WORKSPACE : IPTTT_OK;
 }
 
+// The products of the backward from 8 bits, without their tensors: dH = dG W_gate +
+// dU W_up, and dW_gate = dG^T H with dW_up = dU^T H.
+ipttt::GemmArgs keep8_dh(const Prob& p) {
+  ipttt::GemmArgs g{};
+  g.dtype = p.dtype;
+  g.M = p.M;
+  g.N = p.d;
+  g.K = p.f;
+  g.b_kmaj = 1;
+  g.two_pairs = 1;
+  return g;
+}
+ipttt::GemmArgs keep8_dw(const Prob& p) {
+  ipttt::GemmArgs g{};
+  g.dtype = p.dtype;
+  g.M = p.f;
+  g.N = p.d;
+  g.K = p.M;
+  g.a_kmaj = g.b_kmaj = 1;
+  g.c_f32 = 1;
+  g.two_products = 1;
+  return g;
+}
+
+// The 8-bit backward's own use of the backward workspace: dG, dU | partial
+// products of dH | of dW_gate and dW_up.
+struct Keep8Bwd {
+  size_t dg, du, part_h, part_w, total;
+};
+Keep8Bwd keep8_bwd_layout(const Prob& p) {
+  const size_t n = align256((size_t)p.M * p.f * elt_bytes(p));
+  size_t h, w;
+  ipttt::gemm_pair_workspace(keep8_dh(p), keep8_dw(p), &h, &w);
+  Keep8Bwd l;
+  l.dg = 0;
+  l.du = n;
+  l.part_h = 2 * n;
+  l.part_w = l.part_h + align256(h);
+  l.total = l.part_w + align256(w);
+  return l;
+}
+
 // Workspace: per-token segment bytes | segment table | one region that each
 // call uses for itself:
 //   ipttt_target       W_target^T, tap-major conv weights, conv output Y
@@ -220,30 +262,7 @@ Layout layout(const Prob& p, Passes ps = {0, 0}) {
 //   target_backward: tap-major conv weights | Y | dY (fp32) | Y^T, dV^T | conv
 //     partials (the 8-wave path keeps dW_target's token-slice partials in Y^T, dV^T)
 //   z_backward: dG, dU | W_gate^T, W_up^T | dG^T, dU^T, H^T
-// The products of the backward from 8 bits, without their tensors: dH = dG W_gate +
-// dU W_up, and dW_gate = dG^T H with dW_up = dU^T H.
-ipttt::GemmArgs keep8_dh(const Prob& p) {
-  ipttt::GemmArgs g{};
-  g.dtype = p.dtype;
-  g.M = p.M;
-  g.N = p.d;
-  g.K = p.f;
-  g.b_kmaj = 1;
-  g.two_pairs = 1;
-  return g;
-}
-ipttt::GemmArgs keep8_dw(const Prob& p) {
-  ipttt::GemmArgs g{};
-  g.dtype = p.dtype;
-  g.M = p.f;
-  g.N = p.d;
-  g.K = p.M;
-  g.a_kmaj = g.b_kmaj = 1;
-  g.c_f32 = 1;
-  g.two_products = 1;
-  return g;
-}
-
+// (z_backward from 8 bits has all of the workspace: keep8_bwd_layout)
 struct BwdLayout {
   size_t table, call, total;
   // scan_apply_backward
@@ -251,7 +270,7 @@ struct BwdLayout {
   // target_backward
   size_t convt, y, dy, yt, dvt, cpart;
   // z_backward
-  size_t dg, du, wgt, wut, dgt, dut, ht, gpart, gpart2;
+  size_t dg, du, wgt, wut, dgt, dut, ht;
   int64_t Mp;
 };
 
@@ -311,10 +330,6 @@ BwdLayout bwd_layout(const Prob& p) {
   l.dgt = take(tnfast ? 0 : (size_t)l.Mp * p.f * e);
   l.dut = take(tnfast ? 0 : (size_t)l.Mp * p.f * e);
   l.ht = take(tnfast ? 0 : (size_t)l.Mp * p.d * e);
-  size_t gx = 0, gw = 0;
-  if (p.dtype == IPTTT_BF16) ipttt::gemm_pair_workspace(keep8_dh(p), keep8_dw(p), &gx, &gw);
-  l.gpart = take(gx);
-  l.gpart2 = take(gw);
   const size_t zb = o;
   l.total = l.call + std::max(sa, std::max(tg, zb));
   return l;
@@ -758,7 +773,8 @@ ipttt_status ipttt_scan_apply_carry(const ipttt_problem* q, const void* Z, const
 size_t ipttt_backward_workspace_bytes(const ipttt_problem* q) {
   Prob p;
   if (check_problem(q, &p) != IPTTT_OK) return 0;
-  return bwd_layout(p).total;
+  const size_t n = bwd_layout(p).total;
+  return p.dtype == IPTTT_BF16 ? std::max(n, keep8_bwd_layout(p).total) : n;
 }
 
 }  // extern "C"
@@ -1017,11 +1033,10 @@ ipttt_status ipttt_target_backward(const ipttt_problem* q, const void* X0, const
 
 namespace {
 
-// GU: the G and U the forward saved (ipttt_z_save), or NULL (recomputed, or
-// read in 8 bits from k8).
+// GU: the G and U the forward saved (ipttt_z_save), or NULL (recomputed).
 ipttt_status z_backward(const ipttt_problem* q, const void* H, const void* W_gate, const void* W_up, const void* GU,
-                        const ipttt::Keep8* k8, const void* dZ, void* dH, float* dW_gate, float* dW_up, void* ws,
-                        size_t ws_bytes, void* stream) {
+                        const void* dZ, void* dH, float* dW_gate, float* dW_up, void* ws, size_t ws_bytes,
+                        void* stream) {
   Prob p;
   BwdLayout l;
   ipttt_status s;
@@ -1033,32 +1048,8 @@ ipttt_status z_backward(const ipttt_problem* q, const void* H, const void* W_gat
   uint8_t* segs;
   int32_t* table;
   char* c;
-  if (k8 == nullptr) {
-    if ((s = bwd_segments(q, p, ws, l, st, &segs, &table, &c)) != IPTTT_OK) return s;
-  } else {
-    c = static_cast<char*>(ws) + l.call;  // its products ask no segments
-  }
+  if ((s = bwd_segments(q, p, ws, l, st, &segs, &table, &c)) != IPTTT_OK) return s;
   void *dG = c + l.dg, *dU = c + l.du;
-  if (k8 != nullptr) {
-    IPTTT_TRY(ipttt::launch_gated_grad8(p, *k8, dZ, dG, dU, st));
-    // both products of dH summed in one, both weight gradients as one
-    ipttt::GemmArgs g = keep8_dh(p);
-    g.a = Rows{dG, p.f};
-    g.a2 = Rows{dU, p.f};
-    g.b = Rows{const_cast<void*>(W_gate), p.d};
-    g.b2 = Rows{const_cast<void*>(W_up), p.d};
-    g.c = Rows{dH, p.d};
-    g.part = reinterpret_cast<float*>(c + l.gpart);
-    ipttt::GemmArgs w = keep8_dw(p);
-    w.a = Rows{dG, p.f};
-    w.a2 = Rows{dU, p.f};
-    w.b = Rows{const_cast<void*>(H), p.d};
-    w.c = Rows{dW_gate, p.d};
-    w.c2 = Rows{dW_up, p.d};
-    w.part = reinterpret_cast<float*>(c + l.gpart2);
-    IPTTT_TRY(ipttt::launch_gemm_pair(g, w, st));
-    return IPTTT_OK;
-  }
   if (GU != nullptr) {
     IPTTT_TRY(ipttt::launch_gated_grad(p, GU, dZ, dG, dU, st));
   } else {
@@ -1114,14 +1105,14 @@ extern "C" {
 ipttt_status ipttt_z_backward(const ipttt_problem* q, const void* H, const void* W_gate, const void* W_up,
                               const void* dZ, void* dH, float* dW_gate, float* dW_up, void* ws, size_t ws_bytes,
                               void* stream) {
-  return z_backward(q, H, W_gate, W_up, nullptr, nullptr, dZ, dH, dW_gate, dW_up, ws, ws_bytes, stream);
+  return z_backward(q, H, W_gate, W_up, nullptr, dZ, dH, dW_gate, dW_up, ws, ws_bytes, stream);
 }
 
 ipttt_status ipttt_z_backward_saved(const ipttt_problem* q, const void* H, const void* W_gate, const void* W_up,
                                     const void* GU, const void* dZ, void* dH, float* dW_gate, float* dW_up, void* ws,
                                     size_t ws_bytes, void* stream) {
   if (GU == nullptr) return IPTTT_ERR_NULL;
-  return z_backward(q, H, W_gate, W_up, GU, nullptr, dZ, dH, dW_gate, dW_up, ws, ws_bytes, stream);
+  return z_backward(q, H, W_gate, W_up, GU, dZ, dH, dW_gate, dW_up, ws, ws_bytes, stream);
 }
 
 ipttt_status ipttt_z_backward_saved8(const ipttt_problem* q, const void* H, const void* W_gate, const void* W_up,
@@ -1130,9 +1121,34 @@ ipttt_status ipttt_z_backward_saved8(const ipttt_problem* q, const void* H, cons
   Prob p;
   ipttt_status s = check_problem(q, &p);
   if (s != IPTTT_OK) return s;
-  Keep8Layout l;
-  if ((s = check_keep8(p, kept, kept_bytes, &l)) != IPTTT_OK) return s;
-  return z_backward(q, H, W_gate, W_up, nullptr, &l.k, dZ, dH, dW_gate, dW_up, ws, ws_bytes, stream);
+  Keep8Layout k;
+  if ((s = check_keep8(p, kept, kept_bytes, &k)) != IPTTT_OK) return s;
+  const Keep8Bwd l = keep8_bwd_layout(p);
+  if (ws == nullptr || ws_bytes < l.total) return IPTTT_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255) != 0) return IPTTT_ERR_ALIGN;
+  if (any_null(H, W_gate, W_up, dZ, dH, dW_gate, dW_up)) return IPTTT_ERR_NULL;
+  if (!all_aligned(H, W_gate, W_up, dZ, dH, dW_gate, dW_up)) return IPTTT_ERR_ALIGN;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  char* c = static_cast<char*>(ws);
+  void *dG = c + l.dg, *dU = c + l.du;
+  if ((s = hip_status(ipttt::launch_gated_grad8(p, k.k, dZ, dG, dU, st))) != IPTTT_OK) return s;
+  // both products of dH summed in one, both weight gradients as one; none asks segments
+  ipttt::GemmArgs g = keep8_dh(p);
+  g.a = Rows{dG, p.f};
+  g.a2 = Rows{dU, p.f};
+  g.b = Rows{const_cast<void*>(W_gate), p.d};
+  g.b2 = Rows{const_cast<void*>(W_up), p.d};
+  g.c = Rows{dH, p.d};
+  g.part = reinterpret_cast<float*>(c + l.part_h);
+  ipttt::GemmArgs w = keep8_dw(p);
+  w.a = Rows{dG, p.f};
+  w.a2 = Rows{dU, p.f};
+  w.b = Rows{const_cast<void*>(H), p.d};
+  w.c = Rows{dW_gate, p.d};
+  w.c2 = Rows{dW_up, p.d};
+  w.part = reinterpret_cast<float*>(c + l.part_w);
+  return hip_status(ipttt::launch_gemm_pair(g, w, st));
 }
 
 }  // extern "C"

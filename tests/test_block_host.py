@@ -224,6 +224,34 @@ def test_8_bits_are_for_bf16_and_need_their_buffer():
     assert b.GU is None and b.GU8.numel() == need
 
 
+@needs_lib
+def test_8_bits_add_nothing_to_the_backward_workspace_of_the_others():
+    """A shape of the general path whose largest backward call is Z's: its transposes
+    take more than the 8-bit products' parts, which lie in the same place."""
+    t, d, f, c = 16384, 72, 4104, 512
+
+    def r(n):
+        return -(-n // 256) * 256
+
+    own = 2 * r(t * f * 2) + 2 * r(d * f * 2) + 2 * r(t * f * 2) + r(t * d * 2)
+    assert ip.ipttt_backward_workspace_bytes(ip.Problem(1, t, d, f, c)) == r(t) + r(t // c * 12) + own
+
+
+@needs_lib
+@pytest.mark.skipif(torch.cuda.is_available(), reason="host-only check: the addresses are none of a device's")
+def test_8_bits_backward_asks_for_its_own_workspace_only():
+    lib, t, d, f = ip.library(), 16384, 72, 4104
+    p = ip.Problem(1, t, d, f, 512)
+    need = ip.ipttt_saved8_bytes(p)
+
+    def back(n):
+        return lib.ipttt_z_backward_saved8(p.ref, at(1), at(2), at(3), at(5), need, at(4), at(6), at(7), at(8), at(9), n, None)
+
+    # dG, dU and at most two tiles of 128 x 128 floats a compute unit for either product
+    assert back(2 * t * f * 2 - 1) == WORKSPACE
+    assert back(2 * t * f * 2 + 2 * 512 * 65536) not in (OK, WORKSPACE)
+
+
 # --------------------------------------------------------------- the binding
 
 class _Stream:
