@@ -552,7 +552,8 @@ typedef struct {
  *          else may overlap it
  *   w, b [dim] (dtype), either NULL: left out
  * The mean is subtracted before the squares are summed, so a row's mean may be
- * far larger than its spread.  One launch. */
+ * far larger than its spread.  The squares are fp32: they overflow from 2^64 on,
+ * their sum somewhat before.  One launch. */
 ipttt_status ipttt_norm(const ipttt_norm_problem *p, const ipttt_rows *x, const void *w, const void *b,
                         const ipttt_rows *y, void *stream);
 
@@ -578,7 +579,8 @@ ipttt_status ipttt_norm_backward(const ipttt_norm_problem *p, const ipttt_rows *
 typedef enum { IPTTT_ACT_NONE = 0, IPTTT_ACT_SILU = 1, IPTTT_ACT_GELU = 2 } ipttt_act;
 
 typedef struct {
-  int64_t rows;        /* m: 1 .. 2^26 - 4                                       */
+  int64_t rows;        /* m: 1 .. 2^26 - 4; of m, k and n no two may make 2^24    */
+                       /* tiles of 128 x 128 or more (IPTTT_ERR_SHAPE)           */
   int64_t in_dim;      /* k: multiple of 8, 8 .. 2^20                            */
   int64_t out_dim;     /* n: multiple of 8, 8 .. 2^20                            */
   int32_t dtype;       /* ipttt_dtype of x, W, b, res, y, pre, dy and dx          */

@@ -11,11 +11,13 @@ using ipttt::Rows;
 
 namespace {
 
-constexpr int64_t kMaxRows = (int64_t(1) << 26) - 4;  // four rows a workgroup of 256 threads in a grid's x dimension
+constexpr int64_t kMaxRows = (int64_t(1) << 26) - 4;  // 2^20 tiles of 64 rows, which the plans count in int
 constexpr int64_t kMaxStride = int64_t(1) << 22;
 constexpr int64_t kMaxNorm = 16384;                   // elements of a row in one workgroup's registers
 constexpr int64_t kMaxLinear = int64_t(1) << 20;
-constexpr int64_t kMaxTiles = (int64_t(1) << 24) - 1; // workgroups of 256 threads in a grid's x dimension
+// Tiles of 128 x 128 of a product: there are four times as many of 64 x 64, and the plans
+// and walks count those, and the parts of cut ones, in int.
+constexpr int64_t kMaxTiles = (int64_t(1) << 24) - 1;
 
 #define IPTTT_TRY(e)                         \
   do {                                       \

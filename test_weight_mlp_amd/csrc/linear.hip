@@ -99,9 +99,12 @@ template <typename T, int N>
 using Vec = typename Run<T, N>::type;
 
 // One row's NJ neighbouring columns of a finished tile; res: the residual's.  A tile's
-// rows are stored past the caches (STREAM), which keeps the operands in them: 32768 x
-// 4096 x 2560 485 us and then 468, 1999 x 1024 x 4096 21.1 and 19.3.  (The column by column
-// stores of K-major products are short pieces that the L2 has to join.)
+// rows are stored past the caches (STREAM), which keeps the operands in them.  In bf16,
+// so and through the caches, a product alone: 1999 x 1024 x 4096 20.9 and 22.1 us, 32768 x
+// 4096 x 2560 with a residual 533 and 528; with the product that reads it next: 1024 ->
+// 4096 -> 1024 of 4096 rows 89 and 86, of 8192 152 and 150, of 32768 512 and 545, 2560 ->
+// 9728 -> 2560 of 4096 rows 387 and 415.  (The column by column stores of K-major products
+// are short pieces that the L2 has to join.)
 template <bool STREAM, typename T, int NJ>
 __device__ __forceinline__ void finish_row(const GemmArgs& g, int64_t m, int64_t n, const float (&bias)[NJ],
                                            const Vec<T, NJ>& res, float (&v)[NJ]) {
@@ -330,6 +333,8 @@ __global__ __launch_bounds__((ring::Geo<T, NW>::NT)) void ring_join_kernel(GemmA
   finish_block<T, NW, BK>(g, c, m0, n0, i, res, acc);
 }
 
+// A constant, not asked of the device, so that a workspace's size does not depend on the
+// device that is current when it is asked for.
 constexpr int kCus = 256;
 
 // The cut for which an estimate of the product's time is least (in us); only: 0, or the
@@ -340,11 +345,13 @@ RingPlan plan_ring(const GemmArgs& g, int only, double* us) {
   const bool h = g.dtype == 1;
   // us of a stage, of a workgroup alone on its CU and on a full one, of an item beside its
   // stages and of joining, fitted to some 1000 products of both types in all cuts (33 to
-  // 16384 rows): the cut so chosen takes 1 % longer than the best one on average.  In bf16
-  // small tiles are for few of them (512 x 1024 x 1024 8.4 us on 64 x 64, 13.0 on 128 x 128;
-  // 1999 x 1024 x 4096 21.0 on 128 x 128, 28 on 256 x 256); in fp32, where products take
-  // 16 times as long, 128 x 128 took 19 % longer than 64 x 64 on average and up to 4 % less
-  // (8192 x 2560 x 2560), 256 x 256 up to four times as long.
+  // 16384 rows): over 240 others the cut so chosen takes 0.7 % longer than the best one on
+  // average in bf16 and 0.5 % in fp32, 6 % at the ninth tenth, a third at most (dW of 4229
+  // rows, 64 -> 256: 14.7 us, in 6 parts 11.0).  In bf16 small tiles are for few of them
+  // (512 x 1024 x 1024 8.4 us on 64 x 64, 13.0 on 128 x 128; 1999 x 1024 x 4096 21.0 on 128 x
+  // 128, 28 on 256 x 256); in fp32, where products take 16 times as long, 128 x 128 took 19 %
+  // longer than 64 x 64 on average and up to 4 % less (8192 x 2560 x 2560), 256 x 256 up to
+  // four times as long.
   const struct Cost {
     int nw;
     double lone, full, item;
@@ -452,10 +459,11 @@ size_t ring_bytes(const RingPlan& p) {
 // fragments of 16x16 products (rows: 16 FB outputs, columns: rows of x), with all
 // their loads in flight; 16 waves take every 16th slice of K and are summed through
 // LDS.  A lane ends up with four neighbouring outputs of one row.
-// Bound by the launch and the weights' way from HBM: one row 2560 -> 6144 in bf16 8.9 us
-// for 31 MB (3.5 TB/s), 32 rows 4096 -> 2560 12.9 us, where each of 160 workgroups reads
-// the 262 KB of x beside 131 KB of weights.  Two neighbouring slices a wave, so that it
-// reads whole lines, changed nothing (9.1 and 13.0).
+// Bound by the launch and the weights' way to the CUs: one row 2560 -> 6144 in bf16 8.5 us
+// for 31 MB that the memory-side cache holds (3.7 TB/s) and 10.8 where they come from HBM
+// (2.9 TB/s), as those of a decoder's layers do; 32 rows 4096 -> 2560 13.1 and 14.6 us,
+// where each of 160 workgroups reads the 262 KB of x beside 131 KB of weights.  Two
+// neighbouring slices a wave, so that it reads whole lines, changed nothing.
 template <typename T, int MT, int FB>
 __global__ __launch_bounds__(1024) void few_kernel(GemmArgs g) {
   constexpr int W = 16;
@@ -520,10 +528,17 @@ __global__ __launch_bounds__(1024) void few_kernel(GemmArgs g) {
 // Where the tiles take less: from 65 rows on, and before that for large weights, which
 // every workgroup's reads of all of x hold up here (they grow with the rows and K; the
 // outputs cost little until there are more than 256 workgroups).  Us here and on the
-// tiles: bf16, 64 rows, 1024 -> 2048 6.9 and 8.0, 2560 -> 2560 13.9 and 11.6; 32 rows,
-// 2560 -> 6144 11.7 and 12.9, 2560 -> 9728 22.1 and 19.8; fp32, 32 rows, 1024 -> 2048 10.9
-// and 12.7, 4096 -> 2560 28.7 and 22.3; 16 rows, 4096 -> 2560 18.4 and 22.2, 2560 -> 9728
-// 46.0 and 33.8; 8 rows 34.7 and 33.8.
+// tiles, with weights that the memory-side cache holds, and [with weights from HBM]:
+//   bf16, 64 rows  1024 -> 4096 7.3, 7.6 [7.9, 14.0]    1024 -> 6144 12.7, 7.7 [13.7, 14.3]
+//                  1280 -> 4096 8.3, 9.9 [9.7, 12.1]    2560 -> 2560 13.7, 10.5 [16.8, 13.6]
+//         32 rows  2560 -> 6144 12.0, 13.1 [15.7, 15.4] 2560 -> 9728 22.5, 20.0 [25.9, 30.6]
+//         16 rows  2560 -> 9728 17.2, 19.6 [20.1, 30.2] 9728 -> 2560 19.4, 17.5 [24.1, 21.0]
+//   fp32, 32 rows  1024 -> 2048 11.3, 12.5 [11.9, 13.5] 2560 -> 2560 21.2, 17.0 [24.7, 19.4]
+//         16 rows  4096 -> 2560 18.5, 22.7 [21.3, 23.3] 2560 -> 9728 39.9, 33.3 [48.0, 34.9]
+//          8 rows  4096 -> 2560 15.9, 22.5 [18.1, 23.3] 2560 -> 9728 31.4, 33.2 [36.4, 34.8]
+// The bounds are those of weights in the cache.  On their wrong side lie, in bf16, 64 rows
+// 1536 -> 4096 (here 9.4, tiles 10.1), 32 rows 4096 -> 2560 (13.1, 11.2) and, from HBM, 32
+// rows 2560 -> 9728.
 bool few_rows(const GemmArgs& g) {
   if (g.a_kmaj || g.b_kmaj) return false;
   const bool h = g.dtype == 1;

@@ -34,12 +34,13 @@
 // lane ends up with neighbouring columns of C and stores 16 bytes at once.
 //
 // Measured (one MI355X, TFLOP/s; both K contiguous, B K-major, both K-major):
-// 8192^3 1519, 1501, 1474; 8192 x 6144 x 2560 1418, 1292, 1399.  The steady loop without
-// branches made these of 1434, 1340, 1325 and 1339, 1256, 1213; next to those stood, with
+// 8192^3 1370, 1394, 1380; 8192 x 6144 x 2560 1366, 1255, 1279; fp32: 8192 x 6144 x 2560 139,
+// 137, 136, 1021 x 4096 x 1024 128, 126.  Cards differ in their clock under load: on another,
+// bf16 was 1519, 1501, 1474 and 1418, 1292, 1399, and there the steady loop without branches
+// made these of 1434, 1340, 1325 and 1339, 1256, 1213; next to those stood, with
 // two whole stages instead of the ring, 1283, 1341, 1332 and 1294, 1251, 1265; with
 // 32x32x16 products 1372 and 1271 (first only); both parts' loads issued in one phase
-// 1354; four waves of 128 x 128 instead of eight 1040.  fp32: 8192 x 6144 x 2560 139, 142,
-// 141, 1021 x 4096 x 1024 123.
+// 1354; four waves of 128 x 128 instead of eight 1040.
 #pragma once
 
 #include <type_traits>
@@ -279,7 +280,7 @@ struct Walk {
 // epilogue(t, acc, idle) takes the finished tile, with idle two slots that nothing
 // reads or loads until the next barrier that all waves meet after it (waves may
 // still be reading them when it begins): block (i, j), element e of a lane is
-// row wm * 64 + i * 16 + 4 * (lane / 16) + e and LDS row wn * WN + j * 16 + lane % 16
+// row wm * WM + i * 16 + 4 * (lane / 16) + e and LDS row wn * WN + j * 16 + lane % 16
 // of B.  A and B are restrict so that the compiler tells the LDS reads apart from
 // the direct loads and puts no wait for those in front of them; the ring's own
 // waits order them.
